@@ -16,7 +16,8 @@ import math
 from . import _lib
 
 __all__ = ["attention_fwd", "attention_bwd", "attention_fwd_varlen", "attention_bwd_varlen",
-           "hadamard_quant_fp8", "attention_fwd_fp8"]
+           "hadamard_quant_fp8", "attention_fwd_fp8", "paged_tables", "paged_append", "attention_fwd_paged",
+           "attention_fwd_paged_prefix"]
 
 
 def _default_scale(d: int) -> float:
@@ -132,4 +133,96 @@ def attention_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, causal: bool 
     lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q8.device)
     _lib.fa_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, causal,
                     _default_scale(d) if scale is None else scale, stream)
+    return o, lse
+
+
+def _on(stream):
+    """Context in which outputs are allocated: the stream that writes them."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def paged_tables(cached_lens, new_lens, block_table, free_pages, page_size: int, num_pages: int, total: int,
+                 free_start=None, stream=None):
+    """Hands pages to each request's new tokens and maps the tokens to slots.
+
+    All tensors are int32 on the device: ``cached_lens`` and ``new_lens`` [B],
+    ``block_table`` [B,max_pages] (its new cells are filled in place),
+    ``free_pages`` the pool's unused pages, of which those from position
+    ``free_start`` (one element; default 0) on are handed out.  ``total`` is
+    the number of rows to map, at least the sum of ``new_lens``.  Returns
+    (seq_lens [B], cu_seqlens [B+1], slots [total], counts [2]): lengths with
+    the new tokens, row offsets, a slot per row (-1 for rows behind the last
+    request and for requests the pool had no pages for), and the next
+    ``free_start`` with the number of pages lacking."""
+    import torch
+    B, dev = block_table.shape[0], block_table.device
+    with _on(stream):
+        seq_lens, cu_seqlens, slots, counts = (torch.empty(n, dtype=torch.int32, device=dev)
+                                               for n in (B, B + 1, total, 2))
+    _lib.fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots,
+                         counts, page_size, num_pages, stream)
+    return seq_lens, cu_seqlens, slots, counts
+
+
+def paged_append(k, v, slots, k_cache, v_cache, stream=None):
+    """Writes k, v [total,Hkv,d] into the slots of k_cache, v_cache
+    [pages,Hkv,page_size,d] in place; a negative slot skips its row, and no
+    slot may occur twice."""
+    _lib.fa_paged_append(k, v, slots, k_cache, v_cache, stream)
+
+
+def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, prefix_len, workspace, stream):
+    """(O, LSE, workspace, max_new) of a paged forward call."""
+    import torch
+    total, Hq, d = q.shape
+    Hkv, page_size = k_cache.shape[1], k_cache.shape[2]
+    B, max_pages = block_table.shape
+    if max_new is None:
+        max_new = 1 if cu_seqlens is None else int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
+    if max_new == 0:
+        raise ValueError("no request has a row")
+    with _on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    return o, lse, workspace, max_new
+
+
+def attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, max_new: int | None = None,
+                        scale: float | None = None, window: int | None = None, workspace=None, stream=None):
+    """Attention of new tokens to a paged cache that holds their keys and
+    values.  q [total,Hq,d]: request b's rows are cu_seqlens[b] ..
+    cu_seqlens[b+1]-1, or row b alone without ``cu_seqlens``; the last of them
+    sees all seq_lens[b] keys, each row before it one less (``window`` leaves
+    a row its last ``window`` ones).  ``max_new`` bounds a request's rows
+    (default: the longest, read back from the device once).  Returns
+    (O [total,Hq,d], LSE [Hq,total] fp32); rows of no request stay unwritten."""
+    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, 0, workspace, stream)
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    _lib.fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new,
+                      _default_scale(q.shape[-1]) if scale is None else scale, workspace, window or 0, stream)
+    return o, lse
+
+
+def attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, seq_lens,
+                               cu_seqlens=None, max_new: int | None = None, scale: float | None = None,
+                               window: int | None = None, workspace=None, stream=None):
+    """``attention_fwd_paged`` for requests that all begin with the same
+    ``prefix_len`` tokens, stored once on ``prefix_pages`` (int32, on the
+    device): the prefix is read once for the whole batch.  ``block_table`` and
+    ``seq_lens`` describe each request's own keys behind it."""
+    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, prefix_len, workspace,
+                                                stream)
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    _lib.fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, cu_seqlens, o,
+                             lse, max_new, _default_scale(q.shape[-1]) if scale is None else scale, workspace,
+                             window or 0, stream)
     return o, lse

@@ -22,6 +22,7 @@ EXPORTS = (
     "fa_bwd_noalloc", "fa_hadamard_quant_fp8",
     "fa_hadamard_quant_workspace_bytes", "fa_fwd_fp8", "fa_get_device_status",
     "fa_selftest_bounded_wait", "fa_status_string", "fa_fwd_f32_out", "fa_probe_exp2", "fa_fwd_persistent",
+    "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_fwd_paged_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -65,6 +66,12 @@ def load():
         lib.fa_hadamard_quant_workspace_bytes.argtypes = [L, I]
         lib.fa_hadamard_quant_workspace_bytes.restype = Z
         lib.fa_fwd_fp8.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P]
+        lib.fa_paged_tables.argtypes = [P] * 9 + [I] * 6 + [P]
+        lib.fa_paged_append.argtypes = [P] * 5 + [I] * 6 + [P]
+        lib.fa_fwd_paged.argtypes = [P] * 8 + [I] * 10 + [F, I, P, Z, P]
+        lib.fa_fwd_paged_prefix.argtypes = [P] * 4 + [I] + [P] * 5 + [I] * 10 + [F, I, P, Z, P]
+        lib.fa_fwd_paged_workspace_bytes.argtypes = [I] * 9
+        lib.fa_fwd_paged_workspace_bytes.restype = Z
         lib.fa_get_device_status.argtypes = [P]
         lib.fa_selftest_bounded_wait.argtypes = [I, P]
         lib.fa_probe_exp2.argtypes = [P, I, I, P]
@@ -73,6 +80,7 @@ def load():
         lib.fa_status_string.restype = ctypes.c_char_p
         for name in ("fa_fwd", "fa_fwd_local", "fa_fwd_f32_out", "fa_fwd_persistent", "fa_bwd_local", "fa_fwd_varlen", "fa_bwd_varlen",
                      "fa_bwd", "fa_bwd_two_pass", "fa_bwd_noalloc", "fa_hadamard_quant_fp8", "fa_fwd_fp8",
+                     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix",
                      "fa_get_device_status", "fa_selftest_bounded_wait"):
             getattr(lib, name).restype = I
         _lib = lib
@@ -295,6 +303,124 @@ def fa_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, causal: bool
     _check("fa_fwd_fp8", load().fa_fwd_fp8(
         _ptr(q8), _ptr(k8), _ptr(v8), _ptr(q_descale), _ptr(k_descale), _ptr(v_descale), _ptr(o),
         _ptr(lse), B, Hq, Hkv, N, d, int(causal), float(scale), _stream(stream)))
+
+
+def _need_all(device, **tensors):
+    """Refuses what a paged call's pointers cannot take: a tensor off `device`
+    (which must be the current one: the library launches there), or one that
+    is not contiguous.  None passes."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensor must be contiguous")
+
+
+def _need_i32(**tensors):
+    """Checks (tensor, numel) pairs of int32 arrays; numel None: any."""
+    import torch
+    for name, (t, n) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name}: element type {t.dtype}, expected torch.int32")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
+
+
+def _same_type(q, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name}: element type {t.dtype}, expected {q.dtype}")
+
+
+def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots, counts,
+                    page_size: int, num_pages: int, stream=None):
+    """Pages and slots for a step's new tokens; int32 tensors as in fa.h."""
+    B, max_pages = block_table.shape
+    _need_all(block_table.device, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
+              free_start=free_start, block_table=block_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens, slots=slots,
+              counts=counts)
+    _need_i32(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_pages=(free_pages, None),
+              free_start=(free_start, 1), block_table=(block_table, None), seq_lens=(seq_lens, B),
+              cu_seqlens=(cu_seqlens, B + 1), slots=(slots, None), counts=(counts, 2))
+    num_free = free_pages.numel()
+    _check("fa_paged_tables", load().fa_paged_tables(
+        _ptr(cached_lens), _ptr(new_lens), _ptr(free_pages) if num_free else None, _ptr(free_start),
+        _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(slots), _ptr(counts), B, max_pages, int(page_size),
+        int(num_pages), num_free, slots.numel(), _stream(stream)))
+
+
+def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
+    """Writes k, v [total,Hkv,d] into slots of the caches [pages,Hkv,page_size,d]."""
+    total, Hkv, d = k.shape
+    num_pages, _, page_size, _ = k_cache.shape
+    code = _dtype_code(k)
+    _need_all(k.device, k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
+    _same_type(k, v=v, k_cache=k_cache, v_cache=v_cache)
+    _need_i32(slots=(slots, total))
+    if v.shape != k.shape or v_cache.shape != k_cache.shape or k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+        raise ValueError("k, v must be [total,Hkv,d] and the caches [pages,Hkv,page_size,d] of the same heads")
+    _check("fa_paged_append", load().fa_paged_append(_ptr(k), _ptr(v), _ptr(slots), _ptr(k_cache), _ptr(v_cache),
+                                                     total, Hkv, d, page_size, num_pages, code, _stream(stream)))
+
+
+def fa_fwd_paged_workspace_bytes(B: int, total: int, max_new: int, Hq: int, Hkv: int, d: int, max_pages: int,
+                                 page_size: int, prefix_len: int = 0) -> int:
+    return int(load().fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len))
+
+
+def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace, prefix=None):
+    """Checks shared by the paged forwards; returns their common sizes."""
+    import torch
+    total, Hq, d = q.shape
+    num_pages, Hkv, page_size, dk = k_cache.shape
+    B, max_pages = block_table.shape
+    code = _dtype_code(q)
+    _need_all(q.device, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
+              cu_seqlens=cu_seqlens, o=o, lse=lse, workspace=workspace, prefix_pages=prefix)
+    _same_type(q, k_cache=k_cache, v_cache=v_cache, o=o)
+    if lse.dtype != torch.float32:
+        raise TypeError(f"lse: element type {lse.dtype}, expected torch.float32")
+    _need_i32(block_table=(block_table, None), seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1),
+              prefix_pages=(prefix, None))
+    if dk != d or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
+    if o.shape != q.shape or lse.shape != (Hq, total):
+        raise ValueError("o must have q's shape and lse be [Hq,total]")
+    ws_bytes = workspace.numel() * workspace.element_size()
+    return B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages, code, ws_bytes
+
+
+def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new: int, scale: float,
+                 workspace, window: int = 0, stream=None):
+    """Attention of new rows q [total,Hq,d] to a paged cache (fa.h)."""
+    B, total, mn, Hq, Hkv, d, mp, ps, pages, code, ws_bytes = _paged_call(
+        q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace)
+    _check("fa_fwd_paged", load().fa_fwd_paged(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(o),
+        _ptr(lse), B, total, mn, Hq, Hkv, d, mp, ps, pages, int(window), float(scale), code, _ptr(workspace),
+        ws_bytes, _stream(stream)))
+
+
+def fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, seq_lens, cu_seqlens, o,
+                        lse, max_new: int, scale: float, workspace, window: int = 0, stream=None):
+    """fa_fwd_paged for requests that share their first prefix_len keys."""
+    B, total, mn, Hq, Hkv, d, mp, ps, pages, code, ws_bytes = _paged_call(
+        q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace, prefix_pages)
+    if prefix_pages.numel() * ps < prefix_len:
+        raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages of {ps} hold fewer than {prefix_len} tokens")
+    _check("fa_fwd_paged_prefix", load().fa_fwd_paged_prefix(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_pages), int(prefix_len), _ptr(block_table),
+        _ptr(seq_lens), _ptr(cu_seqlens), _ptr(o), _ptr(lse), B, total, mn, Hq, Hkv, d, mp, ps, pages, int(window),
+        float(scale), code, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:

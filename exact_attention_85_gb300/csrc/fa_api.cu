@@ -8,6 +8,7 @@
 
 #include "../../include/fa.h"
 #include "host_util.h"
+#include "paged.h"
 #include "ptx.cuh"
 
 // Optional NVTX ranges around every entry point that launches work (built
@@ -375,6 +376,119 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8, const flo
     fa::Fp8FwdArgs a{q8, k8, v8, q_descale, k_descale, v_descale, o_bf16, lse, B, Hq, Hkv, N, d,
                      causal ? 1 : 0, scale};
     return from_cuda(fa::launch_fwd_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// Checks shared by the paged-cache entry points.
+fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t dtype) {
+    if (Hkv < 1 || d < 1 || num_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return FA_ERR_UNSUPPORTED;
+    // slots and (page x head) planes are counted in 32 bits
+    if ((long long)num_pages * page_size > 0x7FFFFFFFll || (long long)num_pages * Hkv > 0x7FFFFFFFll)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_bytes) {
+    if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.lse || !a.block_table || !a.seq_lens) return FA_ERR_INVALID_ARG;
+    const void *ptrs[] = {a.q, a.k_cache, a.v_cache, a.o, a.lse};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(a.block_table) || !aligned4(a.seq_lens) || !aligned4(a.cu_seqlens) || !aligned4(a.prefix_pages))
+        return FA_ERR_INVALID_ARG;
+    if (a.B < 1 || a.total < 1 || a.max_new < 1 || a.Hq < 1 || a.max_pages < 1 || a.window < 0) return FA_ERR_INVALID_ARG;
+    if (a.Hkv < 1 || a.Hq % a.Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return FA_ERR_INVALID_ARG;
+    if (!a.cu_seqlens && (a.max_new != 1 || a.total < a.B)) return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(a.Hkv, a.d, a.page_size, a.num_pages, dtype);
+    if (s != FA_OK) return s;
+    if ((long long)a.max_pages * a.page_size + a.prefix_len > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll)
+        return FA_ERR_UNSUPPORTED;
+    const size_t need = fa::fwd_paged_workspace(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
+                                                a.prefix_len);
+    if (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u))
+        return FA_ERR_WORKSPACE;
+    return FA_OK;
+}
+}  // namespace
+
+fa_status_t fa_paged_tables(const int *cached_lens, const int *new_lens, const int *free_pages, const int *free_start,
+                            int *block_table, int *seq_lens, int *cu_seqlens, int *slots, int *counts, int B,
+                            int max_pages, int page_size, int num_pages, int num_free, int total, void *stream) {
+    FA_RANGE("fa_paged_tables");
+    if (!cached_lens || !new_lens || !block_table || !seq_lens || !cu_seqlens || !slots || !counts)
+        return FA_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || total < 1 || num_free < 0 || (num_free > 0 && !free_pages)) return FA_ERR_INVALID_ARG;
+    const int *in[] = {cached_lens, new_lens, free_pages, free_start};
+    int *out[] = {block_table, seq_lens, cu_seqlens, slots, counts};
+    for (const int *p : in)
+        if (!aligned4(p)) return FA_ERR_INVALID_ARG;
+    for (int *p : out) {
+        if (!aligned4(p)) return FA_ERR_INVALID_ARG;
+        for (const int *i : in)
+            if (p == i) return FA_ERR_INVALID_ARG;
+    }
+    if (!aligned16(slots)) return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(1, 128, page_size, num_pages, FA_BF16);
+    if (s != FA_OK) return s;
+    if (B > FA_PAGED_TABLES_MAX_B || (long long)max_pages * page_size > 0x7FFFFFFFll ||
+        (long long)B * max_pages > 0x7FFFFFFFll)
+        return FA_ERR_UNSUPPORTED;
+    fa::TablesArgs a{cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots, counts,
+                     B, max_pages, page_size, num_pages, num_free, total};
+    return from_cuda(fa::launch_paged_tables(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void *k_cache, void *v_cache, int total,
+                            int Hkv, int d, int page_size, int num_pages, fa_dtype_t dtype, void *stream) {
+    FA_RANGE("fa_paged_append");
+    if (!k || !v || !slots || !k_cache || !v_cache || total < 1) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots))
+        return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(Hkv, d, page_size, num_pages, dtype);
+    if (s != FA_OK) return s;
+    fa::AppendArgs a{k, v, slots, k_cache, v_cache, total, Hkv, d, page_size, num_pages};
+    return from_cuda(fa::launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
+                                    int page_size, int prefix_len) {
+    if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
+        page_size < 1 || prefix_len < 0)
+        return 0;
+    return fa::fwd_paged_workspace(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len);
+}
+
+fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *block_table,
+                         const int *seq_lens, const int *cu_seqlens, void *o, float *lse, int B, int total,
+                         int max_new, int Hq, int Hkv, int d, int max_pages, int page_size, int num_pages, int window,
+                         float scale, fa_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    FA_RANGE("fa_fwd_paged");
+    fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, nullptr, o, lse, B, total, max_new, Hq,
+                    Hkv, d, max_pages, page_size, num_pages, 0, window, scale, dtype == FA_BF16, workspace};
+    fa_status_t s = check_paged(a, dtype, workspace_bytes);
+    if (s != FA_OK) return s;
+    return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_fwd_paged_prefix(const void *q, const void *k_cache, const void *v_cache, const int *prefix_pages,
+                                int prefix_len, const int *block_table, const int *seq_lens, const int *cu_seqlens,
+                                void *o, float *lse, int B, int total, int max_new, int Hq, int Hkv, int d,
+                                int max_pages, int page_size, int num_pages, int window, float scale, fa_dtype_t dtype,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    FA_RANGE("fa_fwd_paged_prefix");
+    if (!prefix_pages || prefix_len < 1) return FA_ERR_INVALID_ARG;
+    fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, prefix_pages, o, lse, B, total, max_new,
+                    Hq, Hkv, d, max_pages, page_size, num_pages, prefix_len, window, scale, dtype == FA_BF16,
+                    workspace};
+    fa_status_t s = check_paged(a, dtype, workspace_bytes);
+    if (s != FA_OK) return s;
+    return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));
 }
 
 fa_status_t fa_get_device_status(void *stream) {

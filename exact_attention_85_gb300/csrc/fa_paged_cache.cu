@@ -1,0 +1,255 @@
+// fa_paged_cache.cu -- the bookkeeping and the writes of a paged key/value
+// cache: pages and slots for new tokens (fa_paged_tables), and the copy of
+// their keys and values into those slots (fa_paged_append).
+#include "../../include/fa.h"
+#include "host_util.h"
+#include "paged.h"
+#include "status.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kTabThreads = 256;
+constexpr int kRowsPerThread = 4;
+
+struct TablesParams {
+    TablesArgs a;
+    int shift;  // log2(page_size)
+    unsigned int *status;
+};
+
+__device__ __forceinline__ int pages_of(long long tokens, int shift) {
+    return (int)((tokens + (1ll << shift) - 1) >> shift);
+}
+
+// A request's lengths as they count: both non-negative, their sum within the
+// table's row.  A request that breaks this gets no rows and no pages.
+__device__ __forceinline__ bool request_lens(const TablesParams &p, int b, int &cached, int &fresh) {
+    cached = p.a.cached_lens[b];
+    fresh = p.a.new_lens[b];
+    if (cached >= 0 && fresh >= 0 && (long long)cached + fresh <= ((long long)p.a.max_pages << p.shift)) return true;
+    cached = 0;
+    fresh = 0;
+    return false;
+}
+
+// Pages and slots in one launch.  Request b needs
+//   need_b = ceil((c_b + n_b) / ps) - ceil(c_b / ps)
+// pages and takes those at first_b = sum of the needs before it in the free
+// list; its new rows start at cu_b = sum of the n before it.  Both sums run
+// over all requests, and every slot needs both.  A launch of its own for the
+// sums would cost more than the sums: so every block forms them for itself
+// (two integers a request, read from L2) and then writes its share of the
+// slots, looking a row's request up by bisection of cu in shared memory.  No
+// block waits for another: a slot in a page that this call hands out takes
+// the page from the free list, not from the table cell another block writes.
+__global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesParams p) {
+    extern __shared__ int smem[];
+    const int B = p.a.B;
+    int *cu = smem;             // [B + 1], clipped to total
+    int *first = smem + B + 1;  // [B]
+    __shared__ long long warp_rows[kTabThreads / 32], warp_need[kTabThreads / 32];
+    __shared__ int taken;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (B + kTabThreads - 1) / kTabThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+
+    const int start_in = p.a.free_start ? *p.a.free_start : 0;
+    const bool start_ok = start_in >= 0 && start_in <= p.a.num_free;
+    const int start = start_ok ? start_in : 0;
+    const int room = start_ok ? p.a.num_free - start : 0;
+
+    long long rows = 0, need = 0;
+    bool bad = !start_ok;
+    for (int b = b0; b < b1; ++b) {
+        int c, n;
+        if (!request_lens(p, b, c, n)) bad = true;
+        rows += n;
+        need += pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
+    }
+    // exclusive sums over the threads: within the warp, then over the warps
+    long long r_in = rows, n_in = need;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const long long r = __shfl_up_sync(0xffffffffu, r_in, s), n = __shfl_up_sync(0xffffffffu, n_in, s);
+        if (lane >= s) {
+            r_in += r;
+            n_in += n;
+        }
+    }
+    if (lane == 31) {
+        warp_rows[warp] = r_in;
+        warp_need[warp] = n_in;
+    }
+    if (tid == 0) taken = 0x7FFFFFFF;
+    __syncthreads();
+    long long r_at = r_in - rows, n_at = n_in - need, r_all = 0, n_all = 0;
+#pragma unroll
+    for (int w = 0; w < kTabThreads / 32; ++w) {
+        if (w < warp) {
+            r_at += warp_rows[w];
+            n_at += warp_need[w];
+        }
+        r_all += warp_rows[w];
+        n_all += warp_need[w];
+    }
+    if (r_all > p.a.total) bad = true;
+    for (int b = b0; b < b1; ++b) {
+        int c, n;
+        request_lens(p, b, c, n);
+        const int nd = pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
+        cu[b] = (int)min(r_at, (long long)p.a.total);
+        first[b] = (int)min(n_at, 0x7FFFFFFFll);
+        // the first request that does not fit ends what is taken
+        if (nd > 0 && n_at + nd > room) atomicMin(&taken, first[b]);
+        r_at += n;
+        n_at += nd;
+    }
+    if (tid == 0) cu[B] = (int)min(r_all, (long long)p.a.total);
+    __syncthreads();
+    if (bad && blockIdx.x == 0) record_bad_args(p.status);
+
+    if (blockIdx.x == 0 && tid == 0) {
+        const bool all = n_all <= room;
+        p.a.counts[0] = start + (all ? (int)n_all : taken);
+        p.a.counts[1] = all ? 0 : (int)min(n_all - room, 0x7FFFFFFFll);
+        p.a.cu_seqlens[B] = cu[B];
+    }
+    // lengths, offsets and table cells: a warp per request, dealt over all blocks
+    for (int b = blockIdx.x * (kTabThreads / 32) + warp; b < B; b += gridDim.x * (kTabThreads / 32)) {
+        int c, n;
+        request_lens(p, b, c, n);
+        const int old = pages_of(c, p.shift), nd = pages_of((long long)c + n, p.shift) - old;
+        const bool served = nd == 0 || (long long)first[b] + nd <= room;
+        if (lane == 0) {
+            p.a.seq_lens[b] = served ? c + n : c;
+            p.a.cu_seqlens[b] = cu[b];
+        }
+        if (served)
+            for (int i = lane; i < nd; i += 32) {
+                const int page = p.a.free_pages[start + first[b] + i];
+                if (page < 0 || page >= p.a.num_pages) record_bad_args(p.status);
+                p.a.block_table[(size_t)b * p.a.max_pages + old + i] = page;
+            }
+    }
+    // slots: four consecutive rows a thread
+    const long long stride = (long long)gridDim.x * kTabThreads * kRowsPerThread;
+    for (long long r0 = ((long long)blockIdx.x * kTabThreads + tid) * kRowsPerThread; r0 < p.a.total; r0 += stride) {
+        int out[kRowsPerThread];
+        int b = -1, c = 0, old = 0, page_at = -1, page = -1;
+        bool served = false;
+#pragma unroll
+        for (int k = 0; k < kRowsPerThread; ++k) {
+            const int r = (int)min(r0 + k, (long long)0x7FFFFFFE);
+            out[k] = -1;
+            if (r >= cu[B]) continue;
+            if (b < 0 || r >= cu[b + 1]) {
+                int lo = 0, hi = B - 1;  // the last request that starts at or before r
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (cu[mid] <= r) lo = mid; else hi = mid - 1;
+                }
+                b = lo;
+                int n;
+                request_lens(p, b, c, n);
+                old = pages_of(c, p.shift);
+                const int nd = pages_of((long long)c + n, p.shift) - old;
+                served = nd == 0 || (long long)first[b] + nd <= room;
+                page_at = -1;
+            }
+            if (!served) continue;
+            const int at = c + (r - cu[b]);
+            const int pg = at >> p.shift;
+            if (pg != page_at) {
+                page = pg < old ? p.a.block_table[(size_t)b * p.a.max_pages + pg]
+                                : p.a.free_pages[start + first[b] + pg - old];
+                if (page < 0 || page >= p.a.num_pages) {
+                    record_bad_args(p.status);
+                    page = -1;
+                }
+                page_at = pg;
+            }
+            if (page >= 0) out[k] = (page << p.shift) + (at & ((1 << p.shift) - 1));
+        }
+        if (r0 + kRowsPerThread <= p.a.total)
+            *reinterpret_cast<int4 *>(p.a.slots + r0) = make_int4(out[0], out[1], out[2], out[3]);
+        else
+            for (int k = 0; r0 + k < p.a.total; ++k) p.a.slots[r0 + k] = out[k];
+    }
+}
+
+// ------------------------------------------------------------------ append
+
+constexpr int kAppThreads = 256;
+
+struct AppendParams {
+    AppendArgs a;
+    int chunks;          // 16-byte pieces of one row: Hkv * d / 8
+    int rows_per_block;
+    int shift, d_chunks;  // log2(page_size), d / 8
+    unsigned int *status;
+};
+
+// One 16-byte piece of k and of v per thread and step: a copy whose
+// destination row comes from slots[].  [total][Hkv][d] -> [page][Hkv][ps][d]:
+// a (row, head) piece of d values is contiguous on both sides.
+__global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendParams p) {
+    const int row0 = blockIdx.x * p.rows_per_block;
+    const int rows = min(p.rows_per_block, p.a.total - row0);
+    const uint4 *k = static_cast<const uint4 *>(p.a.k) + (size_t)row0 * p.chunks;
+    const uint4 *v = static_cast<const uint4 *>(p.a.v) + (size_t)row0 * p.chunks;
+    uint4 *kc = static_cast<uint4 *>(p.a.k_cache), *vc = static_cast<uint4 *>(p.a.v_cache);
+    const int limit = p.a.num_pages << p.shift;
+    for (int i = threadIdx.x; i < rows * p.chunks; i += kAppThreads) {
+        const int row = i / p.chunks;
+        const int rest = i - row * p.chunks;
+        const int slot = p.a.slots[row0 + row];
+        if (slot < 0 || slot >= limit) {
+            if (slot >= limit) record_bad_args(p.status);
+            continue;
+        }
+        const int h = rest / p.d_chunks, c = rest - h * p.d_chunks;
+        const size_t to =
+            ((((size_t)(slot >> p.shift) * p.a.Hkv + h) << p.shift) + (slot & ((1 << p.shift) - 1))) * p.d_chunks + c;
+        kc[to] = k[i];
+        vc[to] = v[i];
+    }
+}
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
+    TablesParams p{a, log2_of(a.page_size), device_status_ptr()};
+    const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int);
+    cudaError_t e;
+    if (smem > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+            cudaSuccess)
+        return e;
+    const long long per_block = kTabThreads * kRowsPerThread;
+    const long long blocks = (a.total + per_block - 1) / per_block;
+    paged_tables_kernel<<<(unsigned)(blocks < 304 ? blocks : 304), kTabThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
+    AppendParams p;
+    p.a = a;
+    p.d_chunks = a.d / 8;
+    p.chunks = a.Hkv * p.d_chunks;
+    p.rows_per_block = p.chunks >= 1024 ? 1 : 1024 / p.chunks;
+    p.shift = log2_of(a.page_size);
+    p.status = device_status_ptr();
+    const unsigned blocks = (unsigned)((a.total + (long long)p.rows_per_block - 1) / p.rows_per_block);
+    paged_append_kernel<<<blocks, kAppThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace fa

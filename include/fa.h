@@ -338,6 +338,133 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8,
                        float scale, void *stream);
 
 /*
+ * Paged key/value cache: the serving side of the forward pass.  The pages of
+ * a cache hold `page_size` tokens each, in any order, so that requests of
+ * unknown final length share one pool:
+ *   k_cache, v_cache  [num_pages][Hkv][page_size][d], 16-bit, dense
+ *   block_table       int32 [B][max_pages]: request b's token t is row
+ *                     t % page_size of page block_table[b][t / page_size]
+ *   slot              page * page_size + row, one int32 per token
+ * page_size is a power of two, 16 .. 256; num_pages * page_size, max_pages *
+ * page_size and B * max_pages are at most 2^31 - 1.  Lengths, offsets, tables and slots are read
+ * on the device: page numbers outside 0 .. num_pages - 1 and lengths that
+ * break the rules below are reported by fa_get_device_status as
+ * FA_ERR_INVALID_ARG and never read or write out of range; what they concern
+ * is left unwritten or unspecified.  None of the pages of the cited articles
+ * describes a cache; the attention itself is theirs ([V2] section 6.1).
+ */
+
+/* Most requests of one fa_paged_tables call. */
+#define FA_PAGED_TABLES_MAX_B 16384
+
+/*
+ * Pages and slots for one step's new tokens, in one launch.  Request b holds
+ * cached_lens[b] tokens and gets new_lens[b] more; with ceil(x) in pages it
+ * needs need_b = ceil(cached + new) - ceil(cached) pages and takes them from
+ * the free list behind those of the requests before it:
+ *   first_b = free_start + sum of need over the requests before b
+ *   block_table[b][ceil(cached) + i] = free_pages[first_b + i], i < need_b
+ * A request with need_b > 0 whose pages would pass the end of the list is
+ * not served (nor is any later one with a need): its table row is left as it
+ * is, seq_lens[b] stays cached_lens[b] and its slots are -1.
+ *   cached_lens, new_lens [B] (in), new_lens >= 0, their sum at most
+ *       max_pages * page_size; sum of new_lens at most `total`
+ *   free_pages [num_free] (in; may be NULL if num_free = 0)
+ *   free_start [1] (in): first entry of free_pages to hand out, 0 ..
+ *       num_free; NULL = 0
+ *   block_table [B][max_pages] (in/out; only the new cells are written)
+ *   seq_lens [B] (out): cached + new
+ *   cu_seqlens [B + 1] (out): prefix sums of new_lens
+ *   slots [total] (out, 16-byte aligned): row cu_seqlens[b] + i is token
+ *       cached_lens[b] + i of request b; -1 behind the last request's rows
+ *   counts [2] (out): the next free_start, and how many pages were lacking
+ * All arrays are int32 on the device.  Outputs must not overlap inputs (the
+ * blocks of the launch read the inputs at any time; equal pointers are
+ * refused).  B <= FA_PAGED_TABLES_MAX_B (FA_ERR_UNSUPPORTED otherwise).
+ */
+fa_status_t fa_paged_tables(const int *cached_lens, const int *new_lens,
+                            const int *free_pages, const int *free_start,
+                            int *block_table, int *seq_lens, int *cu_seqlens,
+                            int *slots, int *counts, int B, int max_pages,
+                            int page_size, int num_pages, int num_free,
+                            int total, void *stream);
+
+/*
+ * Writes new keys and values into their slots of the cache.
+ *   k, v [total][Hkv][d] (in, token-major as in fa_fwd_varlen)
+ *   slots int32 [total] (in): row r goes to slot slots[r]; a negative slot
+ *       skips the row.  No slot may occur twice (which of its rows would
+ *       stay, and whether K's and V's are the same one, is not defined).
+ *   k_cache, v_cache (in/out): only the named slots are written
+ */
+fa_status_t fa_paged_append(const void *k, const void *v, const int *slots,
+                            void *k_cache, void *v_cache, int total, int Hkv,
+                            int d, int page_size, int num_pages,
+                            fa_dtype_t dtype, void *stream);
+
+/*
+ * Device workspace of fa_fwd_paged (prefix_len = 0) and fa_fwd_paged_prefix:
+ * partial results of key ranges that different blocks work on.
+ */
+size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq,
+                                    int Hkv, int d, int max_pages,
+                                    int page_size, int prefix_len);
+
+/*
+ * Forward attention of new tokens to a paged cache that already holds their
+ * own keys and values: decoding (one row a request), drafted tokens, and
+ * prompts read in by chunks, mixed at will.  [V2] section 6.1 with the
+ * softmax of a row split over key ranges where one block's share would leave
+ * the GPU idle: the ranges' (max, sum, O~) are merged by the same rescaling.
+ *   q, o [total][Hq][d] (in / out); lse [Hq][total] fp32 (out)
+ *   block_table [B][max_pages], seq_lens [B] (in): keys of each request
+ *   cu_seqlens [B + 1] (in): request b's rows are cu_seqlens[b] ..
+ *       cu_seqlens[b + 1] - 1, non-decreasing within 0 .. total, at most
+ *       max_new a request.  NULL: row b is request b's only one (max_new 1).
+ *   Row i of n_b rows stands at place p = seq_lens[b] - n_b + i and sees the
+ *   request's keys 0 .. p (the mask is aligned to the last key, unlike
+ *   fa_fwd's); window > 0 leaves it the `window` last of them.  Pages that
+ *   no row of the request sees are not read, nor are their table entries.
+ *   A row that sees nothing (p < 0) gets O = 0 and LSE = -infinity.
+ *   Rows of no request are left unwritten.  What a page holds behind its
+ *   request's last key has no effect, whatever it is.
+ *   workspace: at least fa_fwd_paged_workspace_bytes(..., prefix_len = 0)
+ *       bytes, 256-byte aligned, contents on entry do not matter; calls that
+ *       may run at the same time need workspaces of their own.
+ * Equal calls give equal bits.
+ */
+fa_status_t fa_fwd_paged(const void *q, const void *k_cache,
+                         const void *v_cache, const int *block_table,
+                         const int *seq_lens, const int *cu_seqlens, void *o,
+                         float *lse, int B, int total, int max_new, int Hq,
+                         int Hkv, int d, int max_pages, int page_size,
+                         int num_pages, int window, float scale,
+                         fa_dtype_t dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * fa_fwd_paged for requests that all continue one prefix, stored once: every
+ * request's keys are the prefix' prefix_len tokens and then its own.  The
+ * prefix is read once for all rows of the batch (they are the query rows of
+ * one tile of its keys), not once per request.
+ *   prefix_pages int32 [ceil(prefix_len / page_size)] (in), prefix_len >= 1
+ *   block_table, seq_lens: the requests' own keys only, on pages of their own
+ *   Places count from the prefix' start: p = prefix_len + seq_lens[b] - n_b
+ *   + i, for the causal mask and the window alike.  Otherwise as
+ *   fa_fwd_paged.
+ */
+fa_status_t fa_fwd_paged_prefix(const void *q, const void *k_cache,
+                                const void *v_cache, const int *prefix_pages,
+                                int prefix_len, const int *block_table,
+                                const int *seq_lens, const int *cu_seqlens,
+                                void *o, float *lse, int B, int total,
+                                int max_new, int Hq, int Hkv, int d,
+                                int max_pages, int page_size, int num_pages,
+                                int window, float scale, fa_dtype_t dtype,
+                                void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
  * Reads and clears the current device's status, which kernels set when
  * a bounded wait runs out, when packed sequence offsets read on the device
  * break the rules of fa_fwd_varlen, or when a kernel finds its shared-memory
