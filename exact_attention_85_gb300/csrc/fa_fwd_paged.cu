@@ -1,18 +1,622 @@
-// fa_fwd_paged.cu -- forward attention from a paged key/value cache.
+// fa_fwd_paged.cu -- forward attention from a paged key/value cache for
+// requests with few query rows (decoding, drafted tokens).
 //
 // Row i of request b (n_b new rows, len_b keys of its own, of which the last
 // n_b belong to the rows) stands at place p = len_b - n_b + i and sees its
-// own keys max(0, p - W + 1) .. p; with a shared prefix of P keys in front,
-// places count from the prefix' start.  One warp per (row, query head), keys
-// one by one with the running maximum and sum of the softmax.
+// own keys max(0, p - W + 1) .. p.  The n_b * g rows that read one key/value
+// head (g = Hq / Hkv query heads share it) form the one 16-row tile of a
+// warp-level MMA: S = Q K^T and O~ += P V with the running maximum and sum of
+// the softmax, exactly [V2] section 6.1 with 16 rows.  At 16 rows a key costs
+// 4 d bytes and 64 d tensor operations, far below the ratio the tensor cores
+// could sustain: the kernel is bound by reading the cache, and everything
+// here serves to keep copies in flight.
+//
+// Work is cut into units of one tile of keys (32 KB of K and V).  All units
+// of all (request, key/value head) pairs are numbered in order and every CTA
+// takes an equal, contiguous range, so a batch of any mixture of lengths
+// keeps every SM reading to the end; a CTA's range covers the end of one
+// pair, some whole pairs and the beginning of another.  Whole pairs are
+// written out directly; the parts of a pair that several CTAs share go to
+// the workspace as (O~ / l, log2 sum) and a second kernel merges them.
+//   warps 0-3  each a quarter of every tile's keys, all 16 rows; their four
+//              results are merged through the last tile's buffer
+//   warp 4     producer: plans the CTA's range, reads block-table entries,
+//              starts one TMA copy per (page, 64-column half) and one small
+//              copy of Q per pair, and describes each tile to the others
 #include "../../include/fa.h"
 #include "host_util.h"
+#include "mma_sync.cuh"
 #include "paged.h"
+#include "paged_dev.cuh"
 #include "ptx.cuh"
 
 namespace fa {
 
 namespace {
+
+constexpr int kConsumers = 4;  // warps
+constexpr int kFewThreads = 32 * (kConsumers + 1);
+constexpr int kMaxCtas = 304;  // two per SM
+constexpr int kMaxRows = 16;   // rows of a pair
+constexpr int kStages = 3;
+constexpr int kMinUnits = 2;   // tiles a CTA takes at least
+
+enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16 };
+
+// What the producer tells the consumers about a tile.
+struct TileInfo {
+    int row0, n, len, kv0;
+    int hk, flags, pad0, pad1;
+};
+
+// What a CTA whose last pair goes on in the next CTA leaves for the merge.
+struct PieceHeader {
+    int row0, n, hk, pieces;  // pieces 0: nothing to merge
+};
+
+template <int D>
+struct FewLayout {
+    static constexpr int TK = D == 128 ? 64 : 128;  // keys per tile
+    static constexpr int KW = TK / kConsumers;      // keys per warp and tile
+    static constexpr int HALVES = D / 64;           // 64-column boxes
+    static constexpr int HALF = TK * 128;           // bytes of one box column of a tile
+    static constexpr int TILE = HALF * HALVES;      // K or V
+    static constexpr int QBYTES = kMaxRows * D * 2;
+    static constexpr int OFF_Q = kStages * 2 * TILE;
+    static constexpr int OFF_INFO = OFF_Q + kStages * QBYTES;
+    static constexpr int OFF_BAR = OFF_INFO + kStages * (int)sizeof(TileInfo);
+    static constexpr int OFF_ML = OFF_BAR + 2 * kStages * 8;           // [3][4 warps][16]
+    static constexpr int OFF_MISC = OFF_ML + 3 * kConsumers * 16 * 4;  // abort flag, sums
+    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int ALLOC = BYTES + 1024;
+    static_assert(2 * (ALLOC + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(kConsumers * kMaxRows * D * 4 <= 2 * TILE, "the merge fits one stage");
+};
+
+struct FewParams {
+    PagedArgs a;
+    int shift;   // log2(page_size)
+    int group;   // query heads per key/value head
+    float scale_log2;
+    unsigned int *status;
+    PieceHeader *headers;  // [gridDim.x]
+    float *part_o;         // [gridDim.x][2][16][D]
+    float *part_lse2;      // [gridDim.x][2][16]
+    int split;             // 0: a pair is never shared between CTAs
+};
+
+// First tile and number of tiles of a pair of request r (at least one, so
+// that rows that see nothing are written).
+template <int TK>
+__device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, int &t0) {
+    const int lo = a.window > 0 ? max(0, r.len - r.n + 1 - a.window) : 0;
+    t0 = lo / TK;
+    return max(1, (r.len + TK - 1) / TK - t0);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const FewParams p) {
+    using L = FewLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR), *empty = full + kStages;
+    TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::OFF_INFO);
+    float *sm_m = reinterpret_cast<float *>(smem + L::OFF_ML);  // [4][16], then l, then exact l
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC);
+    unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = p.a.B, Hkv = p.a.Hkv;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 33);  // the tile's bytes, and every producer lane's share of Q
+            mbar_init(&empty[s], kConsumers);
+        }
+        *abort_flag = 0;
+        *sm_units = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    {   // tiles of the whole batch
+        unsigned long long mine = 0;
+        for (int b = threadIdx.x; b < B; b += kFewThreads) {
+            Request r;
+            int t0;
+            if (!load_request(p.a, p.shift, b, r)) {
+                if (blockIdx.x == 0) record_bad_args(p.status);
+            } else if (r.n > 0) {
+                mine += pair_tiles<L::TK>(p.a, r, t0);
+            }
+        }
+        if (mine) atomicAdd(sm_units, mine * Hkv);
+    }
+    __syncthreads();
+    const long long T = (long long)*sm_units;
+    const int G = (int)min((long long)gridDim.x, max(1ll, T / kMinUnits));
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------------------ producer
+        const int c = blockIdx.x;
+        const long long u0 = c < G ? c * T / G : T, u1 = c < G ? (c + 1ll) * T / G : T;
+        if (lane == 0) {
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+        }
+        PieceHeader head{0, 0, 0, 0};
+        // the request that holds unit u0
+        int b = 0;
+        long long base = 0;  // first unit of request b
+        if (u0 < u1) {
+            for (; b < B; b += 32) {
+                Request r;
+                int t0;
+                long long units = 0;
+                if (b + lane < B && load_request(p.a, p.shift, b + lane, r) && r.n > 0)
+                    units = (long long)pair_tiles<L::TK>(p.a, r, t0) * Hkv;
+                long long incl = units;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const long long x = __shfl_up_sync(0xffffffffu, incl, s);
+                    if (lane >= s) incl += x;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + incl > u0);
+                if (past) {
+                    const int k = __ffs(past) - 1;
+                    base += __shfl_sync(0xffffffffu, incl - units, k);
+                    b += k;
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        // this lane's box: tensor, 64-column half and page of the tile
+        const int page_keys = min(1 << p.shift, L::TK);  // keys of one box
+        const int per_tile = L::TK / page_keys;
+        const int box_bytes = page_keys * 128;
+        const bool boxed = lane < 2 * L::HALVES * per_tile;
+        const int tensor = lane & 1, half = (lane >> 1) % L::HALVES, sub = (lane >> 1) / L::HALVES;
+        int st = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        long long u = u0;
+        while (ok && u < u1 && b < B) {
+            Request r;
+            int t0;
+            if (!load_request(p.a, p.shift, b, r) || r.n == 0) {
+                ++b;
+                continue;
+            }
+            const int nt = pair_tiles<L::TK>(p.a, r, t0);
+            int hk = (int)((u - base) / nt);
+            for (; ok && hk < Hkv && u < u1; ++hk) {
+                const long long pair0 = base + (long long)hk * nt;
+                const int j0 = (int)(u - pair0), j1 = (int)min((long long)nt, u1 - pair0);
+                const bool whole = j0 == 0 && j1 == nt;
+                const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window) : 0;
+                const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window) : 0;
+                const int hi_min = r.len - r.n + 1;
+                if (!whole && j0 == 0)  // goes on in the next CTA: the merge's owner
+                    head = PieceHeader{r.row0, r.n, hk, (int)(((pair0 + nt) * G - 1) / T) - c + 1};
+                for (int j = j0; j < j1; ++j) {
+                    const int kv0 = (t0 + j) * L::TK;
+                    // pages that hold no visible key are neither looked up nor read
+                    const int key0 = kv0 + sub * page_keys;
+                    const bool live = boxed && key0 < r.len && key0 + page_keys > lo_min;
+                    int page = 0;
+                    if (live) {
+                        page = p.a.block_table[(size_t)b * p.a.max_pages + (key0 >> p.shift)];
+                        if (page < 0 || page >= p.a.num_pages) {
+                            record_bad_args(p.status);
+                            page = p.a.num_pages;  // out of the tensor: the copy fills zeros
+                        }
+                    }
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, live));
+                    const bool got = issued < kStages || mbar_wait(&empty[st], phase ^ 1, abort_flag, p.status, 21);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        TileInfo t;
+                        t.row0 = r.row0;
+                        t.n = r.n;
+                        t.len = r.len;
+                        t.kv0 = kv0;
+                        t.hk = hk;
+                        t.flags = (j == j0 ? kFirst : 0) | (j + 1 == j1 ? kLast : 0) |
+                                  (kv0 < lo_max || kv0 + L::TK > hi_min ? kMask : 0) | (whole ? 0 : kPart) |
+                                  (j0 == 0 ? kSlot1 : 0);
+                        info[st] = t;
+                        mbar_arrive_expect_tx(&full[st], boxes * box_bytes);
+                    }
+                    __syncwarp();
+                    if (live)
+                        tma_load_3d(smem + (st * 2 + tensor) * L::TILE + half * L::HALF + sub * box_bytes,
+                                    tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.shift) - 1),
+                                    page * Hkv + hk);
+                    if (j == j0) {
+                        // Q rows of the pair: row r is head r % g of token r / g
+                        constexpr int CH = D / 8;  // 16-byte pieces of a row
+                        const int rows = r.n * p.group;
+                        for (int i = lane; i < rows * CH; i += 32) {
+                            const int row = i / CH, ch = i % CH;
+                            const int t = row / p.group;
+                            const uint4 *src =
+                                static_cast<const uint4 *>(p.a.q) +
+                                ((size_t)(r.row0 + t) * p.a.Hq + hk * p.group + (row - t * p.group)) * CH + ch;
+                            cp_async_16(smem_u32(smem + L::OFF_Q + st * L::QBYTES) + row * (D * 2) +
+                                            ((ch ^ (row & 7)) << 4),
+                                        src);
+                        }
+                    }
+                    cp_async_arrive(&full[st]);
+                    ++issued;
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+                u = pair0 + j1;
+            }
+            if (hk == Hkv) {
+                base += (long long)nt * Hkv;
+                ++b;
+            }
+        }
+        if (!ok && lane == 0) {
+            // let copies in flight land before the CTA exits
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, 10000000ull);
+        }
+        if (lane == 0 && p.split) p.headers[blockIdx.x] = head;
+        __syncwarp();
+        if (lane == 0) {
+            // a tile that ends the stream
+            const bool got = !ok || issued < kStages || mbar_wait(&empty[st], phase ^ 1, abort_flag, p.status, 22);
+            if (ok && got) {
+                info[st].flags = -1;
+                mbar_arrive_expect_tx(&full[st], 0);
+            }
+        }
+        __syncwarp();
+        if (ok) cp_async_arrive(&full[st]);
+    } else {
+        // ----------------------------------------------------------- consumers
+        const int quad = lane & 3, rw = lane >> 2;  // this lane's rows: rw, rw + 8
+        uint32_t qf[D / 16][4];
+        float acc[D / 8][4];
+        float m[2], l[2], le[2];
+        int hi[2], lo[2];
+        int st = 0;
+        uint32_t phase = 0;
+        for (;;) {
+            bool ok = mbar_wait(&full[st], phase, abort_flag, p.status, 23);
+            ok = __all_sync(0xffffffffu, ok);
+            TileInfo t;
+            t.flags = 0;
+            if (ok) {
+                t = info[st];
+                if (t.flags == -1) break;
+            } else {
+                // every warp reaches the barrier below once per pair, so that
+                // none is left waiting there
+                named_bar_and(1, kConsumers * 32, false);
+                break;
+            }
+            const uint32_t ks = smem_u32(smem + st * 2 * L::TILE), vs = ks + L::TILE;
+            if (t.flags & kFirst) {
+                // rows past the pair's own hold whatever the buffer held: they
+                // touch no other row and are never written
+                const uint32_t qs = smem_u32(smem + L::OFF_Q + st * L::QBYTES);
+                const int row = lane & 15;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ldmatrix_x4(qf[kk], qs + row * (D * 2) + (((2 * kk + (lane >> 4)) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    m[x] = -INFINITY;
+                    l[x] = le[x] = 0.f;
+                    hi[x] = t.len - t.n + (rw + 8 * x) / p.group + 1;
+                    lo[x] = p.a.window > 0 ? hi[x] - p.a.window : 0;
+                }
+            }
+            // S: this warp's KW keys
+            float s[L::KW / 8][4];
+            const int w0 = warp * L::KW;
+#pragma unroll
+            for (int i = 0; i < L::KW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+                for (int i = 0; i < L::KW / 16; ++i) {
+                    const int key = w0 + i * 16 + ((lane >> 4) << 3) + (lane & 7);
+                    const int ch = 2 * kk + ((lane >> 3) & 1);
+                    uint32_t kf[4];
+                    ldmatrix_x4(kf, ks + (ch >> 3) * L::HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                    mma_16x8x16<BF16>(s[2 * i], qf[kk], kf[0], kf[1]);
+                    mma_16x8x16<BF16>(s[2 * i + 1], qf[kk], kf[2], kf[3]);
+                }
+            }
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < L::KW / 8; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = e >> 1;
+                    if (t.flags & kMask) {
+                        const int key = t.kv0 + w0 + i * 8 + quad * 2 + (e & 1);
+                        if (key >= hi[x] || key < lo[x]) s[i][e] = -INFINITY;
+                    }
+                    mx[x] = fmaxf(mx[x], s[i][e]);
+                }
+            }
+            float neg[2];
+            bool moved = false;
+            float alpha[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+                const float to = fmaxf(m[x], mx[x] * p.scale_log2);
+                moved |= to > m[x];
+                // a row that has seen nothing yet keeps -inf: 0 stands in for it
+                neg[x] = to == -INFINITY ? 0.f : -to;
+                alpha[x] = ex2_approx(m[x] + neg[x]);
+                m[x] = to;
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    l[x] *= alpha[x];
+                    le[x] *= alpha[x];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    acc[i][0] *= alpha[0];
+                    acc[i][1] *= alpha[0];
+                    acc[i][2] *= alpha[1];
+                    acc[i][3] *= alpha[1];
+                }
+            }
+            // P, rounded to the 16-bit type; l sums the rounded P that the MMA
+            // reads (O~ / l is then an exactly normalised mix of V rows), le
+            // the unrounded ones (LSE)
+            uint32_t pf[L::KW / 16][4];
+#pragma unroll
+            for (int i = 0; i < L::KW / 8; ++i) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float a = ex2_approx(fmaf(s[i][2 * x], p.scale_log2, neg[x]));
+                    const float c = ex2_approx(fmaf(s[i][2 * x + 1], p.scale_log2, neg[x]));
+                    const uint32_t pk = BF16 ? pack_bf16x2(a, c) : pack_f16x2(a, c);
+                    const float2 w = unpack2<BF16>(pk);
+                    l[x] += w.x + w.y;
+                    le[x] += a + c;
+                    pf[i >> 1][(i & 1) * 2 + x] = pk;
+                }
+            }
+            // O~ += P V
+            const int k_end = t.len - t.kv0 - w0;  // keys of this warp that exist
+            const int k_low = p.a.window > 0 ? t.len - t.n + 1 - p.a.window - t.kv0 - w0 : 0;
+#pragma unroll
+            for (int i = 0; i < L::KW / 16; ++i) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    const int key = w0 + i * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
+                    const int ch = 2 * j + (lane >> 4);
+                    uint32_t vf[4];
+                    ldmatrix_x4_trans(vf, vs + (ch >> 3) * L::HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                    if (t.flags & kMask) {
+                        // what no row sees may hold anything, and 0 * NaN is NaN
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k0 = i * 16 + (e & 1) * 8 + quad * 2;
+                            if (k0 >= k_end || k0 < k_low) vf[e] &= 0xFFFF0000u;
+                            if (k0 + 1 >= k_end || k0 + 1 < k_low) vf[e] &= 0x0000FFFFu;
+                        }
+                    }
+                    mma_16x8x16<BF16>(acc[2 * j], pf[i], vf[0], vf[1]);
+                    mma_16x8x16<BF16>(acc[2 * j + 1], pf[i], vf[2], vf[3]);
+                }
+            }
+            if (t.flags & kLast) {
+                // merge the four warps' results through this tile's buffer
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+                    le[x] += __shfl_xor_sync(0xffffffffu, le[x], 1);
+                    le[x] += __shfl_xor_sync(0xffffffffu, le[x], 2);
+                }
+                if (!named_bar_and(1, kConsumers * 32, true)) break;  // all warps have read the tile
+                float *buf = reinterpret_cast<float *>(smem + st * 2 * L::TILE) + warp * (kMaxRows * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int row = rw + 8 * x;
+                        // columns exchanged by row: no bank conflicts
+                        *reinterpret_cast<float2 *>(buf + row * D + ((i * 8 + quad * 2) ^ ((row & 3) << 3))) =
+                            make_float2(acc[i][2 * x], acc[i][2 * x + 1]);
+                    }
+                }
+                if (quad == 0) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int at = warp * 16 + rw + 8 * x;
+                        sm_m[at] = m[x];
+                        sm_m[kConsumers * 16 + at] = l[x];
+                        sm_m[2 * kConsumers * 16 + at] = le[x];
+                    }
+                }
+                named_bar_sync(2, kConsumers * 32);
+                // eight threads a row, four neighbouring columns at a time
+                const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+                if (row < t.n * p.group) {
+                    float top = -INFINITY, sum = 0.f, exact = 0.f, f[kConsumers];
+#pragma unroll
+                    for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, sm_m[w * 16 + row]);
+                    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                    for (int w = 0; w < kConsumers; ++w) {
+                        f[w] = ex2_approx(sm_m[w * 16 + row] - ref);
+                        sum += f[w] * sm_m[kConsumers * 16 + w * 16 + row];
+                        exact += f[w] * sm_m[2 * kConsumers * 16 + w * 16 + row];
+                    }
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
+                    const float *from = reinterpret_cast<const float *>(smem + st * 2 * L::TILE) + row * D;
+                    const int tok = row / p.group;
+                    const int h = t.hk * p.group + row - tok * p.group;
+                    const size_t out_row = (size_t)(t.row0 + tok) * p.a.Hq + h;
+                    const size_t slot = (size_t)blockIdx.x * 2 + (t.flags & kSlot1 ? 1 : 0);
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        const int c = c0 + part * 4;
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < kConsumers; ++w) {
+                            const float4 x = *reinterpret_cast<const float4 *>(from + w * (kMaxRows * D) +
+                                                                               (c ^ ((row & 3) << 3)));
+                            o.x = fmaf(f[w], x.x, o.x);
+                            o.y = fmaf(f[w], x.y, o.y);
+                            o.z = fmaf(f[w], x.z, o.z);
+                            o.w = fmaf(f[w], x.w, o.w);
+                        }
+                        o.x *= inv;
+                        o.y *= inv;
+                        o.z *= inv;
+                        o.w *= inv;
+                        if (t.flags & kPart) {
+                            *reinterpret_cast<float4 *>(p.part_o + (slot * kMaxRows + row) * D + c) = o;
+                        } else {
+                            const uint2 w = BF16 ? make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w))
+                                                 : make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w));
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.o) + out_row * D + c) = w;
+                        }
+                    }
+                    if (part == 0) {
+                        if (t.flags & kPart)
+                            p.part_lse2[slot * kMaxRows + row] = lse2;
+                        else
+                            p.a.lse[(size_t)h * p.a.total + t.row0 + tok] = lse2 * 0.69314718055994530942f;
+                    }
+                }
+                fence_proxy_async_smem();  // the buffer's next writer is a TMA copy
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+    }
+}
+
+// Merges the parts of pairs that several CTAs shared.  Block x belongs to CTA
+// x of the main kernel (its header says whether a pair began there and went
+// on), block y to four of the 16 rows; two warps a row take every other part.
+constexpr int kMergeRows = 4;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(64 * kMergeRows) paged_merge_kernel(const FewParams p) {
+    const PieceHeader head = p.headers[blockIdx.x];
+    if (head.pieces == 0) return;
+    const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 6);
+    const int rows = head.n * p.group;
+    const int sub = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
+    constexpr int E = D / 32;
+    __shared__ float sm_o[kMergeRows][D], sm_lse[kMergeRows];
+    float acc[E], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (row < rows) {
+        for (int k = sub; k < head.pieces; k += 2) {
+            const size_t slot = (size_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0);
+            const float lse2 = p.part_lse2[slot * kMaxRows + row];
+            const float *o = p.part_o + (slot * kMaxRows + row) * D + lane * E;
+            const float to = fmaxf(top, lse2);
+            if (to == -INFINITY) continue;
+            const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
+            sum = sum * a + w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * o[e];
+            top = to;
+        }
+        if (sub == 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) sm_o[threadIdx.x >> 6][lane * E + e] = sum > 0.f ? acc[e] / sum : 0.f;
+            if (lane == 0) sm_lse[threadIdx.x >> 6] = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        }
+    }
+    __syncthreads();
+    if (row >= rows || sub == 1) return;
+    {
+        const float lse2 = sm_lse[threadIdx.x >> 6];
+        const float to = fmaxf(top, lse2);
+        if (to != -INFINITY) {
+            const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
+            sum = sum * a + w;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * sm_o[threadIdx.x >> 6][lane * E + e];
+            top = to;
+        }
+    }
+    const int tok = row / p.group;
+    const int h = head.hk * p.group + row - tok * p.group;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint16_t *out = static_cast<uint16_t *>(p.a.o) + ((size_t)(head.row0 + tok) * p.a.Hq + h) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(out + e) =
+            BF16 ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+        p.a.lse[(size_t)h * p.a.total + head.row0 + tok] =
+            sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D, bool BF16>
+cudaError_t launch_few(const PagedArgs &a, int shift, cudaStream_t st) {
+    using L = FewLayout<D>;
+    const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tk, tv;
+    const uint32_t rows = a.page_size < L::TK ? a.page_size : L::TK;
+    const uint64_t planes = (uint64_t)a.num_pages * a.Hkv;
+    if (!make_tmap_3d(&tk, a.k_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tmap_3d(&tv, a.v_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kernel = paged_few_kernel<D, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    FewParams p;
+    p.a = a;
+    p.shift = shift;
+    p.group = a.Hq / a.Hkv;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.status = device_status_ptr();
+    char *ws = static_cast<char *>(a.workspace);
+    p.headers = reinterpret_cast<PieceHeader *>(ws);
+    ws += round256(kMaxCtas * sizeof(PieceHeader));
+    p.part_lse2 = reinterpret_cast<float *>(ws);
+    ws += round256(kMaxCtas * 2 * kMaxRows * sizeof(float));
+    p.part_o = reinterpret_cast<float *>(ws);
+    p.split = 1;
+    const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    kernel<<<grid, kFewThreads, L::ALLOC, st>>>(tk, tv, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    paged_merge_kernel<D, BF16><<<dim3(grid, kMaxRows / kMergeRows), 64 * kMergeRows, 0, st>>>(p);
+    return cudaGetLastError();
+}
 
 struct RowsParams {
     PagedArgs a;
@@ -119,11 +723,18 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(const RowsParams p) {
 
 }  // namespace
 
-size_t fwd_paged_workspace(int, int, int, int, int, int, int, int, int) { return 256; }
+size_t fwd_paged_workspace(int, int, int, int, int, int d, int, int, int) {
+    return round256(kMaxCtas * sizeof(PieceHeader)) + round256(kMaxCtas * 2 * kMaxRows * sizeof(float)) +
+           round256((size_t)kMaxCtas * 2 * kMaxRows * d * sizeof(float));
+}
 
 cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st) {
     RowsParams p{a, 0, a.scale * 1.4426950408889634f, device_status_ptr()};
     while ((1 << p.shift) < a.page_size) ++p.shift;
+    if (a.prefix_len == 0 && (long long)a.max_new * (a.Hq / a.Hkv) <= kMaxRows) {
+        if (a.d == 128) return a.bf16 ? launch_few<128, true>(a, p.shift, st) : launch_few<128, false>(a, p.shift, st);
+        return a.bf16 ? launch_few<64, true>(a, p.shift, st) : launch_few<64, false>(a, p.shift, st);
+    }
     const unsigned grid = (unsigned)(((long long)a.total * a.Hq + 3) / 4);
     if (a.d == 128) {
         if (a.bf16) paged_rows_kernel<128, true><<<grid, 128, 0, st>>>(p);

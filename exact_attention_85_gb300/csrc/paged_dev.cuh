@@ -1,0 +1,38 @@
+// paged_dev.cuh -- device-side pieces shared by the paged forward kernels.
+#pragma once
+
+#include "paged.h"
+#include "status.cuh"
+
+namespace fa {
+
+// A request as the kernels see it: its rows are row0 .. row0 + n - 1 of q and
+// its own keys 0 .. len - 1.
+struct Request {
+    int row0, n, len;
+};
+
+// False if what the device holds for request b breaks the rules of the call
+// (offsets, row bound, length): it then has no rows.
+__device__ __forceinline__ bool load_request(const PagedArgs &a, int shift, int b, Request &r) {
+    r.row0 = b;
+    r.n = 1;
+    if (a.cu_seqlens) {
+        r.row0 = a.cu_seqlens[b];
+        const int end = a.cu_seqlens[b + 1];
+        if (r.row0 < 0 || end < r.row0 || end > a.total || end - r.row0 > a.max_new) return false;
+        r.n = end - r.row0;
+    }
+    r.len = a.seq_lens[b];
+    return r.len >= 0 && r.len <= (a.max_pages << shift);
+}
+
+// A partial result of a row: O~ / l in fp32 and log2 of the sum of
+// exponentials (-inf: the row saw nothing).  Two merge as
+//   O = (w1 O1 + w2 O2) / (w1 + w2), w = 2^(lse2 - max).
+struct PartialView {
+    float *o;     // [pieces][rows][D]
+    float *lse2;  // [pieces][rows]
+};
+
+}  // namespace fa
