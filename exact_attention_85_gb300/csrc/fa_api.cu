@@ -407,7 +407,8 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
     fa_status_t s = check_cache(a.Hkv, a.d, a.page_size, a.num_pages, dtype);
     if (s != FA_OK) return s;
     if ((long long)a.max_pages * a.page_size + a.prefix_len > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
-    if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll)
+    if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
+        (long long)a.B * a.Hq > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
     const size_t need = fa::fwd_paged_workspace(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
                                                 a.prefix_len);

@@ -82,7 +82,29 @@ struct FewParams {
     PieceHeader *headers;  // [gridDim.x]
     float *part_o;         // [gridDim.x][2][16][D]
     float *part_lse2;      // [gridDim.x][2][16]
-    int split;             // 0: a pair is never shared between CTAs
+    int planes;            // parts of the shared prefix' keys (0: none) ...
+    const float *plane_o, *plane_lse2;  // ... [planes][total][Hq] (x D)
+};
+
+// Weights of a row's own result and of the prefix planes' in their mix.
+struct PlaneWeights {
+    float top, inv;  // largest lse2, 1 / sum of the weights
+    // Takes the planes in: returns the own result's weight, lse2 becomes the mix'.
+    __device__ __forceinline__ float join(const float *plane_lse2, size_t stride, int planes, float &lse2) {
+        top = lse2;
+        for (int s = 0; s < planes; ++s) top = fmaxf(top, plane_lse2[s * stride]);
+        inv = 0.f;
+        if (top == -INFINITY) return 0.f;
+        const float own = ex2_approx(lse2 - top);
+        float sum = own;
+        for (int s = 0; s < planes; ++s) sum += ex2_approx(plane_lse2[s * stride] - top);
+        inv = 1.f / sum;
+        lse2 = top + log2f(sum);
+        return own * inv;
+    }
+    __device__ __forceinline__ float weight(float lse2) const {
+        return lse2 == -INFINITY ? 0.f : ex2_approx(lse2 - top) * inv;
+    }
 };
 
 // First tile and number of tiles of a pair of request r (at least one, so
@@ -270,7 +292,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, 10000000ull);
         }
-        if (lane == 0 && p.split) p.headers[blockIdx.x] = head;
+        if (lane == 0) p.headers[blockIdx.x] = head;
         __syncwarp();
         if (lane == 0) {
             // a tile that ends the stream
@@ -467,13 +489,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         sum += f[w] * sm_m[kConsumers * 16 + w * 16 + row];
                         exact += f[w] * sm_m[2 * kConsumers * 16 + w * 16 + row];
                     }
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    const float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
+                    float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
                     const float *from = reinterpret_cast<const float *>(smem + st * 2 * L::TILE) + row * D;
                     const int tok = row / p.group;
                     const int h = t.hk * p.group + row - tok * p.group;
                     const size_t out_row = (size_t)(t.row0 + tok) * p.a.Hq + h;
                     const size_t slot = (size_t)blockIdx.x * 2 + (t.flags & kSlot1 ? 1 : 0);
+                    // a whole pair takes the shared prefix' parts in as well
+                    const int planes = t.flags & kPart ? 0 : p.planes;
+                    const size_t stride = (size_t)p.a.total * p.a.Hq;
+                    PlaneWeights pw;
+                    if (planes) inv *= pw.join(p.plane_lse2 + out_row, stride, planes, lse2);
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         const int c = c0 + part * 4;
@@ -491,6 +518,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         o.y *= inv;
                         o.z *= inv;
                         o.w *= inv;
+                        for (int s2 = 0; s2 < planes; ++s2) {
+                            const float w = pw.weight(p.plane_lse2[s2 * stride + out_row]);
+                            if (w == 0.f) continue;
+                            const float4 x =
+                                *reinterpret_cast<const float4 *>(p.plane_o + (s2 * stride + out_row) * D + c);
+                            o.x = fmaf(w, x.x, o.x);
+                            o.y = fmaf(w, x.y, o.y);
+                            o.z = fmaf(w, x.z, o.z);
+                            o.w = fmaf(w, x.w, o.w);
+                        }
                         if (t.flags & kPart) {
                             *reinterpret_cast<float4 *>(p.part_o + (slot * kMaxRows + row) * D + c) = o;
                         } else {
@@ -530,18 +567,23 @@ __global__ void __launch_bounds__(64 * kMergeRows) paged_merge_kernel(const FewP
     const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 6);
     const int rows = head.n * p.group;
     const int sub = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
+    const int tok = row / p.group;
+    const int h = head.hk * p.group + row - tok * p.group;
+    const size_t out_row = (size_t)(head.row0 + tok) * p.a.Hq + h;
     constexpr int E = D / 32;
     __shared__ float sm_o[kMergeRows][D], sm_lse[kMergeRows];
     float acc[E], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     if (row < rows) {
-        for (int k = sub; k < head.pieces; k += 2) {
+        for (int k = sub; k < head.pieces + p.planes; k += 2) {
             const size_t slot = (size_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0);
-            const float lse2 = p.part_lse2[slot * kMaxRows + row];
-            const float *o = p.part_o + (slot * kMaxRows + row) * D + lane * E;
+            const bool own = k < head.pieces;
+            const size_t at = own ? slot * kMaxRows + row : (size_t)(k - head.pieces) * p.a.total * p.a.Hq + out_row;
+            const float lse2 = (own ? p.part_lse2 : p.plane_lse2)[at];
+            const float *o = (own ? p.part_o : p.plane_o) + at * D + lane * E;
+            if (lse2 == -INFINITY) continue;
             const float to = fmaxf(top, lse2);
-            if (to == -INFINITY) continue;
             const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
             sum = sum * a + w;
 #pragma unroll
@@ -567,10 +609,8 @@ __global__ void __launch_bounds__(64 * kMergeRows) paged_merge_kernel(const FewP
             top = to;
         }
     }
-    const int tok = row / p.group;
-    const int h = head.hk * p.group + row - tok * p.group;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t *out = static_cast<uint16_t *>(p.a.o) + ((size_t)(head.row0 + tok) * p.a.Hq + h) * D + lane * E;
+    uint16_t *out = static_cast<uint16_t *>(p.a.o) + out_row * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t *>(out + e) =
@@ -580,10 +620,14 @@ __global__ void __launch_bounds__(64 * kMergeRows) paged_merge_kernel(const FewP
             sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
+// Workspace: the few-row kernel's headers and parts, then the planes.
+constexpr size_t kHeaderBytes = (kMaxCtas * sizeof(PieceHeader) + 255) & ~size_t(255);
+constexpr size_t kFewLseBytes = (kMaxCtas * 2 * kMaxRows * sizeof(float) + 255) & ~size_t(255);
+
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 template <int D, bool BF16>
-cudaError_t launch_few(const PagedArgs &a, int shift, cudaStream_t st) {
+cudaError_t launch_few(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st) {
     using L = FewLayout<D>;
     const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tk, tv;
@@ -606,11 +650,11 @@ cudaError_t launch_few(const PagedArgs &a, int shift, cudaStream_t st) {
     p.status = device_status_ptr();
     char *ws = static_cast<char *>(a.workspace);
     p.headers = reinterpret_cast<PieceHeader *>(ws);
-    ws += round256(kMaxCtas * sizeof(PieceHeader));
-    p.part_lse2 = reinterpret_cast<float *>(ws);
-    ws += round256(kMaxCtas * 2 * kMaxRows * sizeof(float));
-    p.part_o = reinterpret_cast<float *>(ws);
-    p.split = 1;
+    p.part_lse2 = reinterpret_cast<float *>(ws + kHeaderBytes);
+    p.part_o = reinterpret_cast<float *>(ws + kHeaderBytes + kFewLseBytes);
+    p.planes = w.prefix_splits;
+    p.plane_o = w.part_o;
+    p.plane_lse2 = w.part_lse2;
     const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     kernel<<<grid, kFewThreads, L::ALLOC, st>>>(tk, tv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -618,132 +662,71 @@ cudaError_t launch_few(const PagedArgs &a, int shift, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-struct RowsParams {
-    PagedArgs a;
-    int shift;  // log2(page_size)
-    float scale_log2;
-    unsigned int *status;
-};
+}  // namespace
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_rows_kernel(const RowsParams p) {
-    constexpr int E = D / 32;  // elements a lane holds
-    const int lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id >= (long long)p.a.total * p.a.Hq) return;
-    const int row = (int)(id / p.a.Hq), h = (int)(id - (long long)row * p.a.Hq);
-    const int hk = h / (p.a.Hq / p.a.Hkv);
-    // the row's request
-    int b, i = 0, n = 1;
-    if (!p.a.cu_seqlens) {
-        if (row >= p.a.B) return;
-        b = row;
-    } else {
-        const int *cu = p.a.cu_seqlens;
-        int lo = 0, hi = p.a.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (cu[mid] <= row) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
-        i = row - cu[b];
-        n = cu[b + 1] - cu[b];
-        if (i < 0 || i >= n) return;  // behind the last sequence
-        if (n > p.a.max_new || cu[b] < 0 || cu[b + 1] > p.a.total) {
-            record_bad_args(p.status);
-            return;
-        }
-    }
-    const int len = p.a.seq_lens[b];
-    if (len < 0 || len > (p.a.max_pages << p.shift)) {
-        record_bad_args(p.status);
-        return;
-    }
-    const int P = p.a.prefix_len;
-    const int hi = P + len - n + i + 1;  // keys 0 .. hi - 1 from the prefix' start
-    const int lo = p.a.window > 0 ? max(0, hi - p.a.window) : 0;
-    using T = uint16_t;
-    auto widen = [](const T *s, float *x) {
-        if constexpr (E == 4) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(s);
-            const float2 a = unpack2<BF16>(w.x), c = unpack2<BF16>(w.y);
-            x[0] = a.x; x[1] = a.y; x[2] = c.x; x[3] = c.y;
-        } else {
-            const float2 a = unpack2<BF16>(*reinterpret_cast<const uint32_t *>(s));
-            x[0] = a.x; x[1] = a.y;
-        }
-    };
-    float q[E], acc[E];
-    widen(static_cast<const T *>(p.a.q) + ((size_t)row * p.a.Hq + h) * D + lane * E, q);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    // with a prefix, a row at a negative place still sees the prefix
-    for (int key = lo; key < hi; ++key) {
-        const bool front = key < P;
-        const int at = front ? key : key - P;
-        const int page = front ? p.a.prefix_pages[at >> p.shift]
-                               : p.a.block_table[(size_t)b * p.a.max_pages + (at >> p.shift)];
-        if (page < 0 || page >= p.a.num_pages) {
-            if (lane == 0) record_bad_args(p.status);
-            continue;
-        }
-        const size_t off =
-            ((((size_t)page * p.a.Hkv + hk) << p.shift) + (at & ((1 << p.shift) - 1))) * D + lane * E;
-        float x[E];
-        widen(static_cast<const T *>(p.a.k_cache) + off, x);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], x[e], s);
-#pragma unroll
-        for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= p.scale_log2;
-        if (s > m) {
-            const float f = exp2f(m - s);
-            l *= f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= f;
-            m = s;
-        }
-        const float w = exp2f(s - m);
-        l += w;
-        widen(static_cast<const T *>(p.a.v_cache) + off, x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    T *o = static_cast<T *>(p.a.o) + ((size_t)row * p.a.Hq + h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(o + e) =
-            BF16 ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-        p.a.lse[(size_t)h * p.a.total + row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+namespace {
+
+constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
+
+// Rows of a pair: max_new * group.  Up to 16 go to the kernel of this file,
+// whose tile has 16 rows, more to the 256-row one.
+bool few_rows(int max_new, int group) { return (long long)max_new * group <= kMaxRows; }
+
+int clamp_splits(long long ctas, long long tiles) {
+    const long long s = ctas > 0 ? kSms / ctas : 1;
+    return (int)(s < 1 ? 1 : s < tiles ? s : tiles);
 }
+
+// Enough key ranges that the blocks fill the SMs once, and no more.
+WidePlan plan_wide(int B, int total, int max_new, int Hq, int Hkv, int max_pages, int page_size, int prefix_len) {
+    WidePlan w{};
+    const int g = Hq / Hkv;
+    const long long row_blocks = ((long long)total * g + 255) / 256;
+    if (prefix_len > 0) {
+        w.prefix_blocks = (int)row_blocks;
+        w.prefix_splits = clamp_splits(row_blocks * Hkv, (prefix_len + 127ll) / 128);
+    }
+    if (!few_rows(max_new, g)) {
+        const long long most = (long long)B * (((long long)max_new * g + 255) / 256);
+        const long long blocks = row_blocks + B < most ? row_blocks + B : most;
+        w.own_blocks = (int)blocks;
+        w.own_splits = clamp_splits(blocks * Hkv, ((long long)max_pages * page_size + 127) / 128);
+    }
+    return w;
+}
+
+size_t wide_planes(const WidePlan &w) {
+    // a single range of a request's own keys is final
+    if (w.prefix_splits == 0 && w.own_splits == 1) return 0;
+    return (size_t)w.prefix_splits + w.own_splits;
+}
+
+size_t few_bytes(int d) { return kHeaderBytes + kFewLseBytes + (size_t)kMaxCtas * 2 * kMaxRows * d * sizeof(float); }
 
 }  // namespace
 
-size_t fwd_paged_workspace(int, int, int, int, int, int d, int, int, int) {
-    return round256(kMaxCtas * sizeof(PieceHeader)) + round256(kMaxCtas * 2 * kMaxRows * sizeof(float)) +
-           round256((size_t)kMaxCtas * 2 * kMaxRows * d * sizeof(float));
+size_t fwd_paged_workspace(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
+                           int prefix_len) {
+    const WidePlan w = plan_wide(B, total, max_new, Hq, Hkv, max_pages, page_size, prefix_len);
+    const size_t rows = (size_t)total * Hq * wide_planes(w);
+    return (few_rows(max_new, Hq / Hkv) ? few_bytes(d) : 256) + round256(rows * sizeof(float)) +
+           rows * d * sizeof(float);
 }
 
 cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st) {
-    RowsParams p{a, 0, a.scale * 1.4426950408889634f, device_status_ptr()};
-    while ((1 << p.shift) < a.page_size) ++p.shift;
-    if (a.prefix_len == 0 && (long long)a.max_new * (a.Hq / a.Hkv) <= kMaxRows) {
-        if (a.d == 128) return a.bf16 ? launch_few<128, true>(a, p.shift, st) : launch_few<128, false>(a, p.shift, st);
-        return a.bf16 ? launch_few<64, true>(a, p.shift, st) : launch_few<64, false>(a, p.shift, st);
+    int shift = 0;
+    while ((1 << shift) < a.page_size) ++shift;
+    WidePlan w = plan_wide(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.max_pages, a.page_size, a.prefix_len);
+    const bool few = few_rows(a.max_new, a.Hq / a.Hkv);
+    char *ws = static_cast<char *>(a.workspace) + (few ? few_bytes(a.d) : 256);
+    w.part_lse2 = reinterpret_cast<float *>(ws);
+    w.part_o = reinterpret_cast<float *>(ws + round256((size_t)a.total * a.Hq * wide_planes(w) * sizeof(float)));
+    if (w.prefix_splits || w.own_splits) {
+        const cudaError_t e = launch_paged_wide(a, shift, w, st);
+        if (e != cudaSuccess || !few) return e;
     }
-    const unsigned grid = (unsigned)(((long long)a.total * a.Hq + 3) / 4);
-    if (a.d == 128) {
-        if (a.bf16) paged_rows_kernel<128, true><<<grid, 128, 0, st>>>(p);
-        else paged_rows_kernel<128, false><<<grid, 128, 0, st>>>(p);
-    } else {
-        if (a.bf16) paged_rows_kernel<64, true><<<grid, 128, 0, st>>>(p);
-        else paged_rows_kernel<64, false><<<grid, 128, 0, st>>>(p);
-    }
-    return cudaGetLastError();
+    if (a.d == 128) return a.bf16 ? launch_few<128, true>(a, shift, w, st) : launch_few<128, false>(a, shift, w, st);
+    return a.bf16 ? launch_few<64, true>(a, shift, w, st) : launch_few<64, false>(a, shift, w, st);
 }
 
 }  // namespace fa

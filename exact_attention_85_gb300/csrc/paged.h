@@ -41,6 +41,19 @@ struct PagedArgs {
     void *workspace;
 };
 
+// How a call is divided for the 256-row kernel (fa_fwd_paged_wide.cu): row
+// blocks (upper bounds, the real ones depend on the device's offsets) and key
+// ranges per block, for the shared prefix and for the requests' own keys; 0
+// ranges: not this kernel's.  Partial results are planes [range][total][Hq],
+// the prefix' first.
+struct WidePlan {
+    int prefix_blocks, prefix_splits;
+    int own_blocks, own_splits;
+    float *part_o, *part_lse2;
+};
+
+cudaError_t launch_paged_wide(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st);
+
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st);

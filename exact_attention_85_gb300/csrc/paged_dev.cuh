@@ -27,12 +27,8 @@ __device__ __forceinline__ bool load_request(const PagedArgs &a, int shift, int 
     return r.len >= 0 && r.len <= (a.max_pages << shift);
 }
 
-// A partial result of a row: O~ / l in fp32 and log2 of the sum of
-// exponentials (-inf: the row saw nothing).  Two merge as
-//   O = (w1 O1 + w2 O2) / (w1 + w2), w = 2^(lse2 - max).
-struct PartialView {
-    float *o;     // [pieces][rows][D]
-    float *lse2;  // [pieces][rows]
-};
+// A partial result of a row is O~ / l in fp32 and lse2, log2 of the sum of
+// exponentials (-inf: the row saw nothing there, and its O is not written).
+// Several merge as O = sum w_i O_i / sum w_i with w_i = 2^(lse2_i - max).
 
 }  // namespace fa
