@@ -110,6 +110,13 @@ bool make_tmap_tiles(CUtensorMap *map, const void *base, CUtensorMapDataType dty
                             CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool make_tmap_pages(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
+                     int keys) {
+    return make_tmap_3d(map, base, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, d,
+                        page_size, (uint64_t)num_pages * heads, 64, page_size < keys ? page_size : keys,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 void *current_context() {
     static CtxGetCurrentFn fn = [] {
         void *f = nullptr;
@@ -410,8 +417,9 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
     if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
         (long long)a.B * a.Hq > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
-    const size_t need = fa::fwd_paged_workspace(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
-                                                a.prefix_len);
+    const size_t need = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size, a.prefix_len,
+                                       nullptr)
+                            .bytes;
     if (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u))
         return FA_ERR_WORKSPACE;
     return FA_OK;
@@ -460,9 +468,10 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
                                     int page_size, int prefix_len) {
     if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
-        page_size < 1 || prefix_len < 0)
+        page_size < 1 || prefix_len < 0 || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
+        (long long)max_pages * page_size + prefix_len > 0x7FFFFFFFll)
         return 0;
-    return fa::fwd_paged_workspace(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len);
+    return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, nullptr).bytes;
 }
 
 fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *block_table,
@@ -471,7 +480,7 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache
                          float scale, fa_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
     FA_RANGE("fa_fwd_paged");
     fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, nullptr, o, lse, B, total, max_new, Hq,
-                    Hkv, d, max_pages, page_size, num_pages, 0, window, scale, dtype == FA_BF16, workspace};
+                    Hkv, d, max_pages, page_size, num_pages, 0, window, scale, dtype == FA_BF16, workspace, 0};
     fa_status_t s = check_paged(a, dtype, workspace_bytes);
     if (s != FA_OK) return s;
     return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));
@@ -486,7 +495,7 @@ fa_status_t fa_fwd_paged_prefix(const void *q, const void *k_cache, const void *
     if (!prefix_pages || prefix_len < 1) return FA_ERR_INVALID_ARG;
     fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, prefix_pages, o, lse, B, total, max_new,
                     Hq, Hkv, d, max_pages, page_size, num_pages, prefix_len, window, scale, dtype == FA_BF16,
-                    workspace};
+                    workspace, 0};
     fa_status_t s = check_paged(a, dtype, workspace_bytes);
     if (s != FA_OK) return s;
     return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));

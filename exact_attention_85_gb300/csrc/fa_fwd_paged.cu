@@ -17,7 +17,8 @@
 // keeps every SM reading to the end; a CTA's range covers the end of one
 // pair, some whole pairs and the beginning of another.  Whole pairs are
 // written out directly; the parts of a pair that several CTAs share go to
-// the workspace as (O~ / l, log2 sum) and a second kernel merges them.
+// the workspace as (O~ / l, log2 sum) and a second kernel merges them (with a
+// shared prefix, everything does, and is merged with the prefix' results).
 //   warps 0-3  each a quarter of every tile's keys, all 16 rows; their four
 //              results are merged through the last tile's buffer
 //   warp 4     producer: plans the CTA's range, reads block-table entries,
@@ -46,12 +47,9 @@ enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16 };
 // What the producer tells the consumers about a tile.
 struct TileInfo {
     int row0, n, len, kv0;
-    int hk, flags, pad0, pad1;
-};
-
-// What a CTA whose last pair goes on in the next CTA leaves for the merge.
-struct PieceHeader {
-    int row0, n, hk, pieces;  // pieces 0: nothing to merge
+    int hk, flags;
+    int code;  // of the pair's rows, but for the row number (PartView)
+    int pad;
 };
 
 template <int D>
@@ -75,36 +73,10 @@ struct FewLayout {
 
 struct FewParams {
     PagedArgs a;
-    int shift;   // log2(page_size)
     int group;   // query heads per key/value head
     float scale_log2;
     unsigned int *status;
-    PieceHeader *headers;  // [gridDim.x]
-    float *part_o;         // [gridDim.x][2][16][D]
-    float *part_lse2;      // [gridDim.x][2][16]
-    int planes;            // parts of the shared prefix' keys (0: none) ...
-    const float *plane_o, *plane_lse2;  // ... [planes][total][Hq] (x D)
-};
-
-// Weights of a row's own result and of the prefix planes' in their mix.
-struct PlaneWeights {
-    float top, inv;  // largest lse2, 1 / sum of the weights
-    // Takes the planes in: returns the own result's weight, lse2 becomes the mix'.
-    __device__ __forceinline__ float join(const float *plane_lse2, size_t stride, int planes, float &lse2) {
-        top = lse2;
-        for (int s = 0; s < planes; ++s) top = fmaxf(top, plane_lse2[s * stride]);
-        inv = 0.f;
-        if (top == -INFINITY) return 0.f;
-        const float own = ex2_approx(lse2 - top);
-        float sum = own;
-        for (int s = 0; s < planes; ++s) sum += ex2_approx(plane_lse2[s * stride] - top);
-        inv = 1.f / sum;
-        lse2 = top + log2f(sum);
-        return own * inv;
-    }
-    __device__ __forceinline__ float weight(float lse2) const {
-        return lse2 == -INFINITY ? 0.f : ex2_approx(lse2 - top) * inv;
-    }
+    PartView part;
 };
 
 // First tile and number of tiles of a pair of request r (at least one, so
@@ -146,7 +118,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
             int t0;
-            if (!load_request(p.a, p.shift, b, r)) {
+            if (!load_request(p.a, b, r)) {
                 if (blockIdx.x == 0) record_bad_args(p.status);
             } else if (r.n > 0) {
                 mine += pair_tiles<L::TK>(p.a, r, t0);
@@ -158,6 +130,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const long long T = (long long)*sm_units;
     const int G = (int)min((long long)gridDim.x, max(1ll, T / kMinUnits));
 
+    launch_dependents();
+
     if (warp == kConsumers) {
         // ------------------------------------------------------------ producer
         const int c = blockIdx.x;
@@ -166,7 +140,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
-        PieceHeader head{0, 0, 0, 0};
         // the request that holds unit u0
         int b = 0;
         long long base = 0;  // first unit of request b
@@ -175,7 +148,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 Request r;
                 int t0;
                 long long units = 0;
-                if (b + lane < B && load_request(p.a, p.shift, b + lane, r) && r.n > 0)
+                if (b + lane < B && load_request(p.a, b + lane, r) && r.n > 0)
                     units = (long long)pair_tiles<L::TK>(p.a, r, t0) * Hkv;
                 long long incl = units;
 #pragma unroll
@@ -194,7 +167,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
         }
         // this lane's box: tensor, 64-column half and page of the tile
-        const int page_keys = min(1 << p.shift, L::TK);  // keys of one box
+        const int page_keys = min(1 << p.a.shift, L::TK);  // keys of one box
         const int per_tile = L::TK / page_keys;
         const int box_bytes = page_keys * 128;
         const bool boxed = lane < 2 * L::HALVES * per_tile;
@@ -206,7 +179,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         while (ok && u < u1 && b < B) {
             Request r;
             int t0;
-            if (!load_request(p.a, p.shift, b, r) || r.n == 0) {
+            if (!load_request(p.a, b, r) || r.n == 0) {
                 ++b;
                 continue;
             }
@@ -219,8 +192,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window) : 0;
                 const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window) : 0;
                 const int hi_min = r.len - r.n + 1;
-                if (!whole && j0 == 0)  // goes on in the next CTA: the merge's owner
-                    head = PieceHeader{r.row0, r.n, hk, (int)(((pair0 + nt) * G - 1) / T) - c + 1};
+                // a pair that goes on in the next CTA belongs to the one it began in
+                const int code =
+                    !whole && j0 == 0 ? part_code((int)(((pair0 + nt) * G - 1) / T) - c + 1, c, 0) : 0;
                 for (int j = j0; j < j1; ++j) {
                     const int kv0 = (t0 + j) * L::TK;
                     // pages that hold no visible key are neither looked up nor read
@@ -228,7 +202,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     const bool live = boxed && key0 < r.len && key0 + page_keys > lo_min;
                     int page = 0;
                     if (live) {
-                        page = p.a.block_table[(size_t)b * p.a.max_pages + (key0 >> p.shift)];
+                        page = p.a.block_table[(size_t)b * p.a.max_pages + (key0 >> p.a.shift)];
                         if (page < 0 || page >= p.a.num_pages) {
                             record_bad_args(p.status);
                             page = p.a.num_pages;  // out of the tensor: the copy fills zeros
@@ -247,6 +221,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         t.len = r.len;
                         t.kv0 = kv0;
                         t.hk = hk;
+                        t.code = code;
                         t.flags = (j == j0 ? kFirst : 0) | (j + 1 == j1 ? kLast : 0) |
                                   (kv0 < lo_max || kv0 + L::TK > hi_min ? kMask : 0) | (whole ? 0 : kPart) |
                                   (j0 == 0 ? kSlot1 : 0);
@@ -256,7 +231,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     __syncwarp();
                     if (live)
                         tma_load_3d(smem + (st * 2 + tensor) * L::TILE + half * L::HALF + sub * box_bytes,
-                                    tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.shift) - 1),
+                                    tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.a.shift) - 1),
                                     page * Hkv + hk);
                     if (j == j0) {
                         // Q rows of the pair: row r is head r % g of token r / g
@@ -292,8 +267,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, 10000000ull);
         }
-        if (lane == 0) p.headers[blockIdx.x] = head;
-        __syncwarp();
         if (lane == 0) {
             // a tile that ends the stream
             const bool got = !ok || issued < kStages || mbar_wait(&empty[st], phase ^ 1, abort_flag, p.status, 22);
@@ -489,18 +462,21 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         sum += f[w] * sm_m[kConsumers * 16 + w * 16 + row];
                         exact += f[w] * sm_m[2 * kConsumers * 16 + w * 16 + row];
                     }
-                    float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
                     const float *from = reinterpret_cast<const float *>(smem + st * 2 * L::TILE) + row * D;
                     const int tok = row / p.group;
                     const int h = t.hk * p.group + row - tok * p.group;
                     const size_t out_row = (size_t)(t.row0 + tok) * p.a.Hq + h;
-                    const size_t slot = (size_t)blockIdx.x * 2 + (t.flags & kSlot1 ? 1 : 0);
-                    // a whole pair takes the shared prefix' parts in as well
-                    const int planes = t.flags & kPart ? 0 : p.planes;
-                    const size_t stride = (size_t)p.a.total * p.a.Hq;
-                    PlaneWeights pw;
-                    if (planes) inv *= pw.join(p.plane_lse2 + out_row, stride, planes, lse2);
+                    // a whole pair's result is final, or goes to the plane to be
+                    // merged with the shared prefix'; a part goes to its slot
+                    float *to_o = p.part.plane, *to_lse2 = p.part.plane_lse2;
+                    size_t at = out_row;
+                    if (t.flags & kPart) {
+                        to_o = p.part.slot;
+                        to_lse2 = p.part.slot_lse2;
+                        at = ((size_t)blockIdx.x * 2 + (t.flags & kSlot1 ? 1 : 0)) * kMaxRows + row;
+                    }
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         const int c = c0 + part * 4;
@@ -518,18 +494,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         o.y *= inv;
                         o.z *= inv;
                         o.w *= inv;
-                        for (int s2 = 0; s2 < planes; ++s2) {
-                            const float w = pw.weight(p.plane_lse2[s2 * stride + out_row]);
-                            if (w == 0.f) continue;
-                            const float4 x =
-                                *reinterpret_cast<const float4 *>(p.plane_o + (s2 * stride + out_row) * D + c);
-                            o.x = fmaf(w, x.x, o.x);
-                            o.y = fmaf(w, x.y, o.y);
-                            o.z = fmaf(w, x.z, o.z);
-                            o.w = fmaf(w, x.w, o.w);
-                        }
-                        if (t.flags & kPart) {
-                            *reinterpret_cast<float4 *>(p.part_o + (slot * kMaxRows + row) * D + c) = o;
+                        if (to_o) {
+                            *reinterpret_cast<float4 *>(to_o + at * D + c) = o;
                         } else {
                             const uint2 w = BF16 ? make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w))
                                                  : make_uint2(pack_f16x2(o.x, o.y), pack_f16x2(o.z, o.w));
@@ -537,10 +503,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         }
                     }
                     if (part == 0) {
-                        if (t.flags & kPart)
-                            p.part_lse2[slot * kMaxRows + row] = lse2;
+                        if (to_lse2)
+                            to_lse2[at] = lse2;
                         else
                             p.a.lse[(size_t)h * p.a.total + t.row0 + tok] = lse2 * 0.69314718055994530942f;
+                        if (!(t.flags & kPart) || (t.flags & kSlot1))
+                            p.part.code[out_row] = t.code ? t.code + part_code(0, 0, row) : 0;
                     }
                 }
                 fence_proxy_async_smem();  // the buffer's next writer is a TMA copy
@@ -553,180 +521,234 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
         }
     }
+    // the merge, which waits for this kernel, then also has the prefix' results
+    wait_previous();
 }
 
-// Merges the parts of pairs that several CTAs shared.  Block x belongs to CTA
-// x of the main kernel (its header says whether a pair began there and went
-// on), block y to four of the 16 rows; two warps a row take every other part.
-constexpr int kMergeRows = 4;
+// Merges the parts of every row that has several: W warps a row (1 or 8 of
+// the block's), each taking every W-th part.
+struct MergeParams {
+    PagedArgs a;
+    PartView own, prefix;
+    int warps;
+};
+
+constexpr int kMergeWarps = 8;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(64 * kMergeRows) paged_merge_kernel(const FewParams p) {
-    const PieceHeader head = p.headers[blockIdx.x];
-    if (head.pieces == 0) return;
-    const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 6);
-    const int rows = head.n * p.group;
-    const int sub = (threadIdx.x >> 5) & 1, lane = threadIdx.x & 31;
-    const int tok = row / p.group;
-    const int h = head.hk * p.group + row - tok * p.group;
-    const size_t out_row = (size_t)(head.row0 + tok) * p.a.Hq + h;
-    constexpr int E = D / 32;
-    __shared__ float sm_o[kMergeRows][D], sm_lse[kMergeRows];
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams p) {
+    constexpr int E = D / 32;  // columns of a lane
+    __shared__ float sm_o[kMergeWarps][D], sm_top[kMergeWarps], sm_sum[kMergeWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int W = p.warps, sub = warp % W;
+    const long long id = (long long)blockIdx.x * (kMergeWarps / W) + warp / W;
+    const long long rows = (long long)p.a.total * p.a.Hq;
+    wait_previous();
+    const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
+    bool mine = id < rows;
+    // the row's request: the last that starts at or before it, 32 offsets a step
+    if (mine) {
+        int b = tok;
+        if (p.a.cu_seqlens) {
+            int lo = 0, hi = p.a.B;  // starts at or before tok in [lo, hi)
+            while (hi - lo > 1) {
+                const int step = (hi - lo + 31) / 32;
+                const int at = lo + lane * step;
+                const unsigned under = __ballot_sync(0xffffffffu, at < hi && p.a.cu_seqlens[at] <= tok);
+                const int k = under ? 31 - __clz(under) : 0;
+                lo += k * step;
+                hi = min(hi, lo + step);
+            }
+            b = lo;
+        }
+        Request r;
+        mine = b < p.a.B && load_request(p.a, b, r) && tok >= r.row0 && tok < r.row0 + r.n;
+    }
+    // the row's parts: the own pass', then the prefix'
+    int n_own = 0, n_all = 0, c_own = 0, c_pre = 0;
+    if (mine) {
+        c_own = p.own.code[id];
+        n_own = c_own ? c_own & kMaxPieces : p.own.plane ? 1 : 0;
+        n_all = n_own;
+        if (p.prefix.code) {
+            c_pre = p.prefix.code[id];
+            n_all += c_pre ? c_pre & kMaxPieces : 1;
+        }
+    }
     float acc[E], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (row < rows) {
-        for (int k = sub; k < head.pieces + p.planes; k += 2) {
-            const size_t slot = (size_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0);
-            const bool own = k < head.pieces;
-            const size_t at = own ? slot * kMaxRows + row : (size_t)(k - head.pieces) * p.a.total * p.a.Hq + out_row;
-            const float lse2 = (own ? p.part_lse2 : p.plane_lse2)[at];
-            const float *o = (own ? p.part_o : p.plane_o) + at * D + lane * E;
-            if (lse2 == -INFINITY) continue;
-            const float to = fmaxf(top, lse2);
-            const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
+    constexpr int U = 4;  // parts in flight
+    for (int k0 = sub; k0 < n_all; k0 += W * U) {
+        float lse2[U], x[U][E];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int k = k0 + i * W;
+            lse2[i] = -INFINITY;
+            if (k >= n_all) continue;
+            const bool own = k < n_own;
+            const PartView &v = own ? p.own : p.prefix;
+            const int code = own ? c_own : c_pre, piece = own ? k : k - n_own;
+            const size_t at = code ? ((size_t)((code >> 9 & kMaxPieces) + piece) * 2 + (piece == 0 ? 1 : 0)) * v.slot_rows +
+                                         (code >> 18)
+                                   : (size_t)id;
+            lse2[i] = (code ? v.slot_lse2 : v.plane_lse2)[at];
+            const float *o = (code ? v.slot : v.plane) + at * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(o);
+                x[i][0] = w.x; x[i][1] = w.y; x[i][2] = w.z; x[i][3] = w.w;
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(o);
+                x[i][0] = w.x; x[i][1] = w.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (lse2[i] == -INFINITY) continue;
+            const float to = fmaxf(top, lse2[i]);
+            const float a = ex2_approx(top - to), w = ex2_approx(lse2[i] - to);
             sum = sum * a + w;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * o[e];
-            top = to;
-        }
-        if (sub == 1) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) sm_o[threadIdx.x >> 6][lane * E + e] = sum > 0.f ? acc[e] / sum : 0.f;
-            if (lane == 0) sm_lse[threadIdx.x >> 6] = sum > 0.f ? top + log2f(sum) : -INFINITY;
-        }
-    }
-    __syncthreads();
-    if (row >= rows || sub == 1) return;
-    {
-        const float lse2 = sm_lse[threadIdx.x >> 6];
-        const float to = fmaxf(top, lse2);
-        if (to != -INFINITY) {
-            const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
-            sum = sum * a + w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * sm_o[threadIdx.x >> 6][lane * E + e];
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * x[i][e];
             top = to;
         }
     }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+        if (lane == 0) {
+            sm_top[warp] = top;
+            sm_sum[warp] = sum;
+        }
+        __syncthreads();
+        if (sub) return;
+        for (int k = 1; k < W; ++k) {
+            const float t2 = sm_top[warp + k];
+            if (t2 == -INFINITY) continue;
+            const float to = fmaxf(top, t2);
+            const float a = ex2_approx(top - to), w = ex2_approx(t2 - to);
+            sum = sum * a + w * sm_sum[warp + k];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * sm_o[warp + k][lane * E + e];
+            top = to;
+        }
+    }
+    if (n_all == 0) return;  // final already, or a row of no request
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t *out = static_cast<uint16_t *>(p.a.o) + out_row * D + lane * E;
+    uint16_t *out = static_cast<uint16_t *>(p.a.o) + (size_t)id * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t *>(out + e) =
             BF16 ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0)
-        p.a.lse[(size_t)h * p.a.total + head.row0 + tok] =
-            sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+        p.a.lse[(size_t)h * p.a.total + tok] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
-// Workspace: the few-row kernel's headers and parts, then the planes.
-constexpr size_t kHeaderBytes = (kMaxCtas * sizeof(PieceHeader) + 255) & ~size_t(255);
-constexpr size_t kFewLseBytes = (kMaxCtas * 2 * kMaxRows * sizeof(float) + 255) & ~size_t(255);
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
-template <int D, bool BF16>
-cudaError_t launch_few(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st) {
-    using L = FewLayout<D>;
-    const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tk, tv;
-    const uint32_t rows = a.page_size < L::TK ? a.page_size : L::TK;
-    const uint64_t planes = (uint64_t)a.num_pages * a.Hkv;
-    if (!make_tmap_3d(&tk, a.k_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_3d(&tv, a.v_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    auto kernel = paged_few_kernel<D, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
-    if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    FewParams p;
-    p.a = a;
-    p.shift = shift;
-    p.group = a.Hq / a.Hkv;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.status = device_status_ptr();
-    char *ws = static_cast<char *>(a.workspace);
-    p.headers = reinterpret_cast<PieceHeader *>(ws);
-    p.part_lse2 = reinterpret_cast<float *>(ws + kHeaderBytes);
-    p.part_o = reinterpret_cast<float *>(ws + kHeaderBytes + kFewLseBytes);
-    p.planes = w.prefix_splits;
-    p.plane_o = w.part_o;
-    p.plane_lse2 = w.part_lse2;
-    const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    kernel<<<grid, kFewThreads, L::ALLOC, st>>>(tk, tv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    paged_merge_kernel<D, BF16><<<dim3(grid, kMaxRows / kMergeRows), 64 * kMergeRows, 0, st>>>(p);
-    return cudaGetLastError();
+// Rounded up to whole 256-byte steps of the workspace.
+template <typename T>
+T *take(uintptr_t &at, size_t n) {
+    T *p = reinterpret_cast<T *>(at);
+    at += (n * sizeof(T) + 255) & ~size_t(255);
+    return p;
 }
 
-}  // namespace
-
-namespace {
+int at_most(long long want, int most) { return (int)(want < 1 ? 1 : want < most ? want : most); }
 
 constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
 
-// Rows of a pair: max_new * group.  Up to 16 go to the kernel of this file,
-// whose tile has 16 rows, more to the 256-row one.
-bool few_rows(int max_new, int group) { return (long long)max_new * group <= kMaxRows; }
-
-int clamp_splits(long long ctas, long long tiles) {
-    const long long s = ctas > 0 ? kSms / ctas : 1;
-    return (int)(s < 1 ? 1 : s < tiles ? s : tiles);
+template <int D, bool BF16>
+cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st) {
+    using L = FewLayout<D>;
+    CUtensorMap tk, tv;
+    if (!make_tmap_pages(&tk, a.k_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK) ||
+        !make_tmap_pages(&tv, a.v_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK))
+        return cudaErrorInvalidValue;
+    FewParams p;
+    p.a = a;
+    p.group = a.Hq / a.Hkv;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.status = device_status_ptr();
+    p.part = w.own;
+    return launch_after(paged_few_kernel<D, BF16>, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
 }
 
-// Enough key ranges that the blocks fill the SMs once, and no more.
-WidePlan plan_wide(int B, int total, int max_new, int Hq, int Hkv, int max_pages, int page_size, int prefix_len) {
-    WidePlan w{};
-    const int g = Hq / Hkv;
-    const long long row_blocks = ((long long)total * g + 255) / 256;
-    if (prefix_len > 0) {
-        w.prefix_blocks = (int)row_blocks;
-        w.prefix_splits = clamp_splits(row_blocks * Hkv, (prefix_len + 127ll) / 128);
-    }
-    if (!few_rows(max_new, g)) {
-        const long long most = (long long)B * (((long long)max_new * g + 255) / 256);
-        const long long blocks = row_blocks + B < most ? row_blocks + B : most;
-        w.own_blocks = (int)blocks;
-        w.own_splits = clamp_splits(blocks * Hkv, ((long long)max_pages * page_size + 127) / 128);
-    }
-    return w;
+template <int D, bool BF16>
+cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t st) {
+    MergeParams p;
+    p.a = a;
+    p.own = w.own;
+    p.prefix = w.prefix;
+    // few rows can have many parts each, many rows have few
+    const long long rows = (long long)a.total * a.Hq;
+    p.warps = rows <= 1024 ? 8 : rows <= 8192 ? 2 : 1;
+    const long long per_block = kMergeWarps / p.warps;
+    return launch_after(paged_merge_kernel<D, BF16>, (unsigned)((rows + per_block - 1) / per_block), 32 * kMergeWarps,
+                        0, true, st, p);
 }
-
-size_t wide_planes(const WidePlan &w) {
-    // a single range of a request's own keys is final
-    if (w.prefix_splits == 0 && w.own_splits == 1) return 0;
-    return (size_t)w.prefix_splits + w.own_splits;
-}
-
-size_t few_bytes(int d) { return kHeaderBytes + kFewLseBytes + (size_t)kMaxCtas * 2 * kMaxRows * d * sizeof(float); }
 
 }  // namespace
 
-size_t fwd_paged_workspace(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
-                           int prefix_len) {
-    const WidePlan w = plan_wide(B, total, max_new, Hq, Hkv, max_pages, page_size, prefix_len);
-    const size_t rows = (size_t)total * Hq * wide_planes(w);
-    return (few_rows(max_new, Hq / Hkv) ? few_bytes(d) : 256) + round256(rows * sizeof(float)) +
-           rows * d * sizeof(float);
+PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
+                     int prefix_len, void *workspace) {
+    PagedPlan w{};
+    const int g = Hq / Hkv;
+    const size_t rows = (size_t)total * Hq;
+    const long long row_blocks = ((long long)total * g + kWideRows - 1) / kWideRows;
+    const long long keys = (long long)max_pages * page_size;
+    // Rows of a (request, key/value head) pair: up to 16 fill the tile of the
+    // few-row kernel, more go to the 256-row one.
+    w.few = (long long)max_new * g <= kMaxRows;
+    uintptr_t at = reinterpret_cast<uintptr_t>(workspace);
+    w.own.code = take<int>(at, rows);
+    if (w.few) {
+        const long long tiles = (keys + (d == 128 ? 63 : 127)) / (d == 128 ? 64 : 128);
+        w.own.ctas = at_most(B * (long long)Hkv * tiles / kMinUnits, kMaxCtas);
+        w.own.slot_rows = kMaxRows;
+    } else {
+        const long long most = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
+        const long long blocks = row_blocks + B < most ? row_blocks + B : most;
+        w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys) / kWideMinUnits, kSms);
+        w.own.slot_rows = kWideRows;
+    }
+    if (prefix_len > 0) {
+        w.prefix.ctas = at_most(row_blocks * Hkv * ((prefix_len + kWideKeys - 1ll) / kWideKeys) / kWideMinUnits, kSms);
+        w.prefix.slot_rows = kWideRows;
+        w.prefix.code = take<int>(at, rows);
+        w.own.plane_lse2 = take<float>(at, rows);
+        w.own.plane = take<float>(at, rows * d);
+        w.prefix.plane_lse2 = take<float>(at, rows);
+        w.prefix.plane = take<float>(at, rows * d);
+        w.prefix.slot_lse2 = take<float>(at, (size_t)w.prefix.ctas * 2 * kWideRows);
+        w.prefix.slot = take<float>(at, (size_t)w.prefix.ctas * 2 * kWideRows * d);
+    }
+    w.own.slot_lse2 = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows);
+    w.own.slot = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows * d);
+    w.bytes = at - reinterpret_cast<uintptr_t>(workspace);
+    return w;
 }
 
-cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st) {
-    int shift = 0;
-    while ((1 << shift) < a.page_size) ++shift;
-    WidePlan w = plan_wide(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.max_pages, a.page_size, a.prefix_len);
-    const bool few = few_rows(a.max_new, a.Hq / a.Hkv);
-    char *ws = static_cast<char *>(a.workspace) + (few ? few_bytes(a.d) : 256);
-    w.part_lse2 = reinterpret_cast<float *>(ws);
-    w.part_o = reinterpret_cast<float *>(ws + round256((size_t)a.total * a.Hq * wide_planes(w) * sizeof(float)));
-    if (w.prefix_splits || w.own_splits) {
-        const cudaError_t e = launch_paged_wide(a, shift, w, st);
-        if (e != cudaSuccess || !few) return e;
-    }
-    if (a.d == 128) return a.bf16 ? launch_few<128, true>(a, shift, w, st) : launch_few<128, false>(a, shift, w, st);
-    return a.bf16 ? launch_few<64, true>(a, shift, w, st) : launch_few<64, false>(a, shift, w, st);
+cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st) {
+    if (a.d == 128) return a.bf16 ? launch_few_t<128, true>(a, w, after, st) : launch_few_t<128, false>(a, w, after, st);
+    return a.bf16 ? launch_few_t<64, true>(a, w, after, st) : launch_few_t<64, false>(a, w, after, st);
+}
+
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st) {
+    if (a.d == 128) return a.bf16 ? launch_merge_t<128, true>(a, w, st) : launch_merge_t<128, false>(a, w, st);
+    return a.bf16 ? launch_merge_t<64, true>(a, w, st) : launch_merge_t<64, false>(a, w, st);
+}
+
+cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
+    PagedArgs a = args;
+    a.shift = 0;
+    while ((1 << a.shift) < a.page_size) ++a.shift;
+    const PagedPlan w = plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size, a.prefix_len,
+                                   a.workspace);
+    cudaError_t e = cudaSuccess;
+    const bool front = w.prefix.ctas > 0;
+    if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;
+    e = w.few ? launch_paged_few(a, w, front, st) : launch_paged_wide(a, w, false, front, st);
+    if (e != cudaSuccess) return e;
+    return launch_paged_merge(a, w, st);
 }
 
 }  // namespace fa

@@ -2,9 +2,9 @@
 // many query rows: prompts read in by chunks, and the rows of a whole batch
 // against a prefix that all its requests share.
 //
-// One CTA owns 256 query rows of one key/value head and a range of its key
-// tiles.  A row is a (token, query head) pair: the g = Hq / Hkv heads that
-// read the key/value head are neighbouring rows of the tile, so grouped
+// A segment of work is 256 query rows of one key/value head and a range of
+// its key tiles.  A row is a (token, query head) pair: the g = Hq / Hkv heads
+// that read the key/value head are neighbouring rows of the tile, so grouped
 // heads share every K/V tile that is read, and with a shared prefix so do all
 // requests (their rows stand one behind the other in q).  The loop is that of
 // the dense forward (fa_fwd.cu): two 128-row Q tiles A and B walk the same
@@ -12,10 +12,17 @@
 // rescaled lazily and exactly, and P is read from tensor memory.  What
 // differs: K/V tiles are gathered page by page (one TMA box per page and
 // 64-column half), Q rows are copied into the swizzled operand layout by the
-// softmax threads, every row has its own visible range of keys, and a CTA may
-// take only part of the key tiles and leave (O~ / l, log2 sum) for a merge.
-//   warps 0-3 softmax + epilogue of tile A, 4-7 of tile B, 8 producer,
-//   9 MMA issuer (owns the tensor memory)
+// softmax threads, and every row has its own visible range of keys.
+//
+// The key tiles of all (row block, key/value head) pairs are numbered in
+// order and every CTA (one per SM) takes an equal, contiguous range, as in
+// the few-row kernel: chunks behind contexts of any lengths then keep all SMs
+// busy to the end, at the price of merging the blocks that a range's border
+// cuts (at most one border a CTA).  The K/V ring, the barriers and the tensor
+// memory carry on from segment to segment; the next segment's Q is loaded
+// and its first S issued before the epilogue of the one before.
+//   warps 0-3 softmax + epilogue of tile A, 4-7 of tile B, 8 producer (plans
+//   the segments and tells the others), 9 MMA issuer (owns the tensor memory)
 #include "../../include/fa.h"
 #include "host_util.h"
 #include "paged.h"
@@ -27,7 +34,8 @@ namespace fa {
 namespace {
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kRows = 2 * kBM;
+constexpr int kRows = kWideRows;
+static_assert(kRows == 2 * kBM && kBN == kWideKeys, "tile sizes of the plan");
 constexpr int kThreads = 320;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;
@@ -45,26 +53,35 @@ struct WideLayout {
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_BAR = OFF_V + VS * TILE;
     // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2],
-    // p_full[2], o_final[2], drain
-    static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 2 + 2 + 2 + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int BYTES = OFF_MISC + 48;
+    // p_full[2], o_final[2], seg_full[2], seg_empty[2], drain
+    static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 2 + 2 + 2 + 2 + 2 + 1;
+    static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
+    static constexpr int OFF_MISC = OFF_SEG + 2 * 48;
+    static constexpr int BYTES = OFF_MISC + 32;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
 
 struct WideParams {
     PagedArgs a;
-    int shift;        // log2(page_size)
-    int group;        // query heads per key/value head
-    int prefix;       // 1: rows of the whole batch against the shared prefix
-    int blocks;       // row blocks (upper bound)
-    int splits;       // key ranges
-    float *part_o;    // [splits][total][Hq][D], or null: O and LSE are final
-    float *part_lse2; // [splits][total][Hq]
+    int group;   // query heads per key/value head
+    int prefix;  // 1: rows of the whole batch against the shared prefix
+    PartView part;
     float scale_log2;
     unsigned int *status;
 };
+
+// Part of a row block's keys, as the producer tells it to the others.
+struct Segment {
+    int row0, n, len;    // rows of q and keys of the request (prefix: of the batch, of the prefix)
+    int r0;              // first row of the block, counted in (token, head) pairs
+    int hk, j0, nj;      // key/value head; first key tile, number of them (-1: the end)
+    int key_lo, key_hi;  // keys some row of the block sees
+    int code;            // of the block's rows (PartView), 0 if the block is whole
+    int slot;            // -1: whole, else the CTA's slot that the part goes to
+    int pad;
+};
+static_assert(sizeof(Segment) == 48, "shared-memory slot");
 
 // The request of a row of q: the last one that starts at or before it.
 __device__ __forceinline__ int request_of(const PagedArgs &a, int row) {
@@ -75,6 +92,56 @@ __device__ __forceinline__ int request_of(const PagedArgs &a, int row) {
         if (a.cu_seqlens[mid] <= row) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Row blocks of a request, and the keys that block k of it sees.
+__device__ __forceinline__ int blocks_of(const Request &r, int group) {
+    return (int)(((long long)r.n * group + kRows - 1) / kRows);
+}
+__device__ __forceinline__ void block_keys(const WideParams &p, const Request &r, int k, int prefix_lo, int &lo,
+                                           int &hi) {
+    if (p.prefix) {
+        lo = prefix_lo;
+        hi = r.len;
+        return;
+    }
+    const int first = (int)((long long)k * kRows / p.group);
+    const int last = (int)min((long long)r.n - 1, ((long long)(k + 1) * kRows - 1) / p.group);
+    hi = max(0, r.len - r.n + last + 1);
+    lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
+}
+// Key tiles of a range; at least one, so that rows that see nothing are written.
+__device__ __forceinline__ int range_tiles(int lo, int hi) { return max(1, (hi + kBN - 1) / kBN - lo / kBN); }
+
+// Key tiles of all blocks of a request, for one key/value head.  The sums of
+// 32 requests, one a lane: a lane walks its own request's blocks where they
+// are few, the warp walks them together where a request has many.
+__device__ __forceinline__ int request_tiles(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
+    int sum = 0;
+    if (!__any_sync(0xffffffffu, nb > 8)) {
+        for (int k = 0; k < nb; ++k) {
+            int lo, hi;
+            block_keys(p, r, k, prefix_lo, lo, hi);
+            sum += range_tiles(lo, hi);
+        }
+        return sum;
+    }
+    for (int i = 0; i < 32; ++i) {
+        Request o;
+        o.row0 = 0;
+        o.n = __shfl_sync(0xffffffffu, r.n, i);
+        o.len = __shfl_sync(0xffffffffu, r.len, i);
+        const int n = __shfl_sync(0xffffffffu, nb, i);
+        int mine = 0;
+        for (int k = lane; k < n; k += 32) {
+            int lo, hi;
+            block_keys(p, o, k, prefix_lo, lo, hi);
+            mine += range_tiles(lo, hi);
+        }
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == i) sum = mine;
+    }
+    return sum;
 }
 
 template <int D, bool BF16>
@@ -93,133 +160,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = v_empty + L::VS;  // [2]
     uint64_t *p_full = s_full + 2;       // [2]
     uint64_t *o_final = p_full + 2;      // [2]
-    uint64_t *drain = o_final + 2;
+    uint64_t *seg_full = o_final + 2;    // [2]
+    uint64_t *seg_empty = seg_full + 2;  // [2]
+    uint64_t *drain = seg_empty + 2;
+    Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
-    int *block_at = reinterpret_cast<int *>(smem + L::OFF_MISC + 8);  // request, block within it
-    int *low_key = reinterpret_cast<int *>(smem + L::OFF_MISC + 16);
+    int *prefix_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 8);
+    unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    // (key range, key/value head, row block): the key ranges of one block are
-    // far apart in the grid, neighbouring CTAs read the same keys
-    const int hk = (blockIdx.x / p.blocks) % p.a.Hkv;
-    const int split = blockIdx.x / p.blocks / p.a.Hkv;
-    const int block = blockIdx.x % p.blocks;
-
-    // ------------------------------------------- the block's rows and keys
-    int row0 = 0, n = 0, len = 0, r0 = 0;  // request's rows and keys; first row of the block
-    const int *table = p.a.prefix_pages;
-    if (p.prefix) {
-        n = p.a.cu_seqlens ? p.a.cu_seqlens[p.a.B] : p.a.B;
-        // offsets that end outside q are reported with their request; the
-        // sound ones may have rows anywhere
-        if (n < 0 || n > p.a.total) n = p.a.total;
-        len = p.a.prefix_len;
-        r0 = block * kRows;
-    } else {
-        // blocks are numbered through the requests' rows
-        if (warp == 0) {
-            if (lane == 0) block_at[0] = -1;
-            int at = 0;  // blocks before request b
-            for (int b = 0; b < p.a.B; b += 32) {
-                Request r;
-                int mine = 0;
-                if (b + lane < p.a.B) {
-                    if (!load_request(p.a, p.shift, b + lane, r)) {
-                        if (blockIdx.x == 0) record_bad_args(p.status);
-                    } else {
-                        mine = (int)(((long long)r.n * p.group + kRows - 1) / kRows);
-                    }
-                }
-                int incl = mine;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, incl, s);
-                    if (lane >= s) incl += x;
-                }
-                const unsigned past = __ballot_sync(0xffffffffu, at + incl > block);
-                if (past) {
-                    if (lane == __ffs(past) - 1) {
-                        block_at[0] = b + lane;
-                        block_at[1] = block - (at + incl - mine);
-                    }
-                    if (blockIdx.x != 0) break;  // CTA 0 goes through all, to report bad ones
-                    at = -0x40000000;
-                    continue;
-                }
-                at += __shfl_sync(0xffffffffu, incl, 31);
-            }
-        }
-        __syncthreads();
-        const int b = block_at[0];
-        if (b < 0) return;  // more blocks than the batch has: nothing started yet
-        Request r;
-        load_request(p.a, p.shift, b, r);
-        row0 = r.row0;
-        n = r.n;
-        len = r.len;
-        r0 = block_at[1] * kRows;
-        table = p.a.block_table + (size_t)b * p.a.max_pages;
-    }
-    const int rows = (int)min((long long)n * p.group - r0, (long long)kRows);  // of this block
-    if (rows <= 0) return;
-    const int t_first = r0 / p.group, t_last = (r0 + rows - 1) / p.group;
-
-    // this thread's row (softmax warps): where it is and which keys it sees
-    const int row = threadIdx.x;
-    const bool valid = row < rows;
-    int tok = 0, head = 0, hi = 0x7FFFFFFF, lo = -0x7FFFFFFF;
-    if (valid) {
-        const int t = (r0 + row) / p.group;
-        head = hk * p.group + (r0 + row) - t * p.group;
-        tok = row0 + t;
-        if (p.prefix) {
-            const int b = request_of(p.a, tok);
-            Request r;
-            if (load_request(p.a, p.shift, b, r)) {
-                hi = p.a.prefix_len + r.len - r.n + (tok - r.row0) + 1;
-                lo = p.a.window > 0 ? hi - p.a.window : 0;
-            }
-        } else {
-            hi = len - n + t + 1;
-            lo = p.a.window > 0 ? hi - p.a.window : 0;
-        }
-    }
-    // keys some row of the block sees
-    int key_lo = 0, key_hi = len;
-    if (p.prefix) {
-        if (p.a.window > 0) {
-            if (threadIdx.x == 0) *low_key = 0x7FFFFFFF;
-            __syncthreads();
-            if (valid) atomicMin(low_key, max(0, min(lo, len)));
-            __syncthreads();
-            key_lo = *low_key;
-        }
-    } else {
-        key_hi = max(0, len - n + t_last + 1);
-        if (p.a.window > 0) key_lo = max(0, len - n + t_first + 1 - p.a.window);
-    }
-    const int t0 = key_lo / kBN;
-    const int tiles = max(0, (key_hi + kBN - 1) / kBN - t0);
-    // this CTA's tiles; with nothing to see, one fully masked tile keeps the
-    // path the same
-    const int j0 = t0 + (int)((long long)tiles * split / p.splits);
-    const int j1 = t0 + (int)((long long)tiles * (split + 1) / p.splits);
-    const int nj = j1 - j0;
-    const bool two = rows > kBM;
-
-    if (nj == 0) {  // uniform: an empty range (few tiles, many ranges)
-        if (valid) {
-            if (p.part_o) {
-                p.part_lse2[((size_t)split * p.a.total + tok) * p.a.Hq + head] = -INFINITY;
-            } else {
-                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + ((size_t)tok * p.a.Hq + head) * D);
-                for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
-                p.a.lse[(size_t)head * p.a.total + tok] = -INFINITY;
-            }
-        }
-        return;
-    }
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 2 * kBM);
@@ -229,9 +178,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], kBM);
             mbar_init(&o_final[x], 1);
+            mbar_init(&seg_full[x], 1);
+            mbar_init(&seg_empty[x], 9);  // the MMA warp and eight softmax warps
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *prefix_low = 0x7FFFFFFF;
+        *sm_units = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -242,6 +195,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    launch_dependents();
+
+    // ---------------------------------------------- the batch's units of work
+    const int B = p.prefix ? 1 : p.a.B;
+    Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
+    int prefix_lo = 0;
+    if (p.prefix) {
+        whole.n = p.a.cu_seqlens ? p.a.cu_seqlens[p.a.B] : p.a.B;
+        // offsets that end outside q are reported with their request; the
+        // sound ones may have rows anywhere
+        if (whole.n < 0 || whole.n > p.a.total) whole.n = p.a.total;
+        if (p.a.window > 0) {  // the first key that any row sees
+            for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
+                Request r;
+                if (load_request(p.a, b, r) && r.n > 0)
+                    atomicMin(prefix_low, max(0, p.a.prefix_len + r.len - r.n + 1 - p.a.window));
+            }
+            __syncthreads();
+            prefix_lo = min(*prefix_low, p.a.prefix_len);
+        }
+        if (threadIdx.x == 0)
+            *sm_units = (unsigned long long)blocks_of(whole, p.group) * range_tiles(prefix_lo, whole.len) * p.a.Hkv;
+    } else {
+        for (int b = warp * 32; b < B; b += kThreads) {
+            Request r{0, 0, 0};
+            if (b + lane < B && !load_request(p.a, b + lane, r)) {
+                if (blockIdx.x == 0) record_bad_args(p.status);
+                r.n = 0;
+            }
+            const int tiles = request_tiles(p, r, blocks_of(r, p.group), 0, lane);
+            if (tiles) atomicAdd(sm_units, (unsigned long long)tiles * p.a.Hkv);
+        }
+    }
+    __syncthreads();
+    const long long T = (long long)*sm_units;
+    const int G = (int)min((long long)gridDim.x, max(1ll, T / kWideMinUnits));
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------ TMA producer
@@ -249,53 +238,161 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
-        const int page_keys = min(1 << p.shift, kBN);
+        const int page_keys = min(1 << p.a.shift, kBN);
         const int box_bytes = page_keys * 128;
         const int half = lane % L::NBOX, sub = lane / L::NBOX;
         const bool boxed = lane < L::NBOX * (kBN / page_keys);
-        int done = 0;
-        bool v_missing = false;
-        for (int u = 0; u < nj; ++u) {
-            // pages that hold no key of the block's range are not looked up
-            const int key0 = (j0 + u) * kBN + sub * page_keys;
-            const bool live = boxed && key0 < key_hi && key0 + page_keys > key_lo;
-            int page = 0;
-            if (live) {
-                page = table[key0 >> p.shift];
-                if (page < 0 || page >= p.a.num_pages) {
-                    record_bad_args(p.status);
-                    page = p.a.num_pages;  // out of the tensor: the copy fills zeros
+        const int c = blockIdx.x;
+        const long long u0 = c < G ? c * T / G : T, u1 = c < G ? (c + 1ll) * T / G : T;
+        int nk = 0, nv = 0, ns = 0;  // K and V tiles and segments handed on
+        bool ok = true;
+        // hands a segment to the other warps
+        auto tell = [&](const Segment &sg) {
+            const int slot = ns & 1;
+            const bool got = ns < 2 || mbar_wait(&seg_empty[slot], ((ns >> 1) + 1) & 1, abort_flag, p.status, 39);
+            ok = __all_sync(0xffffffffu, got);
+            if (ok && lane == 0) {
+                segs[slot] = sg;
+                mbar_arrive(&seg_full[slot]);
+            }
+            ++ns;
+        };
+        auto load = [&](int b, Request &r) -> bool {
+            if (!p.prefix) return load_request(p.a, b, r);
+            r = whole;
+            return true;
+        };
+        // the request that holds unit u0, and its first unit
+        int b = 0;
+        long long base = 0;
+        if (u0 < u1 && !p.prefix) {
+            for (; b < B; b += 32) {
+                Request r{0, 0, 0};
+                if (b + lane < B && !load_request(p.a, b + lane, r)) r.n = 0;
+                const long long units = (long long)request_tiles(p, r, blocks_of(r, p.group), 0, lane) * p.a.Hkv;
+                long long incl = units;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const long long x = __shfl_up_sync(0xffffffffu, incl, s);
+                    if (lane >= s) incl += x;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + incl > u0);
+                if (past) {
+                    const int k = __ffs(past) - 1;
+                    base += __shfl_sync(0xffffffffu, incl - units, k);
+                    b += k;
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        long long u = u0;
+        bool fresh = true;  // the place within the request is still to be found
+        int hk = 0, blk = 0;
+        long long blk0 = base;  // first unit of (hk, blk)
+        for (; ok && u < u1 && b < B; ++b, fresh = false, hk = 0, blk = 0) {
+            Request r;
+            if (!load(b, r) || r.n == 0) continue;
+            const int nb = blocks_of(r, p.group);
+            if (fresh) {
+                Request mine{0, 0, 0};
+                if (lane == 0) mine = r;
+                const int per_head =
+                    __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, prefix_lo, lane), 0);
+                hk = (int)((u - base) / per_head);
+                blk0 = base + (long long)hk * per_head;
+                // the block of that head: 32 at a time
+                for (blk = 0; blk < nb; blk += 32) {
+                    int lo, hi, tiles = 0;
+                    if (blk + lane < nb) {
+                        block_keys(p, r, blk + lane, prefix_lo, lo, hi);
+                        tiles = range_tiles(lo, hi);
+                    }
+                    int incl = tiles;
+#pragma unroll
+                    for (int s = 1; s < 32; s <<= 1) {
+                        const int x = __shfl_up_sync(0xffffffffu, incl, s);
+                        if (lane >= s) incl += x;
+                    }
+                    const unsigned past = __ballot_sync(0xffffffffu, blk0 + incl > u);
+                    if (past) {
+                        const int k = __ffs(past) - 1;
+                        blk0 += __shfl_sync(0xffffffffu, incl - tiles, k);
+                        blk += k;
+                        break;
+                    }
+                    blk0 += __shfl_sync(0xffffffffu, incl, 31);
                 }
             }
-            const int bytes = __popc(__ballot_sync(0xffffffffu, live)) * box_bytes;
-            const int ks = u % L::KS, vs = u % L::VS;
-            bool ok = u < L::KS || mbar_wait(&k_empty[ks], ((u / L::KS) + 1) & 1, abort_flag, p.status, 31);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
-            __syncwarp();
-            const int in_page = key0 & ((1 << p.shift) - 1);
-            if (live)
-                tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k, &k_full[ks],
-                            half * 64, in_page, page * p.a.Hkv + hk);
-            ok = u < L::VS || mbar_wait(&v_empty[vs], ((u / L::VS) + 1) & 1, abort_flag, p.status, 32);
-            if (!__all_sync(0xffffffffu, ok)) {
-                v_missing = true;
-                break;
+            const int *table = p.prefix ? p.a.prefix_pages : p.a.block_table + (size_t)b * p.a.max_pages;
+            for (; ok && hk < p.a.Hkv && u < u1; ++hk, blk = 0) {
+                for (; ok && blk < nb && u < u1; ++blk) {
+                    Segment sg;
+                    sg.row0 = r.row0;
+                    sg.n = r.n;
+                    sg.len = r.len;
+                    sg.r0 = blk * kRows;
+                    sg.hk = hk;
+                    block_keys(p, r, blk, prefix_lo, sg.key_lo, sg.key_hi);
+                    const int nt = range_tiles(sg.key_lo, sg.key_hi);
+                    const int first = (int)(u - blk0), end = (int)min((long long)nt, u1 - blk0);
+                    const bool is_whole = first == 0 && end == nt;
+                    sg.j0 = sg.key_lo / kBN + first;
+                    sg.nj = end - first;
+                    sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
+                    // a block that goes on in the next CTA belongs to the one it began in
+                    sg.code = sg.slot == 1 ? part_code((int)(((blk0 + nt) * G - 1) / T) - c + 1, c, 0) : 0;
+                    sg.pad = 0;
+                    tell(sg);
+                    for (int i = 0; ok && i < sg.nj; ++i) {
+                        // pages that hold no key of the block's range are not looked up
+                        const int key0 = (sg.j0 + i) * kBN + sub * page_keys;
+                        const bool live = boxed && key0 < sg.key_hi && key0 + page_keys > sg.key_lo;
+                        int page = 0;
+                        if (live) {
+                            page = table[key0 >> p.a.shift];
+                            if (page < 0 || page >= p.a.num_pages) {
+                                record_bad_args(p.status);
+                                page = p.a.num_pages;  // out of the tensor: the copy fills zeros
+                            }
+                        }
+                        const int bytes = __popc(__ballot_sync(0xffffffffu, live)) * box_bytes;
+                        const int in_page = key0 & ((1 << p.a.shift) - 1);
+                        const int ks = nk % L::KS, vs = nv % L::VS;
+                        bool got =
+                            nk < L::KS || mbar_wait(&k_empty[ks], ((nk / L::KS) + 1) & 1, abort_flag, p.status, 31);
+                        if (!(ok = __all_sync(0xffffffffu, got))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
+                        __syncwarp();
+                        if (live)
+                            tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
+                                        &k_full[ks], half * 64, in_page, page * p.a.Hkv + hk);
+                        ++nk;
+                        got = nv < L::VS || mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
+                        if (!(ok = __all_sync(0xffffffffu, got))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
+                        __syncwarp();
+                        if (live)
+                            tma_load_3d(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v,
+                                        &v_full[vs], half * 64, in_page, page * p.a.Hkv + hk);
+                        ++nv;
+                    }
+                    blk0 += nt;
+                    u = u1 < blk0 ? u1 : blk0;
+                }
             }
-            if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
-            __syncwarp();
-            if (live)
-                tma_load_3d(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v, &v_full[vs],
-                            half * 64, in_page, page * p.a.Hkv + hk);
-            ++done;
         }
-        if (done < nj && lane == 0) {
+        if (ok) {
+            Segment sg{};
+            sg.nj = -1;
+            tell(sg);
+        }
+        if (!ok && lane == 0) {
             // given up: let copies in flight land before the CTA exits
-            const int nk = done + (v_missing ? 1 : 0);
-            for (int u = max(0, nk - L::KS); u < nk; ++u)
-                mbar_wait_drain(&k_full[u % L::KS], (u / L::KS) & 1, 10000000ull);
-            for (int u = max(0, done - L::VS); u < done; ++u)
-                mbar_wait_drain(&v_full[u % L::VS], (u / L::VS) & 1, 10000000ull);
+            for (int i = max(0, nk - L::KS); i < nk; ++i)
+                mbar_wait_drain(&k_full[i % L::KS], (i / L::KS) & 1, 10000000ull);
+            for (int i = max(0, nv - L::VS); i < nv; ++i)
+                mbar_wait_drain(&v_full[i % L::VS], (i / L::VS) & 1, 10000000ull);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -307,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
         const uint64_t k_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
         const uint64_t v_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_V), L::BOX, 1024);
+        // u counts K/V tiles over all segments, first: a segment's first tile
         auto issue_s = [&](int x, int u) {
             const uint64_t q_desc = sdesc_advance(q_desc0, x * L::TILE);
             const uint64_t k_desc = sdesc_advance(k_desc0, (u % L::KS) * L::TILE);
@@ -318,68 +416,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_commit(&s_full[x]);
         };
-        auto issue_pv = [&](int x, int u) {
+        auto issue_pv = [&](int x, int u, bool first) {
             const uint64_t v_desc = sdesc_advance(v_desc0, (u % L::VS) * L::TILE);
             const uint32_t p_col = tmem + kColS + x * 128;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
                 mma_f16_ts(tmem + kColO + x * 128, p_col + kk * 8, sdesc_advance(v_desc, kk * 2048), idesc_pv,
-                           (u > 0 || kk > 0) ? 1u : 0u);
+                           (!first || kk > 0) ? 1u : 0u);
         };
         auto wait = [&](uint64_t *bar, int parity, int site) -> bool {
             const bool got = mbar_wait(bar, parity, abort_flag, p.status, site);
             tc_fence_after();
             return __all_sync(0xffffffffu, got);
         };
-        bool ok = wait(q_full, 0, 33) && wait(&k_full[0], 0, 34);
-        if (ok && lane == 0) {
-            issue_s(0, 0);
-            if (two) issue_s(1, 0);
-            mma_commit(&k_empty[0]);
-        }
-        for (int u = 0; ok && u < nj; ++u) {
-            const int vs = u % L::VS;
-            if (!(ok = wait(&v_full[vs], (u / L::VS) & 1, 35))) break;
-            const int kv0 = (j0 + u) * kBN;
-            if (kv0 < key_lo || kv0 + kBN > key_hi) {
-                // V rows that no row of the block sees may hold anything (the
-                // rest of a page, a buffer that was not filled), and 0 * NaN
-                // is NaN: clear them
-                uint8_t *v = smem + L::OFF_V + vs * L::TILE;
-                for (int i = lane; i < kBN * 8 * L::NBOX; i += 32) {
-                    const int key = kv0 + ((i >> 3) & (kBN - 1));
-                    if (key < key_lo || key >= key_hi) reinterpret_cast<uint4 *>(v)[i] = make_uint4(0, 0, 0, 0);
+        bool ok = true;
+        int u = 0, step_b = 0;  // tiles of all segments; of those that have a tile B
+        for (int g = 0; ok; ++g) {
+            if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
+            const Segment sg = segs[g & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[g & 1]);
+            if (sg.nj < 0) break;
+            const bool two = (long long)sg.n * p.group - sg.r0 > kBM;
+            if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
+            if (lane == 0) {
+                issue_s(0, u);
+                if (two) issue_s(1, u);
+                mma_commit(&k_empty[u % L::KS]);
+            }
+            for (int i = 0; i < sg.nj; ++i, ++u) {
+                const int vs = u % L::VS, kn = (u + 1) % L::KS;
+                const bool last = i + 1 == sg.nj;
+                if (!(ok = wait(&v_full[vs], (u / L::VS) & 1, 35))) break;
+                const int kv0 = (sg.j0 + i) * kBN;
+                if (kv0 < sg.key_lo || kv0 + kBN > sg.key_hi) {
+                    // V rows that no row of the block sees may hold anything
+                    // (the rest of a page, a buffer that was not filled), and
+                    // 0 * NaN is NaN: clear them
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + L::OFF_V + vs * L::TILE);
+                    for (int k = lane; k < kBN * 8 * L::NBOX; k += 32) {
+                        const int key = kv0 + ((k >> 3) & (kBN - 1));
+                        if (key < sg.key_lo || key >= sg.key_hi) v[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
+                if (!(ok = wait(&p_full[0], u & 1, 36))) break;
+                if (lane == 0) {
+                    issue_pv(0, u, i == 0);
+                    if (last) mma_commit(&o_final[0]);
+                }
+                if (!last) {
+                    if (!(ok = wait(&k_full[kn], ((u + 1) / L::KS) & 1, 34))) break;
+                    if (lane == 0) {
+                        issue_s(0, u + 1);
+                        if (!two) mma_commit(&k_empty[kn]);
+                    }
+                }
+                if (two) {
+                    if (!(ok = wait(&p_full[1], step_b & 1, 36))) break;
+                    ++step_b;
+                    if (lane == 0) {
+                        issue_pv(1, u, i == 0);
+                        if (last) mma_commit(&o_final[1]);
+                    }
+                }
+                if (lane == 0) {
+                    mma_commit(&v_empty[vs]);
+                    if (two && !last) {
+                        issue_s(1, u + 1);
+                        mma_commit(&k_empty[kn]);
+                    }
+                }
                 __syncwarp();
             }
-            if (!(ok = wait(&p_full[0], u & 1, 36))) break;
-            if (lane == 0) {
-                issue_pv(0, u);
-                if (u + 1 == nj) mma_commit(&o_final[0]);
-            }
-            if (u + 1 < nj) {
-                if (!(ok = wait(&k_full[(u + 1) % L::KS], ((u + 1) / L::KS) & 1, 34))) break;
-                if (lane == 0) {
-                    issue_s(0, u + 1);
-                    if (!two) mma_commit(&k_empty[(u + 1) % L::KS]);
-                }
-            }
-            if (two) {
-                if (!(ok = wait(&p_full[1], u & 1, 36))) break;
-                if (lane == 0) {
-                    issue_pv(1, u);
-                    if (u + 1 == nj) mma_commit(&o_final[1]);
-                }
-            }
-            if (lane == 0) {
-                mma_commit(&v_empty[vs]);
-                if (two && u + 1 < nj) {
-                    issue_s(1, u + 1);
-                    mma_commit(&k_empty[(u + 1) % L::KS]);
-                }
-            }
-            __syncwarp();
         }
         if (lane == 0) {
             // every MMA issued above has completed once `drain` flips
@@ -393,33 +503,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t col_s = kColS + x * 128, col_o = kColO + x * 128;
-        {
-            // Q into the operand layout: 16-byte pieces, a row's pieces by
-            // neighbouring lanes; rows past the block's own are zeros
+        const int row = threadIdx.x;
+        const float sl2 = p.scale_log2;
+        // waits for segment g and loads its Q (which the last S of the segment
+        // before has read) into the operand layout: 16-byte pieces, a row's
+        // pieces by neighbouring lanes; rows past the block's own are zeros
+        auto next_segment = [&](int g, Segment &sg) -> bool {
+            const bool got = mbar_wait(&seg_full[g & 1], (g >> 1) & 1, abort_flag, p.status, 41);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            sg = segs[g & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[g & 1]);
+            if (sg.nj < 0) return true;
+            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
             constexpr int CH = D / 8;
+#pragma unroll 8
             for (int i = threadIdx.x; i < kRows * CH; i += kRows) {
                 const int r = i / CH, ch = i % CH;
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if (r < rows) {
-                    const int t = (r0 + r) / p.group;
+                    const int t = (sg.r0 + r) / p.group;
                     w = static_cast<const uint4 *>(
-                        p.a.q)[((size_t)(row0 + t) * p.a.Hq + hk * p.group + (r0 + r) - t * p.group) * CH + ch];
+                        p.a.q)[((size_t)(sg.row0 + t) * p.a.Hq + sg.hk * p.group + (sg.r0 + r) - t * p.group) * CH + ch];
                 }
                 *reinterpret_cast<uint4 *>(smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX +
                                            (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full);
-        }
-        const float sl2 = p.scale_log2;
-        float m_ref = -INFINITY;
-        float l_sum = 0.0f;    // sum of the rounded P fed to the MMA: normalises O
-        float l_exact = 0.0f;  // sum of the unrounded P: gives L
-        const int hi_w = __reduce_min_sync(0xffffffffu, hi), lo_w = __reduce_max_sync(0xffffffffu, lo);
-        const bool active = x == 0 || two;
-        bool ok = true;
-        for (int u = 0; ok && active && u < nj; ++u) {
-            const bool got_s = mbar_wait(&s_full[x], u & 1, abort_flag, p.status, 37);
+            return true;
+        };
+        Segment sg;
+        int step = 0, finals = 0;  // tiles of this warpgroup's Q tile, and segments that had it
+        bool ok = next_segment(0, sg);
+        for (int g = 0; ok && sg.nj >= 0; ++g) {
+            // this thread's row: where it is and which keys it sees
+            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
+            const bool two = rows > kBM, active = x == 0 || two, valid = row < rows;
+            int tok = 0, head = 0, hi = 0x7FFFFFFF, lo = -0x7FFFFFFF;
+            if (valid) {
+                const int t = (sg.r0 + row) / p.group;
+                head = sg.hk * p.group + (sg.r0 + row) - t * p.group;
+                tok = sg.row0 + t;
+                if (p.prefix) {
+                    const int b = request_of(p.a, tok);
+                    Request r;
+                    if (load_request(p.a, b, r)) {
+                        hi = p.a.prefix_len + r.len - r.n + (tok - r.row0) + 1;
+                        lo = p.a.window > 0 ? hi - p.a.window : 0;
+                    }
+                } else {
+                    hi = sg.len - sg.n + t + 1;
+                    lo = p.a.window > 0 ? hi - p.a.window : 0;
+                }
+            }
+            const int key_lo = sg.key_lo, key_hi = sg.key_hi, nj = sg.nj, j0 = sg.j0;
+            float m_ref = -INFINITY;
+            float l_sum = 0.0f;    // sum of the rounded P fed to the MMA: normalises O
+            float l_exact = 0.0f;  // sum of the unrounded P: gives L
+            const int hi_w = __reduce_min_sync(0xffffffffu, hi), lo_w = __reduce_max_sync(0xffffffffu, lo);
+            for (int u = 0; ok && active && u < nj; ++u, ++step) {
+            const bool got_s = mbar_wait(&s_full[x], step & 1, abort_flag, p.status, 37);
             if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
             tc_fence_after();
             uint32_t s[128];
@@ -513,14 +657,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(&p_full[x]);
         }
-        if (active) {
-            if (ok) ok = mbar_wait(&o_final[x], 0, abort_flag, p.status, 38);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                tc_fence_after();
+            // a warpgroup without rows waits for the other's, so as not to
+            // overwrite a Q that is still read
+            const bool final_ok =
+                ok && mbar_wait(&o_final[active ? x : 0], (active ? finals : g) & 1, abort_flag, p.status, 38);
+            if (active) ++finals;
+            if (!(ok = __all_sync(0xffffffffu, final_ok))) break;
+            tc_fence_after();
+            // the next segment's S is issued while this one's O is stored
+            Segment next;
+            if (!(ok = next_segment(g + 1, next))) break;
+            if (active) {
                 const float inv_l = l_sum > 0.f ? 1.0f / l_sum : 0.f;
-                const size_t at = (size_t)tok * p.a.Hq + head;
-                const size_t part = (size_t)split * p.a.total * p.a.Hq + at;
+                const size_t out_row = (size_t)tok * p.a.Hq + head;
+                // whole blocks are final, or go to the plane to be merged with
+                // the other pass'; parts go to their slot
+                float *to_o = p.part.plane, *to_lse2 = p.part.plane_lse2;
+                size_t at = out_row;
+                if (sg.slot >= 0) {
+                    to_o = p.part.slot;
+                    to_lse2 = p.part.slot_lse2;
+                    at = ((size_t)blockIdx.x * 2 + sg.slot) * kRows + row;
+                }
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
@@ -528,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait_x32(o);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
-                    if (valid && p.part_o) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + part * D + c0);
+                    if (valid && to_o) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(to_o + at * D + c0);
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
@@ -551,12 +709,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (valid) {
                     const float lse2 = l_exact > 0.f ? m_ref + log2f(l_exact) : -INFINITY;
-                    if (p.part_o)
-                        p.part_lse2[part] = lse2;
+                    if (to_lse2)
+                        to_lse2[at] = lse2;
                     else
                         p.a.lse[(size_t)head * p.a.total + tok] = lse2 * 0.69314718055994530942f;
+                    if (sg.slot != 0) p.part.code[out_row] = sg.code ? sg.code + part_code(0, 0, row) : 0;
                 }
+                // the reads of O above come before the MMAs that a later arrive permits
+                tc_fence_before();
             }
+            sg = next;
         }
         __syncwarp();
     }
@@ -567,94 +729,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    // the merge, which waits for this kernel, then also has the other pass'
+    wait_previous();
 }
 
-// Merges the key ranges of every row: a warp per row and head.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_merge_rows_kernel(const WideParams p) {
-    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id >= (long long)p.a.total * p.a.Hq) return;
-    const int lane = threadIdx.x & 31;
-    const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
-    Request r;
-    if (p.a.cu_seqlens ? false : tok >= p.a.B) return;
-    if (!load_request(p.a, p.shift, request_of(p.a, tok), r)) return;
-    if (tok < r.row0 || tok >= r.row0 + r.n) return;  // a row of no request
-    constexpr int E = D / 32;
-    float acc[E], top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const size_t at = (size_t)s * p.a.total * p.a.Hq + id;
-        const float lse2 = p.part_lse2[at];
-        if (lse2 == -INFINITY) continue;
-        const float to = fmaxf(top, lse2);
-        const float a = ex2_approx(top - to), w = ex2_approx(lse2 - to);
-        sum = sum * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * p.part_o[at * D + lane * E + e];
-        top = to;
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t *out = static_cast<uint16_t *>(p.a.o) + (size_t)id * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(out + e) =
-            BF16 ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-        p.a.lse[(size_t)h * p.a.total + tok] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st) {
+    using L = WideLayout<D>;
+    CUtensorMap tk, tv;
+    if (!make_tmap_pages(&tk, a.k_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, kBN) ||
+        !make_tmap_pages(&tv, a.v_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, kBN))
+        return cudaErrorInvalidValue;
+    WideParams p;
+    p.a = a;
+    p.group = a.Hq / a.Hkv;
+    p.prefix = prefix ? 1 : 0;
+    p.part = prefix ? w.prefix : w.own;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.status = device_status_ptr();
+    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, after, st, tk, tv, p);
 }
 
 }  // namespace
 
-template <int D, bool BF16>
-static cudaError_t launch_wide_t(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st) {
-    using L = WideLayout<D>;
-    const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tk, tv;
-    const uint32_t rows = a.page_size < kBN ? a.page_size : kBN;
-    const uint64_t planes = (uint64_t)a.num_pages * a.Hkv;
-    if (!make_tmap_3d(&tk, a.k_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tmap_3d(&tv, a.v_cache, dt, 2, D, a.page_size, planes, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    auto kernel = paged_wide_kernel<D, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
-    if (e != cudaSuccess) return e;
-    WideParams p;
-    p.a = a;
-    p.shift = shift;
-    p.group = a.Hq / a.Hkv;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
-    p.status = device_status_ptr();
-    const size_t plane = (size_t)a.total * a.Hq;
-    if (w.prefix_splits) {
-        p.prefix = 1;
-        p.blocks = w.prefix_blocks;
-        p.splits = w.prefix_splits;
-        p.part_o = w.part_o;
-        p.part_lse2 = w.part_lse2;
-        kernel<<<(unsigned)(p.blocks * a.Hkv * p.splits), kThreads, L::ALLOC, st>>>(tk, tv, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (!w.own_splits) return cudaSuccess;
-    p.prefix = 0;
-    p.blocks = w.own_blocks;
-    p.splits = w.own_splits;
-    const bool direct = w.prefix_splits == 0 && w.own_splits == 1;
-    p.part_o = direct ? nullptr : w.part_o + plane * D * w.prefix_splits;
-    p.part_lse2 = direct ? nullptr : w.part_lse2 + plane * w.prefix_splits;
-    kernel<<<(unsigned)(p.blocks * a.Hkv * p.splits), kThreads, L::ALLOC, st>>>(tk, tv, p);
-    if ((e = cudaGetLastError()) != cudaSuccess || direct) return e;
-    p.part_o = w.part_o;
-    p.part_lse2 = w.part_lse2;
-    p.splits = w.prefix_splits + w.own_splits;
-    paged_merge_rows_kernel<D, BF16><<<(unsigned)((plane + 3) / 4), 128, 0, st>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_paged_wide(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st) {
-    if (a.d == 128) return a.bf16 ? launch_wide_t<128, true>(a, shift, w, st) : launch_wide_t<128, false>(a, shift, w, st);
-    return a.bf16 ? launch_wide_t<64, true>(a, shift, w, st) : launch_wide_t<64, false>(a, shift, w, st);
+cudaError_t launch_paged_wide(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st) {
+    if (a.d == 128)
+        return a.bf16 ? launch_wide_t<128, true>(a, w, prefix, after, st)
+                      : launch_wide_t<128, false>(a, w, prefix, after, st);
+    return a.bf16 ? launch_wide_t<64, true>(a, w, prefix, after, st)
+                  : launch_wide_t<64, false>(a, w, prefix, after, st);
 }
 
 }  // namespace fa

@@ -40,6 +40,35 @@ bool make_tmap_3d_box(CUtensorMap *map, const void *base, CUtensorMapDataType dt
 bool make_tmap_tiles(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int d, const SeqLayout &lay,
                      int heads, uint32_t rows);
 
+// TMA descriptor over the pages of a 16-bit cache [num_pages][heads]
+// [page_size][d]: boxes of 64 columns and `keys` rows, or a page's if those
+// are fewer; coordinates (column, row of the page, page * heads + head).
+bool make_tmap_pages(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
+                     int keys);
+
+// Launches `kernel` with `smem` bytes of dynamic shared memory.  `after`: it
+// may start before the stream's previous kernel has finished, once all of
+// that one's CTAs have asked for it (programmatic dependent launch).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, bool after,
+                         cudaStream_t st, const A &...args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Device address of this library's status words (status.cuh) on the current device
 // (looked up once per device and context, cached).
 unsigned int *device_status_ptr();

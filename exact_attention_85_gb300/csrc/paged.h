@@ -39,26 +39,48 @@ struct PagedArgs {
     float scale;
     bool bf16;
     void *workspace;
+    int shift;  // log2(page_size)
 };
 
-// How a call is divided for the 256-row kernel (fa_fwd_paged_wide.cu): row
-// blocks (upper bounds, the real ones depend on the device's offsets) and key
-// ranges per block, for the shared prefix and for the requests' own keys; 0
-// ranges: not this kernel's.  Partial results are planes [range][total][Hq],
-// the prefix' first.
-struct WidePlan {
-    int prefix_blocks, prefix_splits;
-    int own_blocks, own_splits;
-    float *part_o, *part_lse2;
+// Where the partial results of one pass over keys (the shared prefix', or the
+// requests' own) lie.  A pass gives every row one result, or several where
+// CTAs shared the row's keys.  Each is O~ / l in fp32 and lse2, log2 of the
+// sum of exponentials (-inf: nothing seen); several merge as
+//   O = sum w_i O_i / sum w_i,  w_i = 2^(lse2_i - max).
+// code[row] says which a row has (row = token * Hq + head): 0 one, final or in
+// the plane; otherwise pieces | first CTA << 9 | row within the slot << 18:
+// slot 1 of the first CTA and slot 0 of the following ones.
+struct PartView {
+    int *code;                  // [total * Hq]
+    float *plane_lse2, *plane;  // [total * Hq] (x d); null where one result is final
+    float *slot_lse2, *slot;    // [ctas][2][slot_rows] (x d)
+    int slot_rows, ctas;
+};
+constexpr int kWideRows = 256, kWideKeys = 128;  // row block and key tile of the 256-row kernel
+constexpr int kWideMinUnits = 3;                 // key tiles a CTA of it takes at least
+constexpr int kMaxPieces = 511;  // 9 bits, also of CTA numbers
+
+__host__ __device__ constexpr int part_code(int pieces, int cta, int row) { return pieces | cta << 9 | row << 18; }
+
+// How a call is divided among the kernels.
+struct PagedPlan {
+    bool few;         // own keys by the 16-row kernel, else by the 256-row one
+    PartView own;     // ctas: of the kernel that takes the own keys
+    PartView prefix;  // ctas 0: no shared prefix
+    size_t bytes;     // workspace
 };
 
-cudaError_t launch_paged_wide(const PagedArgs &a, int shift, const WidePlan &w, cudaStream_t st);
+PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
+                     int prefix_len, void *workspace);
+
+// The kernels of a forward call.  `after` marks a launch that may start while
+// the call's previous one still runs (programmatic dependent launch).
+cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st);
+cudaError_t launch_paged_wide(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st);
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st);
 
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st);
-// Workspace bytes of launch_fwd_paged (shapes only, no device query).
-size_t fwd_paged_workspace(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
-                           int prefix_len);
 
 }  // namespace fa

@@ -14,7 +14,7 @@ struct Request {
 
 // False if what the device holds for request b breaks the rules of the call
 // (offsets, row bound, length): it then has no rows.
-__device__ __forceinline__ bool load_request(const PagedArgs &a, int shift, int b, Request &r) {
+__device__ __forceinline__ bool load_request(const PagedArgs &a, int b, Request &r) {
     r.row0 = b;
     r.n = 1;
     if (a.cu_seqlens) {
@@ -24,11 +24,13 @@ __device__ __forceinline__ bool load_request(const PagedArgs &a, int shift, int 
         r.n = end - r.row0;
     }
     r.len = a.seq_lens[b];
-    return r.len >= 0 && r.len <= (a.max_pages << shift);
+    return r.len >= 0 && r.len <= (a.max_pages << a.shift);
 }
 
-// A partial result of a row is O~ / l in fp32 and lse2, log2 of the sum of
-// exponentials (-inf: the row saw nothing there, and its O is not written).
-// Several merge as O = sum w_i O_i / sum w_i with w_i = 2^(lse2_i - max).
+// Programmatic dependent launch: lets the stream's next kernel start as soon
+// as every CTA of this one has started, and waits until the kernel before
+// this one has finished and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace fa
