@@ -12,7 +12,7 @@
 // rescaled lazily and exactly, and P is read from tensor memory.  What
 // differs: K/V tiles are gathered page by page (one TMA box per page and
 // 64-column half), Q rows are copied into the swizzled operand layout by the
-// softmax threads, and every row has its own visible range of keys.
+// helper warps, and every row has its own visible range of keys.
 //
 // The key tiles of all (row block, key/value head) pairs are numbered in
 // order and every CTA (one per SM) takes an equal, contiguous range, as in
@@ -22,9 +22,11 @@
 // memory carry on from segment to segment; the next segment's Q is loaded
 // and its first S issued before the epilogue of the one before.
 //   warps 0-3 softmax + epilogue of tile A, 4-7 of tile B, 8 producer (plans
-//   the segments and tells the others), 9 MMA issuer (owns the tensor memory)
+//   the segments and tells the others), 9 MMA issuer (owns the tensor memory),
+//   10-11 helpers (Q, and the V rows that nobody may see)
 #include "../../include/fa.h"
 #include "host_util.h"
+#include "mma_sync.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
 #include "ptx.cuh"
@@ -36,7 +38,8 @@ namespace {
 constexpr int kBM = 128, kBN = 128;
 constexpr int kRows = kWideRows;
 static_assert(kRows == 2 * kBM && kBN == kWideKeys, "tile sizes of the plan");
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+constexpr int kHelperWarps = 2;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
@@ -53,8 +56,8 @@ struct WideLayout {
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_BAR = OFF_V + VS * TILE;
     // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2],
-    // p_full[2], o_final[2], seg_full[2], seg_empty[2], drain
-    static constexpr int NBAR = 1 + 2 * KS + 2 * VS + 2 + 2 + 2 + 2 + 2 + 1;
+    // p_full[2], o_final[2], seg_full[2], seg_empty[2], q_empty, v_clean[VS], drain
+    static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
     static constexpr int OFF_MISC = OFF_SEG + 2 * 48;
     static constexpr int BYTES = OFF_MISC + 32;
@@ -66,6 +69,7 @@ struct WideParams {
     PagedArgs a;
     int group;   // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
+    int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
     unsigned int *status;
@@ -110,6 +114,8 @@ __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r
     hi = max(0, r.len - r.n + last + 1);
     lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
 }
+// Whether a key tile holds keys that no row of the block sees.
+__device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return kv0 < key_lo || kv0 + kBN > key_hi; }
 // Key tiles of a range; at least one, so that rows that see nothing are written.
 __device__ __forceinline__ int range_tiles(int lo, int hi) { return max(1, (hi + kBN - 1) / kBN - lo / kBN); }
 
@@ -162,7 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *o_final = p_full + 2;      // [2]
     uint64_t *seg_full = o_final + 2;    // [2]
     uint64_t *seg_empty = seg_full + 2;  // [2]
-    uint64_t *drain = seg_empty + 2;
+    uint64_t *q_empty = seg_empty + 2;
+    uint64_t *v_clean = q_empty + 1;  // [VS]
+    uint64_t *drain = v_clean + L::VS;
     Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
@@ -171,7 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 2 * kBM);
+        mbar_init(q_full, 32 * kHelperWarps);
+        mbar_init(q_empty, 1);
+        for (int s = 0; s < L::VS; ++s) mbar_init(&v_clean[s], 32 * kHelperWarps);
         for (int s = 0; s < L::KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
         for (int s = 0; s < L::VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); }
         for (int x = 0; x < 2; ++x) {
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&p_full[x], kBM);
             mbar_init(&o_final[x], 1);
             mbar_init(&seg_full[x], 1);
-            mbar_init(&seg_empty[x], 9);  // the MMA warp and eight softmax warps
+            mbar_init(&seg_empty[x], 9 + kHelperWarps);  // every warp but the producer
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------------- MMA issuer
-        // lane 0 issues; the whole warp follows, to clear V rows (below)
+        if (lane == 0) {
         constexpr uint32_t fmt = BF16 ? 1u : 0u;
         constexpr uint32_t idesc_s = make_idesc(kBM, kBN, fmt, false, false);
         constexpr uint32_t idesc_pv = make_idesc(kBM, D, fmt, false, true);
@@ -427,74 +437,128 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](uint64_t *bar, int parity, int site) -> bool {
             const bool got = mbar_wait(bar, parity, abort_flag, p.status, site);
             tc_fence_after();
-            return __all_sync(0xffffffffu, got);
+            return got;
         };
         bool ok = true;
         int u = 0, step_b = 0;  // tiles of all segments; of those that have a tile B
+        uint32_t cleans = 0;    // a bit per V stage: parity of its clears
         for (int g = 0; ok; ++g) {
             if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
-            const Segment sg = segs[g & 1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[g & 1]);
-            if (sg.nj < 0) break;
-            const bool two = (long long)sg.n * p.group - sg.r0 > kBM;
+            const int nj = segs[g & 1].nj, kv0 = segs[g & 1].j0 * kBN;
+            const int key_lo = segs[g & 1].key_lo, key_hi = segs[g & 1].key_hi;
+            const bool two = (long long)segs[g & 1].n * p.group - segs[g & 1].r0 > kBM;
+            mbar_arrive(&seg_empty[g & 1]);
+            if (nj < 0) break;
             if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
-            if (lane == 0) {
-                issue_s(0, u);
-                if (two) issue_s(1, u);
-                mma_commit(&k_empty[u % L::KS]);
-            }
-            for (int i = 0; i < sg.nj; ++i, ++u) {
-                const int vs = u % L::VS, kn = (u + 1) % L::KS;
-                const bool last = i + 1 == sg.nj;
-                if (!(ok = wait(&v_full[vs], (u / L::VS) & 1, 35))) break;
-                const int kv0 = (sg.j0 + i) * kBN;
-                if (kv0 < sg.key_lo || kv0 + kBN > sg.key_hi) {
-                    // V rows that no row of the block sees may hold anything
-                    // (the rest of a page, a buffer that was not filled), and
-                    // 0 * NaN is NaN: clear them
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + L::OFF_V + vs * L::TILE);
-                    for (int k = lane; k < kBN * 8 * L::NBOX; k += 32) {
-                        const int key = kv0 + ((k >> 3) & (kBN - 1));
-                        if (key < sg.key_lo || key >= sg.key_hi) v[k] = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+            issue_s(0, u);
+            if (two) issue_s(1, u);
+            mma_commit(&k_empty[u % L::KS]);
+            if (nj == 1) mma_commit(q_empty);
+            // V of the segment's first tile
+            if (!(ok = wait(&v_full[u % L::VS], (u / L::VS) & 1, 35))) break;
+            for (int i = 0; i < nj; ++i, ++u) {
+                const int vs = u % L::VS, kn = (u + 1) % L::KS, vn = (u + 1) % L::VS;
+                const bool last = i + 1 == nj;
+                if (hides(kv0 + i * kBN, key_lo, key_hi)) {
+                    if (!(ok = wait(&v_clean[vs], cleans >> vs & 1, 42))) break;
+                    cleans ^= 1u << vs;
                 }
                 if (!(ok = wait(&p_full[0], u & 1, 36))) break;
-                if (lane == 0) {
-                    issue_pv(0, u, i == 0);
-                    if (last) mma_commit(&o_final[0]);
-                }
-                if (!last) {
+                issue_pv(0, u, i == 0);
+                if (last) {
+                    mma_commit(&o_final[0]);
+                } else {
                     if (!(ok = wait(&k_full[kn], ((u + 1) / L::KS) & 1, 34))) break;
-                    if (lane == 0) {
-                        issue_s(0, u + 1);
-                        if (!two) mma_commit(&k_empty[kn]);
+                    issue_s(0, u + 1);
+                    if (!two) {
+                        mma_commit(&k_empty[kn]);
+                        if (i + 2 == nj) mma_commit(q_empty);
                     }
                 }
                 if (two) {
                     if (!(ok = wait(&p_full[1], step_b & 1, 36))) break;
                     ++step_b;
-                    if (lane == 0) {
-                        issue_pv(1, u, i == 0);
-                        if (last) mma_commit(&o_final[1]);
-                    }
+                    issue_pv(1, u, i == 0);
+                    if (last) mma_commit(&o_final[1]);
                 }
-                if (lane == 0) {
-                    mma_commit(&v_empty[vs]);
-                    if (two && !last) {
-                        issue_s(1, u + 1);
-                        mma_commit(&k_empty[kn]);
-                    }
+                mma_commit(&v_empty[vs]);
+                if (last) continue;
+                if (!(ok = wait(&v_full[vn], ((u + 1) / L::VS) & 1, 35))) break;
+                if (two) {
+                    issue_s(1, u + 1);
+                    mma_commit(&k_empty[kn]);
+                    if (i + 2 == nj) mma_commit(q_empty);
                 }
-                __syncwarp();
             }
         }
-        if (lane == 0) {
-            // every MMA issued above has completed once `drain` flips
-            mma_commit(drain);
-            mbar_wait_drain(drain, 0, 100000000ull);
+        // every MMA issued above has completed once `drain` flips
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0, 100000000ull);
+        }
+        __syncwarp();
+    } else if (warp >= kMmaWarp + 1) {
+        // ------------------------------------------------------------ helpers
+        const int id = threadIdx.x - 32 * (kMmaWarp + 1);
+        constexpr int CH = D / 8, STEP = 32 * kHelperWarps / CH;  // 16-byte pieces of a row; rows a pass
+        bool ok = true;
+        int u = 0;
+        for (int g = 0; ok; ++g) {
+            bool got = mbar_wait(&seg_full[g & 1], (g >> 1) & 1, abort_flag, p.status, 43);
+            if (!__all_sync(0xffffffffu, got)) break;
+            const Segment sg = segs[g & 1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[g & 1]);
+            if (sg.nj < 0) break;
+            // Q into the operand layout, a row's pieces by neighbouring lanes,
+            // once the last S of the segment before has read its own; rows
+            // past the block's are zeros
+            got = g == 0 || mbar_wait(q_empty, (g - 1) & 1, abort_flag, p.status, 44);
+            if (!__all_sync(0xffffffffu, got)) break;
+            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
+            const int ch = id % CH;
+            int t = (sg.r0 + id / CH) / p.group, h = (sg.r0 + id / CH) % p.group;
+            const int dt = STEP / p.group, dh = STEP % p.group;
+            const uint4 *src = static_cast<const uint4 *>(p.a.q) + ((size_t)sg.row0 * p.a.Hq + sg.hk * p.group) * CH + ch;
+            for (int r = id / CH; r < kRows; r += STEP) {
+                uint8_t *dst = smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX + (r & 127) * 128 +
+                               (((ch & 7) ^ (r & 7)) << 4);
+                if (r < rows)
+                    cp_async_16(smem_u32(dst), src + ((size_t)t * p.a.Hq + h) * CH);
+                else
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+                t += dt;
+                h += dh;
+                if (h >= p.group) {
+                    h -= p.group;
+                    ++t;
+                }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+            // V rows that no row of the block sees may hold anything (the rest
+            // of a page, a buffer that was not filled), and 0 * NaN is NaN:
+            // clear them in the tiles that have some, the first and the last
+            for (int i = 0; ok && i < sg.nj; i += max(1, sg.nj - 1)) {
+                const int kv0 = (sg.j0 + i) * kBN;
+                if (!hides(kv0, sg.key_lo, sg.key_hi)) continue;
+                const int vs = (u + i) % L::VS;
+                // the last S of the segment is through: the tile that the V
+                // buffer held before has arrived then, so the wait below is
+                // for this one
+                got = i == 0 || mbar_wait(q_empty, g & 1, abort_flag, p.status, 46);
+                if (!(ok = __all_sync(0xffffffffu, got))) break;
+                got = mbar_wait(&v_full[vs], ((u + i) / L::VS) & 1, abort_flag, p.status, 45);
+                if (!(ok = __all_sync(0xffffffffu, got))) break;
+                uint4 *v = reinterpret_cast<uint4 *>(smem + L::OFF_V + vs * L::TILE);
+                for (int k = id; k < kBN * 8 * L::NBOX; k += 32 * kHelperWarps) {
+                    const int key = kv0 + ((k >> 3) & (kBN - 1));
+                    if (key < sg.key_lo || key >= sg.key_hi) v[k] = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&v_clean[vs]);
+            }
+            u += sg.nj;
         }
         __syncwarp();
     } else {
@@ -505,32 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = kColS + x * 128, col_o = kColO + x * 128;
         const int row = threadIdx.x;
         const float sl2 = p.scale_log2;
-        // waits for segment g and loads its Q (which the last S of the segment
-        // before has read) into the operand layout: 16-byte pieces, a row's
-        // pieces by neighbouring lanes; rows past the block's own are zeros
         auto next_segment = [&](int g, Segment &sg) -> bool {
             const bool got = mbar_wait(&seg_full[g & 1], (g >> 1) & 1, abort_flag, p.status, 41);
             if (!__all_sync(0xffffffffu, got)) return false;
             sg = segs[g & 1];
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[g & 1]);
-            if (sg.nj < 0) return true;
-            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
-            constexpr int CH = D / 8;
-#pragma unroll 8
-            for (int i = threadIdx.x; i < kRows * CH; i += kRows) {
-                const int r = i / CH, ch = i % CH;
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int t = (sg.r0 + r) / p.group;
-                    w = static_cast<const uint4 *>(
-                        p.a.q)[((size_t)(sg.row0 + t) * p.a.Hq + sg.hk * p.group + (sg.r0 + r) - t * p.group) * CH + ch];
-                }
-                *reinterpret_cast<uint4 *>(smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX +
-                                           (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
             return true;
         };
         Segment sg;
@@ -657,16 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(&p_full[x]);
         }
-            // a warpgroup without rows waits for the other's, so as not to
-            // overwrite a Q that is still read
-            const bool final_ok =
-                ok && mbar_wait(&o_final[active ? x : 0], (active ? finals : g) & 1, abort_flag, p.status, 38);
-            if (active) ++finals;
-            if (!(ok = __all_sync(0xffffffffu, final_ok))) break;
-            tc_fence_after();
-            // the next segment's S is issued while this one's O is stored
-            Segment next;
-            if (!(ok = next_segment(g + 1, next))) break;
+            if (active) {
+                const bool got = ok && mbar_wait(&o_final[x], finals & 1, abort_flag, p.status, 38);
+                ++finals;
+                ok = __all_sync(0xffffffffu, got);
+                tc_fence_after();
+            }
+            if (!ok) break;
             if (active) {
                 const float inv_l = l_sum > 0.f ? 1.0f / l_sum : 0.f;
                 const size_t out_row = (size_t)tok * p.a.Hq + head;
@@ -687,22 +728,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
                     if (valid && to_o) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(to_o + at * D + c0);
+                        float *dst = to_o + at * D + c0;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        for (int q = 0; q < 4; ++q) st_global_v8(dst + 8 * q, o + 8 * q);  // whole sectors
                     } else if (valid) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + at * D + c0);
+                        uint16_t *dst = static_cast<uint16_t *>(p.a.o) + at * D + c0;
+                        uint32_t w[16];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[4];
+                        for (int k = 0; k < 16; ++k) {
+                            const float a = __uint_as_float(o[2 * k]), b = __uint_as_float(o[2 * k + 1]);
+                            w[k] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+                        }
+                        if (p.o32) {
+                            st_global_v8(dst, w);
+                            st_global_v8(dst + 16, w + 8);
+                        } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float a = __uint_as_float(o[8 * q + 2 * k]);
-                                const float b = __uint_as_float(o[8 * q + 2 * k + 1]);
-                                w[k] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
-                            }
-                            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int q = 0; q < 4; ++q)
+                                reinterpret_cast<uint4 *>(dst)[q] =
+                                    make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
                         }
                     }
                     __syncwarp();  // the loads above are the whole warp's
@@ -718,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the reads of O above come before the MMAs that a later arrive permits
                 tc_fence_before();
             }
-            sg = next;
+            ok = next_segment(g + 1, sg);
         }
         __syncwarp();
     }
@@ -744,6 +788,7 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.a = a;
     p.group = a.Hq / a.Hkv;
     p.prefix = prefix ? 1 : 0;
+    p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();

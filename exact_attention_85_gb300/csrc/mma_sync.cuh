@@ -42,6 +42,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Waits for this thread's cp.async copies.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Arrives on `bar` when this thread's cp.async copies so far have landed
 // (counted among the barrier's expected arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
