@@ -119,16 +119,22 @@ __device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return 
 // Key tiles of a range; at least one, so that rows that see nothing are written.
 __device__ __forceinline__ int range_tiles(int lo, int hi) { return max(1, (hi + kBN - 1) / kBN - lo / kBN); }
 
-// Key tiles of all blocks of a request, for one key/value head.  The sums of
+// A block costs its key tiles and as much as kBlockCost tiles more for the
+// change from the block before (first Q, K and S with nothing to overlap,
+// last P V and epilogue).  Counted among the units, so that CTAs whose range
+// has many short blocks get fewer tiles.
+constexpr int kBlockCost = 3;
+
+// Units of all blocks of a request, for one key/value head.  The sums of
 // 32 requests, one a lane: a lane walks its own request's blocks where they
 // are few, the warp walks them together where a request has many.
-__device__ __forceinline__ int request_tiles(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
+__device__ __forceinline__ int request_units(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
     int sum = 0;
     if (!__any_sync(0xffffffffu, nb > 8)) {
         for (int k = 0; k < nb; ++k) {
             int lo, hi;
             block_keys(p, r, k, prefix_lo, lo, hi);
-            sum += range_tiles(lo, hi);
+            sum += range_tiles(lo, hi) + kBlockCost;
         }
         return sum;
     }
@@ -142,7 +148,7 @@ __device__ __forceinline__ int request_tiles(const WideParams &p, const Request 
         for (int k = lane; k < n; k += 32) {
             int lo, hi;
             block_keys(p, o, k, prefix_lo, lo, hi);
-            mine += range_tiles(lo, hi);
+            mine += range_tiles(lo, hi) + kBlockCost;
         }
         mine = __reduce_add_sync(0xffffffffu, mine);
         if (lane == i) sum = mine;
@@ -226,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefix_lo = min(*prefix_low, p.a.prefix_len);
         }
         if (threadIdx.x == 0)
-            *sm_units = (unsigned long long)blocks_of(whole, p.group) * range_tiles(prefix_lo, whole.len) * p.a.Hkv;
+            *sm_units = (unsigned long long)blocks_of(whole, p.group) * (range_tiles(prefix_lo, whole.len) + kBlockCost) *
+                        p.a.Hkv;
     } else {
         for (int b = warp * 32; b < B; b += kThreads) {
             Request r{0, 0, 0};
@@ -234,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (blockIdx.x == 0) record_bad_args(p.status);
                 r.n = 0;
             }
-            const int tiles = request_tiles(p, r, blocks_of(r, p.group), 0, lane);
-            if (tiles) atomicAdd(sm_units, (unsigned long long)tiles * p.a.Hkv);
+            const int units = request_units(p, r, blocks_of(r, p.group), 0, lane);
+            if (units) atomicAdd(sm_units, (unsigned long long)units * p.a.Hkv);
         }
     }
     __syncthreads();
@@ -279,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; b < B; b += 32) {
                 Request r{0, 0, 0};
                 if (b + lane < B && !load_request(p.a, b + lane, r)) r.n = 0;
-                const long long units = (long long)request_tiles(p, r, blocks_of(r, p.group), 0, lane) * p.a.Hkv;
+                const long long units = (long long)request_units(p, r, blocks_of(r, p.group), 0, lane) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -308,17 +315,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Request mine{0, 0, 0};
                 if (lane == 0) mine = r;
                 const int per_head =
-                    __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, prefix_lo, lane), 0);
+                    __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, prefix_lo, lane), 0);
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    int lo, hi, tiles = 0;
+                    int lo, hi, units = 0;
                     if (blk + lane < nb) {
                         block_keys(p, r, blk + lane, prefix_lo, lo, hi);
-                        tiles = range_tiles(lo, hi);
+                        units = range_tiles(lo, hi) + kBlockCost;
                     }
-                    int incl = tiles;
+                    int incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
                         const int x = __shfl_up_sync(0xffffffffu, incl, s);
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const unsigned past = __ballot_sync(0xffffffffu, blk0 + incl > u);
                     if (past) {
                         const int k = __ffs(past) - 1;
-                        blk0 += __shfl_sync(0xffffffffu, incl - tiles, k);
+                        blk0 += __shfl_sync(0xffffffffu, incl - units, k);
                         blk += k;
                         break;
                     }
@@ -345,13 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.hk = hk;
                     block_keys(p, r, blk, prefix_lo, sg.key_lo, sg.key_hi);
                     const int nt = range_tiles(sg.key_lo, sg.key_hi);
-                    const int first = (int)(u - blk0), end = (int)min((long long)nt, u1 - blk0);
+                    const long long tile0 = blk0 + kBlockCost;  // unit of its first tile
+                    const int first = (int)max(0ll, u - tile0), end = (int)min((long long)nt, u1 - tile0);
+                    blk0 = tile0 + nt;
+                    u = u1 < blk0 ? u1 : blk0;
+                    if (end <= first) continue;  // the range ends before the block's first tile
                     const bool is_whole = first == 0 && end == nt;
                     sg.j0 = sg.key_lo / kBN + first;
                     sg.nj = end - first;
                     sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
                     // a block that goes on in the next CTA belongs to the one it began in
-                    sg.code = sg.slot == 1 ? part_code((int)(((blk0 + nt) * G - 1) / T) - c + 1, c, 0) : 0;
+                    sg.code = sg.slot == 1 ? part_code((int)((blk0 * G - 1) / T) - c + 1, c, 0) : 0;
                     sg.pad = 0;
                     tell(sg);
                     for (int i = 0; ok && i < sg.nj; ++i) {
@@ -387,8 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         &v_full[vs], half * 64, in_page, page * p.a.Hkv + hk);
                         ++nv;
                     }
-                    blk0 += nt;
-                    u = u1 < blk0 ? u1 : blk0;
                 }
             }
         }
