@@ -54,7 +54,7 @@ struct TileInfo {
 
 template <int D>
 struct FewLayout {
-    static constexpr int TK = D == 128 ? 64 : 128;  // keys per tile
+    static constexpr int TK = kFewKeys<D>;          // keys per tile
     static constexpr int KW = TK / kConsumers;      // keys per warp and tile
     static constexpr int HALVES = D / 64;           // 64-column boxes
     static constexpr int HALF = TK * 128;           // bytes of one box column of a tile
@@ -73,20 +73,12 @@ struct FewLayout {
 
 struct FewParams {
     PagedArgs a;
-    int group;   // query heads per key/value head
+    FastDiv group;  // query heads per key/value head
     float scale_log2;
     unsigned int *status;
     PartView part;
+    int sms;  // of the GPU
 };
-
-// First tile and number of tiles of a pair of request r (at least one, so
-// that rows that see nothing are written).
-template <int TK>
-__device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, int &t0) {
-    const int lo = a.window > 0 ? max(0, r.len - r.n + 1 - a.window) : 0;
-    t0 = lo / TK;
-    return max(1, (r.len + TK - 1) / TK - t0);
-}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kFewThreads, 2)
@@ -100,6 +92,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     float *sm_m = reinterpret_cast<float *>(smem + L::OFF_ML);  // [4][16], then l, then exact l
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC);
     unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 8);
+    int *sm_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.a.B, Hkv = p.a.Hkv;
 
@@ -110,11 +103,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         *abort_flag = 0;
         *sm_units = 0;
+        *sm_low = p.a.prefix_len;
         fence_barrier_init();
     }
     __syncthreads();
     {   // tiles of the whole batch
         unsigned long long mine = 0;
+        int low = p.a.prefix_len;
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
             int t0;
@@ -122,20 +117,28 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 if (blockIdx.x == 0) record_bad_args(p.status);
             } else if (r.n > 0) {
                 mine += pair_tiles<L::TK>(p.a, r, t0);
+                low = min(low, prefix_low(p.a, r));
             }
         }
         if (mine) atomicAdd(sm_units, mine * Hkv);
+        if (p.a.prefix_len > 0) atomicMin(sm_low, low);
     }
     __syncthreads();
     const long long T = (long long)*sm_units;
-    const int G = (int)min((long long)gridDim.x, max(1ll, T / kMinUnits));
-
+    int most = gridDim.x;
+    if (p.a.prefix_len > 0) {
+        // the prefix pass has some of the SMs to itself
+        const long long units = prefix_units(p.a, prefix_rows(p.a), p.group.d, *sm_low);
+        most = min(most, 2 * (p.sms - prefix_sms(units, T, p.sms)));
+    }
+    const int G = (int)min((long long)most, max(1ll, T / kMinUnits));
+    const Ranges ranges(T, G);
     launch_dependents();
 
     if (warp == kConsumers) {
         // ------------------------------------------------------------ producer
         const int c = blockIdx.x;
-        const long long u0 = c < G ? c * T / G : T, u1 = c < G ? (c + 1ll) * T / G : T;
+        const long long u0 = c < G ? ranges.start(c) : T, u1 = c < G ? ranges.start(c + 1) : T;
         if (lane == 0) {
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 const int hi_min = r.len - r.n + 1;
                 // a pair that goes on in the next CTA belongs to the one it began in
                 const int code =
-                    !whole && j0 == 0 ? part_code((int)(((pair0 + nt) * G - 1) / T) - c + 1, c, 0) : 0;
+                    !whole && j0 == 0 ? part_code(ranges.owner(pair0 + nt - 1) - c + 1, c, 0) : 0;
                 for (int j = j0; j < j1; ++j) {
                     const int kv0 = (t0 + j) * L::TK;
                     // pages that hold no visible key are neither looked up nor read
@@ -236,13 +239,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     if (j == j0) {
                         // Q rows of the pair: row r is head r % g of token r / g
                         constexpr int CH = D / 8;  // 16-byte pieces of a row
-                        const int rows = r.n * p.group;
+                        const int rows = r.n * p.group.d;
                         for (int i = lane; i < rows * CH; i += 32) {
                             const int row = i / CH, ch = i % CH;
                             const int t = row / p.group;
                             const uint4 *src =
                                 static_cast<const uint4 *>(p.a.q) +
-                                ((size_t)(r.row0 + t) * p.a.Hq + hk * p.group + (row - t * p.group)) * CH + ch;
+                                ((size_t)(r.row0 + t) * p.a.Hq + hk * p.group.d + (row - t * p.group.d)) * CH + ch;
                             cp_async_16(smem_u32(smem + L::OFF_Q + st * L::QBYTES) + row * (D * 2) +
                                             ((ch ^ (row & 7)) << 4),
                                         src);
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 named_bar_sync(2, kConsumers * 32);
                 // eight threads a row, four neighbouring columns at a time
                 const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
-                if (row < t.n * p.group) {
+                if (row < t.n * p.group.d) {
                     float top = -INFINITY, sum = 0.f, exact = 0.f, f[kConsumers];
 #pragma unroll
                     for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, sm_m[w * 16 + row]);
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     const float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
                     const float *from = reinterpret_cast<const float *>(smem + st * 2 * L::TILE) + row * D;
                     const int tok = row / p.group;
-                    const int h = t.hk * p.group + row - tok * p.group;
+                    const int h = t.hk * p.group.d + row - tok * p.group.d;
                     const size_t out_row = (size_t)(t.row0 + tok) * p.a.Hq + h;
                     // a whole pair's result is final, or goes to the plane to be
                     // merged with the shared prefix'; a part goes to its slot
@@ -545,35 +548,29 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
     const long long rows = (long long)p.a.total * p.a.Hq;
     wait_previous();
     const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
+    // rows of a request; an unsound request's, whose codes are not written,
+    // may pass, so a code is held to the slots there are
     bool mine = id < rows;
-    // the row's request: the last that starts at or before it, 32 offsets a step
     if (mine) {
-        int b = tok;
-        if (p.a.cu_seqlens) {
-            int lo = 0, hi = p.a.B;  // starts at or before tok in [lo, hi)
-            while (hi - lo > 1) {
-                const int step = (hi - lo + 31) / 32;
-                const int at = lo + lane * step;
-                const unsigned under = __ballot_sync(0xffffffffu, at < hi && p.a.cu_seqlens[at] <= tok);
-                const int k = under ? 31 - __clz(under) : 0;
-                lo += k * step;
-                hi = min(hi, lo + step);
-            }
-            b = lo;
-        }
-        Request r;
-        mine = b < p.a.B && load_request(p.a, b, r) && tok >= r.row0 && tok < r.row0 + r.n;
+        if (p.a.cu_seqlens)
+            mine = tok >= p.a.cu_seqlens[0] && tok < p.a.cu_seqlens[p.a.B];
+        else
+            mine = tok < p.a.B;
     }
     // the row's parts: the own pass', then the prefix'
+    auto parts_of = [](const PartView &v, int code) {
+        const int pieces = code & kMaxPieces, cta = code >> 9 & kMaxPieces, slot_row = code >> 18;
+        if (code == 0) return v.plane ? 1 : 0;
+        return pieces < 2 || cta + pieces > v.ctas || slot_row < 0 || slot_row >= v.slot_rows ? 0 : pieces;
+    };
     int n_own = 0, n_all = 0, c_own = 0, c_pre = 0;
-    if (mine) {
+    if (id < rows) {
         c_own = p.own.code[id];
-        n_own = c_own ? c_own & kMaxPieces : p.own.plane ? 1 : 0;
-        n_all = n_own;
-        if (p.prefix.code) {
-            c_pre = p.prefix.code[id];
-            n_all += c_pre ? c_pre & kMaxPieces : 1;
-        }
+        if (p.prefix.code) c_pre = p.prefix.code[id];
+    }
+    if (mine) {
+        n_own = parts_of(p.own, c_own);
+        n_all = n_own + (p.prefix.code ? parts_of(p.prefix, c_pre) : 0);
     }
     float acc[E], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -654,8 +651,6 @@ T *take(uintptr_t &at, size_t n) {
 
 int at_most(long long want, int most) { return (int)(want < 1 ? 1 : want < most ? want : most); }
 
-constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
-
 template <int D, bool BF16>
 cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st) {
     using L = FewLayout<D>;
@@ -665,10 +660,11 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
         return cudaErrorInvalidValue;
     FewParams p;
     p.a = a;
-    p.group = a.Hq / a.Hkv;
+    p.group = fast_div(a.Hq / a.Hkv);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.part = w.own;
+    p.sms = kSms;
     return launch_after(paged_few_kernel<D, BF16>, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
 }
 

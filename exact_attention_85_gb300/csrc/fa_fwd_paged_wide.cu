@@ -67,8 +67,10 @@ struct WideLayout {
 
 struct WideParams {
     PagedArgs a;
-    int group;   // query heads per key/value head
+    FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
+    int shared;  // prefix: the few-row kernel runs at the same time
+    int sms;     // of the GPU
     int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
@@ -99,8 +101,8 @@ __device__ __forceinline__ int request_of(const PagedArgs &a, int row) {
 }
 
 // Row blocks of a request, and the keys that block k of it sees.
-__device__ __forceinline__ int blocks_of(const Request &r, int group) {
-    return (int)(((long long)r.n * group + kRows - 1) / kRows);
+__device__ __forceinline__ int blocks_of(const Request &r, const FastDiv &group) {
+    return (int)(((unsigned)(r.n * group.d) + kRows - 1) / kRows);
 }
 __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r, int k, int prefix_lo, int &lo,
                                            int &hi) {
@@ -109,26 +111,17 @@ __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r
         hi = r.len;
         return;
     }
-    const int first = (int)((long long)k * kRows / p.group);
-    const int last = (int)min((long long)r.n - 1, ((long long)(k + 1) * kRows - 1) / p.group);
+    const int first = (k * kRows) / p.group;
+    const int last = (r.n * p.group.d - k * kRows > kRows ? (k + 1) * kRows - 1 : r.n * p.group.d - 1) / p.group;
     hi = max(0, r.len - r.n + last + 1);
     lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
 }
 // Whether a key tile holds keys that no row of the block sees.
 __device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return kv0 < key_lo || kv0 + kBN > key_hi; }
-// Key tiles of a range; at least one, so that rows that see nothing are written.
-__device__ __forceinline__ int range_tiles(int lo, int hi) { return max(1, (hi + kBN - 1) / kBN - lo / kBN); }
-
-// A block costs its key tiles and as much as kBlockCost tiles more for the
-// change from the block before (first Q, K and S with nothing to overlap,
-// last P V and epilogue).  Counted among the units, so that CTAs whose range
-// has many short blocks get fewer tiles.
-constexpr int kBlockCost = 3;
-
 // Units of all blocks of a request, for one key/value head.  The sums of
 // 32 requests, one a lane: a lane walks its own request's blocks where they
 // are few, the warp walks them together where a request has many.
-__device__ __forceinline__ int request_units(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
+__device__ __noinline__ int request_units(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
     int sum = 0;
     if (!__any_sync(0xffffffffu, nb > 8)) {
         for (int k = 0; k < nb; ++k) {
@@ -180,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
-    int *prefix_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 8);
+    int *sm_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 8);
     unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -199,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
-        *prefix_low = 0x7FFFFFFF;
+        *sm_low = p.a.prefix_len;
         *sm_units = 0;
         fence_barrier_init();
     }
@@ -216,24 +209,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- the batch's units of work
     const int B = p.prefix ? 1 : p.a.B;
     Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
-    int prefix_lo = 0;
+    int most = gridDim.x, prefix_lo = 0;
     if (p.prefix) {
-        whole.n = p.a.cu_seqlens ? p.a.cu_seqlens[p.a.B] : p.a.B;
-        // offsets that end outside q are reported with their request; the
-        // sound ones may have rows anywhere
-        if (whole.n < 0 || whole.n > p.a.total) whole.n = p.a.total;
-        if (p.a.window > 0) {  // the first key that any row sees
-            for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
-                Request r;
-                if (load_request(p.a, b, r) && r.n > 0)
-                    atomicMin(prefix_low, max(0, p.a.prefix_len + r.len - r.n + 1 - p.a.window));
-            }
-            __syncthreads();
-            prefix_lo = min(*prefix_low, p.a.prefix_len);
+        // the first key that any row sees, and the few-row kernel's tiles
+        whole.n = prefix_rows(p.a);
+        int low = p.a.prefix_len;
+        unsigned long long few = 0;
+        for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
+            Request r;
+            int t;
+            if (!load_request(p.a, b, r) || r.n == 0) continue;
+            low = min(low, prefix_low(p.a, r));
+            few += pair_tiles<kFewKeys<D>>(p.a, r, t);
         }
-        if (threadIdx.x == 0)
-            *sm_units = (unsigned long long)blocks_of(whole, p.group) * (range_tiles(prefix_lo, whole.len) + kBlockCost) *
-                        p.a.Hkv;
+        atomicMin(sm_low, low);
+        if (few && p.shared) atomicAdd(sm_units, few * p.a.Hkv);
     } else {
         for (int b = warp * 32; b < B; b += kThreads) {
             Request r{0, 0, 0};
@@ -246,8 +236,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    const long long T = (long long)*sm_units;
-    const int G = (int)min((long long)gridDim.x, max(1ll, T / kWideMinUnits));
+    long long T = (long long)*sm_units;
+    if (p.prefix) {
+        prefix_lo = *sm_low;
+        const long long few = T;
+        T = prefix_units(p.a, whole.n, p.group.d, prefix_lo);
+        if (p.shared) most = min(most, prefix_sms(T, few, p.sms));
+    }
+    const int G = (int)min((long long)most, max(1ll, T / kWideMinUnits));
+    const Ranges ranges(T, G);
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------ TMA producer
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = lane % L::NBOX, sub = lane / L::NBOX;
         const bool boxed = lane < L::NBOX * (kBN / page_keys);
         const int c = blockIdx.x;
-        const long long u0 = c < G ? c * T / G : T, u1 = c < G ? (c + 1ll) * T / G : T;
+        const long long u0 = c < G ? ranges.start(c) : T, u1 = c < G ? ranges.start(c + 1) : T;
         int nk = 0, nv = 0, ns = 0;  // K and V tiles and segments handed on
         bool ok = true;
         // hands a segment to the other warps
@@ -315,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Request mine{0, 0, 0};
                 if (lane == 0) mine = r;
                 const int per_head =
-                    __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, prefix_lo, lane), 0);
+                    p.prefix ? nb * (range_tiles(prefix_lo, r.len) + kBlockCost)
+                             : __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, 0, lane), 0);
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.nj = end - first;
                     sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
                     // a block that goes on in the next CTA belongs to the one it began in
-                    sg.code = sg.slot == 1 ? part_code((int)((blk0 * G - 1) / T) - c + 1, c, 0) : 0;
+                    sg.code = sg.slot == 1 ? part_code(ranges.owner(blk0 - 1) - c + 1, c, 0) : 0;
                     sg.pad = 0;
                     tell(sg);
                     for (int i = 0; ok && i < sg.nj; ++i) {
@@ -455,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
             const int nj = segs[g & 1].nj, kv0 = segs[g & 1].j0 * kBN;
             const int key_lo = segs[g & 1].key_lo, key_hi = segs[g & 1].key_hi;
-            const bool two = (long long)segs[g & 1].n * p.group - segs[g & 1].r0 > kBM;
+            const bool two = segs[g & 1].n * p.group.d - segs[g & 1].r0 > kBM;
             mbar_arrive(&seg_empty[g & 1]);
             if (nj < 0) break;
             if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
@@ -523,24 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // past the block's are zeros
             got = g == 0 || mbar_wait(q_empty, (g - 1) & 1, abort_flag, p.status, 44);
             if (!__all_sync(0xffffffffu, got)) break;
-            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
+            const int rows = min(sg.n * p.group.d - sg.r0, kRows);
             const int ch = id % CH;
-            int t = (sg.r0 + id / CH) / p.group, h = (sg.r0 + id / CH) % p.group;
-            const int dt = STEP / p.group, dh = STEP % p.group;
-            const uint4 *src = static_cast<const uint4 *>(p.a.q) + ((size_t)sg.row0 * p.a.Hq + sg.hk * p.group) * CH + ch;
+            const int t0 = sg.r0 / p.group, h0 = sg.r0 - t0 * p.group.d;
+            const uint4 *src =
+                static_cast<const uint4 *>(p.a.q) + ((size_t)(sg.row0 + t0) * p.a.Hq + sg.hk * p.group.d) * CH + ch;
+#pragma unroll 8
             for (int r = id / CH; r < kRows; r += STEP) {
                 uint8_t *dst = smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX + (r & 127) * 128 +
                                (((ch & 7) ^ (r & 7)) << 4);
+                const int t = (h0 + r) / p.group, h = h0 + r - t * p.group.d;
                 if (r < rows)
                     cp_async_16(smem_u32(dst), src + ((size_t)t * p.a.Hq + h) * CH);
                 else
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-                t += dt;
-                h += dh;
-                if (h >= p.group) {
-                    h -= p.group;
-                    ++t;
-                }
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
@@ -591,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = next_segment(0, sg);
         for (int g = 0; ok && sg.nj >= 0; ++g) {
             // this thread's row: where it is and which keys it sees
-            const int rows = (int)min((long long)sg.n * p.group - sg.r0, (long long)kRows);
+            const int rows = min(sg.n * p.group.d - sg.r0, kRows);
             const bool two = rows > kBM, active = x == 0 || two, valid = row < rows;
             int tok = 0, head = 0, hi = 0x7FFFFFFF, lo = -0x7FFFFFFF;
             if (valid) {
                 const int t = (sg.r0 + row) / p.group;
-                head = sg.hk * p.group + (sg.r0 + row) - t * p.group;
+                head = sg.hk * p.group.d + (sg.r0 + row) - t * p.group.d;
                 tok = sg.row0 + t;
                 if (p.prefix) {
                     const int b = request_of(p.a, tok);
@@ -795,8 +789,10 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
         return cudaErrorInvalidValue;
     WideParams p;
     p.a = a;
-    p.group = a.Hq / a.Hkv;
+    p.group = fast_div(a.Hq / a.Hkv);
     p.prefix = prefix ? 1 : 0;
+    p.shared = prefix && w.few ? 1 : 0;
+    p.sms = kSms;
     p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;

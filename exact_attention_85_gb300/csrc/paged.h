@@ -42,6 +42,21 @@ struct PagedArgs {
     int shift;  // log2(page_size)
 };
 
+// Division of x < 2^31 by a fixed d >= 1 as a multiplication: with s the
+// smallest such that 2^s >= d and mul = floor(2^32 (2^s - d) / d) + 1,
+// x / d = (hi32(x mul) + x) >> s  (Granlund and Montgomery, 1994).
+struct FastDiv {
+    uint32_t mul;
+    int shift, d;
+};
+
+inline FastDiv fast_div(int d) {
+    FastDiv f{0, 0, d};
+    while ((1ll << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+    return f;
+}
+
 // Where the partial results of one pass over keys (the shared prefix', or the
 // requests' own) lie.  A pass gives every row one result, or several where
 // CTAs shared the row's keys.  Each is O~ / l in fp32 and lse2, log2 of the
@@ -56,6 +71,7 @@ struct PartView {
     float *slot_lse2, *slot;    // [ctas][2][slot_rows] (x d)
     int slot_rows, ctas;
 };
+constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
 constexpr int kWideRows = 256, kWideKeys = 128;  // row block and key tile of the 256-row kernel
 constexpr int kWideMinUnits = 4;                 // units of work a CTA of it takes at least
 constexpr int kMaxPieces = 511;  // 9 bits, also of CTA numbers

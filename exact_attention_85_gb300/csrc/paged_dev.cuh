@@ -27,6 +27,80 @@ __device__ __forceinline__ bool load_request(const PagedArgs &a, int b, Request 
     return r.len >= 0 && r.len <= (a.max_pages << a.shift);
 }
 
+__device__ __forceinline__ int operator/(int x, const FastDiv &f) {
+    return (int)((__umulhi((uint32_t)x, f.mul) + (uint32_t)x) >> f.shift);
+}
+
+// [u0, u1): the units of CTA c of G that share T units, and the CTA that has
+// unit u.  The first T % G CTAs take one more than the others.
+struct Ranges {
+    long long each, more;
+    __device__ __forceinline__ Ranges(long long T, int G) : each(T / G), more(T % G) {}
+    __device__ __forceinline__ long long start(int c) const { return c * each + min((long long)c, more); }
+    __device__ __forceinline__ int owner(long long u) const {
+        const long long big = more * (each + 1);
+        return (int)(u < big ? u / (each + 1) : more + (u - big) / each);
+    }
+};
+
+// ------------------------------------------------- units of the two kernels
+
+// Keys per tile of the few-row kernel (32 KB of K and V).
+template <int D>
+constexpr int kFewKeys = D == 128 ? 64 : 128;
+
+// First tile and number of tiles of a (request, key/value head) pair; at
+// least one, so that rows that see nothing are written.
+template <int TK>
+__device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, int &t0) {
+    const int lo = a.window > 0 ? max(0, r.len - r.n + 1 - a.window) : 0;
+    t0 = lo / TK;
+    return max(1, (r.len + TK - 1) / TK - t0);
+}
+
+// A row block of the 256-row kernel costs its key tiles and as much as
+// kBlockCost tiles more for the change from the block before (first Q, K and
+// S with nothing to overlap, last P V and epilogue).  Counted among the
+// units, so that CTAs whose range has many short blocks get fewer tiles.
+constexpr int kBlockCost = 3;
+
+// Key tiles of a range; at least one.
+__device__ __forceinline__ int range_tiles(int lo, int hi) {
+    return max(1, (hi + kWideKeys - 1) / kWideKeys - lo / kWideKeys);
+}
+
+// Rows of the prefix pass: all of the batch.  Offsets that end outside q are
+// reported with their request; the sound ones may have rows anywhere.
+__device__ __forceinline__ int prefix_rows(const PagedArgs &a) {
+    const int n = a.cu_seqlens ? a.cu_seqlens[a.B] : a.B;
+    return n < 0 || n > a.total ? a.total : n;
+}
+// First key of the prefix that request r's rows see (prefix_len: none).
+__device__ __forceinline__ int prefix_low(const PagedArgs &a, const Request &r) {
+    const long long lo = (long long)a.prefix_len + r.len - r.n + 1 - a.window;
+    return a.window > 0 ? (int)max(0ll, min(lo, (long long)a.prefix_len)) : 0;
+}
+__device__ __forceinline__ long long prefix_units(const PagedArgs &a, int rows, int group, int lo) {
+    const long long blocks = ((long long)rows * group + kWideRows - 1) / kWideRows;
+    return blocks * a.Hkv * (range_tiles(lo, a.prefix_len) + kBlockCost);
+}
+
+// A shared prefix' pass is bound by the tensor cores and the few-row kernel
+// by memory, so they run at the same time, each on SMs of its own: the number
+// that the prefix gets, of `sms`.  Times in us: a unit of the 256-row kernel
+// takes 1.8 on one SM, with 8 to start and end; a few-row tile 32 KB at 6.8
+// TB/s, or at 90 GB/s an SM where those are few.  32 candidates, one a lane;
+// each kernel decides for itself, so a difference would cost time only.
+__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles, int sms) {
+    const int g = max(1, (int)(sms * ((threadIdx.x & 31) + 1) / 33));
+    const float wide = 8.f + (float)prefix_units * 1.8f / (float)g;
+    const float few = (float)few_tiles * fmaxf(0.0048f, 0.364f / (float)(sms - g));
+    // the least of the larger times, and the first to have it
+    const uint32_t cost = __float_as_uint(fmaxf(wide, few)) & ~31u;
+    const uint32_t best = __reduce_min_sync(0xffffffffu, cost | (threadIdx.x & 31));
+    return __shfl_sync(0xffffffffu, g, best & 31);
+}
+
 // Programmatic dependent launch: lets the stream's next kernel start as soon
 // as every CTA of this one has started, and waits until the kernel before
 // this one has finished and its writes are visible.
