@@ -37,7 +37,11 @@ namespace {
 
 constexpr int kConsumers = 4;  // warps
 constexpr int kFewThreads = 32 * (kConsumers + 1);
-constexpr int kMaxCtas = 304;  // two per SM
+// Two CTAs fit an SM, but with 96 KB of copies in flight each, fewer do
+// better: 64 requests of 8-16k keys took 470 us on 304 CTAs, 460 on 260, 458
+// on 228, 473 on 190; 32 requests of 333-7506 keys 89.4, 86.3, 88.8, 92.2.
+constexpr float kCtasPerSm = 1.64f;
+constexpr int kMaxCtas = (int)(kCtasPerSm * kSms);
 constexpr int kMaxRows = 16;   // rows of a pair
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;   // tiles a CTA takes at least
@@ -64,8 +68,8 @@ struct FewLayout {
     static constexpr int OFF_INFO = OFF_Q + kStages * QBYTES;
     static constexpr int OFF_BAR = OFF_INFO + kStages * (int)sizeof(TileInfo);
     static constexpr int OFF_ML = OFF_BAR + 2 * kStages * 8;           // [3][4 warps][16]
-    static constexpr int OFF_MISC = OFF_ML + 3 * kConsumers * 16 * 4;  // abort flag, sums
-    static constexpr int BYTES = OFF_MISC + 64;
+    static constexpr int OFF_MISC = OFF_ML + 3 * kConsumers * 16 * 4;  // abort flag, the warps' sums
+    static constexpr int BYTES = OFF_MISC + 16 + (kConsumers + 1) * (int)sizeof(PlanSum);
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(2 * (ALLOC + 1024) <= 228 * 1024, "two CTAs per SM");
     static_assert(kConsumers * kMaxRows * D * 4 <= 2 * TILE, "the merge fits one stage");
@@ -77,7 +81,6 @@ struct FewParams {
     float scale_log2;
     unsigned int *status;
     PartView part;
-    int sms;  // of the GPU
 };
 
 template <int D, bool BF16>
@@ -91,8 +94,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::OFF_INFO);
     float *sm_m = reinterpret_cast<float *>(smem + L::OFF_ML);  // [4][16], then l, then exact l
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC);
-    unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 8);
-    int *sm_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 16);
+    PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.a.B, Hkv = p.a.Hkv;
 
@@ -102,11 +104,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             mbar_init(&empty[s], kConsumers);
         }
         *abort_flag = 0;
-        *sm_units = 0;
-        *sm_low = p.a.prefix_len;
         fence_barrier_init();
     }
-    __syncthreads();
+    launch_dependents();
     {   // tiles of the whole batch
         unsigned long long mine = 0;
         int low = p.a.prefix_len;
@@ -120,29 +120,34 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 low = min(low, prefix_low(p.a, r));
             }
         }
-        if (mine) atomicAdd(sm_units, mine * Hkv);
-        if (p.a.prefix_len > 0) atomicMin(sm_low, low);
+        mine = warp_sum(mine);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane == 0) sums[warp] = PlanSum{mine, low, 0};
     }
     __syncthreads();
-    const long long T = (long long)*sm_units;
-    int most = gridDim.x;
-    if (p.a.prefix_len > 0) {
-        // the prefix pass has some of the SMs to itself
-        const long long units = prefix_units(p.a, prefix_rows(p.a), p.group.d, *sm_low);
-        most = min(most, 2 * (p.sms - prefix_sms(units, T, p.sms)));
-    }
-    const int G = (int)min((long long)most, max(1ll, T / kMinUnits));
-    const Ranges ranges(T, G);
-    launch_dependents();
 
     if (warp == kConsumers) {
         // ------------------------------------------------------------ producer
-        const int c = blockIdx.x;
-        const long long u0 = c < G ? ranges.start(c) : T, u1 = c < G ? ranges.start(c + 1) : T;
         if (lane == 0) {
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
+        long long T = 0;
+        int low = p.a.prefix_len, most = gridDim.x;
+#pragma unroll
+        for (int w = 0; w <= kConsumers; ++w) {
+            T += (long long)sums[w].units * Hkv;
+            low = min(low, sums[w].low);
+        }
+        if (p.a.prefix_len > 0) {
+            // the prefix pass has some of the SMs to itself
+            const long long units = prefix_units(p.a, prefix_rows(p.a), p.group.d, low);
+            most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, T))));
+        }
+        const int G = (int)min((long long)most, max(1ll, T / kMinUnits));
+        const Ranges ranges(T, G);
+        const int c = blockIdx.x;
+        const long long u0 = c < G ? ranges.start(c) : T, u1 = c < G ? ranges.start(c + 1) : T;
         // the request that holds unit u0
         int b = 0;
         long long base = 0;  // first unit of request b
@@ -173,6 +178,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const int page_keys = min(1 << p.a.shift, L::TK);  // keys of one box
         const int per_tile = L::TK / page_keys;
         const int box_bytes = page_keys * 128;
+        const uint64_t once = l2_evict_first();  // every key is read by one CTA only
         const bool boxed = lane < 2 * L::HALVES * per_tile;
         const int tensor = lane & 1, half = (lane >> 1) % L::HALVES, sub = (lane >> 1) / L::HALVES;
         int st = 0, issued = 0;
@@ -233,9 +239,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     }
                     __syncwarp();
                     if (live)
-                        tma_load_3d(smem + (st * 2 + tensor) * L::TILE + half * L::HALF + sub * box_bytes,
-                                    tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.a.shift) - 1),
-                                    page * Hkv + hk);
+                        tma_load_3d_hint(smem + (st * 2 + tensor) * L::TILE + half * L::HALF + sub * box_bytes,
+                                         tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.a.shift) - 1),
+                                         page * Hkv + hk, once);
                     if (j == j0) {
                         // Q rows of the pair: row r is head r % g of token r / g
                         constexpr int CH = D / 8;  // 16-byte pieces of a row
@@ -528,117 +534,144 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     wait_previous();
 }
 
-// Merges the parts of every row that has several: W warps a row (1 or 8 of
-// the block's), each taking every W-th part.
+// Merges the parts of every row that has several.  What it waits for is two
+// rounds of loads (codes, then parts), so a warp has several in flight: R rows
+// at a time where there are many rows (R = 4, with few parts each), else U
+// parts of one row at a time, of which every of W warps takes its share.
 struct MergeParams {
     PagedArgs a;
     PartView own, prefix;
-    int warps;
+    int warps;  // W; 1 if R > 1
 };
 
 constexpr int kMergeWarps = 8;
+constexpr int kMergeRows = 4;  // R
 
-template <int D, bool BF16>
+// Parts of a row by its code.  An unsound request's codes are not written, so
+// a code is held to the slots that there are.
+__device__ __forceinline__ int parts_of(const PartView &v, int code) {
+    const int pieces = code & kMaxPieces, cta = code >> 9 & kMaxPieces, slot_row = code >> 18;
+    if (code == 0) return v.plane ? 1 : 0;
+    return pieces < 2 || cta + pieces > v.ctas || slot_row < 0 || slot_row >= v.slot_rows ? 0 : pieces;
+}
+
+template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams p) {
-    constexpr int E = D / 32;  // columns of a lane
+    constexpr int E = D / 32;          // columns of a lane
+    constexpr int U = R > 1 ? 2 : 4;   // parts of a row in flight
     __shared__ float sm_o[kMergeWarps][D], sm_top[kMergeWarps], sm_sum[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int W = p.warps, sub = warp % W;
-    const long long id = (long long)blockIdx.x * (kMergeWarps / W) + warp / W;
+    const long long id0 = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * R;
     const long long rows = (long long)p.a.total * p.a.Hq;
     wait_previous();
-    const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
-    // rows of a request; an unsound request's, whose codes are not written,
-    // may pass, so a code is held to the slots there are
-    bool mine = id < rows;
-    if (mine) {
-        if (p.a.cu_seqlens)
-            mine = tok >= p.a.cu_seqlens[0] && tok < p.a.cu_seqlens[p.a.B];
-        else
-            mine = tok < p.a.B;
+    // rows behind the batch's have no part
+    int begin = 0, end = p.a.B;
+    if (p.a.cu_seqlens) {
+        begin = p.a.cu_seqlens[0];
+        end = p.a.cu_seqlens[p.a.B];
     }
-    // the row's parts: the own pass', then the prefix'
-    auto parts_of = [](const PartView &v, int code) {
-        const int pieces = code & kMaxPieces, cta = code >> 9 & kMaxPieces, slot_row = code >> 18;
-        if (code == 0) return v.plane ? 1 : 0;
-        return pieces < 2 || cta + pieces > v.ctas || slot_row < 0 || slot_row >= v.slot_rows ? 0 : pieces;
-    };
-    int n_own = 0, n_all = 0, c_own = 0, c_pre = 0;
-    if (id < rows) {
-        c_own = p.own.code[id];
-        if (p.prefix.code) c_pre = p.prefix.code[id];
-    }
-    if (mine) {
-        n_own = parts_of(p.own, c_own);
-        n_all = n_own + (p.prefix.code ? parts_of(p.prefix, c_pre) : 0);
-    }
-    float acc[E], top = -INFINITY, sum = 0.f;
+    int c_own[R], c_pre[R], n_own[R], n_all[R], most = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    constexpr int U = 4;  // parts in flight
-    for (int k0 = sub; k0 < n_all; k0 += W * U) {
-        float lse2[U], x[U][E];
+    for (int r = 0; r < R; ++r) {
+        c_own[r] = c_pre[r] = 0;
+        if (id0 + r < rows) {
+            c_own[r] = p.own.code[id0 + r];
+            if (p.prefix.code) c_pre[r] = p.prefix.code[id0 + r];
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int k = k0 + i * W;
-            lse2[i] = -INFINITY;
-            if (k >= n_all) continue;
-            const bool own = k < n_own;
-            const PartView &v = own ? p.own : p.prefix;
-            const int code = own ? c_own : c_pre, piece = own ? k : k - n_own;
-            const size_t at = code ? ((size_t)((code >> 9 & kMaxPieces) + piece) * 2 + (piece == 0 ? 1 : 0)) * v.slot_rows +
-                                         (code >> 18)
-                                   : (size_t)id;
-            lse2[i] = (code ? v.slot_lse2 : v.plane_lse2)[at];
-            const float *o = (code ? v.slot : v.plane) + at * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 w = *reinterpret_cast<const float4 *>(o);
-                x[i][0] = w.x; x[i][1] = w.y; x[i][2] = w.z; x[i][3] = w.w;
-            } else {
-                const float2 w = *reinterpret_cast<const float2 *>(o);
-                x[i][0] = w.x; x[i][1] = w.y;
+    for (int r = 0; r < R; ++r) {
+        // the own pass' parts, then the prefix'
+        const bool mine = id0 + r < min(rows, (long long)end * p.a.Hq) && id0 + r >= (long long)begin * p.a.Hq;
+        n_own[r] = mine ? parts_of(p.own, c_own[r]) : 0;
+        n_all[r] = n_own[r] + (mine && p.prefix.code ? parts_of(p.prefix, c_pre[r]) : 0);
+        most = max(most, n_all[r]);
+    }
+    float acc[R][E], top[R], sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        top[r] = -INFINITY;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+    }
+    for (int k0 = sub; k0 < most; k0 += W * U) {
+        float lse2[R][U], x[R][U][E];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int k = k0 + i * W;
+                lse2[r][i] = -INFINITY;
+                if (k >= n_all[r]) continue;
+                const bool own = k < n_own[r];
+                const PartView &v = own ? p.own : p.prefix;
+                const int code = own ? c_own[r] : c_pre[r], piece = own ? k : k - n_own[r];
+                const size_t at = code ? ((size_t)((code >> 9 & kMaxPieces) + piece) * 2 + (piece == 0 ? 1 : 0)) *
+                                                 v.slot_rows + (code >> 18)
+                                       : (size_t)(id0 + r);
+                lse2[r][i] = (code ? v.slot_lse2 : v.plane_lse2)[at];
+                const float *o = (code ? v.slot : v.plane) + at * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(o);
+                    x[r][i][0] = w.x; x[r][i][1] = w.y; x[r][i][2] = w.z; x[r][i][3] = w.w;
+                } else {
+                    const float2 w = *reinterpret_cast<const float2 *>(o);
+                    x[r][i][0] = w.x; x[r][i][1] = w.y;
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (lse2[i] == -INFINITY) continue;
-            const float to = fmaxf(top, lse2[i]);
-            const float a = ex2_approx(top - to), w = ex2_approx(lse2[i] - to);
-            sum = sum * a + w;
+        for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * x[i][e];
-            top = to;
+            for (int i = 0; i < U; ++i) {
+                if (lse2[r][i] == -INFINITY) continue;
+                const float to = fmaxf(top[r], lse2[r][i]);
+                const float a = ex2_approx(top[r] - to), w = ex2_approx(lse2[r][i] - to);
+                sum[r] = sum[r] * a + w;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[r][e] = acc[r][e] * a + w * x[r][i][e];
+                top[r] = to;
+            }
         }
     }
-    if (W > 1) {
+    if (R == 1 && W > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[0][e];
         if (lane == 0) {
-            sm_top[warp] = top;
-            sm_sum[warp] = sum;
+            sm_top[warp] = top[0];
+            sm_sum[warp] = sum[0];
         }
         __syncthreads();
         if (sub) return;
         for (int k = 1; k < W; ++k) {
             const float t2 = sm_top[warp + k];
             if (t2 == -INFINITY) continue;
-            const float to = fmaxf(top, t2);
-            const float a = ex2_approx(top - to), w = ex2_approx(t2 - to);
-            sum = sum * a + w * sm_sum[warp + k];
+            const float to = fmaxf(top[0], t2);
+            const float a = ex2_approx(top[0] - to), w = ex2_approx(t2 - to);
+            sum[0] = sum[0] * a + w * sm_sum[warp + k];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * sm_o[warp + k][lane * E + e];
-            top = to;
+            for (int e = 0; e < E; ++e) acc[0][e] = acc[0][e] * a + w * sm_o[warp + k][lane * E + e];
+            top[0] = to;
         }
     }
-    if (n_all == 0) return;  // final already, or a row of no request
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t *out = static_cast<uint16_t *>(p.a.o) + (size_t)id * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(out + e) =
-            BF16 ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : pack_f16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-        p.a.lse[(size_t)h * p.a.total + tok] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+    for (int r = 0; r < R; ++r) {
+        if (n_all[r] == 0) continue;  // final already, or a row of no request
+        const long long id = id0 + r;
+        const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
+        uint16_t *out = static_cast<uint16_t *>(p.a.o) + (size_t)id * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t *>(out + e) = BF16 ? pack_bf16x2(acc[r][e] * inv, acc[r][e + 1] * inv)
+                                                          : pack_f16x2(acc[r][e] * inv, acc[r][e + 1] * inv);
+        if (lane == 0) {
+            const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
+            p.a.lse[(size_t)h * p.a.total + tok] =
+                sum[r] > 0.f ? (top[r] + log2f(sum[r])) * 0.69314718055994530942f : -INFINITY;
+        }
+    }
 }
 
 // Rounded up to whole 256-byte steps of the workspace.
@@ -664,7 +697,6 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.part = w.own;
-    p.sms = kSms;
     return launch_after(paged_few_kernel<D, BF16>, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
 }
 
@@ -676,10 +708,16 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     p.prefix = w.prefix;
     // few rows can have many parts each, many rows have few
     const long long rows = (long long)a.total * a.Hq;
-    p.warps = rows <= 1024 ? 8 : rows <= 8192 ? 2 : 1;
+    if (rows > 4096) {
+        p.warps = 1;
+        const long long per_block = kMergeWarps * kMergeRows;
+        return launch_after(paged_merge_kernel<D, BF16, kMergeRows>, (unsigned)((rows + per_block - 1) / per_block),
+                            32 * kMergeWarps, 0, true, st, p);
+    }
+    p.warps = rows <= 1024 ? 8 : 2;
     const long long per_block = kMergeWarps / p.warps;
-    return launch_after(paged_merge_kernel<D, BF16>, (unsigned)((rows + per_block - 1) / per_block), 32 * kMergeWarps,
-                        0, true, st, p);
+    return launch_after(paged_merge_kernel<D, BF16, 1>, (unsigned)((rows + per_block - 1) / per_block),
+                        32 * kMergeWarps, 0, true, st, p);
 }
 
 }  // namespace

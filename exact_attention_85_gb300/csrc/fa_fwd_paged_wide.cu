@@ -60,7 +60,7 @@ struct WideLayout {
     static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
     static constexpr int OFF_MISC = OFF_SEG + 2 * 48;
-    static constexpr int BYTES = OFF_MISC + 32;
+    static constexpr int BYTES = OFF_MISC + 16 + kThreads / 32 * (int)sizeof(PlanSum);
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
@@ -70,7 +70,6 @@ struct WideParams {
     FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
     int shared;  // prefix: the few-row kernel runs at the same time
-    int sms;     // of the GPU
     int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
@@ -121,28 +120,23 @@ __device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return 
 // Units of all blocks of a request, for one key/value head.  The sums of
 // 32 requests, one a lane: a lane walks its own request's blocks where they
 // are few, the warp walks them together where a request has many.
-__device__ __noinline__ int request_units(const WideParams &p, const Request &r, int nb, int prefix_lo, int lane) {
+__device__ __noinline__ int request_units(const WideParams &p, Request r, int nb, int lane) {
     int sum = 0;
-    if (!__any_sync(0xffffffffu, nb > 8)) {
-        for (int k = 0; k < nb; ++k) {
-            int lo, hi;
-            block_keys(p, r, k, prefix_lo, lo, hi);
-            sum += range_tiles(lo, hi) + kBlockCost;
+    const bool alone = !__any_sync(0xffffffffu, nb > 8);
+    for (int i = 0; i < (alone ? 1 : 32); ++i) {
+        Request o = r;
+        int n = nb, mine = 0;
+        if (!alone) {
+            o.n = __shfl_sync(0xffffffffu, r.n, i);
+            o.len = __shfl_sync(0xffffffffu, r.len, i);
+            n = __shfl_sync(0xffffffffu, nb, i);
         }
-        return sum;
-    }
-    for (int i = 0; i < 32; ++i) {
-        Request o;
-        o.row0 = 0;
-        o.n = __shfl_sync(0xffffffffu, r.n, i);
-        o.len = __shfl_sync(0xffffffffu, r.len, i);
-        const int n = __shfl_sync(0xffffffffu, nb, i);
-        int mine = 0;
-        for (int k = lane; k < n; k += 32) {
+        for (int k = alone ? 0 : lane; k < n; k += alone ? 1 : 32) {
             int lo, hi;
-            block_keys(p, o, k, prefix_lo, lo, hi);
+            block_keys(p, o, k, 0, lo, hi);
             mine += range_tiles(lo, hi) + kBlockCost;
         }
+        if (alone) return mine;
         mine = __reduce_add_sync(0xffffffffu, mine);
         if (lane == i) sum = mine;
     }
@@ -173,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
-    int *sm_low = reinterpret_cast<int *>(smem + L::OFF_MISC + 8);
-    unsigned long long *sm_units = reinterpret_cast<unsigned long long *>(smem + L::OFF_MISC + 16);
+    PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -192,59 +185,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
-        *sm_low = p.a.prefix_len;
-        *sm_units = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     launch_dependents();
 
     // ---------------------------------------------- the batch's units of work
     const int B = p.prefix ? 1 : p.a.B;
-    Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
-    int most = gridDim.x, prefix_lo = 0;
-    if (p.prefix) {
-        // the first key that any row sees, and the few-row kernel's tiles
-        whole.n = prefix_rows(p.a);
-        int low = p.a.prefix_len;
-        unsigned long long few = 0;
-        for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
-            Request r;
-            int t;
-            if (!load_request(p.a, b, r) || r.n == 0) continue;
-            low = min(low, prefix_low(p.a, r));
-            few += pair_tiles<kFewKeys<D>>(p.a, r, t);
-        }
-        atomicMin(sm_low, low);
-        if (few && p.shared) atomicAdd(sm_units, few * p.a.Hkv);
-    } else {
-        for (int b = warp * 32; b < B; b += kThreads) {
-            Request r{0, 0, 0};
-            if (b + lane < B && !load_request(p.a, b + lane, r)) {
-                if (blockIdx.x == 0) record_bad_args(p.status);
-                r.n = 0;
+    {
+        PlanSum sum{0, p.a.prefix_len, 0};
+        if (p.prefix) {
+            // the few-row kernel's tiles, and the first key that any row sees
+            for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
+                Request r;
+                int t;
+                if (!load_request(p.a, b, r) || r.n == 0) continue;
+                sum.low = min(sum.low, prefix_low(p.a, r));
+                sum.units += pair_tiles<kFewKeys<D>>(p.a, r, t);
             }
-            const int units = request_units(p, r, blocks_of(r, p.group), 0, lane);
-            if (units) atomicAdd(sm_units, (unsigned long long)units * p.a.Hkv);
+        } else {
+            for (int b = warp * 32; b < B; b += kThreads) {
+                Request r{0, 0, 0};
+                if (b + lane < B && !load_request(p.a, b + lane, r)) {
+                    if (blockIdx.x == 0) record_bad_args(p.status);
+                    r.n = 0;
+                }
+                sum.units += request_units(p, r, blocks_of(r, p.group), lane);
+            }
         }
+        sum.units = warp_sum(sum.units);
+        sum.low = __reduce_min_sync(0xffffffffu, sum.low);
+        if (lane == 0) sums[warp] = sum;
     }
+    tc_fence_before();
     __syncthreads();
-    long long T = (long long)*sm_units;
-    if (p.prefix) {
-        prefix_lo = *sm_low;
-        const long long few = T;
-        T = prefix_units(p.a, whole.n, p.group.d, prefix_lo);
-        if (p.shared) most = min(most, prefix_sms(T, few, p.sms));
-    }
-    const int G = (int)min((long long)most, max(1ll, T / kWideMinUnits));
-    const Ranges ranges(T, G);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------ TMA producer
@@ -252,6 +231,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
+        Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
+        long long T = 0;
+        int most = gridDim.x, prefix_lo = p.a.prefix_len;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            T += (long long)sums[w].units * p.a.Hkv;
+            prefix_lo = min(prefix_lo, sums[w].low);
+        }
+        if (p.prefix) {
+            const long long few = T;
+            whole.n = prefix_rows(p.a);
+            T = prefix_units(p.a, whole.n, p.group.d, prefix_lo);
+            if (p.shared) most = min(most, prefix_sms(T, few));
+        }
+        const int G = (int)min((long long)most, max(1ll, T / kWideMinUnits));
+        const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
         const int box_bytes = page_keys * 128;
         const int half = lane % L::NBOX, sub = lane / L::NBOX;
@@ -283,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; b < B; b += 32) {
                 Request r{0, 0, 0};
                 if (b + lane < B && !load_request(p.a, b + lane, r)) r.n = 0;
-                const long long units = (long long)request_units(p, r, blocks_of(r, p.group), 0, lane) * p.a.Hkv;
+                const long long units = (long long)request_units(p, r, blocks_of(r, p.group), lane) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -313,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mine = r;
                 const int per_head =
                     p.prefix ? nb * (range_tiles(prefix_lo, r.len) + kBlockCost)
-                             : __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, 0, lane), 0);
+                             : __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, lane), 0);
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
@@ -792,7 +787,6 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.group = fast_div(a.Hq / a.Hkv);
     p.prefix = prefix ? 1 : 0;
     p.shared = prefix && w.few ? 1 : 0;
-    p.sms = kSms;
     p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;

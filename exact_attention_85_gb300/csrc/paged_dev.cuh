@@ -31,6 +31,12 @@ __device__ __forceinline__ int operator/(int x, const FastDiv &f) {
     return (int)((__umulhi((uint32_t)x, f.mul) + (uint32_t)x) >> f.shift);
 }
 
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
+#pragma unroll
+    for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+    return x;
+}
+
 // [u0, u1): the units of CTA c of G that share T units, and the CTA that has
 // unit u.  The first T % G CTAs take one more than the others.
 struct Ranges {
@@ -85,16 +91,23 @@ __device__ __forceinline__ long long prefix_units(const PagedArgs &a, int rows, 
     return blocks * a.Hkv * (range_tiles(lo, a.prefix_len) + kBlockCost);
 }
 
+// What every warp of a block adds up of the batch before the block's first
+// barrier; its producer then takes the sums of all.
+struct PlanSum {
+    unsigned long long units;
+    int low, pad;
+};
+
 // A shared prefix' pass is bound by the tensor cores and the few-row kernel
 // by memory, so they run at the same time, each on SMs of its own: the number
-// that the prefix gets, of `sms`.  Times in us: a unit of the 256-row kernel
+// that the prefix gets.  Times in us: a unit of the 256-row kernel
 // takes 1.8 on one SM, with 8 to start and end; a few-row tile 32 KB at 6.8
 // TB/s, or at 90 GB/s an SM where those are few.  32 candidates, one a lane;
 // each kernel decides for itself, so a difference would cost time only.
-__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles, int sms) {
-    const int g = max(1, (int)(sms * ((threadIdx.x & 31) + 1) / 33));
+__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles) {
+    const int g = kSms * ((threadIdx.x & 31) + 1) / 33;
     const float wide = 8.f + (float)prefix_units * 1.8f / (float)g;
-    const float few = (float)few_tiles * fmaxf(0.0048f, 0.364f / (float)(sms - g));
+    const float few = (float)few_tiles * fmaxf(0.0048f, 0.364f / (float)(kSms - g));
     // the least of the larger times, and the first to have it
     const uint32_t cost = __float_as_uint(fmaxf(wide, few)) & ~31u;
     const uint32_t best = __reduce_min_sync(0xffffffffu, cost | (threadIdx.x & 31));
