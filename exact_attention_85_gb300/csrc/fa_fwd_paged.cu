@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         mine = warp_sum(mine);
         low = __reduce_min_sync(0xffffffffu, low);
-        if (lane == 0) sums[warp] = PlanSum{mine, low, 0};
+        if (lane == 0) sums[warp] = PlanSum{mine, 0, low};
     }
     __syncthreads();
 
@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         int low = p.a.prefix_len, most = gridDim.x;
 #pragma unroll
         for (int w = 0; w <= kConsumers; ++w) {
-            T += (long long)sums[w].units * Hkv;
+            T += (long long)sums[w].tiles * Hkv;
             low = min(low, sums[w].low);
         }
         if (p.a.prefix_len > 0) {
             // the prefix pass has some of the SMs to itself
-            const long long units = prefix_units(p.a, prefix_rows(p.a), p.group.d, low);
+            const long long units = prefix_work(p.a, prefix_rows(p.a), p.group.d, low).units();
             most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, T))));
         }
         const int G = (int)min((long long)most, max(1ll, T / kMinUnits));
@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
     __shared__ float sm_o[kMergeWarps][D], sm_top[kMergeWarps], sm_sum[kMergeWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int W = p.warps, sub = warp % W;
-    const long long id0 = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * R;
     const long long rows = (long long)p.a.total * p.a.Hq;
     wait_previous();
     // rows behind the batch's have no part
@@ -571,23 +570,34 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
         begin = p.a.cu_seqlens[0];
         end = p.a.cu_seqlens[p.a.B];
     }
-    int c_own[R], c_pre[R], n_own[R], n_all[R], most = 0;
+    const long long id_lo = (long long)begin * p.a.Hq, id_hi = min(rows, (long long)end * p.a.Hq);
+    const long long step = (long long)gridDim.x * (kMergeWarps / W) * R;
+    long long id0 = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * R;
+    int c_own[R], c_pre[R];
+    auto load_codes = [&](long long id) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        c_own[r] = c_pre[r] = 0;
-        if (id0 + r < rows) {
-            c_own[r] = p.own.code[id0 + r];
-            if (p.prefix.code) c_pre[r] = p.prefix.code[id0 + r];
+        for (int r = 0; r < R; ++r) {
+            c_own[r] = c_pre[r] = 0;
+            if (id + r < rows) {
+                c_own[r] = p.own.code[id + r];
+                if (p.prefix.code) c_pre[r] = p.prefix.code[id + r];
+            }
         }
-    }
+    };
+    load_codes(id0);
+    for (; R == 1 || id0 < rows; id0 += step) {  // once if R == 1, by every warp: there is a barrier
+    int n_own[R], n_all[R], at_own[R], at_pre[R], most = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         // the own pass' parts, then the prefix'
-        const bool mine = id0 + r < min(rows, (long long)end * p.a.Hq) && id0 + r >= (long long)begin * p.a.Hq;
+        const bool mine = id0 + r >= id_lo && id0 + r < id_hi;
         n_own[r] = mine ? parts_of(p.own, c_own[r]) : 0;
         n_all[r] = n_own[r] + (mine && p.prefix.code ? parts_of(p.prefix, c_pre[r]) : 0);
         most = max(most, n_all[r]);
+        at_own[r] = c_own[r];
+        at_pre[r] = c_pre[r];
     }
+    if (R > 1) load_codes(id0 + step);  // the next rows', while these are merged
     float acc[R][E], top[R], sum[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -607,7 +617,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
                 if (k >= n_all[r]) continue;
                 const bool own = k < n_own[r];
                 const PartView &v = own ? p.own : p.prefix;
-                const int code = own ? c_own[r] : c_pre[r], piece = own ? k : k - n_own[r];
+                const int code = own ? at_own[r] : at_pre[r], piece = own ? k : k - n_own[r];
                 const size_t at = code ? ((size_t)((code >> 9 & kMaxPieces) + piece) * 2 + (piece == 0 ? 1 : 0)) *
                                                  v.slot_rows + (code >> 18)
                                        : (size_t)(id0 + r);
@@ -667,10 +677,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
             *reinterpret_cast<uint32_t *>(out + e) = BF16 ? pack_bf16x2(acc[r][e] * inv, acc[r][e + 1] * inv)
                                                           : pack_f16x2(acc[r][e] * inv, acc[r][e + 1] * inv);
         if (lane == 0) {
-            const int tok = (int)(id / p.a.Hq), h = (int)(id - (long long)tok * p.a.Hq);
+            const int tok = (int)id / p.a.Hq, h = (int)id - tok * p.a.Hq;  // total * Hq fits 31 bits
             p.a.lse[(size_t)h * p.a.total + tok] =
                 sum[r] > 0.f ? (top[r] + log2f(sum[r])) * 0.69314718055994530942f : -INFINITY;
         }
+    }
+    if (R == 1) return;
     }
 }
 
@@ -711,7 +723,7 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     if (rows > 4096) {
         p.warps = 1;
         const long long per_block = kMergeWarps * kMergeRows;
-        return launch_after(paged_merge_kernel<D, BF16, kMergeRows>, (unsigned)((rows + per_block - 1) / per_block),
+        return launch_after(paged_merge_kernel<D, BF16, kMergeRows>, at_most((rows + per_block - 1) / per_block, 2 * kSms),
                             32 * kMergeWarps, 0, true, st, p);
     }
     p.warps = rows <= 1024 ? 8 : 2;
@@ -741,11 +753,11 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     } else {
         const long long most = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
         const long long blocks = row_blocks + B < most ? row_blocks + B : most;
-        w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys) / kWideMinUnits, kSms);
+        w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys), kSms);
         w.own.slot_rows = kWideRows;
     }
     if (prefix_len > 0) {
-        w.prefix.ctas = at_most(row_blocks * Hkv * ((prefix_len + kWideKeys - 1ll) / kWideKeys) / kWideMinUnits, kSms);
+        w.prefix.ctas = at_most(row_blocks * Hkv * ((prefix_len + kWideKeys - 1ll) / kWideKeys), kSms);
         w.prefix.slot_rows = kWideRows;
         w.prefix.code = take<int>(at, rows);
         w.own.plane_lse2 = take<float>(at, rows);

@@ -44,6 +44,8 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
 
+constexpr int kKept = 256;  // requests whose tile counts the producer finds in shared memory (a multiple of 32)
+
 template <int D>
 struct WideLayout {
     static constexpr int KS = D == 128 ? 3 : 4;
@@ -60,7 +62,8 @@ struct WideLayout {
     static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
     static constexpr int OFF_MISC = OFF_SEG + 2 * 48;
-    static constexpr int BYTES = OFF_MISC + 16 + kThreads / 32 * (int)sizeof(PlanSum);
+    static constexpr int OFF_KEPT = OFF_MISC + 16 + kThreads / 32 * (int)sizeof(PlanSum);
+    static constexpr int BYTES = OFF_KEPT + kKept * 4;
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(ALLOC <= 227 * 1024, "shared memory");
 };
@@ -70,6 +73,7 @@ struct WideParams {
     FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
     int shared;  // prefix: the few-row kernel runs at the same time
+    int q_box;   // tokens of a 128-row Q tile if the group divides it (TMA), else 0
     int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
@@ -117,10 +121,10 @@ __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r
 }
 // Whether a key tile holds keys that no row of the block sees.
 __device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return kv0 < key_lo || kv0 + kBN > key_hi; }
-// Units of all blocks of a request, for one key/value head.  The sums of
+// Key tiles of all blocks of a request, for one key/value head.  The sums of
 // 32 requests, one a lane: a lane walks its own request's blocks where they
 // are few, the warp walks them together where a request has many.
-__device__ __noinline__ int request_units(const WideParams &p, Request r, int nb, int lane) {
+__device__ __noinline__ int request_tiles(const WideParams &p, Request r, int nb, int lane) {
     int sum = 0;
     const bool alone = !__any_sync(0xffffffffu, nb > 8);
     for (int i = 0; i < (alone ? 1 : 32); ++i) {
@@ -134,7 +138,7 @@ __device__ __noinline__ int request_units(const WideParams &p, Request r, int nb
         for (int k = alone ? 0 : lane; k < n; k += alone ? 1 : 32) {
             int lo, hi;
             block_keys(p, o, k, 0, lo, hi);
-            mine += range_tiles(lo, hi) + kBlockCost;
+            mine += range_tiles(lo, hi);
         }
         if (alone) return mine;
         mine = __reduce_add_sync(0xffffffffu, mine);
@@ -145,8 +149,8 @@ __device__ __noinline__ int request_units(const WideParams &p, Request r, int nb
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const WideParams p) {
+    paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const WideParams p) {
     using L = WideLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -168,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
+    int *kept = reinterpret_cast<int *>(smem + L::OFF_KEPT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- the batch's units of work
     const int B = p.prefix ? 1 : p.a.B;
     {
-        PlanSum sum{0, p.a.prefix_len, 0};
+        PlanSum sum{0, 0, p.a.prefix_len};
         if (p.prefix) {
             // the few-row kernel's tiles, and the first key that any row sees
             for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int t;
                 if (!load_request(p.a, b, r) || r.n == 0) continue;
                 sum.low = min(sum.low, prefix_low(p.a, r));
-                sum.units += pair_tiles<kFewKeys<D>>(p.a, r, t);
+                sum.tiles += pair_tiles<kFewKeys<D>>(p.a, r, t);
             }
         } else {
             for (int b = warp * 32; b < B; b += kThreads) {
@@ -213,10 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (blockIdx.x == 0) record_bad_args(p.status);
                     r.n = 0;
                 }
-                sum.units += request_units(p, r, blocks_of(r, p.group), lane);
+                const int nb = blocks_of(r, p.group), tiles = request_tiles(p, r, nb, lane);
+                sum.tiles += tiles;
+                sum.blocks += nb;
+                if (b + lane < kKept) kept[b + lane] = tiles;
             }
         }
-        sum.units = warp_sum(sum.units);
+        sum.tiles = warp_sum(sum.tiles);
+        sum.blocks = __reduce_add_sync(0xffffffffu, sum.blocks);
         sum.low = __reduce_min_sync(0xffffffffu, sum.low);
         if (lane == 0) sums[warp] = sum;
     }
@@ -228,24 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
+            prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
         Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
-        long long T = 0;
+        WideWork work{0, 0};
         int most = gridDim.x, prefix_lo = p.a.prefix_len;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            T += (long long)sums[w].units * p.a.Hkv;
+            work.tiles += (long long)sums[w].tiles * p.a.Hkv;
+            work.blocks += (long long)sums[w].blocks * p.a.Hkv;
             prefix_lo = min(prefix_lo, sums[w].low);
         }
         if (p.prefix) {
-            const long long few = T;
+            const long long few = work.tiles;
             whole.n = prefix_rows(p.a);
-            T = prefix_units(p.a, whole.n, p.group.d, prefix_lo);
-            if (p.shared) most = min(most, prefix_sms(T, few));
+            work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
+            if (p.shared) most = min(most, prefix_sms(work.units(), few));
         }
-        const int G = (int)min((long long)most, max(1ll, T / kWideMinUnits));
+        const int cost = work.block_cost();
+        const long long T = work.units();
+        const int G = (int)min((long long)most, max(1ll, T));
         const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
         const int box_bytes = page_keys * 128;
@@ -278,7 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; b < B; b += 32) {
                 Request r{0, 0, 0};
                 if (b + lane < B && !load_request(p.a, b + lane, r)) r.n = 0;
-                const long long units = (long long)request_units(p, r, blocks_of(r, p.group), lane) * p.a.Hkv;
+                const int nb = blocks_of(r, p.group);
+                const int tiles = b >= kKept ? request_tiles(p, r, nb, lane) : b + lane < B ? kept[b + lane] : 0;
+                const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -304,11 +319,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!load(b, r) || r.n == 0) continue;
             const int nb = blocks_of(r, p.group);
             if (fresh) {
-                Request mine{0, 0, 0};
-                if (lane == 0) mine = r;
-                const int per_head =
-                    p.prefix ? nb * (range_tiles(prefix_lo, r.len) + kBlockCost)
-                             : __shfl_sync(0xffffffffu, request_units(p, mine, lane == 0 ? nb : 0, lane), 0);
+                int tiles = nb * range_tiles(prefix_lo, r.len);
+                if (!p.prefix && b < kKept) {
+                    tiles = kept[b];
+                } else if (!p.prefix) {
+                    Request mine{0, 0, 0};
+                    if (lane == 0) mine = r;
+                    tiles = __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, lane), 0);
+                }
+                const int per_head = tiles + nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int lo, hi, units = 0;
                     if (blk + lane < nb) {
                         block_keys(p, r, blk + lane, prefix_lo, lo, hi);
-                        units = range_tiles(lo, hi) + kBlockCost;
+                        units = range_tiles(lo, hi) + cost;
                     }
                     int incl = units;
 #pragma unroll
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.hk = hk;
                     block_keys(p, r, blk, prefix_lo, sg.key_lo, sg.key_hi);
                     const int nt = range_tiles(sg.key_lo, sg.key_hi);
-                    const long long tile0 = blk0 + kBlockCost;  // unit of its first tile
+                    const long long tile0 = blk0 + cost;  // unit of its first tile
                     const int first = (int)max(0ll, u - tile0), end = (int)min((long long)nt, u1 - tile0);
                     blk0 = tile0 + nt;
                     u = u1 < blk0 ? u1 : blk0;
@@ -503,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int id = threadIdx.x - 32 * (kMmaWarp + 1);
         constexpr int CH = D / 8, STEP = 32 * kHelperWarps / CH;  // 16-byte pieces of a row; rows a pass
         bool ok = true;
-        int u = 0;
+        int u = 0, boxed_q = -1;  // tiles of the segments before; last segment whose Q came by TMA
         for (int g = 0; ok; ++g) {
             bool got = mbar_wait(&seg_full[g & 1], (g >> 1) & 1, abort_flag, p.status, 43);
             if (!__all_sync(0xffffffffu, got)) break;
@@ -517,6 +536,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             got = g == 0 || mbar_wait(q_empty, (g - 1) & 1, abort_flag, p.status, 44);
             if (!__all_sync(0xffffffffu, got)) break;
             const int rows = min(sg.n * p.group.d - sg.r0, kRows);
+            if (p.q_box) {
+                // whole tokens fill a tile: one box per tile and 64 columns.
+                // Rows past the block's are the next request's, or zeros: they
+                // touch no other row and are never written.
+                boxed_q = g;
+                if (id == 0) {
+                    const int tiles = rows > kBM ? 2 : 1, tok = sg.row0 + sg.r0 / p.group;
+                    mbar_arrive_expect_tx(q_full, tiles * L::TILE);
+                    for (int x = 0; x < tiles; ++x)
+                        for (int bx = 0; bx < L::NBOX; ++bx)
+                            tma_load_4d(smem + L::OFF_Q + x * L::TILE + bx * L::BOX, &tm_q, q_full, bx * 64, 0, sg.hk,
+                                        tok + x * p.q_box);
+                } else {
+                    mbar_arrive(q_full);
+                }
+            } else {
             const int ch = id % CH;
             const int t0 = sg.r0 / p.group, h0 = sg.r0 - t0 * p.group.d;
             const uint4 *src =
@@ -534,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_wait_all();
             fence_proxy_async_smem();
             mbar_arrive(q_full);
+            }
             // V rows that no row of the block sees may hold anything (the rest
             // of a page, a buffer that was not filled), and 0 * NaN is NaN:
             // clear them in the tiles that have some, the first and the last
@@ -558,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             u += sg.nj;
         }
+        // a Q that is still in flight, if the others gave up, lands before the CTA exits
+        if (id == 0 && boxed_q >= 0) mbar_wait_drain(q_full, boxed_q & 1, 10000000ull);
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax + epilogue
@@ -778,20 +816,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool BF16>
 cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st) {
     using L = WideLayout<D>;
-    CUtensorMap tk, tv;
+    CUtensorMap tq, tk, tv;
     if (!make_tmap_pages(&tk, a.k_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, kBN) ||
         !make_tmap_pages(&tv, a.v_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, kBN))
         return cudaErrorInvalidValue;
     WideParams p;
     p.a = a;
-    p.group = fast_div(a.Hq / a.Hkv);
+    const int g = a.Hq / a.Hkv;
+    p.group = fast_div(g);
+    p.q_box = kBM % g == 0 ? kBM / g : 0;
+    if (!make_tmap_rows(&tq, a.q, BF16, D, g, a.Hkv, a.total, p.q_box ? p.q_box : 1)) return cudaErrorInvalidValue;
     p.prefix = prefix ? 1 : 0;
     p.shared = prefix && w.few ? 1 : 0;
     p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, after, st, tk, tv, p);
+    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, after, st, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -46,6 +46,11 @@ bool make_tmap_tiles(CUtensorMap *map, const void *base, CUtensorMapDataType dty
 bool make_tmap_pages(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
                      int keys);
 
+// TMA descriptor over token-major rows [total][heads][group][d], 16-bit:
+// boxes of 64 columns, all of a group and `tokens` tokens; coordinates
+// (column, row of the group, group, token).  group * tokens at most 256.
+bool make_tmap_rows(CUtensorMap *map, const void *base, bool bf16, int d, int group, int heads, int total, int tokens);
+
 // Launches `kernel` with `smem` bytes of dynamic shared memory.  `after`: it
 // may start before the stream's previous kernel has finished, once all of
 // that one's CTAs have asked for it (programmatic dependent launch).

@@ -73,7 +73,6 @@ struct PartView {
 };
 constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
 constexpr int kWideRows = 256, kWideKeys = 128;  // row block and key tile of the 256-row kernel
-constexpr int kWideMinUnits = 4;                 // units of work a CTA of it takes at least
 constexpr int kMaxPieces = 511;  // 9 bits, also of CTA numbers
 
 __host__ __device__ constexpr int part_code(int pieces, int cta, int row) { return pieces | cta << 9 | row << 18; }

@@ -64,11 +64,16 @@ __device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, 
     return max(1, (r.len + TK - 1) / TK - t0);
 }
 
-// A row block of the 256-row kernel costs its key tiles and as much as
-// kBlockCost tiles more for the change from the block before (first Q, K and
-// S with nothing to overlap, last P V and epilogue).  Counted among the
-// units, so that CTAs whose range has many short blocks get fewer tiles.
-constexpr int kBlockCost = 3;
+// Work of the 256-row kernel, in key tiles.  A row block costs its tiles and
+// as much as three more for the change from the block before (first Q, K and
+// S with nothing to overlap, last P V and epilogue).  Counted among the units,
+// so that CTAs whose range has many short blocks get fewer tiles.  Where there
+// are only a few tiles for every SM it would only keep SMs idle.
+struct WideWork {
+    long long tiles, blocks;
+    __device__ __forceinline__ int block_cost() const { return tiles > 4 * kSms ? 3 : 0; }
+    __device__ __forceinline__ long long units() const { return tiles + blocks * block_cost(); }
+};
 
 // Key tiles of a range; at least one.
 __device__ __forceinline__ int range_tiles(int lo, int hi) {
@@ -86,16 +91,16 @@ __device__ __forceinline__ int prefix_low(const PagedArgs &a, const Request &r) 
     const long long lo = (long long)a.prefix_len + r.len - r.n + 1 - a.window;
     return a.window > 0 ? (int)max(0ll, min(lo, (long long)a.prefix_len)) : 0;
 }
-__device__ __forceinline__ long long prefix_units(const PagedArgs &a, int rows, int group, int lo) {
-    const long long blocks = ((long long)rows * group + kWideRows - 1) / kWideRows;
-    return blocks * a.Hkv * (range_tiles(lo, a.prefix_len) + kBlockCost);
+__device__ __forceinline__ WideWork prefix_work(const PagedArgs &a, int rows, int group, int lo) {
+    const long long blocks = ((long long)rows * group + kWideRows - 1) / kWideRows * a.Hkv;
+    return {blocks * range_tiles(lo, a.prefix_len), blocks};
 }
 
 // What every warp of a block adds up of the batch before the block's first
 // barrier; its producer then takes the sums of all.
 struct PlanSum {
-    unsigned long long units;
-    int low, pad;
+    unsigned long long tiles;
+    int blocks, low;
 };
 
 // A shared prefix' pass is bound by the tensor cores and the few-row kernel
