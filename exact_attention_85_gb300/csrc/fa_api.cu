@@ -117,18 +117,35 @@ bool make_tmap_pages(CUtensorMap *map, const void *base, bool bf16, int d, int p
                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-bool make_tmap_rows(CUtensorMap *map, const void *base, bool bf16, int d, int group, int heads, int total, int tokens) {
+namespace {
+bool encode_4d(CUtensorMap *map, const void *base, bool bf16, const cuuint64_t *dims, const cuuint64_t *strides,
+               const cuuint32_t *box) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)heads, (cuuint64_t)total};
-    cuuint64_t strides[3] = {dims[0] * 2, dims[0] * dims[1] * 2, dims[0] * dims[1] * dims[2] * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)(group < 256 ? group : 256), 1, (cuuint32_t)tokens};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     std::memset(map, 0, sizeof(*map));
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool make_tmap_pages_4d(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
+                        int keys) {
+    const cuuint64_t row = (cuuint64_t)d * 2;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)page_size, (cuuint64_t)d / 64, (cuuint64_t)num_pages * heads};
+    const cuuint64_t strides[3] = {row, 128, row * page_size};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(page_size < keys ? page_size : keys), (cuuint32_t)d / 64, 1};
+    return encode_4d(map, base, bf16, dims, strides, box);
+}
+
+bool make_tmap_rows(CUtensorMap *map, const void *base, bool bf16, int d, int group, int heads, int total, int tokens) {
+    const cuuint64_t row = (cuuint64_t)d * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)heads, (cuuint64_t)total};
+    const cuuint64_t strides[3] = {row, row * group, row * group * heads};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(group < 256 ? group : 256), 1, (cuuint32_t)tokens};
+    return encode_4d(map, base, bf16, dims, strides, box);
 }
 
 void *current_context() {

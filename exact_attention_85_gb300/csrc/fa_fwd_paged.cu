@@ -4,12 +4,18 @@
 // Row i of request b (n_b new rows, len_b keys of its own, of which the last
 // n_b belong to the rows) stands at place p = len_b - n_b + i and sees its
 // own keys max(0, p - W + 1) .. p.  The n_b * g rows that read one key/value
-// head (g = Hq / Hkv query heads share it) form the one 16-row tile of a
-// warp-level MMA: S = Q K^T and O~ += P V with the running maximum and sum of
-// the softmax, exactly [V2] section 6.1 with 16 rows.  At 16 rows a key costs
-// 4 d bytes and 64 d tensor operations, far below the ratio the tensor cores
-// could sustain: the kernel is bound by reading the cache, and everything
-// here serves to keep copies in flight.
+// head (g = Hq / Hkv query heads share it), 16 at most, are worked on
+// together: [V2] section 6.1 with the running maximum and sum of the softmax,
+// the maximum moved only when a score passes it by more than 8 (log2 units),
+// as in the dense forward.
+//
+// Few rows make the products narrow, so they are formed transposed, with the
+// keys (S^T = K Q^T) and the head's columns (O~^T += V^T P^T) as the long side
+// of the warp-level MMA and 8 query rows as its short one.  With the rows on
+// the long side the instructions, which this GPU issues at one in nine cycles
+// an SM, held an SM to 54 GB/s of cache; this way it is twice that for up to
+// 8 rows, and the kernel is bound by reading the cache (7.0 TB/s on 64
+// requests of 8-16k keys).  Everything else serves to keep copies in flight.
 //
 // Work is cut into units of one tile of keys (32 KB of K and V).  All units
 // of all (request, key/value head) pairs are numbered in order and every CTA
@@ -19,11 +25,11 @@
 // written out directly; the parts of a pair that several CTAs share go to
 // the workspace as (O~ / l, log2 sum) and a second kernel merges them (with a
 // shared prefix, everything does, and is merged with the prefix' results).
-//   warps 0-3  each a quarter of every tile's keys, all 16 rows; their four
+//   warps 0-3  each a quarter of every tile's keys, all rows; their four
 //              results are merged through the last tile's buffer
 //   warp 4     producer: plans the CTA's range, reads block-table entries,
-//              starts one TMA copy per (page, 64-column half) and one small
-//              copy of Q per pair, and describes each tile to the others
+//              starts one TMA copy per page and one small copy of Q per pair,
+//              and describes each tile to the others
 #include "../../include/fa.h"
 #include "host_util.h"
 #include "mma_sync.cuh"
@@ -45,6 +51,7 @@ constexpr int kMaxCtas = (int)(kCtasPerSm * kSms);
 constexpr int kMaxRows = 16;   // rows of a pair
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;   // tiles a CTA takes at least
+constexpr float kMoveBy = 8.0f;  // log2 units by which a score passes the maximum before that moves
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16 };
 
@@ -60,9 +67,7 @@ template <int D>
 struct FewLayout {
     static constexpr int TK = kFewKeys<D>;          // keys per tile
     static constexpr int KW = TK / kConsumers;      // keys per warp and tile
-    static constexpr int HALVES = D / 64;           // 64-column boxes
-    static constexpr int HALF = TK * 128;           // bytes of one box column of a tile
-    static constexpr int TILE = HALF * HALVES;      // K or V
+    static constexpr int TILE = TK * D * 2;         // K or V
     static constexpr int QBYTES = kMaxRows * D * 2;
     static constexpr int OFF_Q = kStages * 2 * TILE;
     static constexpr int OFF_INFO = OFF_Q + kStages * QBYTES;
@@ -83,7 +88,8 @@ struct FewParams {
     PartView part;
 };
 
-template <int D, bool BF16>
+// NT: 8-row groups of a pair (rows up to 8 * NT).
+template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const FewParams p) {
@@ -174,13 +180,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 base += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        // this lane's box: tensor, 64-column half and page of the tile
-        const int page_keys = min(1 << p.a.shift, L::TK);  // keys of one box
-        const int per_tile = L::TK / page_keys;
-        const int box_bytes = page_keys * 128;
+        // this lane's box: K or V of a page of the tile, its 64-column halves
+        // one behind the other (128-byte swizzled rows)
+        const int page_keys = min(1 << p.a.shift, L::TK);
+        const int box_bytes = page_keys * D * 2;
         const uint64_t once = l2_evict_first();  // every key is read by one CTA only
-        const bool boxed = lane < 2 * L::HALVES * per_tile;
-        const int tensor = lane & 1, half = (lane >> 1) % L::HALVES, sub = (lane >> 1) / L::HALVES;
+        const bool boxed = lane < 2 * (L::TK / page_keys);
+        const int tensor = lane & 1, sub = lane >> 1;
         int st = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -239,9 +245,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     }
                     __syncwarp();
                     if (live)
-                        tma_load_3d_hint(smem + (st * 2 + tensor) * L::TILE + half * L::HALF + sub * box_bytes,
-                                         tensor ? &tm_v : &tm_k, &full[st], half * 64, key0 & ((1 << p.a.shift) - 1),
-                                         page * Hkv + hk, once);
+                        tma_load_4d_hint(smem + (st * 2 + tensor) * L::TILE + sub * box_bytes, tensor ? &tm_v : &tm_k,
+                                         &full[st], 0, key0 & ((1 << p.a.shift) - 1), 0, page * Hkv + hk, once);
                     if (j == j0) {
                         // Q rows of the pair: row r is head r % g of token r / g
                         constexpr int CH = D / 8;  // 16-byte pieces of a row
@@ -288,11 +293,26 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         if (ok) cp_async_arrive(&full[st]);
     } else {
         // ----------------------------------------------------------- consumers
-        const int quad = lane & 3, rw = lane >> 2;  // this lane's rows: rw, rw + 8
-        uint32_t qf[D / 16][4];
-        float acc[D / 8][4];
-        float m[2], l[2], le[2];
-        int hi[2], lo[2];
+        const int quad = lane & 3, rw = lane >> 2;  // this lane's keys rw, rw + 8; rows 2 quad, + 1
+        constexpr int MT = L::KW / 16;              // 16-key groups of this warp
+        // byte offsets of the lane's ldmatrix rows: pages lie one behind the
+        // other in a tile, the halves of a page's rows likewise
+        const int page_shift = min(p.a.shift, D == 128 ? 6 : 7);
+        const int half_bytes = 128 << page_shift;
+        auto row_at = [&](int key) {
+            return (key >> page_shift) * (D / 64 * half_bytes) + (key & ((1 << page_shift) - 1)) * 128;
+        };
+        int k_at[MT], v_at[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            k_at[i] = row_at(warp * L::KW + i * 16 + ((lane >> 3) & 1) * 8 + (lane & 7));
+            v_at[i] = row_at(warp * L::KW + i * 16 + (lane >> 4) * 8 + (lane & 7));
+        }
+        const uint32_t k_swz = ((lane >> 4) ^ (lane & 7)) << 4, v_swz = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
+        uint32_t qf[NT][D / 16][2];
+        float acc[NT][D / 16][4];  // columns rw, rw + 8 of each 16; rows 2 quad, + 1
+        float m[NT][2], l[NT][2], le[NT][2];
+        int hi[NT][2], lo[NT][2];
         int st = 0;
         uint32_t phase = 0;
         for (;;) {
@@ -314,152 +334,183 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 // rows past the pair's own hold whatever the buffer held: they
                 // touch no other row and are never written
                 const uint32_t qs = smem_u32(smem + L::OFF_Q + st * L::QBYTES);
-                const int row = lane & 15;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    ldmatrix_x4(qf[kk], qs + row * (D * 2) + (((2 * kk + (lane >> 4)) ^ (row & 7)) << 4));
+                for (int g = 0; g < NT; ++g) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    m[x] = -INFINITY;
-                    l[x] = le[x] = 0.f;
-                    hi[x] = t.len - t.n + (rw + 8 * x) / p.group + 1;
-                    lo[x] = p.a.window > 0 ? hi[x] - p.a.window : 0;
-                }
-            }
-            // S: this warp's KW keys
-            float s[L::KW / 8][4];
-            const int w0 = warp * L::KW;
-#pragma unroll
-            for (int i = 0; i < L::KW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-                for (int i = 0; i < L::KW / 16; ++i) {
-                    const int key = w0 + i * 16 + ((lane >> 4) << 3) + (lane & 7);
-                    const int ch = 2 * kk + ((lane >> 3) & 1);
-                    uint32_t kf[4];
-                    ldmatrix_x4(kf, ks + (ch >> 3) * L::HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-                    mma_16x8x16<BF16>(s[2 * i], qf[kk], kf[0], kf[1]);
-                    mma_16x8x16<BF16>(s[2 * i + 1], qf[kk], kf[2], kf[3]);
-                }
-            }
-            float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < L::KW / 8; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = e >> 1;
-                    if (t.flags & kMask) {
-                        const int key = t.kv0 + w0 + i * 8 + quad * 2 + (e & 1);
-                        if (key >= hi[x] || key < lo[x]) s[i][e] = -INFINITY;
+                    for (int kk = 0; kk < D / 16; kk += 2) {
+                        uint32_t f[4];
+                        const int row = g * 8 + (lane & 7);
+                        ldmatrix_x4(f, qs + row * (D * 2) + (((2 * kk + (lane >> 3)) ^ (row & 7)) << 4));
+                        qf[g][kk][0] = f[0];
+                        qf[g][kk][1] = f[1];
+                        qf[g][kk + 1][0] = f[2];
+                        qf[g][kk + 1][1] = f[3];
                     }
-                    mx[x] = fmaxf(mx[x], s[i][e]);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) acc[g][i][0] = acc[g][i][1] = acc[g][i][2] = acc[g][i][3] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        m[g][x] = -INFINITY;
+                        l[g][x] = le[g][x] = 0.f;
+                        hi[g][x] = t.len - t.n + (g * 8 + quad * 2 + x) / p.group + 1;
+                        lo[g][x] = p.a.window > 0 ? hi[g][x] - p.a.window : 0;
+                    }
                 }
             }
-            float neg[2];
-            bool moved = false;
-            float alpha[2];
+            // S^T: this warp's KW keys
+            const int w0 = warp * L::KW;
+            float s[MT][NT][4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-                mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-                const float to = fmaxf(m[x], mx[x] * p.scale_log2);
-                moved |= to > m[x];
+            for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                for (int g = 0; g < NT; ++g) s[i][g][0] = s[i][g][1] = s[i][g][2] = s[i][g][3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t kf[4];
+                    ldmatrix_x4(kf, ks + k_at[i] + (kk >> 2) * half_bytes + (((kk & 3) << 5) ^ k_swz));
+#pragma unroll
+                    for (int g = 0; g < NT; ++g) mma_16x8x16<BF16>(s[i][g], kf, qf[g][kk][0], qf[g][kk][1]);
+                }
+            }
+            if (t.flags & kMask) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                    for (int g = 0; g < NT; ++g) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = t.kv0 + w0 + i * 16 + rw + (e >> 1) * 8;
+                            if (key >= hi[g][e & 1] || key < lo[g][e & 1]) s[i][g][e] = -INFINITY;
+                        }
+                    }
+                }
+            }
+            // the maximum of a row moves when a score passes it by 8
+            float mx[NT][2];
+            bool passed = false;
+#pragma unroll
+            for (int g = 0; g < NT; ++g) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = fmaxf(s[0][g][x], s[0][g][x + 2]);
+                    if (MT == 2) v = fmax3(v, s[MT - 1][g][x], s[MT - 1][g][x + 2]);
+                    mx[g][x] = v * p.scale_log2;
+                    passed |= mx[g][x] > m[g][x] + kMoveBy;
+                }
+            }
+            if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+                for (int g = 0; g < NT; ++g) {
+                    float alpha[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v = mx[g][x];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        alpha[x] = 1.f;
+                        if (v > m[g][x] + kMoveBy) {
+                            alpha[x] = ex2_approx(m[g][x] - v);  // 0 for the first visible score
+                            m[g][x] = v;
+                        }
+                        l[g][x] *= alpha[x];
+                        le[g][x] *= alpha[x];
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        acc[g][i][0] *= alpha[0];
+                        acc[g][i][1] *= alpha[1];
+                        acc[g][i][2] *= alpha[0];
+                        acc[g][i][3] *= alpha[1];
+                    }
+                }
+            }
+            // P, rounded to the 16-bit type and turned into P^T; l sums the
+            // rounded P that the MMA reads (O~ / l is then an exactly
+            // normalised mix of V rows), le the unrounded ones (LSE)
+            uint32_t pf[MT][NT][2];
+#pragma unroll
+            for (int g = 0; g < NT; ++g) {
                 // a row that has seen nothing yet keeps -inf: 0 stands in for it
-                neg[x] = to == -INFINITY ? 0.f : -to;
-                alpha[x] = ex2_approx(m[x] + neg[x]);
-                m[x] = to;
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                const float n0 = m[g][0] == -INFINITY ? 0.f : -m[g][0], n1 = m[g][1] == -INFINITY ? 0.f : -m[g][1];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    l[x] *= alpha[x];
-                    le[x] *= alpha[x];
-                }
+                for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    acc[i][0] *= alpha[0];
-                    acc[i][1] *= alpha[0];
-                    acc[i][2] *= alpha[1];
-                    acc[i][3] *= alpha[1];
-                }
-            }
-            // P, rounded to the 16-bit type; l sums the rounded P that the MMA
-            // reads (O~ / l is then an exactly normalised mix of V rows), le
-            // the unrounded ones (LSE)
-            uint32_t pf[L::KW / 16][4];
-#pragma unroll
-            for (int i = 0; i < L::KW / 8; ++i) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float a = ex2_approx(fmaf(s[i][2 * x], p.scale_log2, neg[x]));
-                    const float c = ex2_approx(fmaf(s[i][2 * x + 1], p.scale_log2, neg[x]));
-                    const uint32_t pk = BF16 ? pack_bf16x2(a, c) : pack_f16x2(a, c);
-                    const float2 w = unpack2<BF16>(pk);
-                    l[x] += w.x + w.y;
-                    le[x] += a + c;
-                    pf[i >> 1][(i & 1) * 2 + x] = pk;
+                    for (int y = 0; y < 2; ++y) {
+                        const float a = ex2_approx(fmaf(s[i][g][2 * y], p.scale_log2, n0));
+                        const float c = ex2_approx(fmaf(s[i][g][2 * y + 1], p.scale_log2, n1));
+                        const uint32_t pk = BF16 ? pack_bf16x2(a, c) : pack_f16x2(a, c);
+                        const float2 w = unpack2<BF16>(pk);
+                        l[g][0] += w.x;
+                        l[g][1] += w.y;
+                        le[g][0] += a;
+                        le[g][1] += c;
+                        pf[i][g][y] = transpose_8x8(pk);
+                    }
                 }
             }
-            // O~ += P V
+            // O~^T += V^T P^T
             const int k_end = t.len - t.kv0 - w0;  // keys of this warp that exist
             const int k_low = p.a.window > 0 ? t.len - t.n + 1 - p.a.window - t.kv0 - w0 : 0;
 #pragma unroll
-            for (int i = 0; i < L::KW / 16; ++i) {
+            for (int i = 0; i < MT; ++i) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    const int key = w0 + i * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
-                    const int ch = 2 * j + (lane >> 4);
                     uint32_t vf[4];
-                    ldmatrix_x4_trans(vf, vs + (ch >> 3) * L::HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+                    ldmatrix_x4_trans(vf, vs + v_at[i] + (j >> 2) * half_bytes + (((j & 3) << 5) ^ v_swz));
                     if (t.flags & kMask) {
                         // what no row sees may hold anything, and 0 * NaN is NaN
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int k0 = i * 16 + (e & 1) * 8 + quad * 2;
+                            const int k0 = i * 16 + (e >> 1) * 8 + quad * 2;
                             if (k0 >= k_end || k0 < k_low) vf[e] &= 0xFFFF0000u;
                             if (k0 + 1 >= k_end || k0 + 1 < k_low) vf[e] &= 0x0000FFFFu;
                         }
                     }
-                    mma_16x8x16<BF16>(acc[2 * j], pf[i], vf[0], vf[1]);
-                    mma_16x8x16<BF16>(acc[2 * j + 1], pf[i], vf[2], vf[3]);
+#pragma unroll
+                    for (int g = 0; g < NT; ++g) mma_16x8x16<BF16>(acc[g][j], vf, pf[i][g][0], pf[i][g][1]);
                 }
             }
             if (t.flags & kLast) {
                 // merge the four warps' results through this tile's buffer
+                constexpr int ROWS = 8 * NT;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-                    le[x] += __shfl_xor_sync(0xffffffffu, le[x], 1);
-                    le[x] += __shfl_xor_sync(0xffffffffu, le[x], 2);
-                }
-                if (!named_bar_and(1, kConsumers * 32, true)) break;  // all warps have read the tile
-                float *buf = reinterpret_cast<float *>(smem + st * 2 * L::TILE) + warp * (kMaxRows * D);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int g = 0; g < NT; ++g) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int row = rw + 8 * x;
-                        // columns exchanged by row: no bank conflicts
-                        *reinterpret_cast<float2 *>(buf + row * D + ((i * 8 + quad * 2) ^ ((row & 3) << 3))) =
-                            make_float2(acc[i][2 * x], acc[i][2 * x + 1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) {
+                            l[g][x] += __shfl_xor_sync(0xffffffffu, l[g][x], d);
+                            le[g][x] += __shfl_xor_sync(0xffffffffu, le[g][x], d);
+                        }
                     }
                 }
-                if (quad == 0) {
+                if (!named_bar_and(1, kConsumers * 32, true)) break;  // all warps have read the tile
+                float *buf = reinterpret_cast<float *>(smem + st * 2 * L::TILE) + warp * (ROWS * D);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int at = warp * 16 + rw + 8 * x;
-                        sm_m[at] = m[x];
-                        sm_m[kConsumers * 16 + at] = l[x];
-                        sm_m[2 * kConsumers * 16 + at] = le[x];
+                for (int g = 0; g < NT; ++g) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = g * 8 + quad * 2 + (e & 1), col = i * 16 + rw + (e >> 1) * 8;
+                            buf[row * D + (col ^ (quad << 3))] = acc[g][i][e];  // exchanged by row: no bank conflicts
+                        }
+                    }
+                    if (rw == 0) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int at = warp * 16 + g * 8 + quad * 2 + x;
+                            sm_m[at] = m[g][x];
+                            sm_m[kConsumers * 16 + at] = l[g][x];
+                            sm_m[2 * kConsumers * 16 + at] = le[g][x];
+                        }
                     }
                 }
                 named_bar_sync(2, kConsumers * 32);
-                // eight threads a row, four neighbouring columns at a time
-                const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+                // several threads a row, four neighbouring columns at a time
+                constexpr int TPR = kConsumers * 32 / ROWS;
+                const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
                 if (row < t.n * p.group.d) {
                     float top = -INFINITY, sum = 0.f, exact = 0.f, f[kConsumers];
 #pragma unroll
@@ -487,13 +538,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         at = ((size_t)blockIdx.x * 2 + (t.flags & kSlot1 ? 1 : 0)) * kMaxRows + row;
                     }
 #pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = 0; c0 < D; c0 += TPR * 4) {
                         const int c = c0 + part * 4;
                         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int w = 0; w < kConsumers; ++w) {
-                            const float4 x = *reinterpret_cast<const float4 *>(from + w * (kMaxRows * D) +
-                                                                               (c ^ ((row & 3) << 3)));
+                            const float4 x = *reinterpret_cast<const float4 *>(from + w * (ROWS * D) +
+                                                                               (c ^ (((row >> 1) & 3) << 3)));
                             o.x = fmaf(f[w], x.x, o.x);
                             o.y = fmaf(f[w], x.y, o.y);
                             o.z = fmaf(f[w], x.z, o.z);
@@ -700,8 +751,8 @@ template <int D, bool BF16>
 cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st) {
     using L = FewLayout<D>;
     CUtensorMap tk, tv;
-    if (!make_tmap_pages(&tk, a.k_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK) ||
-        !make_tmap_pages(&tv, a.v_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK))
+    if (!make_tmap_pages_4d(&tk, a.k_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK) ||
+        !make_tmap_pages_4d(&tv, a.v_cache, BF16, D, a.page_size, a.num_pages, a.Hkv, L::TK))
         return cudaErrorInvalidValue;
     FewParams p;
     p.a = a;
@@ -709,7 +760,8 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.part = w.own;
-    return launch_after(paged_few_kernel<D, BF16>, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
+    auto kernel = a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
+    return launch_after(kernel, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
 }
 
 template <int D, bool BF16>

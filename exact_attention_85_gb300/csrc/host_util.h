@@ -46,6 +46,11 @@ bool make_tmap_tiles(CUtensorMap *map, const void *base, CUtensorMapDataType dty
 bool make_tmap_pages(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
                      int keys);
 
+// The same with both 64-column halves of a page's rows in one box, one behind
+// the other: coordinates (column, row of the page, half, page * heads + head).
+bool make_tmap_pages_4d(CUtensorMap *map, const void *base, bool bf16, int d, int page_size, int num_pages, int heads,
+                        int keys);
+
 // TMA descriptor over token-major rows [total][heads][group][d], 16-bit:
 // boxes of 64 columns, all of a group and `tokens` tokens; coordinates
 // (column, row of the group, group, token).  group * tokens at most 256.

@@ -9,7 +9,9 @@ namespace fa {
 
 // d += a (16 x 16, row-major) * b (16 x 8, column-major), fp32 accumulate.
 // Lane L holds of d: rows L / 4 (d[0], d[1]) and L / 4 + 8 (d[2], d[3]),
-// columns 2 (L % 4) and + 1.
+// columns 2 (L % 4) and + 1; of a: rows as of d (a[0], a[2]; a[1], a[3] the
+// + 8), columns 2 (L % 4), + 1 and those + 8 (a[2], a[3]); of b: rows 2 (L %
+// 4), + 1 and those + 8, column L / 4.
 template <bool BF16>
 __device__ __forceinline__ void mma_16x8x16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     if constexpr (BF16)
@@ -36,6 +38,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t *r, uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held as by ldmatrix.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
