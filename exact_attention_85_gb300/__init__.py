@@ -137,11 +137,9 @@ def attention_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, causal: bool 
 
 
 def _on(stream):
-    """Context in which outputs are allocated: the stream that writes them."""
-    import contextlib
+    """Makes `stream` the current one: outputs are allocated on the stream
+    that writes them."""
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
@@ -159,12 +157,16 @@ def paged_tables(cached_lens, new_lens, block_table, free_pages, page_size: int,
     request and for requests the pool had no pages for), and the next
     ``free_start`` with the number of pages lacking."""
     import torch
-    B, dev = block_table.shape[0], block_table.device
-    with _on(stream):
-        seq_lens, cu_seqlens, slots, counts = (torch.empty(n, dtype=torch.int32, device=dev)
-                                               for n in (B, B + 1, total, 2))
+    if stream is not None:
+        with _on(stream):
+            return paged_tables(cached_lens, new_lens, block_table, free_pages, page_size, num_pages, total, free_start)
+    B, dev, empty, i32 = block_table.shape[0], block_table.device, torch.empty, torch.int32
+    seq_lens = empty(B, dtype=i32, device=dev)
+    cu_seqlens = empty(B + 1, dtype=i32, device=dev)
+    slots = empty(total, dtype=i32, device=dev)
+    counts = empty(2, dtype=i32, device=dev)
     _lib.fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots,
-                         counts, page_size, num_pages, stream)
+                         counts, page_size, num_pages)
     return seq_lens, cu_seqlens, slots, counts
 
 
@@ -175,22 +177,23 @@ def paged_append(k, v, slots, k_cache, v_cache, stream=None):
     _lib.fa_paged_append(k, v, slots, k_cache, v_cache, stream)
 
 
-def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, prefix_len, workspace, stream):
+def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace):
     """(O, LSE, workspace, max_new) of a paged forward call."""
     import torch
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
     total, Hq, d = q.shape
-    Hkv, page_size = k_cache.shape[1], k_cache.shape[2]
     B, max_pages = block_table.shape
     if max_new is None:
         max_new = 1 if cu_seqlens is None else int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
-    if max_new == 0:
-        raise ValueError("no request has a row")
-    with _on(stream):
-        o = torch.empty_like(q)
-        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len)
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        if max_new == 0:
+            raise ValueError("no request has a row")
+    o = torch.empty_like(q)
+    lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2],
+                                              prefix_len)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     return o, lse, workspace, max_new
 
 
@@ -203,11 +206,13 @@ def attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=N
     a row its last ``window`` ones).  ``max_new`` bounds a request's rows
     (default: the longest, read back from the device once).  Returns
     (O [total,Hq,d], LSE [Hq,total] fp32); rows of no request stay unwritten."""
-    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, 0, workspace, stream)
-    if window is not None and window < 1:
-        raise ValueError("window must be at least 1")
+    if stream is not None:
+        with _on(stream):
+            return attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, max_new, scale, window,
+                                       workspace)
+    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, 0, workspace)
     _lib.fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new,
-                      _default_scale(q.shape[-1]) if scale is None else scale, workspace, window or 0, stream)
+                      _default_scale(q.shape[-1]) if scale is None else scale, workspace, window or 0)
     return o, lse
 
 
@@ -218,11 +223,13 @@ def attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: in
     ``prefix_len`` tokens, stored once on ``prefix_pages`` (int32, on the
     device): the prefix is read once for the whole batch.  ``block_table`` and
     ``seq_lens`` describe each request's own keys behind it."""
-    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, prefix_len, workspace,
-                                                stream)
-    if window is not None and window < 1:
-        raise ValueError("window must be at least 1")
+    if stream is not None:
+        with _on(stream):
+            return attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens,
+                                              cu_seqlens, max_new, scale, window, workspace)
+    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len,
+                                                workspace)
     _lib.fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, cu_seqlens, o,
                              lse, max_new, _default_scale(q.shape[-1]) if scale is None else scale, workspace,
-                             window or 0, stream)
+                             window or 0)
     return o, lse

@@ -7,6 +7,7 @@ returns an error status, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -38,6 +39,8 @@ class FAError(RuntimeError):
 def load():
     """Load libfa.so (it must already be built: ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -100,7 +103,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -305,122 +309,122 @@ def fa_fwd_fp8(q8, k8, v8, q_descale, k_descale, v_descale, o, lse, causal: bool
         _ptr(lse), B, Hq, Hkv, N, d, int(causal), float(scale), _stream(stream)))
 
 
-def _need_all(device, **tensors):
-    """Refuses what a paged call's pointers cannot take: a tensor off `device`
-    (which must be the current one: the library launches there), or one that
-    is not contiguous.  None passes."""
+def _refuse(name, t, device: int):
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: tensor must be contiguous")
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{torch.cuda.current_device() if device < 0 else device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    raise TypeError(f"{name}: element type {t.dtype}")
 
 
-def _need_i32(**tensors):
-    """Checks (tensor, numel) pairs of int32 arrays; numel None: any."""
+def _need_all(*tensors) -> int:
+    """Refuses what a paged call's pointers cannot take: (name, tensor, type)
+    triples off the current device (where the library launches), of another
+    type, or not contiguous.  None passes.  Returns the device's index."""
     import torch
+    device = tensors[0][1].get_device()
+    if device < 0:
+        raise ValueError(f"{tensors[0][0]}: expected a CUDA tensor, got one on {tensors[0][1].device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t, dtype in tensors:
+        if t is not None and (t.get_device() != device or t.dtype != dtype or not t.is_contiguous()):
+            _refuse(name, t, device)
+    return device
+
+
+def _need_numel(**tensors):
     for name, (t, n) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name}: element type {t.dtype}, expected torch.int32")
-        if n is not None and t.numel() != n:
+        if t is not None and t.numel() != n:
             raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
-
-
-def _same_type(q, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name}: element type {t.dtype}, expected {q.dtype}")
 
 
 def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots, counts,
                     page_size: int, num_pages: int, stream=None):
     """Pages and slots for a step's new tokens; int32 tensors as in fa.h."""
+    import torch
     B, max_pages = block_table.shape
-    _need_all(block_table.device, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages,
-              free_start=free_start, block_table=block_table, seq_lens=seq_lens, cu_seqlens=cu_seqlens, slots=slots,
-              counts=counts)
-    _need_i32(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_pages=(free_pages, None),
-              free_start=(free_start, 1), block_table=(block_table, None), seq_lens=(seq_lens, B),
-              cu_seqlens=(cu_seqlens, B + 1), slots=(slots, None), counts=(counts, 2))
+    i32 = torch.int32
+    _need_all(("block_table", block_table, i32), ("cached_lens", cached_lens, i32), ("new_lens", new_lens, i32),
+              ("free_pages", free_pages, i32), ("free_start", free_start, i32), ("seq_lens", seq_lens, i32),
+              ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
+    _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
+                seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
     num_free = free_pages.numel()
     _check("fa_paged_tables", load().fa_paged_tables(
-        _ptr(cached_lens), _ptr(new_lens), _ptr(free_pages) if num_free else None, _ptr(free_start),
-        _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(slots), _ptr(counts), B, max_pages, int(page_size),
-        int(num_pages), num_free, slots.numel(), _stream(stream)))
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, _ptr(free_start),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), counts.data_ptr(), B,
+        max_pages, page_size, num_pages, num_free, slots.numel(), _stream(stream)))
 
 
 def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     """Writes k, v [total,Hkv,d] into slots of the caches [pages,Hkv,page_size,d]."""
+    import torch
     total, Hkv, d = k.shape
-    num_pages, _, page_size, _ = k_cache.shape
-    code = _dtype_code(k)
-    _need_all(k.device, k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache)
-    _same_type(k, v=v, k_cache=k_cache, v_cache=v_cache)
-    _need_i32(slots=(slots, total))
-    if v.shape != k.shape or v_cache.shape != k_cache.shape or k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+    shape = k_cache.shape
+    num_pages, heads, page_size, dc = shape
+    code, dtype = _dtype_code(k), k.dtype
+    _need_all(("k", k, dtype), ("v", v, dtype), ("slots", slots, torch.int32), ("k_cache", k_cache, dtype),
+              ("v_cache", v_cache, dtype))
+    _need_numel(slots=(slots, total))
+    if v.shape != k.shape or v_cache.shape != shape or heads != Hkv or dc != d:
         raise ValueError("k, v must be [total,Hkv,d] and the caches [pages,Hkv,page_size,d] of the same heads")
-    _check("fa_paged_append", load().fa_paged_append(_ptr(k), _ptr(v), _ptr(slots), _ptr(k_cache), _ptr(v_cache),
-                                                     total, Hkv, d, page_size, num_pages, code, _stream(stream)))
+    _check("fa_paged_append", load().fa_paged_append(
+        k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), total, Hkv, d, page_size,
+        num_pages, code, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def fa_fwd_paged_workspace_bytes(B: int, total: int, max_new: int, Hq: int, Hkv: int, d: int, max_pages: int,
                                  page_size: int, prefix_len: int = 0) -> int:
     return int(load().fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len))
 
 
-def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace, prefix=None):
-    """Checks shared by the paged forwards; returns their common sizes."""
+def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window,
+                prefix=None):
+    """Checks shared by the paged forwards; returns the arguments that follow
+    the tables in the C call, but for the stream."""
     import torch
     total, Hq, d = q.shape
-    num_pages, Hkv, page_size, dk = k_cache.shape
+    shape = k_cache.shape
+    num_pages, Hkv, page_size, dc = shape
     B, max_pages = block_table.shape
-    code = _dtype_code(q)
-    _need_all(q.device, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
-              cu_seqlens=cu_seqlens, o=o, lse=lse, workspace=workspace, prefix_pages=prefix)
-    _same_type(q, k_cache=k_cache, v_cache=v_cache, o=o)
-    if lse.dtype != torch.float32:
-        raise TypeError(f"lse: element type {lse.dtype}, expected torch.float32")
-    _need_i32(block_table=(block_table, None), seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1),
-              prefix_pages=(prefix, None))
-    if dk != d or v_cache.shape != k_cache.shape:
+    code, dtype, i32 = _dtype_code(q), q.dtype, torch.int32
+    _need_all(("q", q, dtype), ("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype),
+              ("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("cu_seqlens", cu_seqlens, i32),
+              ("prefix_pages", prefix, i32), ("o", o, dtype), ("lse", lse, torch.float32),
+              ("workspace", workspace, torch.uint8))
+    _need_numel(seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1))
+    if dc != d or v_cache.shape != shape:
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
-    ws_bytes = workspace.numel() * workspace.element_size()
-    return B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages, code, ws_bytes
+    return (o.data_ptr(), lse.data_ptr(), B, total, max_new, Hq, Hkv, d, max_pages, page_size, num_pages, window, scale,
+            code, workspace.data_ptr(), workspace.numel())
 
 
 def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new: int, scale: float,
                  workspace, window: int = 0, stream=None):
-    """Attention of new rows q [total,Hq,d] to a paged cache (fa.h)."""
-    B, total, mn, Hq, Hkv, d, mp, ps, pages, code, ws_bytes = _paged_call(
-        q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace)
+    """Attention of new rows q [total,Hq,d] to a paged cache (fa.h); the
+    workspace is a uint8 tensor."""
+    rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window)
     _check("fa_fwd_paged", load().fa_fwd_paged(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(o),
-        _ptr(lse), B, total, mn, Hq, Hkv, d, mp, ps, pages, int(window), float(scale), code, _ptr(workspace),
-        ws_bytes, _stream(stream)))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        _ptr(cu_seqlens), *rest, _stream(stream)))
 
 
 def fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, seq_lens, cu_seqlens, o,
                         lse, max_new: int, scale: float, workspace, window: int = 0, stream=None):
     """fa_fwd_paged for requests that share their first prefix_len keys."""
-    B, total, mn, Hq, Hkv, d, mp, ps, pages, code, ws_bytes = _paged_call(
-        q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, workspace, prefix_pages)
-    if prefix_pages.numel() * ps < prefix_len:
-        raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages of {ps} hold fewer than {prefix_len} tokens")
+    rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window,
+                       prefix_pages)
+    if prefix_pages.numel() * k_cache.shape[2] < prefix_len:
+        raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages of {k_cache.shape[2]} hold fewer than "
+                         f"{prefix_len} tokens")
     _check("fa_fwd_paged_prefix", load().fa_fwd_paged_prefix(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_pages), int(prefix_len), _ptr(block_table),
-        _ptr(seq_lens), _ptr(cu_seqlens), _ptr(o), _ptr(lse), B, total, mn, Hq, Hkv, d, mp, ps, pages, int(window),
-        float(scale), code, _ptr(workspace), ws_bytes, _stream(stream)))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_pages.data_ptr(), prefix_len,
+        block_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), *rest, _stream(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:
