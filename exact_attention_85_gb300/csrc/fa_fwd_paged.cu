@@ -585,18 +585,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     wait_previous();
 }
 
-// Merges the parts of every row that has several.  What it waits for is two
-// rounds of loads (codes, then parts), so a warp has several in flight: R rows
-// at a time where there are many rows (R = 4, with few parts each), else U
-// parts of one row at a time, of which every of W warps takes its share.
+// Merges the parts of every row that has several.  A lane has eight columns
+// of a row (32 bytes of a part, 16 of O), so a warp works on 2 rows (d = 128)
+// or 4.  W warps share the parts of their rows, each taking every W-th: one
+// where there are many rows, with few parts each, eight where there are few
+// rows that can have many.  What it waits for is two rounds of loads, codes
+// and then parts: up to four parts are in flight, and the next rows' codes.
+// (With a row a warp, and each lane's share of the addresses and weights for
+// 4 columns only, merging 65 thousand rows of 2 parts took 25 us, bound by
+// issue.)
 struct MergeParams {
     PagedArgs a;
     PartView own, prefix;
-    int warps;  // W; 1 if R > 1
+    FastDiv heads;  // Hq
+    int warps;      // W
 };
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeRows = 4;  // R
 
 // Parts of a row by its code.  An unsound request's codes are not written, so
 // a code is held to the slots that there are.
@@ -606,14 +611,15 @@ __device__ __forceinline__ int parts_of(const PartView &v, int code) {
     return pieces < 2 || cta + pieces > v.ctas || slot_row < 0 || slot_row >= v.slot_rows ? 0 : pieces;
 }
 
-template <int D, bool BF16, int R>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const MergeParams p) {
-    constexpr int E = D / 32;          // columns of a lane
-    constexpr int U = R > 1 ? 2 : 4;   // parts of a row in flight
-    __shared__ float sm_o[kMergeWarps][D], sm_top[kMergeWarps], sm_sum[kMergeWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// PREFIX: the rows have a shared prefix' parts as well.
+template <int D, bool BF16, bool PREFIX>
+__global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const MergeParams p) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+    constexpr int U = 4;
+    __shared__ float sm_o[kMergeWarps][32][9], sm_top[kMergeWarps][32], sm_sum[kMergeWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = (lane % LPR) * 8;
     const int W = p.warps, sub = warp % W;
-    const long long rows = (long long)p.a.total * p.a.Hq;
+    const int rows = p.a.total * p.a.Hq;  // 31 bits, as the entry points see to
     wait_previous();
     // rows behind the batch's have no part
     int begin = 0, end = p.a.B;
@@ -621,119 +627,101 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Mer
         begin = p.a.cu_seqlens[0];
         end = p.a.cu_seqlens[p.a.B];
     }
-    const long long id_lo = (long long)begin * p.a.Hq, id_hi = min(rows, (long long)end * p.a.Hq);
-    const long long step = (long long)gridDim.x * (kMergeWarps / W) * R;
-    long long id0 = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * R;
-    int c_own[R], c_pre[R];
-    auto load_codes = [&](long long id) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            c_own[r] = c_pre[r] = 0;
-            if (id + r < rows) {
-                c_own[r] = p.own.code[id + r];
-                if (p.prefix.code) c_pre[r] = p.prefix.code[id + r];
-            }
-        }
+    const long long id_lo = (long long)begin * p.a.Hq, id_hi = min((long long)rows, (long long)end * p.a.Hq);
+    const long long step = (long long)gridDim.x * (kMergeWarps / W) * RPW;
+    long long id = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * RPW + lane / LPR;
+    int next_own = 0, next_pre = 0;
+    auto load_codes = [&](long long i) {
+        if (i >= rows) return;
+        next_own = p.own.code[i];
+        if (PREFIX) next_pre = p.prefix.code[i];
     };
-    load_codes(id0);
-    for (; R == 1 || id0 < rows; id0 += step) {  // once if R == 1, by every warp: there is a barrier
-    int n_own[R], n_all[R], at_own[R], at_pre[R], most = 0;
+    load_codes(id);
+    // the same number of rounds for every warp of a block: there is a barrier
+    for (long long first = (long long)blockIdx.x * (kMergeWarps / W) * RPW; first < rows; first += step, id += step) {
+        const int c_own = next_own, c_pre = next_pre;
+        load_codes(id + step);
+        int n_own = 0, n_all = 0;
+        if (id >= id_lo && id < id_hi) {
+            n_own = parts_of(p.own, c_own);
+            n_all = n_own + (PREFIX ? parts_of(p.prefix, c_pre) : 0);
+        }
+        float acc[8], top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        // the own pass' parts, then the prefix'
-        const bool mine = id0 + r >= id_lo && id0 + r < id_hi;
-        n_own[r] = mine ? parts_of(p.own, c_own[r]) : 0;
-        n_all[r] = n_own[r] + (mine && p.prefix.code ? parts_of(p.prefix, c_pre[r]) : 0);
-        most = max(most, n_all[r]);
-        at_own[r] = c_own[r];
-        at_pre[r] = c_pre[r];
-    }
-    if (R > 1) load_codes(id0 + step);  // the next rows', while these are merged
-    float acc[R][E], top[R], sum[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        top[r] = -INFINITY;
-        sum[r] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
-    }
-    for (int k0 = sub; k0 < most; k0 += W * U) {
-        float lse2[R][U], x[R][U][E];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        // where the parts of a pass begin: piece k is at one plane row, or two slots further each
+        auto locate = [&](const PartView &v, int code, const float *&lse2, const float *&o, size_t &stride) {
+            const size_t at =
+                code ? ((size_t)(code >> 9 & kMaxPieces) * 2 + 1) * v.slot_rows + (code >> 18) : (size_t)id;
+            lse2 = (code ? v.slot_lse2 : v.plane_lse2) + at;
+            o = (code ? v.slot : v.plane) + at * D + col;
+            stride = v.slot_rows;
+        };
+        const float *lse_own, *o_own, *lse_pre = nullptr, *o_pre = nullptr;
+        size_t stride_own, stride_pre = 0;
+        locate(p.own, c_own, lse_own, o_own, stride_own);
+        if (PREFIX) locate(p.prefix, c_pre, lse_pre, o_pre, stride_pre);
+        for (int k0 = sub; k0 < n_all; k0 += W * U) {
+            float lse2[U];
+            float4 x[U][2];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int k = k0 + i * W;
-                lse2[r][i] = -INFINITY;
-                if (k >= n_all[r]) continue;
-                const bool own = k < n_own[r];
-                const PartView &v = own ? p.own : p.prefix;
-                const int code = own ? at_own[r] : at_pre[r], piece = own ? k : k - n_own[r];
-                const size_t at = code ? ((size_t)((code >> 9 & kMaxPieces) + piece) * 2 + (piece == 0 ? 1 : 0)) *
-                                                 v.slot_rows + (code >> 18)
-                                       : (size_t)(id0 + r);
-                lse2[r][i] = (code ? v.slot_lse2 : v.plane_lse2)[at];
-                const float *o = (code ? v.slot : v.plane) + at * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 w = *reinterpret_cast<const float4 *>(o);
-                    x[r][i][0] = w.x; x[r][i][1] = w.y; x[r][i][2] = w.z; x[r][i][3] = w.w;
-                } else {
-                    const float2 w = *reinterpret_cast<const float2 *>(o);
-                    x[r][i][0] = w.x; x[r][i][1] = w.y;
-                }
+                lse2[i] = -INFINITY;
+                if (k >= n_all) continue;
+                const bool own = !PREFIX || k < n_own;
+                const int piece = own ? k : k - n_own;
+                // piece 0 in slot 1 of its CTA, the others in slot 0 of the next ones
+                const size_t off = piece ? (size_t)(2 * piece - 1) * (own ? stride_own : stride_pre) : 0;
+                lse2[i] = (own ? lse_own : lse_pre)[off];
+                const float4 *o = reinterpret_cast<const float4 *>((own ? o_own : o_pre) + off * D);
+                x[i][0] = o[0];
+                x[i][1] = o[1];
             }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                if (lse2[r][i] == -INFINITY) continue;
-                const float to = fmaxf(top[r], lse2[r][i]);
-                const float a = ex2_approx(top[r] - to), w = ex2_approx(lse2[r][i] - to);
-                sum[r] = sum[r] * a + w;
+                if (lse2[i] == -INFINITY) continue;
+                const float to = fmaxf(top, lse2[i]);
+                const float a = ex2_approx(top - to), w = ex2_approx(lse2[i] - to);
+                const float *v = reinterpret_cast<const float *>(x[i]);
+                sum = fmaf(sum, a, w);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[r][e] = acc[r][e] * a + w * x[r][i][e];
-                top[r] = to;
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], a, w * v[e]);
+                top = to;
             }
         }
-    }
-    if (R == 1 && W > 1) {
+        if (W > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[0][e];
-        if (lane == 0) {
-            sm_top[warp] = top[0];
-            sm_sum[warp] = sum[0];
+            for (int e = 0; e < 8; ++e) sm_o[warp][lane][e] = acc[e];
+            sm_top[warp][lane] = top;
+            sm_sum[warp][lane] = sum;
+            __syncthreads();
+            for (int k = 1; sub == 0 && k < W; ++k) {
+                const float t2 = sm_top[warp + k][lane];
+                if (t2 == -INFINITY) continue;
+                const float to = fmaxf(top, t2);
+                const float a = ex2_approx(top - to), w = ex2_approx(t2 - to);
+                sum = sum * a + w * sm_sum[warp + k][lane];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * sm_o[warp + k][lane][e];
+                top = to;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (sub) return;
-        for (int k = 1; k < W; ++k) {
-            const float t2 = sm_top[warp + k];
-            if (t2 == -INFINITY) continue;
-            const float to = fmaxf(top[0], t2);
-            const float a = ex2_approx(top[0] - to), w = ex2_approx(t2 - to);
-            sum[0] = sum[0] * a + w * sm_sum[warp + k];
+        if (n_all == 0 || sub) continue;  // final already, a row of no request, or another warp's to write
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[0][e] = acc[0][e] * a + w * sm_o[warp + k][lane * E + e];
-            top[0] = to;
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (n_all[r] == 0) continue;  // final already, or a row of no request
-        const long long id = id0 + r;
-        const float inv = sum[r] > 0.f ? 1.f / sum[r] : 0.f;
-        uint16_t *out = static_cast<uint16_t *>(p.a.o) + (size_t)id * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t *>(out + e) = BF16 ? pack_bf16x2(acc[r][e] * inv, acc[r][e + 1] * inv)
-                                                          : pack_f16x2(acc[r][e] * inv, acc[r][e + 1] * inv);
-        if (lane == 0) {
-            const int tok = (int)id / p.a.Hq, h = (int)id - tok * p.a.Hq;  // total * Hq fits 31 bits
+        for (int e = 0; e < 4; ++e)
+            w[e] = BF16 ? pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv)
+                        : pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + (size_t)id * D + col) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+        if (col == 0) {
+            const int tok = (int)id / p.heads, h = (int)id - tok * p.a.Hq;
             p.a.lse[(size_t)h * p.a.total + tok] =
-                sum[r] > 0.f ? (top[r] + log2f(sum[r])) * 0.69314718055994530942f : -INFINITY;
+                sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
         }
-    }
-    if (R == 1) return;
     }
 }
 
@@ -770,18 +758,13 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     p.a = a;
     p.own = w.own;
     p.prefix = w.prefix;
+    p.heads = fast_div(a.Hq);
     // few rows can have many parts each, many rows have few
     const long long rows = (long long)a.total * a.Hq;
-    if (rows > 4096) {
-        p.warps = 1;
-        const long long per_block = kMergeWarps * kMergeRows;
-        return launch_after(paged_merge_kernel<D, BF16, kMergeRows>, at_most((rows + per_block - 1) / per_block, 2 * kSms),
-                            32 * kMergeWarps, 0, true, st, p);
-    }
-    p.warps = rows <= 1024 ? 8 : 2;
-    const long long per_block = kMergeWarps / p.warps;
-    return launch_after(paged_merge_kernel<D, BF16, 1>, (unsigned)((rows + per_block - 1) / per_block),
-                        32 * kMergeWarps, 0, true, st, p);
+    p.warps = rows <= 1024 ? 8 : rows <= 4096 ? 2 : 1;
+    const long long per_block = kMergeWarps / p.warps * (32 / (D / 8));
+    auto kernel = w.prefix.ctas ? paged_merge_kernel<D, BF16, true> : paged_merge_kernel<D, BF16, false>;
+    return launch_after(kernel, at_most((rows + per_block - 1) / per_block, 3 * kSms), 32 * kMergeWarps, 0, true, st, p);
 }
 
 }  // namespace
