@@ -86,6 +86,7 @@ struct FewParams {
     float scale_log2;
     unsigned int *status;
     PartView part;
+    int whole;  // a unit is a whole pair, not a tile
 };
 
 // NT: 8-row groups of a pair (rows up to 8 * NT).
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (!load_request(p.a, b, r)) {
                 if (blockIdx.x == 0) record_bad_args(p.status);
             } else if (r.n > 0) {
-                mine += pair_tiles<L::TK>(p.a, r, t0);
+                const int tiles = pair_tiles<L::TK>(p.a, r, t0);
+                mine += p.whole ? 1 : tiles;
                 low = min(low, prefix_low(p.a, r));
             }
         }
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const long long units = prefix_work(p.a, prefix_rows(p.a), p.group.d, low).units();
             most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, T))));
         }
-        const int G = (int)min((long long)most, max(1ll, T / kMinUnits));
+        const int G = (int)min((long long)most, max(1ll, p.whole ? T : T / kMinUnits));
         const Ranges ranges(T, G);
         const int c = blockIdx.x;
         const long long u0 = c < G ? ranges.start(c) : T, u1 = c < G ? ranges.start(c + 1) : T;
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 int t0;
                 long long units = 0;
                 if (b + lane < B && load_request(p.a, b + lane, r) && r.n > 0)
-                    units = (long long)pair_tiles<L::TK>(p.a, r, t0) * Hkv;
+                    units = (p.whole ? 1ll : (long long)pair_tiles<L::TK>(p.a, r, t0)) * Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -199,10 +201,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 continue;
             }
             const int nt = pair_tiles<L::TK>(p.a, r, t0);
-            int hk = (int)((u - base) / nt);
+            const int per_pair = p.whole ? 1 : nt;  // units
+            int hk = (int)((u - base) / per_pair);
             for (; ok && hk < Hkv && u < u1; ++hk) {
-                const long long pair0 = base + (long long)hk * nt;
-                const int j0 = (int)(u - pair0), j1 = (int)min((long long)nt, u1 - pair0);
+                const long long pair0 = base + (long long)hk * per_pair;
+                const int j0 = (int)(u - pair0), j1 = p.whole ? nt : (int)min((long long)nt, u1 - pair0);
                 const bool whole = j0 == 0 && j1 == nt;
                 const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window) : 0;
                 const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window) : 0;
@@ -269,10 +272,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         phase ^= 1;
                     }
                 }
-                u = pair0 + j1;
+                u = pair0 + (p.whole ? 1 : j1);
             }
             if (hk == Hkv) {
-                base += (long long)nt * Hkv;
+                base += (long long)per_pair * Hkv;
                 ++b;
             }
         }
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                             to_lse2[at] = lse2;
                         else
                             p.a.lse[(size_t)h * p.a.total + t.row0 + tok] = lse2 * 0.69314718055994530942f;
-                        if (!(t.flags & kPart) || (t.flags & kSlot1))
+                        if (!p.whole && (!(t.flags & kPart) || (t.flags & kSlot1)))
                             p.part.code[out_row] = t.code ? t.code + part_code(0, 0, row) : 0;
                     }
                 }
@@ -748,6 +751,7 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.part = w.own;
+    p.whole = w.whole ? 1 : 0;
     auto kernel = a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
     return launch_after(kernel, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
 }
@@ -780,17 +784,23 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     // few-row kernel, more go to the 256-row one.
     w.few = (long long)max_new * g <= kMaxRows;
     uintptr_t at = reinterpret_cast<uintptr_t>(workspace);
-    w.own.code = take<int>(at, rows);
     if (w.few) {
         const long long tiles = (keys + (d == 128 ? 63 : 127)) / (d == 128 ? 64 : 128);
-        w.own.ctas = at_most(B * (long long)Hkv * tiles / kMinUnits, kMaxCtas);
+        // Up to 8 tiles (4 us of one CTA) are not worth a second launch.
+        w.whole = prefix_len == 0 && tiles <= 8;
+        w.own.ctas = at_most(B * (long long)Hkv * (w.whole ? 1 : tiles) / (w.whole ? 1 : kMinUnits), kMaxCtas);
         w.own.slot_rows = kMaxRows;
+        if (w.whole) {
+            w.bytes = 256;  // unused; the entry points want some
+            return w;
+        }
     } else {
         const long long most = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
         const long long blocks = row_blocks + B < most ? row_blocks + B : most;
         w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys), kSms);
         w.own.slot_rows = kWideRows;
     }
+    w.own.code = take<int>(at, rows);
     if (prefix_len > 0) {
         w.prefix.ctas = at_most(row_blocks * Hkv * ((prefix_len + kWideKeys - 1ll) / kWideKeys), kSms);
         w.prefix.slot_rows = kWideRows;
@@ -828,7 +838,7 @@ cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
     const bool front = w.prefix.ctas > 0;
     if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;
     e = w.few ? launch_paged_few(a, w, front, st) : launch_paged_wide(a, w, false, front, st);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || w.whole) return e;
     return launch_paged_merge(a, w, st);
 }
 

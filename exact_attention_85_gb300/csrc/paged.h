@@ -80,6 +80,7 @@ __host__ __device__ constexpr int part_code(int pieces, int cta, int row) { retu
 // How a call is divided among the kernels.
 struct PagedPlan {
     bool few;         // own keys by the 16-row kernel, else by the 256-row one
+    bool whole;       // its CTAs take whole pairs only: nothing to merge
     PartView own;     // ctas: of the kernel that takes the own keys
     PartView prefix;  // ctas 0: no shared prefix
     size_t bytes;     // workspace
