@@ -355,7 +355,7 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, 
     _check("fa_paged_tables", load().fa_paged_tables(
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, _ptr(free_start),
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), counts.data_ptr(), B,
-        max_pages, page_size, num_pages, num_free, slots.numel(), _stream(stream)))
+        max_pages, int(page_size), int(num_pages), num_free, slots.numel(), _stream(stream)))
 
 
 def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
@@ -400,8 +400,8 @@ def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, 
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
-    return (o.data_ptr(), lse.data_ptr(), B, total, max_new, Hq, Hkv, d, max_pages, page_size, num_pages, window, scale,
-            code, workspace.data_ptr(), workspace.numel())
+    return (o.data_ptr(), lse.data_ptr(), B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages,
+            int(window), float(scale), code, workspace.data_ptr(), workspace.numel())
 
 
 def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new: int, scale: float,
@@ -423,7 +423,7 @@ def fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, bloc
         raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages of {k_cache.shape[2]} hold fewer than "
                          f"{prefix_len} tokens")
     _check("fa_fwd_paged_prefix", load().fa_fwd_paged_prefix(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_pages.data_ptr(), prefix_len,
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_pages.data_ptr(), int(prefix_len),
         block_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), *rest, _stream(stream)))
 
 

@@ -424,7 +424,8 @@ fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return FA_ERR_UNSUPPORTED;
     // slots and (page x head) planes are counted in 32 bits
-    if ((long long)num_pages * page_size > 0x7FFFFFFFll || (long long)num_pages * Hkv > 0x7FFFFFFFll)
+    if ((long long)num_pages * page_size > 0x7FFFFFFFll || (long long)num_pages * Hkv > 0x7FFFFFFFll ||
+        (long long)Hkv * d > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }

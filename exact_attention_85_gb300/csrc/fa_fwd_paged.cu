@@ -11,11 +11,13 @@
 //
 // Few rows make the products narrow, so they are formed transposed, with the
 // keys (S^T = K Q^T) and the head's columns (O~^T += V^T P^T) as the long side
-// of the warp-level MMA and 8 query rows as its short one.  With the rows on
-// the long side the instructions, which this GPU issues at one in nine cycles
-// an SM, held an SM to 54 GB/s of cache; this way it is twice that for up to
-// 8 rows, and the kernel is bound by reading the cache (7.0 TB/s on 64
-// requests of 8-16k keys).  Everything else serves to keep copies in flight.
+// of the warp-level MMA and 8 query rows as its short one: half the
+// instructions of the other way for up to 8 rows.  Measured, reading from L2
+// (one CTA alone) and from memory (42 to 72 SMs): 49 and 54 GB/s an SM with
+// the rows on the long side, 59 and 73 this way.  All SMs together are bound
+// by reading the cache: 450 us for 64 requests of 8-16k keys, 7.15 TB/s of
+// the 6.8 that a copy reaches (it writes as well).  Everything else here
+// serves to keep copies in flight.
 //
 // Work is cut into units of one tile of keys (32 KB of K and V).  All units
 // of all (request, key/value head) pairs are numbered in order and every CTA
@@ -50,7 +52,10 @@ constexpr float kCtasPerSm = 1.64f;
 constexpr int kMaxCtas = (int)(kCtasPerSm * kSms);
 constexpr int kMaxRows = 16;   // rows of a pair
 constexpr int kStages = 3;
-constexpr int kMinUnits = 2;   // tiles a CTA takes at least
+constexpr int kMinUnits = 2;   // units a CTA takes at least
+// A pair costs its tiles and about as much as one more (Q, the merge of the
+// warps, the stores), counted when ranges are cut.
+constexpr int kPairCost = 1;
 constexpr float kMoveBy = 8.0f;  // log2 units by which a score passes the maximum before that moves
 
 enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16 };
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     launch_dependents();
     {   // tiles of the whole batch
         unsigned long long mine = 0;
-        int low = p.a.prefix_len;
+        int low = p.a.prefix_len, pairs = 0;
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
             int t0;
@@ -124,13 +129,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 if (blockIdx.x == 0) record_bad_args(p.status);
             } else if (r.n > 0) {
                 const int tiles = pair_tiles<L::TK>(p.a, r, t0);
-                mine += p.whole ? 1 : tiles;
+                mine += tiles;
+                ++pairs;
                 low = min(low, prefix_low(p.a, r));
             }
         }
         mine = warp_sum(mine);
+        pairs = __reduce_add_sync(0xffffffffu, pairs);
         low = __reduce_min_sync(0xffffffffu, low);
-        if (lane == 0) sums[warp] = PlanSum{mine, 0, low};
+        if (lane == 0) sums[warp] = PlanSum{mine, pairs, low};
     }
     __syncthreads();
 
@@ -140,18 +147,20 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
         }
-        long long T = 0;
+        long long tiles = 0, pairs = 0;
         int low = p.a.prefix_len, most = gridDim.x;
 #pragma unroll
         for (int w = 0; w <= kConsumers; ++w) {
-            T += (long long)sums[w].tiles * Hkv;
+            tiles += (long long)sums[w].tiles * Hkv;
+            pairs += (long long)sums[w].blocks * Hkv;
             low = min(low, sums[w].low);
         }
         if (p.a.prefix_len > 0) {
             // the prefix pass has some of the SMs to itself
             const long long units = prefix_work(p.a, prefix_rows(p.a), p.group.d, low).units();
-            most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, T))));
+            most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, tiles, pairs))));
         }
+        const long long T = p.whole ? pairs : tiles + pairs * kPairCost;
         const int G = (int)min((long long)most, max(1ll, p.whole ? T : T / kMinUnits));
         const Ranges ranges(T, G);
         const int c = blockIdx.x;
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 int t0;
                 long long units = 0;
                 if (b + lane < B && load_request(p.a, b + lane, r) && r.n > 0)
-                    units = (p.whole ? 1ll : (long long)pair_tiles<L::TK>(p.a, r, t0)) * Hkv;
+                    units = (p.whole ? 1ll : (long long)pair_tiles<L::TK>(p.a, r, t0) + kPairCost) * Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -201,18 +210,20 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 continue;
             }
             const int nt = pair_tiles<L::TK>(p.a, r, t0);
-            const int per_pair = p.whole ? 1 : nt;  // units
+            const int cost = p.whole ? 0 : kPairCost, per_pair = p.whole ? 1 : nt + cost;  // units
             int hk = (int)((u - base) / per_pair);
             for (; ok && hk < Hkv && u < u1; ++hk) {
-                const long long pair0 = base + (long long)hk * per_pair;
-                const int j0 = (int)(u - pair0), j1 = p.whole ? nt : (int)min((long long)nt, u1 - pair0);
+                const long long pair0 = base + (long long)hk * per_pair, tile0 = pair0 + cost;
+                const int j0 = (int)max(0ll, u - tile0), j1 = p.whole ? nt : (int)min((long long)nt, u1 - tile0);
+                u = u1 < pair0 + per_pair ? u1 : pair0 + per_pair;
+                if (j1 <= j0) continue;  // the range ends before the pair's first tile
                 const bool whole = j0 == 0 && j1 == nt;
                 const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window) : 0;
                 const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window) : 0;
                 const int hi_min = r.len - r.n + 1;
                 // a pair that goes on in the next CTA belongs to the one it began in
                 const int code =
-                    !whole && j0 == 0 ? part_code(ranges.owner(pair0 + nt - 1) - c + 1, c, 0) : 0;
+                    !whole && j0 == 0 ? part_code(ranges.owner(pair0 + per_pair - 1) - c + 1, c, 0) : 0;
                 for (int j = j0; j < j1; ++j) {
                     const int kv0 = (t0 + j) * L::TK;
                     // pages that hold no visible key are neither looked up nor read
@@ -272,7 +283,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         phase ^= 1;
                     }
                 }
-                u = pair0 + (p.whole ? 1 : j1);
             }
             if (hk == Hkv) {
                 base += (long long)per_pair * Hkv;

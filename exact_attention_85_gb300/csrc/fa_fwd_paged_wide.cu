@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!load_request(p.a, b, r) || r.n == 0) continue;
                 sum.low = min(sum.low, prefix_low(p.a, r));
                 sum.tiles += pair_tiles<kFewKeys<D>>(p.a, r, t);
+                ++sum.blocks;
             }
         } else {
             for (int b = warp * 32; b < B; b += kThreads) {
@@ -251,10 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefix_lo = min(prefix_lo, sums[w].low);
         }
         if (p.prefix) {
-            const long long few = work.tiles;
+            const WideWork few = work;
             whole.n = prefix_rows(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
-            if (p.shared) most = min(most, prefix_sms(work.units(), few));
+            if (p.shared) most = min(most, prefix_sms(work.units(), few.tiles, few.blocks));
         }
         const int cost = work.block_cost();
         const long long T = work.units();

@@ -100,22 +100,23 @@ __device__ __forceinline__ WideWork prefix_work(const PagedArgs &a, int rows, in
 // barrier; its producer then takes the sums of all.
 struct PlanSum {
     unsigned long long tiles;
-    int blocks, low;
+    int blocks, low;  // row blocks, or pairs of the few-row kernel; first key of the prefix
 };
 
 // A shared prefix' pass is bound by the tensor cores and the few-row kernel
 // by memory, so they run at the same time, each on SMs of its own: the number
 // that the prefix gets.  Times in us, as measured: a unit of the 256-row
 // kernel takes 1.72 on one SM, with 14 to start and end; a few-row tile (32 KB)
-// 4.8 ns at 6.8 TB/s, or 0.47 us on an SM (70 GB/s) where those are few, with 6
-// to start.  (256 requests of 64-2048 keys on a 16k prefix: 235 us with 36
+// 4.8 ns at 6.8 TB/s, or 0.47 us on an SM (70 GB/s) where those are few, and
+// every pair 1.1 us more there, with 6 to start.  (256 requests of 64-2048 keys on a 16k prefix: 235 us with 36
 // SMs, 217 with 46, 233 with 56, 244 with 70; one after the other 272.)  32
 // candidates, one a lane; each kernel decides for itself, so a difference
 // would cost time only.
-__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles) {
+__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles, long long few_pairs) {
     const int g = kSms * ((threadIdx.x & 31) + 1) / 33;
     const float wide = 14.f + (float)prefix_units * 1.72f / (float)g;
-    const float few = 6.f + (float)few_tiles * fmaxf(0.0048f, 0.47f / (float)(kSms - g));
+    const float few = 6.f + fmaxf(0.0048f * (float)few_tiles,
+                                  (0.47f * (float)few_tiles + 1.1f * (float)few_pairs) / (float)(kSms - g));
     // the least of the larger times, and the first to have it
     const uint32_t cost = __float_as_uint(fmaxf(wide, few)) & ~31u;
     const uint32_t best = __reduce_min_sync(0xffffffffu, cost | (threadIdx.x & 31));

@@ -76,8 +76,9 @@ ATTENTION = [
 
 
 @pytest.mark.parametrize("lens,new,Hq,Hkv,d,ps,dtype,window,prefix", ATTENTION)
-def test_attention_matches_64_bits(cuda_lib, lens, new, Hq, Hkv, d, ps, dtype, window, prefix):
-    p = Problem(lens, new, Hq, Hkv, d, ps, dtype, window, prefix, seed=d + ps)
+@pytest.mark.parametrize("cols", [1, 80])  # a wide table may hold long sequences: their keys are split
+def test_attention_matches_64_bits(cuda_lib, lens, new, Hq, Hkv, d, ps, dtype, window, prefix, cols):
+    p = Problem(lens, new, Hq, Hkv, d, ps, dtype, window, prefix, seed=d + ps, extra_cols=cols)
     want = p.reference()
     check(*_run(p), want, p.rows)
     if all(n == 1 for n in new):  # the same without offsets
@@ -97,7 +98,23 @@ def test_attention_random(cuda_lib, seed):
     window = r.choice([0, 0, r.randint(1, 300)])
     prefix = r.choice([0, 0, r.randint(1, 400)])
     p = Problem(lens, new, Hkv * group, Hkv, d, r.choice([16, 32, 64, 128, 256]), r.choice([BF, HF]), window, prefix,
-                seed=seed, pad_rows=r.choice([0, 3]), sharp=r.choice([1.0, 4.0]))
+                seed=seed, pad_rows=r.choice([0, 3]), sharp=r.choice([1.0, 4.0]), extra_cols=r.choice([1, 100]))
+    # a bound on the rows that no request reaches is as good
+    check(*_run(p, max_new=p.max_new + r.choice([0, 0, 50])), p.reference(), p.rows)
+
+
+@pytest.mark.parametrize("lens,new,Hq,Hkv,d,ps,prefix", [
+    ([3 + (7 * i) % 90 for i in range(700)], [1] * 700, 4, 2, 64, 16, 0),
+    ([3 + (7 * i) % 90 for i in range(700)], [1] * 700, 4, 1, 64, 32, 70),
+    ([20 + (11 * i) % 150 for i in range(300)], [1 + (5 * i) % 19 for i in range(300)], 8, 1, 64, 16, 0),
+    ([20 + (11 * i) % 150 for i in range(300)], [1 + (5 * i) % 19 for i in range(300)], 4, 1, 128, 16, 40),
+    ([300, 5], [2, 2], 128, 1, 64, 64, 0),       # a token fills a tile
+    ([300, 5], [3, 1], 200, 1, 64, 64, 20),      # and does not divide one
+    ([200], [3], 300, 1, 128, 32, 0),            # a token is more than a block
+    ([2500], [2300], 2, 1, 64, 16, 0),           # many blocks of one request
+])
+def test_many_requests_and_wide_groups(cuda_lib, lens, new, Hq, Hkv, d, ps, prefix):
+    p = Problem(lens, new, Hq, Hkv, d, ps, BF, 0, prefix, extra_cols=70)
     check(*_run(p), p.reference(), p.rows)
 
 
