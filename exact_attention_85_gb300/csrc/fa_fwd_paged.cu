@@ -92,6 +92,7 @@ struct FewParams {
     unsigned int *status;
     PartView part;
     int whole;  // a unit is a whole pair, not a tile
+    int after;  // runs beside the shared prefix' pass, which has waited for what came before
 };
 
 // NT: 8-row groups of a pair (rows up to 8 * NT).
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (!p.after) wait_previous();
     launch_dependents();
     {   // tiles of the whole batch
         unsigned long long mine = 0;
@@ -634,6 +636,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
     const int W = p.warps, sub = warp % W;
     const int rows = p.a.total * p.a.Hq;  // 31 bits, as the entry points see to
     wait_previous();
+    launch_dependents();
     // rows behind the batch's have no part
     int begin = 0, end = p.a.B;
     if (p.a.cu_seqlens) {
@@ -762,8 +765,9 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.status = device_status_ptr();
     p.part = w.own;
     p.whole = w.whole ? 1 : 0;
+    p.after = after ? 1 : 0;
     auto kernel = a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
-    return launch_after(kernel, w.own.ctas, kFewThreads, L::ALLOC, after, st, tk, tv, p);
+    return launch_after(kernel, w.own.ctas, kFewThreads, L::ALLOC, st, tk, tv, p);
 }
 
 template <int D, bool BF16>
@@ -778,7 +782,7 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     p.warps = rows <= 1024 ? 8 : rows <= 4096 ? 2 : 1;
     const long long per_block = kMergeWarps / p.warps * (32 / (D / 8));
     auto kernel = w.prefix.ctas ? paged_merge_kernel<D, BF16, true> : paged_merge_kernel<D, BF16, false>;
-    return launch_after(kernel, at_most((rows + per_block - 1) / per_block, 3 * kSms), 32 * kMergeWarps, 0, true, st, p);
+    return launch_after(kernel, at_most((rows + per_block - 1) / per_block, 3 * kSms), 32 * kMergeWarps, 0, st, p);
 }
 
 }  // namespace

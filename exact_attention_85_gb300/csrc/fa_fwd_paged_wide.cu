@@ -74,6 +74,7 @@ struct WideParams {
     int prefix;  // 1: rows of the whole batch against the shared prefix
     int shared;  // prefix: the few-row kernel runs at the same time
     int q_box;   // tokens of a 128-row Q tile if the group divides it (TMA), else 0
+    int after;   // runs beside the shared prefix' pass, which has waited for what came before
     int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    if (!p.after) wait_previous();
     launch_dependents();
 
     // ---------------------------------------------- the batch's units of work
@@ -829,11 +831,12 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     if (!make_tmap_rows(&tq, a.q, BF16, D, g, a.Hkv, a.total, p.q_box ? p.q_box : 1)) return cudaErrorInvalidValue;
     p.prefix = prefix ? 1 : 0;
     p.shared = prefix && w.few ? 1 : 0;
+    p.after = after ? 1 : 0;
     p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, after, st, tq, tk, tv, p);
+    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
 }
 
 }  // namespace

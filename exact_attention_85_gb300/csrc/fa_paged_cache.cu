@@ -4,6 +4,7 @@
 #include "../../include/fa.h"
 #include "host_util.h"
 #include "paged.h"
+#include "paged_dev.cuh"
 #include "status.cuh"
 
 namespace fa {
@@ -55,6 +56,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     const int per = (B + kTabThreads - 1) / kTabThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
 
+    wait_previous();
+    launch_dependents();
     const int start_in = p.a.free_start ? *p.a.free_start : 0;
     const bool start_ok = start_in >= 0 && start_in <= p.a.num_free;
     const int start = start_ok ? start_in : 0;
@@ -185,35 +188,53 @@ constexpr int kAppThreads = 256;
 
 struct AppendParams {
     AppendArgs a;
-    int chunks;          // 16-byte pieces of one row: Hkv * d / 8
+    FastDiv chunks;    // 16-byte pieces of one row: Hkv * d / 8
+    FastDiv d_chunks;  // of one head: d / 8
     int rows_per_block;
-    int shift, d_chunks;  // log2(page_size), d / 8
+    int shift;  // log2(page_size)
     unsigned int *status;
 };
 
-// One 16-byte piece of k and of v per thread and step: a copy whose
-// destination row comes from slots[].  [total][Hkv][d] -> [page][Hkv][ps][d]:
-// a (row, head) piece of d values is contiguous on both sides.
+// 16-byte pieces of k and v; the destination row comes from slots[].
+// [total][Hkv][d] -> [page][Hkv][ps][d]: a (row, head) piece of d values is
+// contiguous on both sides.  A copy: bound by memory, so every thread has four
+// pieces of k and of v in flight at a time.
+constexpr int kAppUnroll = 4;
+
 __global__ void __launch_bounds__(kAppThreads) paged_append_kernel(const AppendParams p) {
     const int row0 = blockIdx.x * p.rows_per_block;
     const int rows = min(p.rows_per_block, p.a.total - row0);
-    const uint4 *k = static_cast<const uint4 *>(p.a.k) + (size_t)row0 * p.chunks;
-    const uint4 *v = static_cast<const uint4 *>(p.a.v) + (size_t)row0 * p.chunks;
+    const uint4 *k = static_cast<const uint4 *>(p.a.k) + (size_t)row0 * p.chunks.d;
+    const uint4 *v = static_cast<const uint4 *>(p.a.v) + (size_t)row0 * p.chunks.d;
     uint4 *kc = static_cast<uint4 *>(p.a.k_cache), *vc = static_cast<uint4 *>(p.a.v_cache);
-    const int limit = p.a.num_pages << p.shift;
-    for (int i = threadIdx.x; i < rows * p.chunks; i += kAppThreads) {
-        const int row = i / p.chunks;
-        const int rest = i - row * p.chunks;
-        const int slot = p.a.slots[row0 + row];
-        if (slot < 0 || slot >= limit) {
+    const int limit = p.a.num_pages << p.shift, pieces = rows * p.chunks.d;
+    wait_previous();
+    launch_dependents();
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAppThreads * kAppUnroll) {
+        size_t to[kAppUnroll];
+        uint4 x[kAppUnroll], y[kAppUnroll];
+        bool live[kAppUnroll];
+#pragma unroll
+        for (int j = 0; j < kAppUnroll; ++j) {
+            const int i = i0 + j * kAppThreads;
+            live[j] = i < pieces;
+            if (!live[j]) continue;
+            const int row = i / p.chunks, rest = i - row * p.chunks.d;
+            const int slot = p.a.slots[row0 + row];
+            const int h = rest / p.d_chunks, c = rest - h * p.d_chunks.d;
+            x[j] = __ldcs(k + i);
+            y[j] = __ldcs(v + i);
+            live[j] = slot >= 0 && slot < limit;
             if (slot >= limit) record_bad_args(p.status);
-            continue;
+            to[j] = ((((size_t)(slot >> p.shift) * p.a.Hkv + h) << p.shift) + (slot & ((1 << p.shift) - 1))) *
+                        p.d_chunks.d + c;
         }
-        const int h = rest / p.d_chunks, c = rest - h * p.d_chunks;
-        const size_t to =
-            ((((size_t)(slot >> p.shift) * p.a.Hkv + h) << p.shift) + (slot & ((1 << p.shift) - 1))) * p.d_chunks + c;
-        kc[to] = k[i];
-        vc[to] = v[i];
+#pragma unroll
+        for (int j = 0; j < kAppUnroll; ++j) {
+            if (!live[j]) continue;
+            kc[to[j]] = x[j];
+            vc[to[j]] = y[j];
+        }
     }
 }
 
@@ -228,28 +249,21 @@ int log2_of(int x) {
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     TablesParams p{a, log2_of(a.page_size), device_status_ptr()};
     const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int);
-    cudaError_t e;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
-            cudaSuccess)
-        return e;
     const long long per_block = kTabThreads * kRowsPerThread;
     const long long blocks = (a.total + per_block - 1) / per_block;
-    paged_tables_kernel<<<(unsigned)(blocks < 304 ? blocks : 304), kTabThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(paged_tables_kernel, (unsigned)(blocks < 2 * kSms ? blocks : 2 * kSms), kTabThreads, smem, st, p);
 }
 
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
     AppendParams p;
     p.a = a;
-    p.d_chunks = a.d / 8;
-    p.chunks = a.Hkv * p.d_chunks;
-    p.rows_per_block = p.chunks >= 1024 ? 1 : 1024 / p.chunks;
+    p.d_chunks = fast_div(a.d / 8);
+    p.chunks = fast_div(a.Hkv * (a.d / 8));
+    p.rows_per_block = p.chunks.d >= 1024 ? 1 : 1024 / p.chunks.d;
     p.shift = log2_of(a.page_size);
     p.status = device_status_ptr();
     const unsigned blocks = (unsigned)((a.total + (long long)p.rows_per_block - 1) / p.rows_per_block);
-    paged_append_kernel<<<blocks, kAppThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_after(paged_append_kernel, blocks, kAppThreads, 0, st, p);
 }
 
 }  // namespace fa

@@ -56,12 +56,14 @@ bool make_tmap_pages_4d(CUtensorMap *map, const void *base, bool bf16, int d, in
 // (column, row of the group, group, token).  group * tokens at most 256.
 bool make_tmap_rows(CUtensorMap *map, const void *base, bool bf16, int d, int group, int heads, int total, int tokens);
 
-// Launches `kernel` with `smem` bytes of dynamic shared memory.  `after`: it
-// may start before the stream's previous kernel has finished, once all of
-// that one's CTAs have asked for it (programmatic dependent launch).
+// Launches `kernel` with `smem` bytes of dynamic shared memory, allowed to
+// start before the stream's previous kernel has finished (programmatic
+// dependent launch): at its end, or once all its CTAs have said so.  The
+// kernel waits for it (griddepcontrol.wait) before it touches memory, so that
+// only launch and set-up overlap.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, bool after,
-                         cudaStream_t st, const A &...args) {
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                         const A &...args) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -75,7 +77,7 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = after ? 1 : 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

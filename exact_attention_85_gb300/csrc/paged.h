@@ -89,8 +89,7 @@ struct PagedPlan {
 PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
                      int prefix_len, void *workspace);
 
-// The kernels of a forward call.  `after` marks a launch that may start while
-// the call's previous one still runs (programmatic dependent launch).
+// The kernels of a forward call.  `after`: beside the shared prefix' pass.
 cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st);
 cudaError_t launch_paged_wide(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st);
