@@ -29,9 +29,11 @@
 // shared prefix, everything does, and is merged with the prefix' results).
 //   warps 0-3  each a quarter of every tile's keys, all rows; their four
 //              results are merged through the last tile's buffer
-//   warp 4     producer: plans the CTA's range, reads block-table entries,
-//              starts one TMA copy per page and one small copy of Q per pair,
-//              and describes each tile to the others
+//   warps 4, 5 producers of K and of V: each plans the CTA's range, reads the
+//              block-table entries and starts one TMA copy per page (the 16
+//              of a tile of 16-key pages at d = 64 took one warp 1.06 us, two
+//              0.87); the first also copies Q, and describes each tile to the
+//              others
 #include "../../include/fa.h"
 #include "host_util.h"
 #include "mma_sync.cuh"
@@ -44,7 +46,8 @@ namespace fa {
 namespace {
 
 constexpr int kConsumers = 4;  // warps
-constexpr int kFewThreads = 32 * (kConsumers + 1);
+constexpr int kFewWarps = kConsumers + 2;  // and two producers
+constexpr int kFewThreads = 32 * kFewWarps;
 // Two CTAs fit an SM, but with 96 KB of copies in flight each, fewer do
 // better: 64 requests of 8-16k keys took 470 us on 304 CTAs, 460 on 260, 458
 // on 228, 473 on 190; 32 requests of 333-7506 keys 89.4, 86.3, 88.8, 92.2.
@@ -79,7 +82,7 @@ struct FewLayout {
     static constexpr int OFF_BAR = OFF_INFO + kStages * (int)sizeof(TileInfo);
     static constexpr int OFF_ML = OFF_BAR + 2 * kStages * 8;           // [3][4 warps][16]
     static constexpr int OFF_MISC = OFF_ML + 3 * kConsumers * 16 * 4;  // abort flag, the warps' sums
-    static constexpr int BYTES = OFF_MISC + 16 + (kConsumers + 1) * (int)sizeof(PlanSum);
+    static constexpr int BYTES = OFF_MISC + 16 + kFewWarps * (int)sizeof(PlanSum);
     static constexpr int ALLOC = BYTES + 1024;
     static_assert(2 * (ALLOC + 1024) <= 228 * 1024, "two CTAs per SM");
     static_assert(kConsumers * kMaxRows * D * 4 <= 2 * TILE, "the merge fits one stage");
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 33);  // the tile's bytes, and every producer lane's share of Q
+            mbar_init(&full[s], 34);  // the bytes of K, of V, and 32 lanes' shares of Q
             mbar_init(&empty[s], kConsumers);
         }
         *abort_flag = 0;
@@ -143,16 +146,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     __syncthreads();
 
-    if (warp == kConsumers) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
-        }
+    if (warp >= kConsumers) {
+        // ----------------------------------------------------------- producers
+        const bool first_one = warp == kConsumers;
+        const CUtensorMap *tm = first_one ? &tm_k : &tm_v;
+        if (lane == 0) prefetch_tmap(tm);
         long long tiles = 0, pairs = 0;
         int low = p.a.prefix_len, most = gridDim.x;
 #pragma unroll
-        for (int w = 0; w <= kConsumers; ++w) {
+        for (int w = 0; w < kFewWarps; ++w) {
             tiles += (long long)sums[w].tiles * Hkv;
             pairs += (long long)sums[w].blocks * Hkv;
             low = min(low, sums[w].low);
@@ -193,13 +195,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 base += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        // this lane's box: K or V of a page of the tile, its 64-column halves
-        // one behind the other (128-byte swizzled rows)
+        // this lane's box: a page of the tile, its 64-column halves one behind
+        // the other (128-byte swizzled rows)
         const int page_keys = min(1 << p.a.shift, L::TK);
         const int box_bytes = page_keys * D * 2;
         const uint64_t once = l2_evict_first();  // every key is read by one CTA only
-        const bool boxed = lane < 2 * (L::TK / page_keys);
-        const int tensor = lane & 1, sub = lane >> 1;
+        const int sub = lane;
+        const bool boxed = sub < L::TK / page_keys;
+        uint8_t *const tiles_at = smem + (first_one ? 0 : L::TILE);
         int st = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
+                    if (lane == 0 && first_one) {
                         TileInfo t;
                         t.row0 = r.row0;
                         t.n = r.n;
@@ -257,13 +260,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                   (kv0 < lo_max || kv0 + L::TK > hi_min ? kMask : 0) | (whole ? 0 : kPart) |
                                   (j0 == 0 ? kSlot1 : 0);
                         info[st] = t;
-                        mbar_arrive_expect_tx(&full[st], boxes * box_bytes);
                     }
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * box_bytes);
                     __syncwarp();
                     if (live)
-                        tma_load_4d_hint(smem + (st * 2 + tensor) * L::TILE + sub * box_bytes, tensor ? &tm_v : &tm_k,
-                                         &full[st], 0, key0 & ((1 << p.a.shift) - 1), 0, page * Hkv + hk, once);
-                    if (j == j0) {
+                        tma_load_4d_hint(tiles_at + st * 2 * L::TILE + sub * box_bytes, tm, &full[st], 0,
+                                         key0 & ((1 << p.a.shift) - 1), 0, page * Hkv + hk, once);
+                    if (first_one && j == j0) {
                         // Q rows of the pair: row r is head r % g of token r / g
                         constexpr int CH = D / 8;  // 16-byte pieces of a row
                         const int rows = r.n * p.group.d;
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                         src);
                         }
                     }
-                    cp_async_arrive(&full[st]);
+                    if (first_one) cp_async_arrive(&full[st]);
                     ++issued;
                     if (++st == kStages) {
                         st = 0;
@@ -300,12 +303,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             // a tile that ends the stream
             const bool got = !ok || issued < kStages || mbar_wait(&empty[st], phase ^ 1, abort_flag, p.status, 22);
             if (ok && got) {
-                info[st].flags = -1;
+                if (first_one) info[st].flags = -1;
                 mbar_arrive_expect_tx(&full[st], 0);
             }
         }
         __syncwarp();
-        if (ok) cp_async_arrive(&full[st]);
+        if (ok && first_one) cp_async_arrive(&full[st]);
     } else {
         // ----------------------------------------------------------- consumers
         const int quad = lane & 3, rw = lane >> 2;  // this lane's keys rw, rw + 8; rows 2 quad, + 1
