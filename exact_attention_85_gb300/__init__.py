@@ -193,7 +193,8 @@ def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_
     if workspace is None:
         n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2],
                                               prefix_len)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     return o, lse, workspace, max_new
 
 

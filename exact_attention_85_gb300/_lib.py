@@ -390,24 +390,40 @@ def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, 
     shape = k_cache.shape
     num_pages, Hkv, page_size, dc = shape
     B, max_pages = block_table.shape
-    code, dtype, i32 = _dtype_code(q), q.dtype, torch.int32
-    _need_all(("q", q, dtype), ("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype),
-              ("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("cu_seqlens", cu_seqlens, i32),
-              ("prefix_pages", prefix, i32), ("o", o, dtype), ("lse", lse, torch.float32),
-              ("workspace", workspace, torch.uint8))
-    _need_numel(seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1))
+    code, dtype, i32, dev = _dtype_code(q), q.dtype, torch.int32, q.get_device()
+    # the checks of _need_all and _need_numel in one expression: a call is a
+    # few microseconds of kernel at times, and this is part of every one
+    if not (dev >= 0 and dev == torch.cuda.current_device() and q.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.dtype == dtype and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
+            and block_table.get_device() == dev and block_table.dtype == i32 and block_table.is_contiguous()
+            and seq_lens.get_device() == dev and seq_lens.dtype == i32 and seq_lens.is_contiguous()
+            and o.get_device() == dev and o.dtype == dtype and o.is_contiguous()
+            and lse.get_device() == dev and lse.dtype == torch.float32 and lse.is_contiguous()
+            and seq_lens.numel() == B
+            and (cu_seqlens is None or (cu_seqlens.get_device() == dev and cu_seqlens.dtype == i32
+                                        and cu_seqlens.is_contiguous() and cu_seqlens.numel() == B + 1))
+            and (prefix is None or (prefix.get_device() == dev and prefix.dtype == i32 and prefix.is_contiguous()))
+            and (workspace is None or (workspace.get_device() == dev and workspace.dtype == torch.uint8
+                                       and workspace.is_contiguous()))):
+        _need_all(("q", q, dtype), ("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype),
+                  ("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("cu_seqlens", cu_seqlens, i32),
+                  ("prefix_pages", prefix, i32), ("o", o, dtype), ("lse", lse, torch.float32),
+                  ("workspace", workspace, torch.uint8))
+        _need_numel(seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1))
     if dc != d or v_cache.shape != shape:
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
     return (o.data_ptr(), lse.data_ptr(), B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages,
-            int(window), float(scale), code, workspace.data_ptr(), workspace.numel())
+            int(window), float(scale), code, None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel())
 
 
 def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new: int, scale: float,
                  workspace, window: int = 0, stream=None):
     """Attention of new rows q [total,Hq,d] to a paged cache (fa.h); the
-    workspace is a uint8 tensor."""
+    workspace is a uint8 tensor, or None where its size is 0."""
     rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window)
     _check("fa_fwd_paged", load().fa_fwd_paged(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),

@@ -439,7 +439,8 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
         if (!aligned16(p)) return FA_ERR_INVALID_ARG;
     if (!aligned4(a.block_table) || !aligned4(a.seq_lens) || !aligned4(a.cu_seqlens) || !aligned4(a.prefix_pages))
         return FA_ERR_INVALID_ARG;
-    if (a.B < 1 || a.total < 1 || a.max_new < 1 || a.Hq < 1 || a.max_pages < 1 || a.window < 0) return FA_ERR_INVALID_ARG;
+    if (a.B < 1 || a.total < 1 || a.max_new < 1 || a.Hq < 1 || a.max_pages < 1 || a.window < 0)
+        return FA_ERR_INVALID_ARG;
     if (a.Hkv < 1 || a.Hq % a.Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return FA_ERR_INVALID_ARG;
     if (!a.cu_seqlens && (a.max_new != 1 || a.total < a.B)) return FA_ERR_INVALID_ARG;
@@ -449,10 +450,11 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
     if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
         (long long)a.B * a.Hq > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
-    const size_t need = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size, a.prefix_len,
-                                       nullptr)
-                            .bytes;
-    if (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u))
+    const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
+                                           a.prefix_len, nullptr);
+    const size_t need = w.bytes;
+    if (need > 0 &&
+        (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)))
         return FA_ERR_WORKSPACE;
     return FA_OK;
 }

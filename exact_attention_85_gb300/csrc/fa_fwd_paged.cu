@@ -807,10 +807,7 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         w.whole = prefix_len == 0 && tiles <= 8;
         w.own.ctas = at_most(B * (long long)Hkv * (w.whole ? 1 : tiles) / (w.whole ? 1 : kMinUnits), kMaxCtas);
         w.own.slot_rows = kMaxRows;
-        if (w.whole) {
-            w.bytes = 256;  // unused; the entry points want some
-            return w;
-        }
+        if (w.whole) return w;  // no workspace
     } else {
         const long long most = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
         const long long blocks = row_blocks + B < most ? row_blocks + B : most;
@@ -836,7 +833,8 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
 }
 
 cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st) {
-    if (a.d == 128) return a.bf16 ? launch_few_t<128, true>(a, w, after, st) : launch_few_t<128, false>(a, w, after, st);
+    if (a.d == 128)
+        return a.bf16 ? launch_few_t<128, true>(a, w, after, st) : launch_few_t<128, false>(a, w, after, st);
     return a.bf16 ? launch_few_t<64, true>(a, w, after, st) : launch_few_t<64, false>(a, w, after, st);
 }
 

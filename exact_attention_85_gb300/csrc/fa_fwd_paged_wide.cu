@@ -432,92 +432,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------------- MMA issuer
         if (lane == 0) {
-        constexpr uint32_t fmt = BF16 ? 1u : 0u;
-        constexpr uint32_t idesc_s = make_idesc(kBM, kBN, fmt, false, false);
-        constexpr uint32_t idesc_pv = make_idesc(kBM, D, fmt, false, true);
-        const uint64_t q_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
-        const uint64_t k_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
-        const uint64_t v_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_V), L::BOX, 1024);
-        // u counts K/V tiles over all segments, first: a segment's first tile
-        auto issue_s = [&](int x, int u) {
-            const uint64_t q_desc = sdesc_advance(q_desc0, x * L::TILE);
-            const uint64_t k_desc = sdesc_advance(k_desc0, (u % L::KS) * L::TILE);
+            constexpr uint32_t fmt = BF16 ? 1u : 0u;
+            constexpr uint32_t idesc_s = make_idesc(kBM, kBN, fmt, false, false);
+            constexpr uint32_t idesc_pv = make_idesc(kBM, D, fmt, false, true);
+            const uint64_t q_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_Q), 16, 1024);
+            const uint64_t k_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_K), 16, 1024);
+            const uint64_t v_desc0 = make_sdesc_sw128(smem_u32(smem + L::OFF_V), L::BOX, 1024);
+            // u counts K/V tiles over all segments, first: a segment's first tile
+            auto issue_s = [&](int x, int u) {
+                const uint64_t q_desc = sdesc_advance(q_desc0, x * L::TILE);
+                const uint64_t k_desc = sdesc_advance(k_desc0, (u % L::KS) * L::TILE);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
-                mma_f16_ss(tmem + kColS + x * 128, sdesc_advance(q_desc, off), sdesc_advance(k_desc, off), idesc_s,
-                           kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&s_full[x]);
-        };
-        auto issue_pv = [&](int x, int u, bool first) {
-            const uint64_t v_desc = sdesc_advance(v_desc0, (u % L::VS) * L::TILE);
-            const uint32_t p_col = tmem + kColS + x * 128;
-#pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-                mma_f16_ts(tmem + kColO + x * 128, p_col + kk * 8, sdesc_advance(v_desc, kk * 2048), idesc_pv,
-                           (!first || kk > 0) ? 1u : 0u);
-        };
-        auto wait = [&](uint64_t *bar, int parity, int site) -> bool {
-            const bool got = mbar_wait(bar, parity, abort_flag, p.status, site);
-            tc_fence_after();
-            return got;
-        };
-        bool ok = true;
-        int u = 0, step_b = 0;  // tiles of all segments; of those that have a tile B
-        uint32_t cleans = 0;    // a bit per V stage: parity of its clears
-        for (int g = 0; ok; ++g) {
-            if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
-            const int nj = segs[g & 1].nj, kv0 = segs[g & 1].j0 * kBN;
-            const int key_lo = segs[g & 1].key_lo, key_hi = segs[g & 1].key_hi;
-            const bool two = segs[g & 1].n * p.group.d - segs[g & 1].r0 > kBM;
-            mbar_arrive(&seg_empty[g & 1]);
-            if (nj < 0) break;
-            if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
-            issue_s(0, u);
-            if (two) issue_s(1, u);
-            mma_commit(&k_empty[u % L::KS]);
-            if (nj == 1) mma_commit(q_empty);
-            // V of the segment's first tile
-            if (!(ok = wait(&v_full[u % L::VS], (u / L::VS) & 1, 35))) break;
-            for (int i = 0; i < nj; ++i, ++u) {
-                const int vs = u % L::VS, kn = (u + 1) % L::KS, vn = (u + 1) % L::VS;
-                const bool last = i + 1 == nj;
-                if (hides(kv0 + i * kBN, key_lo, key_hi)) {
-                    if (!(ok = wait(&v_clean[vs], cleans >> vs & 1, 42))) break;
-                    cleans ^= 1u << vs;
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * L::BOX + (kk & 3) * 32;
+                    mma_f16_ss(tmem + kColS + x * 128, sdesc_advance(q_desc, off), sdesc_advance(k_desc, off), idesc_s,
+                               kk > 0 ? 1u : 0u);
                 }
-                if (!(ok = wait(&p_full[0], u & 1, 36))) break;
-                issue_pv(0, u, i == 0);
-                if (last) {
-                    mma_commit(&o_final[0]);
-                } else {
-                    if (!(ok = wait(&k_full[kn], ((u + 1) / L::KS) & 1, 34))) break;
-                    issue_s(0, u + 1);
-                    if (!two) {
+                mma_commit(&s_full[x]);
+            };
+            auto issue_pv = [&](int x, int u, bool first) {
+                const uint64_t v_desc = sdesc_advance(v_desc0, (u % L::VS) * L::TILE);
+                const uint32_t p_col = tmem + kColS + x * 128;
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_f16_ts(tmem + kColO + x * 128, p_col + kk * 8, sdesc_advance(v_desc, kk * 2048), idesc_pv,
+                               (!first || kk > 0) ? 1u : 0u);
+            };
+            auto wait = [&](uint64_t *bar, int parity, int site) -> bool {
+                const bool got = mbar_wait(bar, parity, abort_flag, p.status, site);
+                tc_fence_after();
+                return got;
+            };
+            bool ok = true;
+            int u = 0, step_b = 0;  // tiles of all segments; of those that have a tile B
+            uint32_t cleans = 0;    // a bit per V stage: parity of its clears
+            for (int g = 0; ok; ++g) {
+                if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
+                const int nj = segs[g & 1].nj, kv0 = segs[g & 1].j0 * kBN;
+                const int key_lo = segs[g & 1].key_lo, key_hi = segs[g & 1].key_hi;
+                const bool two = segs[g & 1].n * p.group.d - segs[g & 1].r0 > kBM;
+                mbar_arrive(&seg_empty[g & 1]);
+                if (nj < 0) break;
+                if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
+                issue_s(0, u);
+                if (two) issue_s(1, u);
+                mma_commit(&k_empty[u % L::KS]);
+                if (nj == 1) mma_commit(q_empty);
+                // V of the segment's first tile
+                if (!(ok = wait(&v_full[u % L::VS], (u / L::VS) & 1, 35))) break;
+                for (int i = 0; i < nj; ++i, ++u) {
+                    const int vs = u % L::VS, kn = (u + 1) % L::KS, vn = (u + 1) % L::VS;
+                    const bool last = i + 1 == nj;
+                    if (hides(kv0 + i * kBN, key_lo, key_hi)) {
+                        if (!(ok = wait(&v_clean[vs], cleans >> vs & 1, 42))) break;
+                        cleans ^= 1u << vs;
+                    }
+                    if (!(ok = wait(&p_full[0], u & 1, 36))) break;
+                    issue_pv(0, u, i == 0);
+                    if (last) {
+                        mma_commit(&o_final[0]);
+                    } else {
+                        if (!(ok = wait(&k_full[kn], ((u + 1) / L::KS) & 1, 34))) break;
+                        issue_s(0, u + 1);
+                        if (!two) {
+                            mma_commit(&k_empty[kn]);
+                            if (i + 2 == nj) mma_commit(q_empty);
+                        }
+                    }
+                    if (two) {
+                        if (!(ok = wait(&p_full[1], step_b & 1, 36))) break;
+                        ++step_b;
+                        issue_pv(1, u, i == 0);
+                        if (last) mma_commit(&o_final[1]);
+                    }
+                    mma_commit(&v_empty[vs]);
+                    if (last) continue;
+                    if (!(ok = wait(&v_full[vn], ((u + 1) / L::VS) & 1, 35))) break;
+                    if (two) {
+                        issue_s(1, u + 1);
                         mma_commit(&k_empty[kn]);
                         if (i + 2 == nj) mma_commit(q_empty);
                     }
                 }
-                if (two) {
-                    if (!(ok = wait(&p_full[1], step_b & 1, 36))) break;
-                    ++step_b;
-                    issue_pv(1, u, i == 0);
-                    if (last) mma_commit(&o_final[1]);
-                }
-                mma_commit(&v_empty[vs]);
-                if (last) continue;
-                if (!(ok = wait(&v_full[vn], ((u + 1) / L::VS) & 1, 35))) break;
-                if (two) {
-                    issue_s(1, u + 1);
-                    mma_commit(&k_empty[kn]);
-                    if (i + 2 == nj) mma_commit(q_empty);
-                }
             }
-        }
-        // every MMA issued above has completed once `drain` flips
-        mma_commit(drain);
-        mbar_wait_drain(drain, 0, 100000000ull);
+            // every MMA issued above has completed once `drain` flips
+            mma_commit(drain);
+            mbar_wait_drain(drain, 0, 100000000ull);
         }
         __syncwarp();
     } else if (warp >= kMmaWarp + 1) {
@@ -555,23 +555,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(q_full);
                 }
             } else {
-            const int ch = id % CH;
-            const int t0 = sg.r0 / p.group, h0 = sg.r0 - t0 * p.group.d;
-            const uint4 *src =
-                static_cast<const uint4 *>(p.a.q) + ((size_t)(sg.row0 + t0) * p.a.Hq + sg.hk * p.group.d) * CH + ch;
+                const int ch = id % CH;
+                const int t0 = sg.r0 / p.group, h0 = sg.r0 - t0 * p.group.d;
+                const uint4 *src =
+                    static_cast<const uint4 *>(p.a.q) + ((size_t)(sg.row0 + t0) * p.a.Hq + sg.hk * p.group.d) * CH + ch;
 #pragma unroll 8
-            for (int r = id / CH; r < kRows; r += STEP) {
-                uint8_t *dst = smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX + (r & 127) * 128 +
-                               (((ch & 7) ^ (r & 7)) << 4);
-                const int t = (h0 + r) / p.group, h = h0 + r - t * p.group.d;
-                if (r < rows)
-                    cp_async_16(smem_u32(dst), src + ((size_t)t * p.a.Hq + h) * CH);
-                else
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
-            }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
+                for (int r = id / CH; r < kRows; r += STEP) {
+                    uint8_t *dst = smem + L::OFF_Q + (r >> 7) * L::TILE + (ch >> 3) * L::BOX + (r & 127) * 128 +
+                                   (((ch & 7) ^ (r & 7)) << 4);
+                    const int t = (h0 + r) / p.group, h = h0 + r - t * p.group.d;
+                    if (r < rows)
+                        cp_async_16(smem_u32(dst), src + ((size_t)t * p.a.Hq + h) * CH);
+                    else
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+                }
+                cp_async_wait_all();
+                fence_proxy_async_smem();
+                mbar_arrive(q_full);
             }
             // V rows that no row of the block sees may hold anything (the rest
             // of a page, a buffer that was not filled), and 0 * NaN is NaN:
@@ -646,100 +646,100 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l_exact = 0.0f;  // sum of the unrounded P: gives L
             const int hi_w = __reduce_min_sync(0xffffffffu, hi), lo_w = __reduce_max_sync(0xffffffffu, lo);
             for (int u = 0; ok && active && u < nj; ++u, ++step) {
-            const bool got_s = mbar_wait(&s_full[x], step & 1, abort_flag, p.status, 37);
-            if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
-            tc_fence_after();
-            uint32_t s[128];
-            const uint32_t s_addr = lane_base + col_s;
-            tmem_ld_x32(s_addr + 0, s + 0);
-            tmem_ld_x32(s_addr + 32, s + 32);
-            tmem_ld_x32(s_addr + 64, s + 64);
-            tmem_ld_x32(s_addr + 96, s + 96);
-            tmem_ld_wait_x32(s + 0);
-            tmem_ld_wait_x32(s + 32);
-            tmem_ld_wait_x32(s + 64);
-            tmem_ld_wait_x32(s + 96);
-            const int kv0 = (j0 + u) * kBN;
-            if (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo)) {  // uniform in the warp
-                const int top = min(hi, key_hi), low = max(lo, key_lo);
+                const bool got_s = mbar_wait(&s_full[x], step & 1, abort_flag, p.status, 37);
+                if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t s[128];
+                const uint32_t s_addr = lane_base + col_s;
+                tmem_ld_x32(s_addr + 0, s + 0);
+                tmem_ld_x32(s_addr + 32, s + 32);
+                tmem_ld_x32(s_addr + 64, s + 64);
+                tmem_ld_x32(s_addr + 96, s + 96);
+                tmem_ld_wait_x32(s + 0);
+                tmem_ld_wait_x32(s + 32);
+                tmem_ld_wait_x32(s + 64);
+                tmem_ld_wait_x32(s + 96);
+                const int kv0 = (j0 + u) * kBN;
+                if (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo)) {  // uniform in the warp
+                    const int top = min(hi, key_hi), low = max(lo, key_lo);
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (kv0 + c >= top || kv0 + c < low) s[c] = __float_as_uint(-INFINITY);
-            }
-            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                    for (int c = 0; c < 128; ++c)
+                        if (kv0 + c >= top || kv0 + c < low) s[c] = __float_as_uint(-INFINITY);
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-                mx0 = fmax3(mx0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-                mx2 = fmax3(mx2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-                mx3 = fmax3(mx3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-            }
-            const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-            float alpha = 1.0f;
-            bool rescale = false;
-            if (mx > m_ref + kRescaleThreshold) {
-                alpha = ex2_approx(m_ref - mx);  // 0 on the first visible tile
-                l_sum *= alpha;
-                l_exact *= alpha;
-                m_ref = mx;
-                rescale = true;
-            }
-            __syncwarp();
-            const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;  // nothing seen yet: P = 0
-            const float2 neg_m = make_float2(-m_use, -m_use);
-            const float2 sl2x2 = make_float2(sl2, sl2);
-            float2 lr01 = make_float2(0.f, 0.f), lr23 = lr01, le01 = lr01, le23 = lr01;
-            constexpr int CH = 32;
+                for (int c = 0; c < 128; c += 8) {
+                    mx0 = fmax3(mx0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                    mx1 = fmax3(mx1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+                    mx2 = fmax3(mx2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+                    mx3 = fmax3(mx3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+                }
+                const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+                float alpha = 1.0f;
+                bool rescale = false;
+                if (mx > m_ref + kRescaleThreshold) {
+                    alpha = ex2_approx(m_ref - mx);  // 0 on the first visible tile
+                    l_sum *= alpha;
+                    l_exact *= alpha;
+                    m_ref = mx;
+                    rescale = true;
+                }
+                __syncwarp();
+                const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;  // nothing seen yet: P = 0
+                const float2 neg_m = make_float2(-m_use, -m_use);
+                const float2 sl2x2 = make_float2(sl2, sl2);
+                float2 lr01 = make_float2(0.f, 0.f), lr23 = lr01, le01 = lr01, le23 = lr01;
+                constexpr int CH = 32;
 #pragma unroll
-            for (int hh = 0; hh < 128 / CH; ++hh) {
-                uint32_t pk[CH / 2];
+                for (int hh = 0; hh < 128 / CH; ++hh) {
+                    uint32_t pk[CH / 2];
 #pragma unroll
-                for (int c = CH * hh; c < CH * hh + CH; c += 4) {
-                    const float2 x01 =
-                        ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2x2, neg_m);
-                    const float2 x23 =
-                        ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2x2, neg_m);
-                    const float p0 = ex2_approx(x01.x), p1 = ex2_approx(x01.y);
-                    const float p2 = ex2_approx(x23.x), p3 = ex2_approx(x23.y);
-                    const int k = (c - CH * hh) / 2;
-                    if constexpr (BF16) {
-                        pk[k] = pack_bf16x2(p0, p1);
-                        pk[k + 1] = pack_bf16x2(p2, p3);
-                        lr01 = add_bf16x2_f32x2(pk[k], lr01);
-                        lr23 = add_bf16x2_f32x2(pk[k + 1], lr23);
-                    } else {
-                        pk[k] = pack_f16x2(p0, p1);
-                        pk[k + 1] = pack_f16x2(p2, p3);
-                        lr01 = fadd2(lr01, unpack2<BF16>(pk[k]));
-                        lr23 = fadd2(lr23, unpack2<BF16>(pk[k + 1]));
+                    for (int c = CH * hh; c < CH * hh + CH; c += 4) {
+                        const float2 x01 =
+                            ffma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2x2, neg_m);
+                        const float2 x23 =
+                            ffma2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2x2, neg_m);
+                        const float p0 = ex2_approx(x01.x), p1 = ex2_approx(x01.y);
+                        const float p2 = ex2_approx(x23.x), p3 = ex2_approx(x23.y);
+                        const int k = (c - CH * hh) / 2;
+                        if constexpr (BF16) {
+                            pk[k] = pack_bf16x2(p0, p1);
+                            pk[k + 1] = pack_bf16x2(p2, p3);
+                            lr01 = add_bf16x2_f32x2(pk[k], lr01);
+                            lr23 = add_bf16x2_f32x2(pk[k + 1], lr23);
+                        } else {
+                            pk[k] = pack_f16x2(p0, p1);
+                            pk[k + 1] = pack_f16x2(p2, p3);
+                            lr01 = fadd2(lr01, unpack2<BF16>(pk[k]));
+                            lr23 = fadd2(lr23, unpack2<BF16>(pk[k + 1]));
+                        }
+                        le01 = fadd2(le01, make_float2(p0, p1));
+                        le23 = fadd2(le23, make_float2(p2, p3));
                     }
-                    le01 = fadd2(le01, make_float2(p0, p1));
-                    le23 = fadd2(le23, make_float2(p2, p3));
+                    tmem_st_x16(lane_base + col_s + 16 * hh, pk);
                 }
-                tmem_st_x16(lane_base + col_s + 16 * hh, pk);
-            }
-            l_sum += (lr01.x + lr01.y) + (lr23.x + lr23.y);
-            l_exact += (le01.x + le01.y) + (le23.x + le23.y);
-            if (u >= 1 && __any_sync(0xffffffffu, rescale)) {
-                uint32_t o[D];
+                l_sum += (lr01.x + lr01.y) + (lr23.x + lr23.y);
+                l_exact += (le01.x + le01.y) + (le23.x + le23.y);
+                if (u >= 1 && __any_sync(0xffffffffu, rescale)) {
+                    uint32_t o[D];
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_x32(lane_base + col_o + c0, o + c0);
+                    for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_x32(lane_base + col_o + c0, o + c0);
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_wait_x32(o + c0);
+                    for (int c0 = 0; c0 < D; c0 += 32) tmem_ld_wait_x32(o + c0);
 #pragma unroll
-                for (int c = 0; c < D; c += 2) {
-                    const float2 r = fmul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])),
-                                           make_float2(alpha, alpha));
-                    o[c] = __float_as_uint(r.x);
-                    o[c + 1] = __float_as_uint(r.y);
+                    for (int c = 0; c < D; c += 2) {
+                        const float2 r = fmul2(make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1])),
+                                               make_float2(alpha, alpha));
+                        o[c] = __float_as_uint(r.x);
+                        o[c + 1] = __float_as_uint(r.y);
+                    }
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) tmem_st_x32(lane_base + col_o + c0, o + c0);
                 }
-#pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) tmem_st_x32(lane_base + col_o + c0, o + c0);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_full[x]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full[x]);
-        }
             if (active) {
                 const bool got = ok && mbar_wait(&o_final[x], finals & 1, abort_flag, p.status, 38);
                 ++finals;

@@ -251,7 +251,8 @@ cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int);
     const long long per_block = kTabThreads * kRowsPerThread;
     const long long blocks = (a.total + per_block - 1) / per_block;
-    return launch_after(paged_tables_kernel, (unsigned)(blocks < 2 * kSms ? blocks : 2 * kSms), kTabThreads, smem, st, p);
+    const unsigned grid = (unsigned)(blocks < 2 * kSms ? blocks : 2 * kSms);
+    return launch_after(paged_tables_kernel, grid, kTabThreads, smem, st, p);
 }
 
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {

@@ -405,7 +405,9 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots,
 
 /*
  * Device workspace of fa_fwd_paged (prefix_len = 0) and fa_fwd_paged_prefix:
- * partial results of key ranges that different blocks work on.
+ * partial results of key ranges that different blocks work on.  0 where none
+ * is needed (a table so narrow that no sequence's keys are divided; NULL is
+ * then as good), and for invalid sizes.
  */
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq,
                                     int Hkv, int d, int max_pages,

@@ -53,7 +53,7 @@ def test_append_refuses(lib, bad, status):
 
 
 def _paged(lib, q=FAKE, kc=FAKE, vc=FAKE, table=FAKE, lens=FAKE, cu=FAKE, o=FAKE, lse=FAKE, B=4, total=8, max_new=2,
-           Hq=4, Hkv=2, d=128, max_pages=8, page_size=16, num_pages=64, window=0, scale=0.1, dtype=1, ws=FAKE,
+           Hq=4, Hkv=2, d=128, max_pages=64, page_size=16, num_pages=64, window=0, scale=0.1, dtype=1, ws=FAKE,
            ws_bytes=1 << 40, front=None, prefix=None):
     rest = (o, lse, B, total, max_new, Hq, Hkv, d, max_pages, page_size, num_pages, window, scale, dtype, ws, ws_bytes,
             None)
@@ -73,6 +73,7 @@ def _paged(lib, q=FAKE, kc=FAKE, vc=FAKE, table=FAKE, lens=FAKE, cu=FAKE, o=FAKE
     (dict(cu=None, max_new=1, total=3), 1),   # fewer rows than requests
     (dict(d=32), 2), (dict(d=256), 2), (dict(page_size=8), 2), (dict(page_size=96), 2), (dict(max_pages=1 << 28), 2),
     (dict(num_pages=1 << 28), 2), (dict(total=1 << 30), 2), (dict(B=1 << 20, max_pages=1 << 12), 2),
+    (dict(B=1 << 30, max_pages=1, total=1 << 20), 2), (dict(Hkv=1 << 25, Hq=1 << 25, num_pages=1), 2),
     (dict(ws=None), 3), (dict(ws=FAKE + 16), 3), (dict(ws_bytes=0), 3),
 ])
 @pytest.mark.parametrize("prefix", [None, 100])
@@ -90,12 +91,13 @@ def test_prefix_refuses(lib):
 
 def test_workspace_bytes(lib):
     size = lib.fa_fwd_paged_workspace_bytes
-    assert size(4, 8, 2, 4, 2, 128, 8, 16, 0) > 0
+    assert size(4, 8, 2, 4, 2, 128, 64, 16, 0) > 0
+    assert size(4, 8, 2, 4, 2, 128, 8, 16, 0) == 0  # no sequence of this table is divided
     for bad in [(0, 8, 2, 4, 2, 128, 8, 16, 0), (4, 0, 2, 4, 2, 128, 8, 16, 0), (4, 8, 0, 4, 2, 128, 8, 16, 0),
                 (4, 8, 2, 5, 2, 128, 8, 16, 0), (4, 8, 2, 4, 2, 128, 0, 16, 0), (4, 8, 2, 4, 2, 128, 8, 16, -1)]:
         assert size(*bad) == 0
     # one byte less than asked for is refused
-    need = size(4, 8, 2, 4, 2, 128, 8, 16, 0)
+    need = size(4, 8, 2, 4, 2, 128, 64, 16, 0)
     assert _paged(lib, ws_bytes=need - 1) == 3
 
 
