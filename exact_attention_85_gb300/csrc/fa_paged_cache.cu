@@ -45,11 +45,13 @@ __device__ __forceinline__ bool request_lens(const TablesParams &p, int b, int &
 // slots, looking a row's request up by bisection of cu in shared memory.  No
 // block waits for another: a slot in a page that this call hands out takes
 // the page from the free list, not from the table cell another block writes.
+// Bound by latency, not by its bytes: lengths, then pages, then stores.
 __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesParams p) {
     extern __shared__ int smem[];
     const int B = p.a.B;
     int *cu = smem;             // [B + 1], clipped to total
-    int *first = smem + B + 1;  // [B]
+    int *first = smem + B + 1;  // [B], saturated
+    int *held = first + B;      // [B], cached lengths
     __shared__ long long warp_rows[kTabThreads / 32], warp_need[kTabThreads / 32];
     __shared__ int taken;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
         const int nd = pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
         cu[b] = (int)min(r_at, (long long)p.a.total);
         first[b] = (int)min(n_at, 0x7FFFFFFFll);
+        held[b] = c;
         // the first request that does not fit ends what is taken
         if (nd > 0 && n_at + nd > room) atomicMin(&taken, first[b]);
         r_at += n;
@@ -121,8 +124,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     }
     // lengths, offsets and table cells: a warp per request, dealt over all blocks
     for (int b = blockIdx.x * (kTabThreads / 32) + warp; b < B; b += gridDim.x * (kTabThreads / 32)) {
-        int c, n;
-        request_lens(p, b, c, n);
+        const int c = held[b], n = cu[b + 1] - cu[b];
         const int old = pages_of(c, p.shift), nd = pages_of((long long)c + n, p.shift) - old;
         const bool served = nd == 0 || (long long)first[b] + nd <= room;
         if (lane == 0) {
@@ -154,8 +156,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
                     if (cu[mid] <= r) lo = mid; else hi = mid - 1;
                 }
                 b = lo;
-                int n;
-                request_lens(p, b, c, n);
+                c = held[b];
+                const int n = cu[b + 1] - cu[b];
                 old = pages_of(c, p.shift);
                 const int nd = pages_of((long long)c + n, p.shift) - old;
                 served = nd == 0 || (long long)first[b] + nd <= room;
@@ -248,10 +250,10 @@ int log2_of(int x) {
 
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     TablesParams p{a, log2_of(a.page_size), device_status_ptr()};
-    const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int);
+    const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
     const long long per_block = kTabThreads * kRowsPerThread;
     const long long blocks = (a.total + per_block - 1) / per_block;
-    const unsigned grid = (unsigned)(blocks < 2 * kSms ? blocks : 2 * kSms);
+    const unsigned grid = (unsigned)(blocks < 4 * kSms ? blocks : 4 * kSms);
     return launch_after(paged_tables_kernel, grid, kTabThreads, smem, st, p);
 }
 

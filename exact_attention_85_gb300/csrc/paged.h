@@ -8,10 +8,6 @@
 
 namespace fa {
 
-// Requests one fa_paged_tables call takes: every block keeps two 32-bit
-// prefix sums per request in shared memory (128 KB of the 227 KB).
-constexpr int kMaxTableRequests = 16384;
-
 struct TablesArgs {
     const int *cached_lens, *new_lens, *free_pages, *free_start;
     int *block_table, *seq_lens, *cu_seqlens, *slots, *counts;

@@ -430,7 +430,9 @@ size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq,
  *   no row of the request sees are not read, nor are their table entries.
  *   A row that sees nothing (p < 0) gets O = 0 and LSE = -infinity.
  *   Rows of no request are left unwritten.  What a page holds behind its
- *   request's last key has no effect, whatever it is.
+ *   request's last key has no effect, whatever it is; the values of keys that
+ *   some row of the request sees must be finite, as for fa_fwd (a row that
+ *   does not see such a key multiplies its value by 0).
  *   workspace: at least fa_fwd_paged_workspace_bytes(..., prefix_len = 0)
  *       bytes, 256-byte aligned, contents on entry do not matter; calls that
  *       may run at the same time need workspaces of their own.
