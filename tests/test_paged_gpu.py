@@ -57,6 +57,11 @@ ATTENTION = [
     ([257, 1000, 5], [257, 130, 1], 3, 1, 64, 16, HF, 0, 0),
     ([640, 900, 33, 128], [1, 513, 1, 128], 8, 1, 128, 32, BF, 0, 0),
     ([400, 129], [70, 129], 5, 1, 128, 128, HF, 0, 0),
+    # up to 128 rows a block, by turns with more: one, two, three and more tiles
+    ([100, 130, 300, 1000, 513], [7, 20, 5, 30, 9], 4, 1, 128, 64, BF, 0, 0),
+    ([200, 1000, 700, 60, 900], [5, 200, 6, 3, 40], 4, 1, 64, 16, HF, 0, 0),
+    ([1500, 900, 260, 1400], [9, 100, 130, 20], 8, 2, 128, 128, BF, 0, 0),
+    ([1300, 700, 900], [20, 6, 31], 4, 1, 128, 32, HF, 300, 0),
     # sliding windows
     ([500, 20, 129], [1] * 3, 4, 2, 128, 16, BF, 100, 0),
     ([500, 20, 129], [1] * 3, 4, 2, 64, 64, HF, 1, 0),
