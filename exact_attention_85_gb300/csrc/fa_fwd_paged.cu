@@ -53,7 +53,6 @@ constexpr int kFewThreads = 32 * kFewWarps;
 // on 228, 473 on 190; 32 requests of 333-7506 keys 89.4, 86.3, 88.8, 92.2.
 constexpr float kCtasPerSm = 1.64f;
 constexpr int kMaxCtas = (int)(kCtasPerSm * kSms);
-constexpr int kMaxRows = 16;   // rows of a pair
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;   // units a CTA takes at least
 // A pair costs its tiles and about as much as one more (Q, the merge of the
@@ -95,8 +94,14 @@ struct FewParams {
     unsigned int *status;
     PartView part;
     int whole;  // a unit is a whole pair, not a tile
-    int after;  // runs beside the shared prefix' pass, which has waited for what came before
+    int after;  // runs beside the call's kernel before, which has waited for what came before
+    int mixed;  // requests of more rows are the 256-row kernel's
 };
+
+// A request of this kernel: one with rows, and no more than it takes.
+__device__ __forceinline__ bool few_request(const FewParams &p, int b, Request &r) {
+    return load_request(p.a, b, r) && r.n > 0 && r.n * p.group.d <= kMaxRows;
+}
 
 // NT: 8-row groups of a pair (rows up to 8 * NT).
 template <int D, bool BF16, int NT>
@@ -125,24 +130,33 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (!p.after) wait_previous();
     launch_dependents();
     {   // tiles of the whole batch
-        unsigned long long mine = 0;
-        int low = p.a.prefix_len, pairs = 0;
+        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0};
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
             int t0;
             if (!load_request(p.a, b, r)) {
                 if (blockIdx.x == 0) record_bad_args(p.status);
-            } else if (r.n > 0) {
-                const int tiles = pair_tiles<L::TK>(p.a, r, t0);
-                mine += tiles;
-                ++pairs;
-                low = min(low, prefix_low(p.a, r));
+                continue;
             }
+            if (r.n == 0) continue;
+            if (r.n * p.group.d <= kMaxRows) {
+                sum.tiles += pair_tiles<L::TK>(p.a, r, t0);
+                ++sum.blocks;
+            } else {
+                int blocks;
+                sum.beside += block_tiles(p.a, r, p.group.d, blocks);
+                sum.beside_blocks += blocks;
+            }
+            sum.low = min(sum.low, prefix_low(p.a, r));
         }
-        mine = warp_sum(mine);
-        pairs = __reduce_add_sync(0xffffffffu, pairs);
-        low = __reduce_min_sync(0xffffffffu, low);
-        if (lane == 0) sums[warp] = PlanSum{mine, pairs, low};
+        sum.tiles = warp_sum(sum.tiles);
+        sum.blocks = __reduce_add_sync(0xffffffffu, sum.blocks);
+        sum.low = __reduce_min_sync(0xffffffffu, sum.low);
+        if (p.mixed) {
+            sum.beside = warp_sum(sum.beside);
+            sum.beside_blocks = __reduce_add_sync(0xffffffffu, sum.beside_blocks);
+        }
+        if (lane == 0) sums[warp] = sum;
     }
     __syncthreads();
 
@@ -152,18 +166,20 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const CUtensorMap *tm = first_one ? &tm_k : &tm_v;
         if (lane == 0) prefetch_tmap(tm);
         long long tiles = 0, pairs = 0;
+        WideWork beside{0, 0};
         int low = p.a.prefix_len, most = gridDim.x;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
             tiles += (long long)sums[w].tiles * Hkv;
             pairs += (long long)sums[w].blocks * Hkv;
+            beside.tiles += (long long)sums[w].beside * Hkv;
+            beside.blocks += (long long)sums[w].beside_blocks * Hkv;
             low = min(low, sums[w].low);
         }
-        if (p.a.prefix_len > 0) {
-            // the prefix pass has some of the SMs to itself
-            const long long units = prefix_work(p.a, prefix_rows(p.a), p.group.d, low).units();
-            most = min(most, (int)(kCtasPerSm * (kSms - prefix_sms(units, tiles, pairs))));
-        }
+        // the kernel beside this one has some of the SMs to itself
+        if (!p.mixed && p.a.prefix_len > 0) beside = prefix_work(p.a, prefix_rows(p.a), p.group.d, low);
+        if (beside.blocks > 0)
+            most = min(most, (int)(kCtasPerSm * (kSms - wide_sms(beside.units(), tiles, pairs))));
         const long long T = p.whole ? pairs : tiles + pairs * kPairCost;
         const int G = (int)min((long long)most, max(1ll, p.whole ? T : T / kMinUnits));
         const Ranges ranges(T, G);
@@ -177,7 +193,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 Request r;
                 int t0;
                 long long units = 0;
-                if (b + lane < B && load_request(p.a, b + lane, r) && r.n > 0)
+                if (b + lane < B && few_request(p, b + lane, r))
                     units = (p.whole ? 1ll : (long long)pair_tiles<L::TK>(p.a, r, t0) + kPairCost) * Hkv;
                 long long incl = units;
 #pragma unroll
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         while (ok && u < u1 && b < B) {
             Request r;
             int t0;
-            if (!load_request(p.a, b, r) || r.n == 0) {
+            if (!few_request(p, b, r)) {
                 ++b;
                 continue;
             }
@@ -586,7 +602,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         else
                             p.a.lse[(size_t)h * p.a.total + t.row0 + tok] = lse2 * 0.69314718055994530942f;
                         if (!p.whole && (!(t.flags & kPart) || (t.flags & kSlot1)))
-                            p.part.code[out_row] = t.code ? t.code + part_code(0, 0, row) : 0;
+                            p.part.code[out_row] = t.code ? t.code + part_code(0, 0, row) + (p.mixed ? kFewCode : 0) : 0;
                     }
                 }
                 fence_proxy_async_smem();  // the buffer's next writer is a TMA copy
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 // issue.)
 struct MergeParams {
     PagedArgs a;
-    PartView own, prefix;
+    PartView own, prefix, beside;
     FastDiv heads;  // Hq
     int warps;      // W
 };
@@ -624,9 +640,9 @@ constexpr int kMergeWarps = 8;
 // Parts of a row by its code.  An unsound request's codes are not written, so
 // a code is held to the slots that there are.
 __device__ __forceinline__ int parts_of(const PartView &v, int code) {
-    const int pieces = code & kMaxPieces, cta = code >> 9 & kMaxPieces, slot_row = code >> 18;
+    const int pieces = code & kMaxPieces, cta = code >> 9 & kMaxPieces, slot_row = code >> 18 & 255;
     if (code == 0) return v.plane ? 1 : 0;
-    return pieces < 2 || cta + pieces > v.ctas || slot_row < 0 || slot_row >= v.slot_rows ? 0 : pieces;
+    return pieces < 2 || cta + pieces > v.ctas || slot_row >= v.slot_rows ? 0 : pieces;
 }
 
 // PREFIX: the rows have a shared prefix' parts as well.
@@ -662,7 +678,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
         load_codes(id + step);
         int n_own = 0, n_all = 0;
         if (id >= id_lo && id < id_hi) {
-            n_own = parts_of(p.own, c_own);
+            n_own = parts_of(c_own & kFewCode ? p.beside : p.own, c_own);
             n_all = n_own + (PREFIX ? parts_of(p.prefix, c_pre) : 0);
         }
         float acc[8], top = -INFINITY, sum = 0.f;
@@ -671,14 +687,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
         // where the parts of a pass begin: piece k is at one plane row, or two slots further each
         auto locate = [&](const PartView &v, int code, const float *&lse2, const float *&o, size_t &stride) {
             const size_t at =
-                code ? ((size_t)(code >> 9 & kMaxPieces) * 2 + 1) * v.slot_rows + (code >> 18) : (size_t)id;
+                code ? ((size_t)(code >> 9 & kMaxPieces) * 2 + 1) * v.slot_rows + (code >> 18 & 255) : (size_t)id;
             lse2 = (code ? v.slot_lse2 : v.plane_lse2) + at;
             o = (code ? v.slot : v.plane) + at * D + col;
             stride = v.slot_rows;
         };
         const float *lse_own, *o_own, *lse_pre = nullptr, *o_pre = nullptr;
         size_t stride_own, stride_pre = 0;
-        locate(p.own, c_own, lse_own, o_own, stride_own);
+        locate(c_own & kFewCode ? p.beside : p.own, c_own, lse_own, o_own, stride_own);
         if (PREFIX) locate(p.prefix, c_pre, lse_pre, o_pre, stride_pre);
         for (int k0 = sub; k0 < n_all; k0 += W * U) {
             float lse2[U];
@@ -766,11 +782,12 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.group = fast_div(a.Hq / a.Hkv);
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    p.part = w.own;
+    p.part = w.mixed ? w.beside : w.own;
     p.whole = w.whole ? 1 : 0;
     p.after = after ? 1 : 0;
-    auto kernel = a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
-    return launch_after(kernel, w.own.ctas, kFewThreads, L::ALLOC, st, tk, tv, p);
+    p.mixed = w.mixed ? 1 : 0;
+    auto kernel = (long long)a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
+    return launch_after(kernel, p.part.ctas, kFewThreads, L::ALLOC, st, tk, tv, p);
 }
 
 template <int D, bool BF16>
@@ -779,6 +796,7 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     p.a = a;
     p.own = w.own;
     p.prefix = w.prefix;
+    p.beside = w.beside;
     p.heads = fast_div(a.Hq);
     // few rows can have many parts each, many rows have few
     const long long rows = (long long)a.total * a.Hq;
@@ -801,11 +819,11 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     // few-row kernel, more go to the 256-row one.
     w.few = (long long)max_new * g <= kMaxRows;
     uintptr_t at = reinterpret_cast<uintptr_t>(workspace);
+    const long long few_tiles = (keys + (d == 128 ? 63 : 127)) / (d == 128 ? 64 : 128);
     if (w.few) {
-        const long long tiles = (keys + (d == 128 ? 63 : 127)) / (d == 128 ? 64 : 128);
         // Up to 8 tiles (4 us of one CTA) are not worth a second launch.
-        w.whole = prefix_len == 0 && tiles <= 8;
-        w.own.ctas = at_most(B * (long long)Hkv * (w.whole ? 1 : tiles) / (w.whole ? 1 : kMinUnits), kMaxCtas);
+        w.whole = prefix_len == 0 && few_tiles <= 8;
+        w.own.ctas = at_most(B * (long long)Hkv * (w.whole ? 1 : few_tiles) / (w.whole ? 1 : kMinUnits), kMaxCtas);
         w.own.slot_rows = kMaxRows;
         if (w.whole) return w;  // no workspace
     } else {
@@ -813,6 +831,16 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         const long long blocks = row_blocks + B < most ? row_blocks + B : most;
         w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys), kSms);
         w.own.slot_rows = kWideRows;
+        // Where the requests have a quarter of the longest one's rows or less
+        // on average, most are short: the few-row kernel takes those.  512
+        // rows and 63 single tokens behind 8k keys each took the 256-row
+        // kernel alone 436 us, both 349; 4 chunks of 512, where the launch
+        // would find nothing, are left to the one.
+        w.mixed = g <= kMaxRows && 4ll * total <= (long long)B * max_new;
+        if (w.mixed) {
+            w.beside.ctas = at_most(B * (long long)Hkv * few_tiles / kMinUnits, kMaxCtas);
+            w.beside.slot_rows = kMaxRows;
+        }
     }
     w.own.code = take<int>(at, rows);
     if (prefix_len > 0) {
@@ -828,6 +856,13 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     }
     w.own.slot_lse2 = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows);
     w.own.slot = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows * d);
+    if (w.mixed) {
+        w.beside.code = w.own.code;
+        w.beside.plane_lse2 = w.own.plane_lse2;
+        w.beside.plane = w.own.plane;
+        w.beside.slot_lse2 = take<float>(at, (size_t)w.beside.ctas * 2 * kMaxRows);
+        w.beside.slot = take<float>(at, (size_t)w.beside.ctas * 2 * kMaxRows * d);
+    }
     w.bytes = at - reinterpret_cast<uintptr_t>(workspace);
     return w;
 }
@@ -852,7 +887,8 @@ cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     const bool front = w.prefix.ctas > 0;
     if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;
-    e = w.few ? launch_paged_few(a, w, front, st) : launch_paged_wide(a, w, false, front, st);
+    if (!w.few && (e = launch_paged_wide(a, w, false, front, st)) != cudaSuccess) return e;
+    if (w.few || w.mixed) e = launch_paged_few(a, w, front || w.mixed, st);
     if (e != cudaSuccess || w.whole) return e;
     return launch_paged_merge(a, w, st);
 }

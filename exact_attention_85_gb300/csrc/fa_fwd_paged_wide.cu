@@ -72,9 +72,10 @@ struct WideParams {
     PagedArgs a;
     FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
-    int shared;  // prefix: the few-row kernel runs at the same time
+    int shared;  // the few-row kernel runs at the same time
+    int above;   // own pass: only requests of more rows a pair
     int q_box;   // tokens of a 128-row Q tile if the group divides it (TMA), else 0
-    int after;   // runs beside the shared prefix' pass, which has waited for what came before
+    int after;   // runs beside the call's kernel before, which has waited for what came before
     int o32;     // O is 32-byte aligned (the entry points promise 16)
     PartView part;
     float scale_log2;
@@ -203,22 +204,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- the batch's units of work
     const int B = p.prefix ? 1 : p.a.B;
     {
-        PlanSum sum{0, 0, p.a.prefix_len};
+        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0};
+        auto beside = [&](const Request &r) {  // a request of the few-row kernel
+            int t;
+            sum.beside += pair_tiles<kFewKeys<D>>(p.a, r, t);
+            ++sum.beside_blocks;
+        };
         if (p.prefix) {
             // the few-row kernel's tiles, and the first key that any row sees
             for (int b = threadIdx.x; b < p.a.B; b += kThreads) {
                 Request r;
-                int t;
                 if (!load_request(p.a, b, r) || r.n == 0) continue;
                 sum.low = min(sum.low, prefix_low(p.a, r));
-                sum.tiles += pair_tiles<kFewKeys<D>>(p.a, r, t);
-                ++sum.blocks;
+                beside(r);
             }
         } else {
             for (int b = warp * 32; b < B; b += kThreads) {
                 Request r{0, 0, 0};
                 if (b + lane < B && !load_request(p.a, b + lane, r)) {
                     if (blockIdx.x == 0) record_bad_args(p.status);
+                    r.n = 0;
+                }
+                if (r.n * p.group.d <= p.above) {
+                    if (r.n > 0) beside(r);
                     r.n = 0;
                 }
                 const int nb = blocks_of(r, p.group), tiles = request_tiles(p, r, nb, lane);
@@ -228,7 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         sum.tiles = warp_sum(sum.tiles);
+        sum.beside = warp_sum(sum.beside);
         sum.blocks = __reduce_add_sync(0xffffffffu, sum.blocks);
+        sum.beside_blocks = __reduce_add_sync(0xffffffffu, sum.beside_blocks);
         sum.low = __reduce_min_sync(0xffffffffu, sum.low);
         if (lane == 0) sums[warp] = sum;
     }
@@ -246,19 +256,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
         WideWork work{0, 0};
+        long long few_tiles = 0, few_pairs = 0;
         int most = gridDim.x, prefix_lo = p.a.prefix_len;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             work.tiles += (long long)sums[w].tiles * p.a.Hkv;
             work.blocks += (long long)sums[w].blocks * p.a.Hkv;
+            few_tiles += (long long)sums[w].beside * p.a.Hkv;
+            few_pairs += (long long)sums[w].beside_blocks * p.a.Hkv;
             prefix_lo = min(prefix_lo, sums[w].low);
         }
         if (p.prefix) {
-            const WideWork few = work;
             whole.n = prefix_rows(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
-            if (p.shared) most = min(most, prefix_sms(work.units(), few.tiles, few.blocks));
         }
+        if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));
         const int cost = work.block_cost();
         const long long T = work.units();
         const int G = (int)min((long long)most, max(1ll, T));
@@ -283,9 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ns;
         };
         auto load = [&](int b, Request &r) -> bool {
-            if (!p.prefix) return load_request(p.a, b, r);
+            if (!p.prefix) return load_request(p.a, b, r) && r.n * p.group.d > p.above;
             r = whole;
-            return true;
+            return r.n > 0;
         };
         // the request that holds unit u0, and its first unit
         int b = 0;
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u0 < u1 && !p.prefix) {
             for (; b < B; b += 32) {
                 Request r{0, 0, 0};
-                if (b + lane < B && !load_request(p.a, b + lane, r)) r.n = 0;
+                if (b + lane < B && !load(b + lane, r)) r.n = 0;
                 const int nb = blocks_of(r, p.group);
                 const int tiles = b >= kKept ? request_tiles(p, r, nb, lane) : b + lane < B ? kept[b + lane] : 0;
                 const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long blk0 = base;  // first unit of (hk, blk)
         for (; ok && u < u1 && b < B; ++b, fresh = false, hk = 0, blk = 0) {
             Request r;
-            if (!load(b, r) || r.n == 0) continue;
+            if (!load(b, r)) continue;
             const int nb = blocks_of(r, p.group);
             if (fresh) {
                 int tiles = nb * range_tiles(prefix_lo, r.len);
@@ -830,7 +842,8 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.q_box = kBM % g == 0 ? kBM / g : 0;
     if (!make_tmap_rows(&tq, a.q, BF16, D, g, a.Hkv, a.total, p.q_box ? p.q_box : 1)) return cudaErrorInvalidValue;
     p.prefix = prefix ? 1 : 0;
-    p.shared = prefix && w.few ? 1 : 0;
+    p.shared = prefix ? w.few : w.mixed;
+    p.above = w.mixed ? kMaxRows : 0;
     p.after = after ? 1 : 0;
     p.o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.part = prefix ? w.prefix : w.own;

@@ -59,8 +59,9 @@ inline FastDiv fast_div(int d) {
 // sum of exponentials (-inf: nothing seen); several merge as
 //   O = sum w_i O_i / sum w_i,  w_i = 2^(lse2_i - max).
 // code[row] says which a row has (row = token * Hq + head): 0 one, final or in
-// the plane; otherwise pieces | first CTA << 9 | row within the slot << 18:
-// slot 1 of the first CTA and slot 0 of the following ones.
+// the plane; otherwise pieces | first CTA << 9 | row within the slot << 18 |
+// kFewCode: slot 1 of the first CTA and slot 0 of the following ones, the
+// few-row kernel's where both kernels share the own pass.
 struct PartView {
     int *code;                  // [total * Hq]
     float *plane_lse2, *plane;  // [total * Hq] (x d); null where one result is final
@@ -68,16 +69,21 @@ struct PartView {
     int slot_rows, ctas;
 };
 constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
+constexpr int kMaxRows = 16;  // rows of a (request, key/value head) pair in the few-row kernel
 constexpr int kWideRows = 256, kWideKeys = 128;  // row block and key tile of the 256-row kernel
 constexpr int kMaxPieces = 511;  // 9 bits, also of CTA numbers
+
+constexpr int kFewCode = 1 << 26;
 
 __host__ __device__ constexpr int part_code(int pieces, int cta, int row) { return pieces | cta << 9 | row << 18; }
 
 // How a call is divided among the kernels.
 struct PagedPlan {
     bool few;         // own keys by the 16-row kernel, else by the 256-row one
-    bool whole;       // its CTAs take whole pairs only: nothing to merge
+    bool mixed;       // by both: requests of at most 16 rows (a pair) by the first
+    bool whole;       // the 16-row kernel's CTAs take whole pairs only: nothing to merge
     PartView own;     // ctas: of the kernel that takes the own keys
+    PartView beside;  // mixed: of the 16-row kernel; codes and planes are own's
     PartView prefix;  // ctas 0: no shared prefix
     size_t bytes;     // workspace
 };
@@ -85,7 +91,7 @@ struct PagedPlan {
 PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
                      int prefix_len, void *workspace);
 
-// The kernels of a forward call.  `after`: beside the shared prefix' pass.
+// The kernels of a forward call.  `after`: beside the call's kernel before.
 cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st);
 cudaError_t launch_paged_wide(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st);

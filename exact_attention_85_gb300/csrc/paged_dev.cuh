@@ -99,22 +99,31 @@ __device__ __forceinline__ WideWork prefix_work(const PagedArgs &a, int rows, in
 // What every warp of a block adds up of the batch before the block's first
 // barrier; its producer then takes the sums of all.
 struct PlanSum {
-    unsigned long long tiles;
-    int blocks, low;  // row blocks, or pairs of the few-row kernel; first key of the prefix
+    unsigned long long tiles, beside;  // of this kernel; of the one that runs beside it
+    int blocks, low;                   // row blocks or pairs; first key of the prefix that a row sees
+    int beside_blocks, pad;
 };
 
-// A shared prefix' pass is bound by the tensor cores and the few-row kernel
-// by memory, so they run at the same time, each on SMs of its own: the number
-// that the prefix gets.  Times in us, as measured: a unit of the 256-row
+// Key tiles of a request's row blocks, each counted as if it saw all keys that
+// any of them sees: what the few-row kernel knows of the 256-row one's work.
+__device__ __forceinline__ long long block_tiles(const PagedArgs &a, const Request &r, int group, int &blocks) {
+    blocks = (int)(((unsigned)(r.n * group) + kWideRows - 1) / kWideRows);
+    return (long long)blocks * range_tiles(a.window > 0 ? max(0, r.len - r.n + 1 - a.window) : 0, r.len);
+}
+
+// The 256-row kernel is bound by the tensor cores and the few-row kernel by
+// memory, so a shared prefix' pass, or the long chunks of a mixed batch, run
+// beside the few-row kernel, each on SMs of its own: the number that the
+// 256-row kernel gets.  Times in us, as measured: a unit of the 256-row
 // kernel takes 1.72 on one SM, with 14 to start and end; a few-row tile (32 KB)
 // 4.8 ns at 6.8 TB/s, or 0.47 us on an SM (70 GB/s) where those are few, and
 // every pair 1.1 us more there, with 6 to start.  (256 requests of 64-2048 keys on a 16k prefix: 235 us with 36
 // SMs, 217 with 46, 233 with 56, 244 with 70; one after the other 272.)  32
 // candidates, one a lane; each kernel decides for itself, so a difference
 // would cost time only.
-__device__ __forceinline__ int prefix_sms(long long prefix_units, long long few_tiles, long long few_pairs) {
+__device__ __forceinline__ int wide_sms(long long wide_units, long long few_tiles, long long few_pairs) {
     const int g = kSms * ((threadIdx.x & 31) + 1) / 33;
-    const float wide = 14.f + (float)prefix_units * 1.72f / (float)g;
+    const float wide = 14.f + (float)wide_units * 1.72f / (float)g;
     const float few = 6.f + fmaxf(0.0048f * (float)few_tiles,
                                   (0.47f * (float)few_tiles + 1.1f * (float)few_pairs) / (float)(kSms - g));
     // the least of the larger times, and the first to have it

@@ -62,6 +62,12 @@ ATTENTION = [
     ([200, 1000, 700, 60, 900], [5, 200, 6, 3, 40], 4, 1, 64, 16, HF, 0, 0),
     ([1500, 900, 260, 1400], [9, 100, 130, 20], 8, 2, 128, 128, BF, 0, 0),
     ([1300, 700, 900], [20, 6, 31], 4, 1, 128, 32, HF, 300, 0),
+    # one long chunk among many short requests: both kernels at once
+    ([400, 90, 1, 700, 64, 0, 129, 1500, 33], [300, 1, 1, 2, 1, 0, 1, 1, 3], 8, 2, 128, 16, BF, 0, 0),
+    ([900, 10, 2000, 77, 65, 300, 8, 1], [260, 4, 1, 5, 1, 2, 8, 1], 4, 2, 64, 64, HF, 0, 0),
+    ([500, 3, 130, 1000, 17, 260, 64, 9, 512, 70], [200, 3, 1, 1, 1, 20, 2, 1, 1, 9], 16, 2, 128, 32, HF, 200, 0),
+    ([200, 1, 40, 300, 5, 64, 128, 2], [150, 1, 4, 1, 1, 1, 2, 1], 8, 2, 64, 16, BF, 0, 333),
+    ([260, 7, 90, 30, 400, 1, 1, 19], [129, 1, 1, 1, 3, 1, 1, 1], 4, 1, 128, 128, BF, 100, 150),
     # sliding windows
     ([500, 20, 129], [1] * 3, 4, 2, 128, 16, BF, 100, 0),
     ([500, 20, 129], [1] * 3, 4, 2, 64, 64, HF, 1, 0),
@@ -117,6 +123,8 @@ def test_attention_random(cuda_lib, seed):
     ([300, 5], [3, 1], 200, 1, 64, 64, 20),      # and does not divide one
     ([200], [3], 300, 1, 128, 32, 0),            # a token is more than a block
     ([2500], [2300], 2, 1, 64, 16, 0),           # many blocks of one request
+    ([30 + (13 * i) % 400 for i in range(400)] + [900], [1 + (3 * i) % 4 for i in range(400)] + [800], 4, 1, 64, 16, 0),
+    ([30 + (13 * i) % 400 for i in range(300)] + [900], [1] * 300 + [500], 8, 2, 128, 32, 60),
 ])
 def test_many_requests_and_wide_groups(cuda_lib, lens, new, Hq, Hkv, d, ps, prefix):
     p = Problem(lens, new, Hq, Hkv, d, ps, BF, 0, prefix, extra_cols=70)
@@ -170,7 +178,7 @@ def test_rows_of_no_request_stay_as_they_are(cuda_lib, new, prefix):
     assert (o[p.rows:] == 7.0).all() and (lse[:, p.rows:] == 7.0).all()
 
 
-@pytest.mark.parametrize("new", [[1, 1, 1], [30, 1, 70]])
+@pytest.mark.parametrize("new", [[1, 1, 1], [30, 1, 70], [2, 1, 190]])
 @pytest.mark.parametrize("prefix", [0, 40])
 @pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length", "offsets", "too many rows"])
 def test_bad_device_values_are_reported(cuda_lib, what, new, prefix):
