@@ -451,7 +451,7 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
         (long long)a.B * a.Hq > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
     const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
-                                           a.prefix_len, nullptr);
+                                           a.prefix_len, a.window, nullptr);
     const size_t need = w.bytes;
     if (need > 0 &&
         (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)))
@@ -505,7 +505,7 @@ size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int H
         page_size < 1 || prefix_len < 0 || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
         (long long)max_pages * page_size + prefix_len > 0x7FFFFFFFll)
         return 0;
-    return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, nullptr).bytes;
+    return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, 0, nullptr).bytes;
 }
 
 fa_status_t fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, const int *block_table,

@@ -809,7 +809,7 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
 }  // namespace
 
 PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
-                     int prefix_len, void *workspace) {
+                     int prefix_len, int window, void *workspace) {
     PagedPlan w{};
     const int g = Hq / Hkv;
     const size_t rows = (size_t)total * Hq;
@@ -819,11 +819,21 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     // few-row kernel, more go to the 256-row one.
     w.few = (long long)max_new * g <= kMaxRows;
     uintptr_t at = reinterpret_cast<uintptr_t>(workspace);
-    const long long few_tiles = (keys + (d == 128 ? 63 : 127)) / (d == 128 ? 64 : 128);
+    const int tile = d == 128 ? 64 : 128;
+    const long long pairs = (long long)B * Hkv, few_tiles = (keys + tile - 1) / tile;
     if (w.few) {
-        // Up to 8 tiles (4 us of one CTA) are not worth a second launch.
-        w.whole = prefix_len == 0 && few_tiles <= 8;
-        w.own.ctas = at_most(B * (long long)Hkv * (w.whole ? 1 : few_tiles) / (w.whole ? 1 : kMinUnits), kMaxCtas);
+        // A CTA takes whole pairs, with nothing to merge, where the second
+        // launch (some 4 us) would cost more than dividing them gains: up to
+        // 12 tiles a pair where every pair has a CTA of its own (24 requests
+        // of 1024 keys in the window: 16.2 us divided, 13.9 whole), or up to
+        // 8 where the CTAs that the last round leaves idle could read little
+        // meanwhile (256 requests of 512 keys in 16-key pages, 2048 pairs:
+        // 86 us divided, 94 whole).
+        const long long seen = window > 0 ? ((long long)window + max_new + tile - 2) / tile + 1 : few_tiles;
+        const long long most = seen < few_tiles ? seen : few_tiles;
+        const long long idle = (pairs + kMaxCtas - 1) / kMaxCtas * kMaxCtas - pairs;
+        w.whole = prefix_len == 0 && (pairs <= kMaxCtas ? most <= 12 : most <= 8 && idle * most <= 800);
+        w.own.ctas = at_most(w.whole ? pairs : pairs * few_tiles / kMinUnits, kMaxCtas);
         w.own.slot_rows = kMaxRows;
         if (w.whole) return w;  // no workspace
     } else {
@@ -838,7 +848,7 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         // would find nothing, are left to the one.
         w.mixed = g <= kMaxRows && 4ll * total <= (long long)B * max_new;
         if (w.mixed) {
-            w.beside.ctas = at_most(B * (long long)Hkv * few_tiles / kMinUnits, kMaxCtas);
+            w.beside.ctas = at_most(pairs * few_tiles / kMinUnits, kMaxCtas);
             w.beside.slot_rows = kMaxRows;
         }
     }
@@ -883,7 +893,7 @@ cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
     a.shift = 0;
     while ((1 << a.shift) < a.page_size) ++a.shift;
     const PagedPlan w = plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size, a.prefix_len,
-                                   a.workspace);
+                                   a.window, a.workspace);
     cudaError_t e = cudaSuccess;
     const bool front = w.prefix.ctas > 0;
     if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;

@@ -88,8 +88,9 @@ struct PagedPlan {
     size_t bytes;     // workspace
 };
 
+// The workspace needed is the largest without a window.
 PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
-                     int prefix_len, void *workspace);
+                     int prefix_len, int window, void *workspace);
 
 // The kernels of a forward call.  `after`: beside the call's kernel before.
 cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st);
