@@ -432,7 +432,7 @@ fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_bytes) {
+fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_bytes) {
     if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.lse || !a.block_table || !a.seq_lens) return FA_ERR_INVALID_ARG;
     const void *ptrs[] = {a.q, a.k_cache, a.v_cache, a.o, a.lse};
     for (const void *p : ptrs)
@@ -448,8 +448,10 @@ fa_status_t check_paged(const fa::PagedArgs &a, fa_dtype_t dtype, size_t workspa
     if (s != FA_OK) return s;
     if ((long long)a.max_pages * a.page_size + a.prefix_len > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
     if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
-        (long long)a.B * a.Hq > 0x7FFFFFFFll)
+        (long long)a.B * a.Hq > 0x7FFFFFFFll || a.B > FA_PAGED_MAX_B)
         return FA_ERR_UNSUPPORTED;
+    // a window that holds every key there can be is none
+    if (a.window >= (long long)a.max_pages * a.page_size + a.prefix_len) a.window = 0;
     const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
                                            a.prefix_len, a.window, nullptr);
     const size_t need = w.bytes;
@@ -502,7 +504,7 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
                                     int page_size, int prefix_len) {
     if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
-        page_size < 1 || prefix_len < 0 || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
+        page_size < 1 || prefix_len < 0 || B > FA_PAGED_MAX_B || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
         (long long)max_pages * page_size + prefix_len > 0x7FFFFFFFll)
         return 0;
     return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, 0, nullptr).bytes;

@@ -347,7 +347,7 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8,
  *   slot              page * page_size + row, one int32 per token
  * page_size is a power of two, 16 .. 256; num_pages * page_size, num_pages *
  * Hkv, max_pages * page_size (+ prefix_len), B * max_pages, B * Hq and total *
- * Hq are at most 2^31 - 1.  Lengths, offsets, tables and slots are read
+ * Hq are at most 2^31 - 1, and B at most FA_PAGED_MAX_B.  Lengths, offsets, tables and slots are read
  * on the device: page numbers outside 0 .. num_pages - 1 and lengths that
  * break the rules below are reported by fa_get_device_status as
  * FA_ERR_INVALID_ARG and never read or write out of range; what they concern
@@ -355,8 +355,9 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8,
  * describes a cache; the attention itself is theirs ([V2] section 6.1).
  */
 
-/* Most requests of one fa_paged_tables call. */
+/* Most requests of one fa_paged_tables call, and of one forward call. */
 #define FA_PAGED_TABLES_MAX_B 16384
+#define FA_PAGED_MAX_B (1 << 20)
 
 /*
  * Pages and slots for one step's new tokens, in one launch.  Request b holds

@@ -73,7 +73,7 @@ def _paged(lib, q=FAKE, kc=FAKE, vc=FAKE, table=FAKE, lens=FAKE, cu=FAKE, o=FAKE
     (dict(cu=None, max_new=1, total=3), 1),   # fewer rows than requests
     (dict(d=32), 2), (dict(d=256), 2), (dict(page_size=8), 2), (dict(page_size=96), 2), (dict(max_pages=1 << 28), 2),
     (dict(num_pages=1 << 28), 2), (dict(total=1 << 30), 2), (dict(B=1 << 20, max_pages=1 << 12), 2),
-    (dict(B=1 << 30, max_pages=1, total=1 << 20), 2), (dict(Hkv=1 << 25, Hq=1 << 25, num_pages=1), 2),
+    (dict(B=1 << 30, max_pages=1, total=1 << 20), 2), (dict(B=(1 << 20) + 1, max_pages=1), 2), (dict(Hkv=1 << 25, Hq=1 << 25, num_pages=1), 2),
     (dict(ws=None), 3), (dict(ws=FAKE + 16), 3), (dict(ws_bytes=0), 3),
 ])
 @pytest.mark.parametrize("prefix", [None, 100])

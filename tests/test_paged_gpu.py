@@ -145,6 +145,29 @@ def test_equal_calls_give_equal_bits(cuda_lib):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("new,prefix", [([1, 1], 0), ([40, 300], 0), ([1, 1], 90), ([200, 1], 90)])
+@pytest.mark.parametrize("window", [1000, 2 ** 31 - 1])
+def test_window_of_all_keys_is_none(cuda_lib, new, prefix, window):
+    p = Problem([300, 310], new, 4, 2, 64, 16, BF, 0, prefix)
+    a = _run(p)
+    p.window = window
+    b = _run(p)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_pages_in_several_places(cuda_lib):
+    """Requests may share pages, and a table name a page twice."""
+    p = Problem([64, 64], [1, 1], 4, 2, 64, 16, BF)
+    table = p.table[:1, [0, 1, 0, 1, 0]].repeat(2, 1).contiguous()
+    q = p.q[:1].repeat(2, 1, 1).contiguous().cuda()
+    o, lse = fa.attention_fwd_paged(q, p.k_cache.cuda(), p.v_cache.cuda(), table.cuda(), _i32([64, 64]), scale=p.scale)
+    p.k[0] = torch.cat([p.k[0][:, :32]] * 2, 1)
+    p.v[0] = torch.cat([p.v[0][:, :32]] * 2, 1)
+    p.lens, p.new, p.rows = p.lens[:1], [1], 1
+    check(o[:1], lse[:, :1], p.reference(), 1)
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[:, 0], lse[:, 1])
+
+
 def test_prefix_equals_the_same_keys_unshared(cuda_lib):
     """Both calls stay within their bounds of the same 64-bit result."""
     p = Problem([70, 5, 129], [1, 1, 1], 8, 2, 128, 16, BF, 0, 160, seed=5)
@@ -407,6 +430,43 @@ def test_captured_step_follows_its_inputs(cuda_lib):
         want = step()
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+
+
+@pytest.mark.parametrize("new,prefix", [([70, 200, 130], 0), ([300, 1, 1, 2, 1, 1], 0), ([1, 1, 1], 200),
+                                        ([300, 1, 1, 2, 1, 1], 200)])
+def test_captured_forward_of_every_kernel(cuda_lib, new, prefix):
+    """Captured with one problem's values, replayed with another's of the same
+    shapes, and next to a graph of the other kernels."""
+    ps = [Problem([n + 37 * i + 90 for i, n in enumerate(new)], new, 8, 2, 128, 16, BF, 0, prefix, seed=s)
+          for s in (1, 2)]
+    names = ("q", "k_cache", "v_cache", "table", "cu")
+    dev = {n: getattr(ps[0], n).cuda() for n in names}
+    dev["lens"], dev["front"] = _i32(ps[0].lens), _i32(ps[0].front or [0])
+
+    def call():
+        args = (dev["q"], dev["k_cache"], dev["v_cache"])
+        tail = (dev["table"], dev["lens"], dev["cu"], max(new))
+        if prefix:
+            return fa.attention_fwd_paged_prefix(*args, dev["front"], prefix, *tail)
+        return fa.attention_fwd_paged(*args, *tail)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first = call()
+        o, lse = call()
+    for p in (ps[1], ps[0]):
+        for n in names:
+            dev[n].copy_(getattr(p, n))
+        dev["lens"].copy_(_i32(p.lens))
+        dev["front"].copy_(_i32(p.front or [0]))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        check(o, lse, p.reference(), p.rows)
+        assert torch.equal(first[0], o) and torch.equal(first[1], lse)
     assert _lib.fa_get_device_status() == _lib.FA_OK
 
 
