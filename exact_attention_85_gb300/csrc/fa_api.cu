@@ -417,6 +417,8 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8, const flo
 }
 
 namespace {
+constexpr long long kMaxKeys = 0x7FFFFFFFll - 1023;  // of a paged sequence
+
 // Checks shared by the paged-cache entry points.
 fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t dtype) {
     if (Hkv < 1 || d < 1 || num_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
@@ -446,7 +448,8 @@ fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_byt
     if (!a.cu_seqlens && (a.max_new != 1 || a.total < a.B)) return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(a.Hkv, a.d, a.page_size, a.num_pages, dtype);
     if (s != FA_OK) return s;
-    if ((long long)a.max_pages * a.page_size + a.prefix_len > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    // keys are counted in 32 bits, rounded up to whole tiles and pages
+    if ((long long)a.max_pages * a.page_size + a.prefix_len > kMaxKeys) return FA_ERR_UNSUPPORTED;
     if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
         (long long)a.B * a.Hq > 0x7FFFFFFFll || a.B > FA_PAGED_MAX_B)
         return FA_ERR_UNSUPPORTED;
@@ -481,7 +484,7 @@ fa_status_t fa_paged_tables(const int *cached_lens, const int *new_lens, const i
     if (!aligned16(slots)) return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(1, 128, page_size, num_pages, FA_BF16);
     if (s != FA_OK) return s;
-    if (B > FA_PAGED_TABLES_MAX_B || (long long)max_pages * page_size > 0x7FFFFFFFll ||
+    if (B > FA_PAGED_TABLES_MAX_B || (long long)max_pages * page_size > kMaxKeys ||
         (long long)B * max_pages > 0x7FFFFFFFll)
         return FA_ERR_UNSUPPORTED;
     fa::TablesArgs a{cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots, counts,
@@ -505,7 +508,7 @@ size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int H
                                     int page_size, int prefix_len) {
     if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
         page_size < 1 || prefix_len < 0 || B > FA_PAGED_MAX_B || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
-        (long long)max_pages * page_size + prefix_len > 0x7FFFFFFFll)
+        (long long)max_pages * page_size + prefix_len > kMaxKeys)
         return 0;
     return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, 0, nullptr).bytes;
 }

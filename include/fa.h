@@ -345,9 +345,10 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8,
  *   block_table       int32 [B][max_pages]: request b's token t is row
  *                     t % page_size of page block_table[b][t / page_size]
  *   slot              page * page_size + row, one int32 per token
- * page_size is a power of two, 16 .. 256; num_pages * page_size, num_pages *
- * Hkv, max_pages * page_size (+ prefix_len), B * max_pages, B * Hq and total *
- * Hq are at most 2^31 - 1, and B at most FA_PAGED_MAX_B.  Lengths, offsets, tables and slots are read
+ * page_size is a power of two, 16 .. 256; max_pages * page_size (+
+ * prefix_len) is at most 2^31 - 1024, num_pages * page_size, num_pages * Hkv,
+ * B * max_pages, B * Hq and total * Hq are at most 2^31 - 1, and B at most
+ * FA_PAGED_MAX_B.  Lengths, offsets, tables and slots are read
  * on the device: page numbers outside 0 .. num_pages - 1 and lengths that
  * break the rules below are reported by fa_get_device_status as
  * FA_ERR_INVALID_ARG and never read or write out of range; what they concern
