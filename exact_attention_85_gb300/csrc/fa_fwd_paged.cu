@@ -26,7 +26,9 @@
 // pair, some whole pairs and the beginning of another.  Whole pairs are
 // written out directly; the parts of a pair that several CTAs share go to
 // the workspace as (O~ / l, log2 sum) and a second kernel merges them (with a
-// shared prefix, everything does, and is merged with the prefix' results).
+// shared prefix that has a pass of its own, everything does, and is merged
+// with that pass' results; a short prefix is simply the first tiles of every
+// pair here).
 //   warps 0-3  each a quarter of every tile's keys, all rows; their four
 //              results are merged through the last tile's buffer
 //   warps 4, 5 producers of K and of V: each plans the CTA's range, reads the
@@ -60,7 +62,7 @@ constexpr int kMinUnits = 2;   // units a CTA takes at least
 constexpr int kPairCost = 1;
 constexpr float kMoveBy = 8.0f;  // log2 units by which a score passes the maximum before that moves
 
-enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16 };
+enum : int { kFirst = 1, kLast = 2, kMask = 4, kPart = 8, kSlot1 = 16, kFront = 32 };
 
 // What the producer tells the consumers about a tile.
 struct TileInfo {
@@ -96,11 +98,29 @@ struct FewParams {
     int whole;  // a unit is a whole pair, not a tile
     int after;  // runs beside the call's kernel before, which has waited for what came before
     int mixed;  // requests of more rows are the 256-row kernel's
+    int joined; // the shared prefix' keys are read with each request's own
 };
 
 // A request of this kernel: one with rows, and no more than it takes.
 __device__ __forceinline__ bool few_request(const FewParams &p, int b, Request &r) {
     return load_request(p.a, b, r) && r.n > 0 && r.n * p.group.d <= kMaxRows;
+}
+
+// First tile and number of tiles of the shared prefix that a request's rows
+// see, where they are read with its own.
+template <int TK>
+__device__ __forceinline__ int front_tiles(const FewParams &p, const Request &r, int &t0) {
+    const int lo = p.joined ? prefix_low(p.a, r) : 0;
+    t0 = lo / TK;
+    return p.joined && lo < p.a.prefix_len ? (p.a.prefix_len + TK - 1) / TK - t0 : 0;
+}
+
+// All tiles of a pair of request r.
+template <int TK>
+__device__ __forceinline__ int all_tiles(const FewParams &p, const Request &r) {
+    int t0;
+    const int front = front_tiles<TK>(p, r, t0);
+    return front + pair_tiles<TK>(p.a, r, t0);
 }
 
 // NT: 8-row groups of a pair (rows up to 8 * NT).
@@ -133,14 +153,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0};
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
-            int t0;
             if (!load_request(p.a, b, r)) {
                 if (blockIdx.x == 0) record_bad_args(p.status);
                 continue;
             }
             if (r.n == 0) continue;
             if (r.n * p.group.d <= kMaxRows) {
-                sum.tiles += pair_tiles<L::TK>(p.a, r, t0);
+                sum.tiles += all_tiles<L::TK>(p, r);
                 ++sum.blocks;
             } else {
                 int blocks;
@@ -177,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             low = min(low, sums[w].low);
         }
         // the kernel beside this one has some of the SMs to itself
-        if (!p.mixed && p.a.prefix_len > 0) beside = prefix_work(p.a, prefix_rows(p.a), p.group.d, low);
+        if (!p.mixed && !p.joined && p.a.prefix_len > 0) beside = prefix_work(p.a, prefix_rows(p.a), p.group.d, low);
         if (beside.blocks > 0)
             most = min(most, (int)(kCtasPerSm * (kSms - wide_sms(beside.units(), tiles, pairs))));
         const long long T = p.whole ? pairs : tiles + pairs * kPairCost;
@@ -191,10 +210,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         if (u0 < u1) {
             for (; b < B; b += 32) {
                 Request r;
-                int t0;
                 long long units = 0;
                 if (b + lane < B && few_request(p, b + lane, r))
-                    units = (p.whole ? 1ll : (long long)pair_tiles<L::TK>(p.a, r, t0) + kPairCost) * Hkv;
+                    units = (p.whole ? 1ll : (long long)all_tiles<L::TK>(p, r) + kPairCost) * Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -225,12 +243,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         long long u = u0;
         while (ok && u < u1 && b < B) {
             Request r;
-            int t0;
             if (!few_request(p, b, r)) {
                 ++b;
                 continue;
             }
-            const int nt = pair_tiles<L::TK>(p.a, r, t0);
+            int front0, own0;  // first tiles
+            const int front = front_tiles<L::TK>(p, r, front0), nt = front + pair_tiles<L::TK>(p.a, r, own0);
             const int cost = p.whole ? 0 : kPairCost, per_pair = p.whole ? 1 : nt + cost;  // units
             int hk = (int)((u - base) / per_pair);
             for (; ok && hk < Hkv && u < u1; ++hk) {
@@ -239,20 +257,24 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 u = u1 < pair0 + per_pair ? u1 : pair0 + per_pair;
                 if (j1 <= j0) continue;  // the range ends before the pair's first tile
                 const bool whole = j0 == 0 && j1 == nt;
-                const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window) : 0;
-                const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window) : 0;
-                const int hi_min = r.len - r.n + 1;
                 // a pair that goes on in the next CTA belongs to the one it began in
                 const int code =
                     !whole && j0 == 0 ? part_code(ranges.owner(pair0 + per_pair - 1) - c + 1, c, 0) : 0;
                 for (int j = j0; j < j1; ++j) {
-                    const int kv0 = (t0 + j) * L::TK;
+                    // the prefix' tiles come first; places count from its start
+                    const bool in_front = j < front;
+                    const int kv0 = (in_front ? front0 + j : own0 + j - front) * L::TK;
+                    const int shift = in_front ? p.a.prefix_len : 0, end = in_front ? p.a.prefix_len : r.len;
+                    const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window + shift) : 0;
+                    const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window + shift) : 0;
+                    const int hi_min = min(end, r.len - r.n + 1 + shift);
+                    const int *table = in_front ? p.a.prefix_pages : p.a.block_table + (size_t)b * p.a.max_pages;
                     // pages that hold no visible key are neither looked up nor read
                     const int key0 = kv0 + sub * page_keys;
-                    const bool live = boxed && key0 < r.len && key0 + page_keys > lo_min;
+                    const bool live = boxed && key0 < end && key0 + page_keys > lo_min;
                     int page = 0;
                     if (live) {
-                        page = p.a.block_table[(size_t)b * p.a.max_pages + (key0 >> p.a.shift)];
+                        page = table[key0 >> p.a.shift];
                         if (page < 0 || page >= p.a.num_pages) {
                             record_bad_args(p.status);
                             page = p.a.num_pages;  // out of the tensor: the copy fills zeros
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         t.code = code;
                         t.flags = (j == j0 ? kFirst : 0) | (j + 1 == j1 ? kLast : 0) |
                                   (kv0 < lo_max || kv0 + L::TK > hi_min ? kMask : 0) | (whole ? 0 : kPart) |
-                                  (j0 == 0 ? kSlot1 : 0);
+                                  (j0 == 0 ? kSlot1 : 0) | (in_front ? kFront : 0);
                         info[st] = t;
                     }
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * box_bytes);
@@ -387,7 +409,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         m[g][x] = -INFINITY;
                         l[g][x] = le[g][x] = 0.f;
                         hi[g][x] = t.len - t.n + (g * 8 + quad * 2 + x) / p.group + 1;
-                        lo[g][x] = p.a.window > 0 ? hi[g][x] - p.a.window : 0;
+                        // no window: below every place (a prefix' first key is at -prefix_len)
+                        lo[g][x] = p.a.window > 0 ? hi[g][x] - p.a.window : -0x7FFFFFFF;
                     }
                 }
             }
@@ -406,6 +429,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int g = 0; g < NT; ++g) mma_16x8x16<BF16>(s[i][g], kf, qf[g][kk][0], qf[g][kk][1]);
                 }
             }
+            // the tile's keys end here, and places of its keys begin there
+            const int end = t.flags & kFront ? p.a.prefix_len : t.len, shift = t.flags & kFront ? p.a.prefix_len : 0;
             if (t.flags & kMask) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -414,7 +439,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = t.kv0 + w0 + i * 16 + rw + (e >> 1) * 8;
-                            if (key >= hi[g][e & 1] || key < lo[g][e & 1]) s[i][g][e] = -INFINITY;
+                            if (key >= end || key - shift >= hi[g][e & 1] || key - shift < lo[g][e & 1])
+                                s[i][g][e] = -INFINITY;
                         }
                     }
                 }
@@ -484,8 +510,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
             }
             // O~^T += V^T P^T
-            const int k_end = t.len - t.kv0 - w0;  // keys of this warp that exist
-            const int k_low = p.a.window > 0 ? t.len - t.n + 1 - p.a.window - t.kv0 - w0 : 0;
+            const int k_end = end - t.kv0 - w0;  // keys of this warp that exist
+            const int k_low = p.a.window > 0 ? t.len - t.n + 1 - p.a.window + shift - t.kv0 - w0 : 0;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -786,6 +812,7 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.whole = w.whole ? 1 : 0;
     p.after = after ? 1 : 0;
     p.mixed = w.mixed ? 1 : 0;
+    p.joined = w.joined ? 1 : 0;
     auto kernel = (long long)a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
     return launch_after(kernel, p.part.ctas, kFewThreads, L::ALLOC, st, tk, tv, p);
 }
@@ -820,7 +847,17 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     w.few = (long long)max_new * g <= kMaxRows;
     uintptr_t at = reinterpret_cast<uintptr_t>(workspace);
     const int tile = d == 128 ? 64 : 128;
-    const long long pairs = (long long)B * Hkv, few_tiles = (keys + tile - 1) / tile;
+    const long long pairs = (long long)B * Hkv;
+    long long few_tiles = (keys + tile - 1) / tile;
+    // A small batch reads the prefix as often as it has requests, in the pass
+    // over their own keys: one launch less, and two when nothing is divided.
+    // What it reads more than once is up to 2000 tiles (64 MB, 10 us).
+    const long long front_tiles = (prefix_len + tile - 1ll) / tile;
+    w.joined = w.few && prefix_len > 0 && (long long)Hkv * front_tiles * (B - 1) <= 2000;
+    if (w.joined) {
+        few_tiles += front_tiles;
+        prefix_len = 0;
+    }
     if (w.few) {
         // A CTA takes whole pairs, with nothing to merge, where the second
         // launch (some 4 us) would cost more than dividing them gains: up to
@@ -829,7 +866,7 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         // 8 where the CTAs that the last round leaves idle could read little
         // meanwhile (256 requests of 512 keys in 16-key pages, 2048 pairs:
         // 86 us divided, 94 whole).
-        const long long seen = window > 0 ? ((long long)window + max_new + tile - 2) / tile + 1 : few_tiles;
+        const long long seen = window > 0 ? ((long long)window + max_new + tile - 2) / tile + 2 : few_tiles;
         const long long most = seen < few_tiles ? seen : few_tiles;
         const long long idle = (pairs + kMaxCtas - 1) / kMaxCtas * kMaxCtas - pairs;
         w.whole = prefix_len == 0 && (pairs <= kMaxCtas ? most <= 12 : most <= 8 && idle * most <= 800);

@@ -80,11 +80,12 @@ __host__ __device__ constexpr int part_code(int pieces, int cta, int row) { retu
 // How a call is divided among the kernels.
 struct PagedPlan {
     bool few;         // own keys by the 16-row kernel, else by the 256-row one
+    bool joined;      // the shared prefix' keys too, with each request's own
     bool mixed;       // by both: requests of at most 16 rows (a pair) by the first
     bool whole;       // the 16-row kernel's CTAs take whole pairs only: nothing to merge
     PartView own;     // ctas: of the kernel that takes the own keys
     PartView beside;  // mixed: of the 16-row kernel; codes and planes are own's
-    PartView prefix;  // ctas 0: no shared prefix
+    PartView prefix;  // ctas 0: no pass over a shared prefix
     size_t bytes;     // workspace
 };
 

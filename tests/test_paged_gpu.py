@@ -83,6 +83,12 @@ ATTENTION = [
     ([80, 10, 300], [1] * 3, 4, 2, 128, 16, BF, 90, 200),  # windows that end in the prefix, and behind it
     ([80, 10, 300], [20, 10, 200], 4, 2, 64, 64, HF, 50, 129),
     ([12] * 70, [1] * 70, 8, 1, 128, 16, BF, 0, 515),   # more rows of one head than one tile
+    # enough requests, on a long enough prefix, that it gets a pass of its own
+    ([1 + (7 * i) % 90 for i in range(70)], [1] * 70, 8, 2, 128, 64, BF, 0, 2100),
+    ([3 + (5 * i) % 50 for i in range(140)], [1 + i % 3 for i in range(140)], 8, 4, 64, 16, HF, 0, 1001),
+    ([2 * (i % 40) for i in range(90)], [1] * 90, 4, 4, 128, 32, BF, 0, 700),       # some without keys of their own
+    ([4 + (11 * i) % 300 for i in range(80)], [1 + i % 4 for i in range(80)], 4, 4, 64, 128, BF, 260, 1200),
+    ([4 + (11 * i) % 300 for i in range(80)], [1 + i % 2 for i in range(80)], 16, 2, 128, 16, HF, 700, 1500),
 ]
 
 
@@ -139,7 +145,9 @@ def test_long_sequence_among_short_ones(cuda_lib):
 
 
 def test_equal_calls_give_equal_bits(cuda_lib):
-    for case in (([3000, 700, 1], [1] * 3, 8, 2, 128, 64, BF, 0, 500), ([800, 300], [300, 70], 4, 1, 64, 16, HF, 0, 0)):
+    for case in (([3000, 700, 1], [1] * 3, 8, 2, 128, 64, BF, 0, 500), ([800, 300], [300, 70], 4, 1, 64, 16, HF, 0, 0),
+                 ([30, 9] * 40, [1] * 80, 8, 2, 128, 16, BF, 0, 2000), ([800, 30, 900] * 4, [250, 1, 1] + [1] * 9, 8, 2,
+                                                                       128, 64, BF, 0, 0)):
         p = Problem(*case)
         a, b = _run(p), _run(p)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
@@ -183,7 +191,7 @@ def test_prefix_equals_the_same_keys_unshared(cuda_lib):
     check(o, lse, want, p.rows)
 
 
-@pytest.mark.parametrize("new,prefix", [([1, 1], 0), ([40, 3], 0), ([1, 1], 50), ([40, 3], 50)])
+@pytest.mark.parametrize("new,prefix", [([1, 1], 0), ([40, 3], 0), ([1, 1], 50), ([40, 3], 50), ([1, 1], 20000)])
 def test_rows_of_no_request_stay_as_they_are(cuda_lib, new, prefix):
     p = Problem([200, 64], new, 4, 2, 128, 16, BF, 0, prefix, pad_rows=37)
     o = torch.full_like(p.q, 7.0).cuda()
@@ -434,11 +442,11 @@ def test_captured_step_follows_its_inputs(cuda_lib):
 
 
 @pytest.mark.parametrize("new,prefix", [([70, 200, 130], 0), ([300, 1, 1, 2, 1, 1], 0), ([1, 1, 1], 200),
-                                        ([300, 1, 1, 2, 1, 1], 200)])
+                                        ([300, 1, 1, 2, 1, 1], 200), ([1, 2] * 40, 2000)])
 def test_captured_forward_of_every_kernel(cuda_lib, new, prefix):
     """Captured with one problem's values, replayed with another's of the same
     shapes, and next to a graph of the other kernels."""
-    ps = [Problem([n + 37 * i + 90 for i, n in enumerate(new)], new, 8, 2, 128, 16, BF, 0, prefix, seed=s)
+    ps = [Problem([n + 37 * (i % 8) + 90 for i, n in enumerate(new)], new, 8, 2, 128, 16, BF, 0, prefix, seed=s)
           for s in (1, 2)]
     names = ("q", "k_cache", "v_cache", "table", "cu")
     dev = {n: getattr(ps[0], n).cuda() for n in names}
@@ -473,7 +481,7 @@ def test_captured_forward_of_every_kernel(cuda_lib, new, prefix):
 def test_two_streams_at_once(cuda_lib):
     """Two calls in flight on streams of their own (outputs and workspace are
     allocated on the stream that is named)."""
-    ps = [Problem([900, 1200, 77], [1] * 3, 8, 2, 128, 64, BF, 0, 300, seed=1),
+    ps = [Problem([90, 12, 77] * 20, [1] * 60, 8, 2, 128, 64, BF, 0, 2200, seed=1),
           Problem([500, 333], [64, 200], 4, 1, 64, 16, HF, 0, 0, seed=2)]
     want = [p.reference() for p in ps]
     streams = [torch.cuda.Stream() for _ in ps]
