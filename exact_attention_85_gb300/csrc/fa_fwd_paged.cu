@@ -50,11 +50,11 @@ namespace {
 constexpr int kConsumers = 4;  // warps
 constexpr int kFewWarps = kConsumers + 2;  // and two producers
 constexpr int kFewThreads = 32 * kFewWarps;
-// Two CTAs fit an SM, but with 96 KB of copies in flight each, fewer do
-// better: 64 requests of 8-16k keys took 470 us on 304 CTAs, 460 on 260, 458
-// on 228, 473 on 190; 32 requests of 333-7506 keys 89.4, 86.3, 88.8, 92.2.
-constexpr float kCtasPerSm = 1.64f;
-constexpr int kMaxCtas = (int)(kCtasPerSm * kSms);
+// Two CTAs per SM.  Alone, 212 to 304 CTAs do as well (449-454 us for 64
+// requests of 8-16k keys, 81-82 for 32 of 333-7506; 190: 463 and 86); beside
+// the 256-row kernel, where the SMs are the limit, an even two are best (256
+// requests on a 16k prefix: 202 us, 1.64 an SM 214).
+constexpr int kMaxCtas = 2 * kSms;
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;   // units a CTA takes at least
 // A pair costs its tiles and about as much as one more (Q, the merge of the
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         // the kernel beside this one has some of the SMs to itself
         if (!p.mixed && !p.joined && p.a.prefix_len > 0) beside = prefix_work(p.a, prefix_rows(p.a), p.group.d, low);
         if (beside.blocks > 0)
-            most = min(most, (int)(kCtasPerSm * (kSms - wide_sms(beside.units(), tiles, pairs))));
+            most = min(most, 2 * (kSms - wide_sms(beside.units(), tiles, pairs)));
         const long long T = p.whole ? pairs : tiles + pairs * kPairCost;
         const int G = (int)min((long long)most, max(1ll, p.whole ? T : T / kMinUnits));
         const Ranges ranges(T, G);

@@ -115,20 +115,24 @@ __device__ __forceinline__ long long block_tiles(const PagedArgs &a, const Reque
 // memory, so a shared prefix' pass, or the long chunks of a mixed batch, run
 // beside the few-row kernel, each on SMs of its own: the number that the
 // 256-row kernel gets.  Times in us, as measured: a unit of the 256-row
-// kernel takes 1.72 on one SM, with 14 to start and end; a few-row tile (32 KB)
-// 4.8 ns at 6.8 TB/s, or 0.47 us on an SM (70 GB/s) where those are few, and
-// every pair 1.1 us more there, with 6 to start.  (256 requests of 64-2048 keys on a 16k prefix: 235 us with 36
-// SMs, 217 with 46, 233 with 56, 244 with 70; one after the other 272.)  32
+// kernel takes 2.05 on one SM, with 14 to start and end; a few-row pair 0.35
+// and 0.5 a tile on one SM, but at least 1.6, with 6 to start; and no division
+// lets more into the SMs than 32 KB in 4.7 ns, of which a few-row tile is one
+// and a unit of the other kernel two.  Where that limit is what counts, the
+// 256-row kernel gets all SMs that cost the other nothing.  (256 requests of
+// 64-2048 keys on a 16k prefix: 220 us with 48 SMs, 211 with 50, 205 with 58,
+// 202 with 62, 211 with 70, 216 with 76; one after the other 272.)  32
 // candidates, one a lane; each kernel decides for itself, so a difference
 // would cost time only.
 __device__ __forceinline__ int wide_sms(long long wide_units, long long few_tiles, long long few_pairs) {
-    const int g = kSms * ((threadIdx.x & 31) + 1) / 33;
-    const float wide = 14.f + (float)wide_units * 1.72f / (float)g;
-    const float few = 6.f + fmaxf(0.0048f * (float)few_tiles,
-                                  (0.47f * (float)few_tiles + 1.1f * (float)few_pairs) / (float)(kSms - g));
+    const int lane = threadIdx.x & 31, g = kSms * (32 - lane) / 33;
+    const float units = (float)wide_units, tiles = (float)few_tiles, pairs = (float)few_pairs;
+    const float wide = 14.f + units * 2.05f / (float)g;
+    const float few = 6.f + fmaxf(0.0047f * (tiles + 2.f * units),
+                                  fmaxf(0.5f * tiles + 0.35f * pairs, 1.6f * pairs) / (float)(kSms - g));
     // the least of the larger times, and the first to have it
     const uint32_t cost = __float_as_uint(fmaxf(wide, few)) & ~31u;
-    const uint32_t best = __reduce_min_sync(0xffffffffu, cost | (threadIdx.x & 31));
+    const uint32_t best = __reduce_min_sync(0xffffffffu, cost | lane);
     return __shfl_sync(0xffffffffu, g, best & 31);
 }
 
