@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             low = min(low, sums[w].low);
         }
         // the kernel beside this one has some of the SMs to itself
-        if (!p.mixed && !p.joined && p.a.prefix_len > 0) beside = prefix_work(p.a, prefix_rows(p.a), p.group.d, low);
+        if (!p.mixed && !p.joined && p.a.prefix_len > 0) beside = prefix_work(p.a, end_row(p.a), p.group.d, low);
         if (beside.blocks > 0)
             most = min(most, 2 * (kSms - wide_sms(beside.units(), tiles, pairs)));
         const long long T = p.whole ? pairs : tiles + pairs * kPairCost;
@@ -683,12 +683,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
     wait_previous();
     launch_dependents();
     // rows behind the batch's have no part
-    int begin = 0, end = p.a.B;
-    if (p.a.cu_seqlens) {
-        begin = p.a.cu_seqlens[0];
-        end = p.a.cu_seqlens[p.a.B];
-    }
-    const long long id_lo = (long long)begin * p.a.Hq, id_hi = min((long long)rows, (long long)end * p.a.Hq);
+    const long long id_lo = (long long)first_row(p.a) * p.a.Hq, id_hi = (long long)end_row(p.a) * p.a.Hq;
     const long long step = (long long)gridDim.x * (kMergeWarps / W) * RPW;
     long long id = ((long long)blockIdx.x * (kMergeWarps / W) + warp / W) * RPW + lane / LPR;
     int next_own = 0, next_pre = 0;

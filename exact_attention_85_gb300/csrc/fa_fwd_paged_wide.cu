@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefix_lo = min(prefix_lo, sums[w].low);
         }
         if (p.prefix) {
-            whole.n = prefix_rows(p.a);
+            whole.n = end_row(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
         }
         if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));

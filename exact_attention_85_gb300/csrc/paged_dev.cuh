@@ -12,6 +12,11 @@ struct Request {
     int row0, n, len;
 };
 
+// Whether a request may have rows from .. to - 1.
+__device__ __forceinline__ bool sound_rows(const PagedArgs &a, int from, int to) {
+    return from >= 0 && to >= from && to <= a.total && to - from <= a.max_new;
+}
+
 // False if what the device holds for request b breaks the rules of the call
 // (offsets, row bound, length): it then has no rows.
 __device__ __forceinline__ bool load_request(const PagedArgs &a, int b, Request &r) {
@@ -20,7 +25,7 @@ __device__ __forceinline__ bool load_request(const PagedArgs &a, int b, Request 
     if (a.cu_seqlens) {
         r.row0 = a.cu_seqlens[b];
         const int end = a.cu_seqlens[b + 1];
-        if (r.row0 < 0 || end < r.row0 || end > a.total || end - r.row0 > a.max_new) return false;
+        if (!sound_rows(a, r.row0, end)) return false;
         r.n = end - r.row0;
     }
     r.len = a.seq_lens[b];
@@ -80,11 +85,18 @@ __device__ __forceinline__ int range_tiles(int lo, int hi) {
     return max(1, (hi + kWideKeys - 1) / kWideKeys - lo / kWideKeys);
 }
 
-// Rows of the prefix pass: all of the batch.  Offsets that end outside q are
-// reported with their request; the sound ones may have rows anywhere.
-__device__ __forceinline__ int prefix_rows(const PagedArgs &a) {
-    const int n = a.cu_seqlens ? a.cu_seqlens[a.B] : a.B;
-    return n < 0 || n > a.total ? a.total : n;
+// Rows of q that requests have: [first_row, end_row).  Where the first or the
+// last request's offsets break the rules (it is reported, and has no rows),
+// the sound ones may have rows anywhere.
+__device__ __forceinline__ int first_row(const PagedArgs &a) {
+    if (!a.cu_seqlens) return 0;
+    const int from = a.cu_seqlens[0];
+    return sound_rows(a, from, a.cu_seqlens[1]) ? from : 0;
+}
+__device__ __forceinline__ int end_row(const PagedArgs &a) {
+    if (!a.cu_seqlens) return a.B;
+    const int to = a.cu_seqlens[a.B];
+    return sound_rows(a, a.cu_seqlens[a.B - 1], to) ? to : a.total;
 }
 // First key of the prefix that request r's rows see (prefix_len: none).
 __device__ __forceinline__ int prefix_low(const PagedArgs &a, const Request &r) {

@@ -352,7 +352,8 @@ fa_status_t fa_fwd_fp8(const void *q8, const void *k8, const void *v8,
  * on the device: page numbers outside 0 .. num_pages - 1 and lengths that
  * break the rules below are reported by fa_get_device_status as
  * FA_ERR_INVALID_ARG and never read or write out of range; what they concern
- * is left unwritten or unspecified.  None of the pages of the cited articles
+ * is left unwritten or unspecified (offsets that decrease may concern every
+ * request's rows).  None of the pages of the cited articles
  * describes a cache; the attention itself is theirs ([V2] section 6.1).
  */
 

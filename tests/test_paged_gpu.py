@@ -245,6 +245,27 @@ def test_bad_device_values_are_reported(cuda_lib, what, new, prefix):
     assert _lib.fa_get_device_status() == _lib.FA_OK
 
 
+@pytest.mark.parametrize("new,prefix", [([1, 1, 1], 0), ([1, 1, 1], 40), ([1, 1, 1], 80000), ([2, 1, 190], 0),
+                                        ([2, 1, 190], 40), ([90, 70, 80], 0), ([90, 70, 80], 2000)])
+@pytest.mark.parametrize("at,value", [(0, -3), (0, 2 ** 30), (3, -1), (3, 0), (3, 2 ** 31 - 1)])
+def test_bad_outer_offsets_concern_their_request(cuda_lib, at, value, new, prefix):
+    """The first or the last offset bounds the rows of all requests: a wrong
+    one must not cut off those of the others."""
+    p = Problem([150, 90, 200], new, 4, 2, 64, 16, BF, 0, prefix, extra_cols=80)
+    want, cu = p.reference(), p.cu.clone()
+    cu[at] = value
+    tail = (p.table.cuda(), _i32(p.lens), cu.cuda(), p.max_new)
+    args = (p.q.cuda(), p.k_cache.cuda(), p.v_cache.cuda())
+    if prefix:
+        o, lse = fa.attention_fwd_paged_prefix(*args, _i32(p.front), prefix, *tail, scale=p.scale)
+    else:
+        o, lse = fa.attention_fwd_paged(*args, *tail, scale=p.scale)
+    assert _lib.fa_get_device_status() == _lib.FA_ERR_INVALID_ARG
+    lo, hi = (int(p.cu[1]), p.rows) if at == 0 else (0, int(p.cu[2]))
+    check(o[lo:hi], lse[:, lo:hi], (want[0][lo:hi], want[1][:, lo:hi], want[2][lo:hi], want[3][:, lo:hi]), hi - lo)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+
+
 # --------------------------------------------------------------- tables
 
 
