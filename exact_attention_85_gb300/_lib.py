@@ -340,6 +340,13 @@ def _need_numel(**tensors):
             raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
 
 
+def _need_int32(**values):
+    # ctypes would pass the low 32 bits of a larger one
+    for name, x in values.items():
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots, counts,
                     page_size: int, num_pages: int, stream=None):
     """Pages and slots for a step's new tokens; int32 tensors as in fa.h."""
@@ -351,6 +358,7 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, 
               ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
     _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
                 seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
+    _need_int32(page_size=page_size, num_pages=num_pages)
     num_free = free_pages.numel()
     _check("fa_paged_tables", load().fa_paged_tables(
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, _ptr(free_start),
@@ -415,6 +423,7 @@ def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, 
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
+    _need_int32(max_new=max_new, window=window)
     return (o.data_ptr(), lse.data_ptr(), B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages,
             int(window), float(scale), code, None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel())
@@ -435,6 +444,7 @@ def fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, bloc
     """fa_fwd_paged for requests that share their first prefix_len keys."""
     rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window,
                        prefix_pages)
+    _need_int32(prefix_len=prefix_len)
     if prefix_pages.numel() * k_cache.shape[2] < prefix_len:
         raise ValueError(f"prefix_pages: {prefix_pages.numel()} pages of {k_cache.shape[2]} hold fewer than "
                          f"{prefix_len} tokens")

@@ -550,6 +550,23 @@ def test_python_layer_refuses(cuda_lib):
         fa.paged_tables(lens, lens[:1], table, lens, 16, p.num_pages, 2)
 
 
+def test_python_layer_refuses_numbers_past_32_bits(cuda_lib):
+    """The low 32 bits of a number would be another one."""
+    p = Problem([50, 20], [1, 1], 4, 2, 64, 16, BF)
+    args = p.q.cuda(), p.k_cache.cuda(), p.v_cache.cuda()
+    table, lens, pages = p.table.cuda(), _i32(p.lens), _i32([0])
+    for window, most in [(2 ** 32 + 1, 1), (None, 2 ** 32 + 1)]:
+        with pytest.raises(ValueError):
+            fa.attention_fwd_paged(*args, table, lens, p.cu.cuda(), most, window=window)
+        with pytest.raises(ValueError):
+            fa.attention_fwd_paged_prefix(*args, pages, 16, table, lens, p.cu.cuda(), most, window=window)
+    with pytest.raises(ValueError):
+        fa.attention_fwd_paged_prefix(*args, pages, 16 - 2 ** 32, table, lens)
+    for page_size, num_pages in [(2 ** 32 + 16, p.num_pages), (16, 2 ** 32 + p.num_pages)]:
+        with pytest.raises(ValueError):
+            fa.paged_tables(lens, _i32([1, 1]), table, pages, page_size, num_pages, 2)
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """A cache of more than 2^31 elements: slots and pages at its far end."""
     ps, Hkv, d = 256, 8, 128
