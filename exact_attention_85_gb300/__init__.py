@@ -156,15 +156,11 @@ def paged_tables(cached_lens, new_lens, block_table, free_pages, page_size: int,
     the new tokens, row offsets, a slot per row (-1 for rows behind the last
     request and for requests the pool had no pages for), and the next
     ``free_start`` with the number of pages lacking."""
-    import torch
     if stream is not None:
         with _on(stream):
             return paged_tables(cached_lens, new_lens, block_table, free_pages, page_size, num_pages, total, free_start)
-    B, dev, empty, i32 = block_table.shape[0], block_table.device, torch.empty, torch.int32
-    seq_lens = empty(B, dtype=i32, device=dev)
-    cu_seqlens = empty(B + 1, dtype=i32, device=dev)
-    slots = empty(total, dtype=i32, device=dev)
-    counts = empty(2, dtype=i32, device=dev)
+    B, empty = block_table.shape[0], block_table.new_empty
+    seq_lens, cu_seqlens, slots, counts = empty(B), empty(B + 1), empty(total), empty(2)
     _lib.fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots,
                          counts, page_size, num_pages)
     return seq_lens, cu_seqlens, slots, counts

@@ -352,12 +352,26 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, 
     """Pages and slots for a step's new tokens; int32 tensors as in fa.h."""
     import torch
     B, max_pages = block_table.shape
-    i32 = torch.int32
-    _need_all(("block_table", block_table, i32), ("cached_lens", cached_lens, i32), ("new_lens", new_lens, i32),
-              ("free_pages", free_pages, i32), ("free_start", free_start, i32), ("seq_lens", seq_lens, i32),
-              ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
-    _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
-                seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
+    i32, dev = torch.int32, block_table.get_device()
+    # the checks of _need_all and _need_numel in one expression: the kernel
+    # takes some 4 us, so they would be a good part of a call
+    if not (dev >= 0 and dev == torch.cuda.current_device() and block_table.dtype == i32 and block_table.is_contiguous()
+            and cached_lens.get_device() == dev and cached_lens.dtype == i32 and cached_lens.is_contiguous()
+            and new_lens.get_device() == dev and new_lens.dtype == i32 and new_lens.is_contiguous()
+            and free_pages.get_device() == dev and free_pages.dtype == i32 and free_pages.is_contiguous()
+            and seq_lens.get_device() == dev and seq_lens.dtype == i32 and seq_lens.is_contiguous()
+            and cu_seqlens.get_device() == dev and cu_seqlens.dtype == i32 and cu_seqlens.is_contiguous()
+            and slots.get_device() == dev and slots.dtype == i32 and slots.is_contiguous()
+            and counts.get_device() == dev and counts.dtype == i32 and counts.is_contiguous()
+            and (free_start is None or (free_start.get_device() == dev and free_start.dtype == i32
+                                        and free_start.numel() == 1))
+            and cached_lens.numel() == B and new_lens.numel() == B and seq_lens.numel() == B
+            and cu_seqlens.numel() == B + 1 and counts.numel() == 2):
+        _need_all(("block_table", block_table, i32), ("cached_lens", cached_lens, i32), ("new_lens", new_lens, i32),
+                  ("free_pages", free_pages, i32), ("free_start", free_start, i32), ("seq_lens", seq_lens, i32),
+                  ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
+        _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
+                    seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
     _need_int32(page_size=page_size, num_pages=num_pages)
     num_free = free_pages.numel()
     _check("fa_paged_tables", load().fa_paged_tables(
@@ -372,10 +386,16 @@ def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     total, Hkv, d = k.shape
     shape = k_cache.shape
     num_pages, heads, page_size, dc = shape
-    code, dtype = _dtype_code(k), k.dtype
-    _need_all(("k", k, dtype), ("v", v, dtype), ("slots", slots, torch.int32), ("k_cache", k_cache, dtype),
-              ("v_cache", v_cache, dtype))
-    _need_numel(slots=(slots, total))
+    code, dtype, dev = _dtype_code(k), k.dtype, k.get_device()
+    if not (dev >= 0 and dev == torch.cuda.current_device() and k.is_contiguous()
+            and v.get_device() == dev and v.dtype == dtype and v.is_contiguous()
+            and slots.get_device() == dev and slots.dtype == torch.int32 and slots.is_contiguous()
+            and slots.numel() == total
+            and k_cache.get_device() == dev and k_cache.dtype == dtype and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()):
+        _need_all(("k", k, dtype), ("v", v, dtype), ("slots", slots, torch.int32), ("k_cache", k_cache, dtype),
+                  ("v_cache", v_cache, dtype))
+        _need_numel(slots=(slots, total))
     if v.shape != k.shape or v_cache.shape != shape or heads != Hkv or dc != d:
         raise ValueError("k, v must be [total,Hkv,d] and the caches [pages,Hkv,page_size,d] of the same heads")
     _check("fa_paged_append", load().fa_paged_append(
