@@ -507,8 +507,8 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
                                     int page_size, int prefix_len) {
     if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
-        page_size < 1 || prefix_len < 0 || B > FA_PAGED_MAX_B || (long long)B * Hq > 0x7FFFFFFFll || (long long)total * Hq > 0x7FFFFFFFll ||
-        (long long)max_pages * page_size + prefix_len > kMaxKeys)
+        page_size < 1 || prefix_len < 0 || B > FA_PAGED_MAX_B || (long long)B * Hq > 0x7FFFFFFFll ||
+        (long long)total * Hq > 0x7FFFFFFFll || (long long)max_pages * page_size + prefix_len > kMaxKeys)
         return 0;
     return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, 0, nullptr).bytes;
 }

@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         else
                             p.a.lse[(size_t)h * p.a.total + t.row0 + tok] = lse2 * 0.69314718055994530942f;
                         if (!p.whole && (!(t.flags & kPart) || (t.flags & kSlot1)))
-                            p.part.code[out_row] = t.code ? t.code + part_code(0, 0, row) + (p.mixed ? kFewCode : 0) : 0;
+                            p.part.code[out_row] =
+                                t.code ? t.code + part_code(0, 0, row) + (p.mixed ? kFewCode : 0) : 0;
                     }
                 }
                 fence_proxy_async_smem();  // the buffer's next writer is a TMA copy
@@ -645,15 +646,17 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     wait_previous();
 }
 
-// Merges the parts of every row that has several.  A lane has eight columns
-// of a row (32 bytes of a part, 16 of O), so a warp works on 2 rows (d = 128)
-// or 4.  W warps share the parts of their rows, each taking every W-th: one
+// Merges the parts of every row that has several.  A lane has C columns of a
+// row.  C = 8 (32 bytes of a part, 16 of O): a warp works on 2 rows (d = 128)
+// or 4, and W warps share the parts of their rows, each taking every W-th: one
 // where there are many rows, with few parts each, eight where there are few
-// rows that can have many.  What it waits for is two rounds of loads, codes
-// and then parts: up to four parts are in flight, and the next rows' codes.
-// (With a row a warp, and each lane's share of the addresses and weights for
-// 4 columns only, merging 65 thousand rows of 2 parts took 25 us, bound by
-// issue.)
+// rows that can have many.  C = 16 from 16 thousand rows on, twice the rows a
+// warp: what it waits for is two rounds of loads, codes and then parts (up to
+// four or two in flight, and the next rows' codes), and what it issues is
+// mostly addresses and weights, the same for 16 columns as for 8.  (A call of
+// 65 thousand rows, most of two parts: 147 us with 8 columns, 144 with 16; one
+// of 8192 rows with some eight: 200.5 and 203.  A row a warp, 4 columns a
+// lane, took the merge of the first from 12 us to 25.)
 struct MergeParams {
     PagedArgs a;
     PartView own, prefix, beside;
@@ -671,14 +674,15 @@ __device__ __forceinline__ int parts_of(const PartView &v, int code) {
     return pieces < 2 || cta + pieces > v.ctas || slot_row >= v.slot_rows ? 0 : pieces;
 }
 
-// PREFIX: the rows have a shared prefix' parts as well.
-template <int D, bool BF16, bool PREFIX>
+// PREFIX: the rows have a shared prefix' parts as well.  C: columns a lane.
+template <int D, bool BF16, bool PREFIX, int C>
 __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const MergeParams p) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes of a row, rows of a warp
-    constexpr int U = 4;
-    __shared__ float sm_o[kMergeWarps][32][9], sm_top[kMergeWarps][32], sm_sum[kMergeWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = (lane % LPR) * 8;
-    const int W = p.warps, sub = warp % W;
+    constexpr int LPR = D / C, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+    constexpr int U = 32 / C;
+    constexpr bool SHARED = C == 8;  // several warps may share a row's parts
+    __shared__ float sm_o[SHARED ? kMergeWarps : 1][32][9], sm_top[kMergeWarps][32], sm_sum[kMergeWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = (lane % LPR) * C;
+    const int W = SHARED ? p.warps : 1, sub = warp % W;
     const int rows = p.a.total * p.a.Hq;  // 31 bits, as the entry points see to
     wait_previous();
     launch_dependents();
@@ -702,9 +706,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
             n_own = parts_of(c_own & kFewCode ? p.beside : p.own, c_own);
             n_all = n_own + (PREFIX ? parts_of(p.prefix, c_pre) : 0);
         }
-        float acc[8], top = -INFINITY, sum = 0.f;
+        float acc[C], top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int e = 0; e < C; ++e) acc[e] = 0.f;
         // where the parts of a pass begin: piece k is at one plane row, or two slots further each
         auto locate = [&](const PartView &v, int code, const float *&lse2, const float *&o, size_t &stride) {
             const size_t at =
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
         if (PREFIX) locate(p.prefix, c_pre, lse_pre, o_pre, stride_pre);
         for (int k0 = sub; k0 < n_all; k0 += W * U) {
             float lse2[U];
-            float4 x[U][2];
+            uint32_t x[U][C];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int k = k0 + i * W;
@@ -730,25 +734,24 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
                 // piece 0 in slot 1 of its CTA, the others in slot 0 of the next ones
                 const size_t off = piece ? (size_t)(2 * piece - 1) * (own ? stride_own : stride_pre) : 0;
                 lse2[i] = (own ? lse_own : lse_pre)[off];
-                const float4 *o = reinterpret_cast<const float4 *>((own ? o_own : o_pre) + off * D);
-                x[i][0] = o[0];
-                x[i][1] = o[1];
+                const float *o = (own ? o_own : o_pre) + off * D;
+#pragma unroll
+                for (int q = 0; q < C; q += 8) ld_global_v8(x[i] + q, o + q);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 if (lse2[i] == -INFINITY) continue;
                 const float to = fmaxf(top, lse2[i]);
                 const float a = ex2_approx(top - to), w = ex2_approx(lse2[i] - to);
-                const float *v = reinterpret_cast<const float *>(x[i]);
                 sum = fmaf(sum, a, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(acc[e], a, w * v[e]);
+                for (int e = 0; e < C; ++e) acc[e] = fmaf(acc[e], a, w * __uint_as_float(x[i][e]));
                 top = to;
             }
         }
-        if (W > 1) {
+        if (SHARED && W > 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sm_o[warp][lane][e] = acc[e];
+            for (int e = 0; e < C; ++e) sm_o[warp][lane][e] = acc[e];
             sm_top[warp][lane] = top;
             sm_sum[warp][lane] = sum;
             __syncthreads();
@@ -759,20 +762,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 3) paged_merge_kernel(const 
                 const float a = ex2_approx(top - to), w = ex2_approx(t2 - to);
                 sum = sum * a + w * sm_sum[warp + k][lane];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * sm_o[warp + k][lane][e];
+                for (int e = 0; e < C; ++e) acc[e] = acc[e] * a + w * sm_o[warp + k][lane][e];
                 top = to;
             }
             __syncthreads();
         }
         if (n_all == 0 || sub) continue;  // final already, a row of no request, or another warp's to write
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        uint32_t w[4];
+        uint32_t w[C / 2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < C / 2; ++e)
             w[e] = BF16 ? pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv)
                         : pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + (size_t)id * D + col) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        uint4 *const to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + (size_t)id * D + col);
+#pragma unroll
+        for (int q = 0; q < C / 8; ++q) to[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
         if (col == 0) {
             const int tok = (int)id / p.heads, h = (int)id - tok * p.a.Hq;
             p.a.lse[(size_t)h * p.a.total + tok] =
@@ -823,8 +827,13 @@ cudaError_t launch_merge_t(const PagedArgs &a, const PagedPlan &w, cudaStream_t 
     // few rows can have many parts each, many rows have few
     const long long rows = (long long)a.total * a.Hq;
     p.warps = rows <= 1024 ? 8 : rows <= 4096 ? 2 : 1;
-    const long long per_block = kMergeWarps / p.warps * (32 / (D / 8));
-    auto kernel = w.prefix.ctas ? paged_merge_kernel<D, BF16, true> : paged_merge_kernel<D, BF16, false>;
+    const int cols = rows <= 16384 ? 8 : 16;  // as measured: at the kernel
+    const long long per_block = kMergeWarps / p.warps * (32 / (D / cols));
+    auto kernel = paged_merge_kernel<D, BF16, false, 8>;
+    if (w.prefix.ctas)
+        kernel = cols == 8 ? paged_merge_kernel<D, BF16, true, 8> : paged_merge_kernel<D, BF16, true, 16>;
+    else if (cols == 16)
+        kernel = paged_merge_kernel<D, BF16, false, 16>;
     return launch_after(kernel, at_most((rows + per_block - 1) / per_block, 3 * kSms), 32 * kMergeWarps, 0, st, p);
 }
 

@@ -342,6 +342,14 @@ __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), FA_I8(0) : "memory");
 }
 
+// The load of the same: 32 bytes at a 32-byte aligned address.
+__device__ __forceinline__ void ld_global_v8(uint32_t *r, const void *p) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 // ------------------------------------------------------------ arithmetic
 
 __device__ __forceinline__ float ex2_approx(float x) {
