@@ -7,12 +7,13 @@
 #include "paged_dev.cuh"
 #include "status.cuh"
 
+#include <algorithm>
+
 namespace fa {
 
 namespace {
 
 constexpr int kTabThreads = 256;
-constexpr int kRowsPerThread = 4;
 
 struct TablesParams {
     TablesArgs a;
@@ -42,10 +43,15 @@ __device__ __forceinline__ bool request_lens(const TablesParams &p, int b, int &
 // over all requests, and every slot needs both.  A launch of its own for the
 // sums would cost more than the sums: so every block forms them for itself
 // (two integers a request, read from L2) and then writes its share of the
-// slots, looking a row's request up by bisection of cu in shared memory.  No
-// block waits for another: a slot in a page that this call hands out takes
-// the page from the free list, not from the table cell another block writes.
-// Bound by latency, not by its bytes: lengths, then pages, then stores.
+// outputs: requests, handed-out pages and rows, each dealt over all threads of
+// the grid, the request of a page or a row looked up by bisection in shared
+// memory.  No block waits for another: a slot in a page that this call hands
+// out takes the page from the free list, not from the table cell another
+// thread writes.  Bound by latency, not by its bytes: lengths, then pages,
+// then stores (one new token each for 8 requests 2.4 us, for 1024 4.0, 16384
+// 14; one prompt of 500 thousand tokens 4.3).  R: consecutive rows a thread; four (one store, and often one
+// page) where there are rows for every SM's threads, else one.
+template <int R>
 __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesParams p) {
     extern __shared__ int smem[];
     const int B = p.a.B;
@@ -55,7 +61,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     __shared__ long long warp_rows[kTabThreads / 32], warp_need[kTabThreads / 32];
     __shared__ int taken;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (B + kTabThreads - 1) / kTabThreads;
+    const int per = (B + kTabThreads - 1) / kTabThreads | 1;  // odd: neighbouring threads in different banks
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
 
     wait_previous();
@@ -65,13 +71,22 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     const int start = start_ok ? start_in : 0;
     const int room = start_ok ? p.a.num_free - start : 0;
 
-    long long rows = 0, need = 0;
     bool bad = !start_ok;
-    for (int b = b0; b < b1; ++b) {
+#pragma unroll 4
+    for (int b = tid; b < B; b += kTabThreads) {
         int c, n;
         if (!request_lens(p, b, c, n)) bad = true;
-        rows += n;
-        need += pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
+        held[b] = c;
+        cu[b] = n;
+    }
+    __syncthreads();
+    auto pages_needed = [&](int c, int n) {
+        return pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
+    };
+    long long rows = 0, need = 0;
+    for (int b = b0; b < b1; ++b) {
+        rows += cu[b];
+        need += pages_needed(held[b], cu[b]);
     }
     // exclusive sums over the threads: within the warp, then over the warps
     long long r_in = rows, n_in = need;
@@ -101,12 +116,9 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
     }
     if (r_all > p.a.total) bad = true;
     for (int b = b0; b < b1; ++b) {
-        int c, n;
-        request_lens(p, b, c, n);
-        const int nd = pages_of((long long)c + n, p.shift) - pages_of(c, p.shift);
+        const int n = cu[b], nd = pages_needed(held[b], n);
         cu[b] = (int)min(r_at, (long long)p.a.total);
         first[b] = (int)min(n_at, 0x7FFFFFFFll);
-        held[b] = c;
         // the first request that does not fit ends what is taken
         if (nd > 0 && n_at + nd > room) atomicMin(&taken, first[b]);
         r_at += n;
@@ -122,44 +134,47 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
         p.a.counts[1] = all ? 0 : (int)min(n_all - room, 0x7FFFFFFFll);
         p.a.cu_seqlens[B] = cu[B];
     }
-    // lengths, offsets and table cells: a warp per request, dealt over all blocks
-    for (int b = blockIdx.x * (kTabThreads / 32) + warp; b < B; b += gridDim.x * (kTabThreads / 32)) {
-        const int c = held[b], n = cu[b + 1] - cu[b];
-        const int old = pages_of(c, p.shift), nd = pages_of((long long)c + n, p.shift) - old;
-        const bool served = nd == 0 || (long long)first[b] + nd <= room;
-        if (lane == 0) {
-            p.a.seq_lens[b] = served ? c + n : c;
-            p.a.cu_seqlens[b] = cu[b];
+    // the last of the requests whose entry (of cu or first) is at most x
+    auto find = [&](const int *at, int x) {
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (at[mid] <= x) lo = mid; else hi = mid - 1;
         }
-        if (served)
-            for (int i = lane; i < nd; i += 32) {
-                const int page = p.a.free_pages[start + first[b] + i];
-                if (page < 0 || page >= p.a.num_pages) record_bad_args(p.status);
-                p.a.block_table[(size_t)b * p.a.max_pages + old + i] = page;
-            }
+        return lo;
+    };
+    const long long id = (long long)blockIdx.x * kTabThreads + tid, threads = (long long)gridDim.x * kTabThreads;
+    for (long long b = id; b < B; b += threads) {
+        const int c = held[b], n = cu[b + 1] - cu[b];
+        const int nd = pages_needed(c, n);
+        p.a.seq_lens[b] = nd == 0 || (long long)first[b] + nd <= room ? c + n : c;
+        p.a.cu_seqlens[b] = cu[b];
     }
-    // slots: four consecutive rows a thread
-    const long long stride = (long long)gridDim.x * kTabThreads * kRowsPerThread;
-    for (long long r0 = ((long long)blockIdx.x * kTabThreads + tid) * kRowsPerThread; r0 < p.a.total; r0 += stride) {
-        int out[kRowsPerThread];
+    // table cells, by the page's place in the free list
+    const int handed = (int)min(n_all, (long long)min(taken, room));
+    for (long long i = id; i < handed; i += threads) {
+        const int page = p.a.free_pages[start + i];
+        if (page < 0 || page >= p.a.num_pages) record_bad_args(p.status);
+        const int b = find(first, (int)i), c = held[b];
+        const int k = (int)i - first[b];
+        if (k < pages_needed(c, cu[b + 1] - cu[b]))
+            p.a.block_table[(size_t)b * p.a.max_pages + pages_of(c, p.shift) + k] = page;
+    }
+    // slots
+    for (long long r0 = id * R; r0 < p.a.total; r0 += threads * R) {
+        int out[R];
         int b = -1, c = 0, old = 0, page_at = -1, page = -1;
         bool served = false;
 #pragma unroll
-        for (int k = 0; k < kRowsPerThread; ++k) {
+        for (int k = 0; k < R; ++k) {
             const int r = (int)min(r0 + k, (long long)0x7FFFFFFE);
             out[k] = -1;
             if (r >= cu[B]) continue;
             if (b < 0 || r >= cu[b + 1]) {
-                int lo = 0, hi = B - 1;  // the last request that starts at or before r
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (cu[mid] <= r) lo = mid; else hi = mid - 1;
-                }
-                b = lo;
+                b = find(cu, r);
                 c = held[b];
-                const int n = cu[b + 1] - cu[b];
                 old = pages_of(c, p.shift);
-                const int nd = pages_of((long long)c + n, p.shift) - old;
+                const int nd = pages_needed(c, cu[b + 1] - cu[b]);
                 served = nd == 0 || (long long)first[b] + nd <= room;
                 page_at = -1;
             }
@@ -177,10 +192,13 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const TablesP
             }
             if (page >= 0) out[k] = (page << p.shift) + (at & ((1 << p.shift) - 1));
         }
-        if (r0 + kRowsPerThread <= p.a.total)
-            *reinterpret_cast<int4 *>(p.a.slots + r0) = make_int4(out[0], out[1], out[2], out[3]);
-        else
-            for (int k = 0; r0 + k < p.a.total; ++k) p.a.slots[r0 + k] = out[k];
+        if (R == 4 && r0 + 4 <= p.a.total) {
+            *reinterpret_cast<int4 *>(p.a.slots + r0) = make_int4(out[0], out[1 % R], out[2 % R], out[3 % R]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (r0 + k < p.a.total) p.a.slots[r0 + k] = out[k];
+        }
     }
 }
 
@@ -251,10 +269,16 @@ int log2_of(int x) {
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     TablesParams p{a, log2_of(a.page_size), device_status_ptr()};
     const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
-    const long long per_block = kTabThreads * kRowsPerThread;
-    const long long blocks = (a.total + per_block - 1) / per_block;
-    const unsigned grid = (unsigned)(blocks < 4 * kSms ? blocks : 4 * kSms);
-    return launch_after(paged_tables_kernel, grid, kTabThreads, smem, st, p);
+    // Threads for the rows, and for the requests and the pages they can get,
+    // but no more than two blocks an SM: each forms the sums, which is most of
+    // what it issues (1024 prompts, 528 thousand rows: one block an SM 10.9
+    // us, two 8.3, four 10.9).
+    constexpr int kBlocks = 2 * kSms;
+    const int per_thread = a.total > kBlocks * kTabThreads ? 4 : 1;
+    const long long items = std::max((a.total + per_thread - 1ll) / per_thread, a.B + (long long)a.total / a.page_size);
+    const unsigned grid = (unsigned)std::min((items + kTabThreads - 1) / kTabThreads, (long long)kBlocks);
+    return launch_after(per_thread == 4 ? paged_tables_kernel<4> : paged_tables_kernel<1>, grid, kTabThreads, smem, st,
+                        p);
 }
 
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {
