@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             } else {
                 int blocks;
                 sum.beside += block_tiles(p.a, r, p.group.d, blocks);
+                if (p.joined) sum.beside += (long long)blocks * ((p.a.prefix_len - prefix_low(p.a, r)) / kWideKeys);
                 sum.beside_blocks += blocks;
             }
             sum.low = min(sum.low, prefix_low(p.a, r));
@@ -853,13 +854,37 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     const int tile = d == 128 ? 64 : 128;
     const long long pairs = (long long)B * Hkv;
     long long few_tiles = (keys + tile - 1) / tile;
+    // Blocks of the 256-row kernel, at most.
+    const long long most_blocks = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
+    const long long blocks = row_blocks + B < most_blocks ? row_blocks + B : most_blocks;
+    // Where the requests have a quarter of the longest one's rows or less on
+    // average, most are short: the few-row kernel takes those.  512 rows and
+    // 63 single tokens behind 8k keys each took the 256-row kernel alone 436
+    // us, both 349; 4 chunks of 512, where the launch would find nothing, are
+    // left to the one.
+    w.mixed = !w.few && g <= kMaxRows && 4ll * total <= (long long)B * max_new;
     // A small batch reads the prefix as often as it has requests, in the pass
     // over their own keys: one launch less, and two when nothing is divided.
     // What it reads more than once is up to 2000 tiles (64 MB, 10 us).
     const long long front_tiles = (prefix_len + tile - 1ll) / tile;
-    w.joined = w.few && prefix_len > 0 && (long long)Hkv * front_tiles * (B - 1) <= 2000;
+    w.joined = prefix_len > 0 && (w.few || w.mixed ? Hkv * front_tiles * (B - 1) <= 2000 : true);
+    const long long wide_front = (prefix_len + kWideKeys - 1ll) / kWideKeys;
+    if (w.joined && !w.few) {
+        // The 256-row kernel is bound by the tensor cores: the prefix' tiles
+        // cost it the same in either pass, but for blocks that the requests'
+        // own rows do not fill (up to 128 rows cost 0.55 of 256).  Without the
+        // pass, a change of segment (3 tiles) for each of its blocks and four
+        // times the rows' fp32 results are saved, at 5 KB in a tile's time.
+        // (8 chunks of 512 behind 2k keys: 218 us with the pass, 152 without;
+        // 16 of 100 rows behind 8k: 124 and 185.)
+        const double part = (long long)max_new * g <= kWideRows / 2 ? 0.55 : 1.0;
+        const double more = (part * (double)blocks - (double)row_blocks) * (double)(wide_front * Hkv);
+        w.joined = more <= 150.0 + 3.0 * (double)(row_blocks * Hkv) + (double)rows * d / 5000;
+    }
+    long long wide_tiles = (keys + kWideKeys - 1) / kWideKeys;
     if (w.joined) {
         few_tiles += front_tiles;
+        wide_tiles += wide_front;
         prefix_len = 0;
     }
     if (w.few) {
@@ -878,16 +903,8 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         w.own.slot_rows = kMaxRows;
         if (w.whole) return w;  // no workspace
     } else {
-        const long long most = (long long)B * (((long long)max_new * g + kWideRows - 1) / kWideRows);
-        const long long blocks = row_blocks + B < most ? row_blocks + B : most;
-        w.own.ctas = at_most(blocks * Hkv * ((keys + kWideKeys - 1) / kWideKeys), kSms);
+        w.own.ctas = at_most(blocks * Hkv * wide_tiles, kSms);
         w.own.slot_rows = kWideRows;
-        // Where the requests have a quarter of the longest one's rows or less
-        // on average, most are short: the few-row kernel takes those.  512
-        // rows and 63 single tokens behind 8k keys each took the 256-row
-        // kernel alone 436 us, both 349; 4 chunks of 512, where the launch
-        // would find nothing, are left to the one.
-        w.mixed = g <= kMaxRows && 4ll * total <= (long long)B * max_new;
         if (w.mixed) {
             w.beside.ctas = at_most(pairs * few_tiles / kMinUnits, kMaxCtas);
             w.beside.slot_rows = kMaxRows;

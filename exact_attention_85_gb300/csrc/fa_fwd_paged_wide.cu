@@ -61,7 +61,7 @@ struct WideLayout {
     // p_full[2], o_final[2], seg_full[2], seg_empty[2], q_empty, v_clean[VS], drain
     static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
-    static constexpr int OFF_MISC = OFF_SEG + 2 * 48;
+    static constexpr int OFF_MISC = OFF_SEG + 2 * 64;
     static constexpr int OFF_KEPT = OFF_MISC + 16 + kThreads / 32 * (int)sizeof(PlanSum);
     static constexpr int BYTES = OFF_KEPT + kKept * 4;
     static constexpr int ALLOC = BYTES + 1024;
@@ -72,6 +72,7 @@ struct WideParams {
     PagedArgs a;
     FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
+    int joined;  // the kernel's JOINED, for the plan
     int shared;  // the few-row kernel runs at the same time
     int above;   // own pass: only requests of more rows a pair
     int q_box;   // tokens of a 128-row Q tile if the group divides it (TMA), else 0
@@ -86,13 +87,30 @@ struct WideParams {
 struct Segment {
     int row0, n, len;    // rows of q and keys of the request (prefix: of the batch, of the prefix)
     int r0;              // first row of the block, counted in (token, head) pairs
-    int hk, j0, nj;      // key/value head; first key tile, number of them (-1: the end)
-    int key_lo, key_hi;  // keys some row of the block sees
+    int hk, j0, nj;      // key/value head; first of the block's key tiles, number of them (-1: the end)
+    int front, front_lo; // tiles of the shared prefix before its own; first key of those that some row sees
+    int key_lo, key_hi;  // keys of its own (prefix pass: of the prefix) that some row sees
     int code;            // of the block's rows (PartView), 0 if the block is whole
     int slot;            // -1: whole, else the CTA's slot that the part goes to
-    int pad;
+    int pad[3];
 };
-static_assert(sizeof(Segment) == 48, "shared-memory slot");
+static_assert(sizeof(Segment) == 64, "shared-memory slot");
+
+// Key tile i of a segment: the prefix' tiles come first, where JOINED.
+template <bool JOINED>
+struct KeyTile {
+    int kv0, lo, hi;  // first key; keys some row of the block sees
+    bool in_front;
+    __device__ __forceinline__ KeyTile(const Segment &sg, int i, int prefix_len) {
+        const int j = sg.j0 + i;
+        in_front = JOINED && j < sg.front;
+        lo = in_front ? sg.front_lo : sg.key_lo;
+        hi = in_front ? prefix_len : sg.key_hi;
+        kv0 = (lo / kBN + j - (!JOINED || in_front ? 0 : sg.front)) * kBN;
+    }
+    // Whether it holds keys that no row of the block sees.
+    __device__ __forceinline__ bool hides() const { return kv0 < lo || kv0 + kBN > hi; }
+};
 
 // The request of a row of q: the last one that starts at or before it.
 __device__ __forceinline__ int request_of(const PagedArgs &a, int row) {
@@ -121,8 +139,22 @@ __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r
     hi = max(0, r.len - r.n + last + 1);
     lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
 }
-// Whether a key tile holds keys that no row of the block sees.
-__device__ __forceinline__ bool hides(int kv0, int key_lo, int key_hi) { return kv0 < key_lo || kv0 + kBN > key_hi; }
+// Key tiles of the shared prefix that block k sees, and the first key of them.
+__device__ __forceinline__ int block_front(const WideParams &p, const Request &r, int k, int &lo) {
+    lo = 0;
+    if (!p.joined) return 0;
+    if (p.a.window > 0) {
+        const long long at = (long long)p.a.prefix_len + r.len - r.n + (k * kRows) / p.group + 1 - p.a.window;
+        lo = (int)max(0ll, min(at, (long long)p.a.prefix_len));
+    }
+    return lo < p.a.prefix_len ? range_tiles(lo, p.a.prefix_len) : 0;
+}
+// All key tiles of block k.
+__device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, int k, int prefix_lo) {
+    int lo, hi, front_lo;
+    block_keys(p, r, k, prefix_lo, lo, hi);
+    return block_front(p, r, k, front_lo) + range_tiles(lo, hi);
+}
 // Key tiles of all blocks of a request, for one key/value head.  The sums of
 // 32 requests, one a lane: a lane walks its own request's blocks where they
 // are few, the warp walks them together where a request has many.
@@ -138,9 +170,7 @@ __device__ __noinline__ int request_tiles(const WideParams &p, Request r, int nb
             n = __shfl_sync(0xffffffffu, nb, i);
         }
         for (int k = alone ? 0 : lane; k < n; k += alone ? 1 : 32) {
-            int lo, hi;
-            block_keys(p, o, k, 0, lo, hi);
-            mine += range_tiles(lo, hi);
+            mine += tiles_of(p, o, k, 0);
         }
         if (alone) return mine;
         mine = __reduce_add_sync(0xffffffffu, mine);
@@ -149,7 +179,8 @@ __device__ __noinline__ int request_tiles(const WideParams &p, Request r, int nb
     return sum;
 }
 
-template <int D, bool BF16>
+// JOINED: the shared prefix' keys are read with each request's own.
+template <int D, bool BF16, bool JOINED>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const WideParams p) {
@@ -182,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_empty, 1);
         for (int s = 0; s < L::VS; ++s) mbar_init(&v_clean[s], 32 * kHelperWarps);
         for (int s = 0; s < L::KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-        for (int s = 0; s < L::VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1); }
+        for (int s = 0; s < L::VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], JOINED ? 1 + kHelperWarps : 1); }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], kBM);
@@ -208,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto beside = [&](const Request &r) {  // a request of the few-row kernel
             int t;
             sum.beside += pair_tiles<kFewKeys<D>>(p.a, r, t);
+            if (p.joined) sum.beside += (p.a.prefix_len - prefix_low(p.a, r)) / kFewKeys<D>;
             ++sum.beside_blocks;
         };
         if (p.prefix) {
@@ -347,11 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    int lo, hi, units = 0;
-                    if (blk + lane < nb) {
-                        block_keys(p, r, blk + lane, prefix_lo, lo, hi);
-                        units = range_tiles(lo, hi) + cost;
-                    }
+                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) + cost : 0;
                     int incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
@@ -368,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     blk0 += __shfl_sync(0xffffffffu, incl, 31);
                 }
             }
-            const int *table = p.prefix ? p.a.prefix_pages : p.a.block_table + (size_t)b * p.a.max_pages;
+            const int *own_table = p.prefix ? p.a.prefix_pages : p.a.block_table + (size_t)b * p.a.max_pages;
             for (; ok && hk < p.a.Hkv && u < u1; ++hk, blk = 0) {
                 for (; ok && blk < nb && u < u1; ++blk) {
                     Segment sg;
@@ -378,24 +406,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.r0 = blk * kRows;
                     sg.hk = hk;
                     block_keys(p, r, blk, prefix_lo, sg.key_lo, sg.key_hi);
-                    const int nt = range_tiles(sg.key_lo, sg.key_hi);
+                    sg.front = block_front(p, r, blk, sg.front_lo);
+                    const int nt = sg.front + range_tiles(sg.key_lo, sg.key_hi);
                     const long long tile0 = blk0 + cost;  // unit of its first tile
                     const int first = (int)max(0ll, u - tile0), end = (int)min((long long)nt, u1 - tile0);
                     blk0 = tile0 + nt;
                     u = u1 < blk0 ? u1 : blk0;
                     if (end <= first) continue;  // the range ends before the block's first tile
                     const bool is_whole = first == 0 && end == nt;
-                    sg.j0 = sg.key_lo / kBN + first;
+                    sg.j0 = first;
                     sg.nj = end - first;
                     sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
                     // a block that goes on in the next CTA belongs to the one it began in
                     sg.code = sg.slot == 1 ? part_code(ranges.owner(blk0 - 1) - c + 1, c, 0) : 0;
-                    sg.pad = 0;
+                    sg.pad[0] = sg.pad[1] = sg.pad[2] = 0;
                     tell(sg);
                     for (int i = 0; ok && i < sg.nj; ++i) {
                         // pages that hold no key of the block's range are not looked up
-                        const int key0 = (sg.j0 + i) * kBN + sub * page_keys;
-                        const bool live = boxed && key0 < sg.key_hi && key0 + page_keys > sg.key_lo;
+                        const KeyTile<JOINED> tile(sg, i, p.a.prefix_len);
+                        const int *table = tile.in_front ? p.a.prefix_pages : own_table;
+                        const int key0 = tile.kv0 + sub * page_keys;
+                        const bool live = boxed && key0 < tile.hi && key0 + page_keys > tile.lo;
                         int page = 0;
                         if (live) {
                             page = table[key0 >> p.a.shift];
@@ -480,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t cleans = 0;    // a bit per V stage: parity of its clears
             for (int g = 0; ok; ++g) {
                 if (!(ok = wait(&seg_full[g & 1], (g >> 1) & 1, 40))) break;
-                const int nj = segs[g & 1].nj, kv0 = segs[g & 1].j0 * kBN;
-                const int key_lo = segs[g & 1].key_lo, key_hi = segs[g & 1].key_hi;
-                const bool two = segs[g & 1].n * p.group.d - segs[g & 1].r0 > kBM;
+                const Segment sg = segs[g & 1];
+                const int nj = sg.nj;
+                const bool two = sg.n * p.group.d - sg.r0 > kBM;
                 mbar_arrive(&seg_empty[g & 1]);
                 if (nj < 0) break;
                 if (!(ok = wait(q_full, g & 1, 33) && wait(&k_full[u % L::KS], (u / L::KS) & 1, 34))) break;
@@ -495,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < nj; ++i, ++u) {
                     const int vs = u % L::VS, kn = (u + 1) % L::KS, vn = (u + 1) % L::VS;
                     const bool last = i + 1 == nj;
-                    if (hides(kv0 + i * kBN, key_lo, key_hi)) {
+                    if (KeyTile<JOINED>(sg, i, p.a.prefix_len).hides()) {
                         if (!(ok = wait(&v_clean[vs], cleans >> vs & 1, 42))) break;
                         cleans ^= 1u << vs;
                     }
@@ -588,24 +619,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // V rows that no row of the block sees may hold anything (the rest
             // of a page, a buffer that was not filled), and 0 * NaN is NaN:
             // clear them in the tiles that have some, the first and the last
-            for (int i = 0; ok && i < sg.nj; i += max(1, sg.nj - 1)) {
-                const int kv0 = (sg.j0 + i) * kBN;
-                if (!hides(kv0, sg.key_lo, sg.key_hi)) continue;
+            // of each sequence.  The wait for a tile must not take an earlier
+            // filling of its buffer for it: where a prefix ends amid the
+            // tiles, a buffer is refilled only after the helpers have seen
+            // what it held; else the last tile is waited for when the last S
+            // of the segment is through, as the one that the buffer held
+            // before has arrived then.
+            for (int i = 0; ok && i < sg.nj; i += JOINED ? 1 : max(1, sg.nj - 1)) {
+                const KeyTile<JOINED> tile(sg, i, p.a.prefix_len);
                 const int vs = (u + i) % L::VS;
-                // the last S of the segment is through: the tile that the V
-                // buffer held before has arrived then, so the wait below is
-                // for this one
-                got = i == 0 || mbar_wait(q_empty, g & 1, abort_flag, p.status, 46);
-                if (!(ok = __all_sync(0xffffffffu, got))) break;
+                if (!JOINED) {
+                    if (!tile.hides()) continue;
+                    got = i == 0 || mbar_wait(q_empty, g & 1, abort_flag, p.status, 46);
+                    if (!(ok = __all_sync(0xffffffffu, got))) break;
+                }
                 got = mbar_wait(&v_full[vs], ((u + i) / L::VS) & 1, abort_flag, p.status, 45);
                 if (!(ok = __all_sync(0xffffffffu, got))) break;
-                uint4 *v = reinterpret_cast<uint4 *>(smem + L::OFF_V + vs * L::TILE);
-                for (int k = id; k < kBN * 8 * L::NBOX; k += 32 * kHelperWarps) {
-                    const int key = kv0 + ((k >> 3) & (kBN - 1));
-                    if (key < sg.key_lo || key >= sg.key_hi) v[k] = make_uint4(0, 0, 0, 0);
+                if (tile.hides()) {
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + L::OFF_V + vs * L::TILE);
+                    for (int k = id; k < kBN * 8 * L::NBOX; k += 32 * kHelperWarps) {
+                        const int key = tile.kv0 + ((k >> 3) & (kBN - 1));
+                        if (key < tile.lo || key >= tile.hi) v[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&v_clean[vs]);
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&v_clean[vs]);
+                if (JOINED && lane == 0) mbar_arrive(&v_empty[vs]);
             }
             u += sg.nj;
         }
@@ -648,11 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo = p.a.window > 0 ? hi - p.a.window : 0;
                     }
                 } else {
+                    // no window: below every place (a prefix' first key is at -prefix_len)
                     hi = sg.len - sg.n + t + 1;
-                    lo = p.a.window > 0 ? hi - p.a.window : 0;
+                    lo = p.a.window > 0 ? hi - p.a.window : -0x7FFFFFFF;
                 }
             }
-            const int key_lo = sg.key_lo, key_hi = sg.key_hi, nj = sg.nj, j0 = sg.j0;
+            const int nj = sg.nj;
             float m_ref = -INFINITY;
             float l_sum = 0.0f;    // sum of the rounded P fed to the MMA: normalises O
             float l_exact = 0.0f;  // sum of the unrounded P: gives L
@@ -671,7 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait_x32(s + 32);
                 tmem_ld_wait_x32(s + 64);
                 tmem_ld_wait_x32(s + 96);
-                const int kv0 = (j0 + u) * kBN;
+                const KeyTile<JOINED> tile(sg, u, p.a.prefix_len);
+                const int shift = tile.in_front ? p.a.prefix_len : 0;  // the tile's keys as places
+                const int kv0 = tile.kv0 - shift, key_lo = tile.lo - shift, key_hi = tile.hi - shift;
                 if (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo)) {  // uniform in the warp
                     const int top = min(hi, key_hi), low = max(lo, key_lo);
 #pragma unroll
@@ -842,6 +885,7 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.q_box = kBM % g == 0 ? kBM / g : 0;
     if (!make_tmap_rows(&tq, a.q, BF16, D, g, a.Hkv, a.total, p.q_box ? p.q_box : 1)) return cudaErrorInvalidValue;
     p.prefix = prefix ? 1 : 0;
+    p.joined = w.joined ? 1 : 0;
     p.shared = prefix ? w.few : w.mixed;
     p.above = w.mixed ? kMaxRows : 0;
     p.after = after ? 1 : 0;
@@ -849,7 +893,8 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    return launch_after(paged_wide_kernel<D, BF16>, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
+    auto kernel = w.joined ? paged_wide_kernel<D, BF16, true> : paged_wide_kernel<D, BF16, false>;
+    return launch_after(kernel, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
 }
 
 }  // namespace

@@ -137,6 +137,32 @@ def test_many_requests_and_wide_groups(cuda_lib, lens, new, Hq, Hkv, d, ps, pref
     check(*_run(p), p.reference(), p.rows)
 
 
+@pytest.mark.parametrize("lens,new,Hq,Hkv,d,ps,dtype,window,prefix", [
+    # the prefix read with each request's own keys: around tiles and pages of it
+    ([70, 200, 130], [70, 200, 130], 4, 2, 128, 64, BF, 0, 1000),
+    ([100, 300, 40], [33, 120, 40], 3, 1, 64, 256, HF, 0, 129),
+    ([200, 500], [200, 150], 8, 1, 64, 16, BF, 0, 128),
+    ([300, 90], [290, 80], 4, 1, 128, 32, HF, 0, 1),
+    ([3000], [200], 3, 1, 128, 128, BF, 0, 5000),          # divided among CTAs, also within the prefix
+    ([5, 0, 300], [100, 40, 300], 4, 2, 64, 16, BF, 0, 77),  # rows inside the prefix, and before it
+    ([0, 0], [300, 150], 2, 2, 128, 64, HF, 0, 700),
+    ([900, 3, 40, 1, 0, 6], [300, 1, 1, 1, 0, 2], 8, 2, 128, 16, BF, 0, 400),  # by both kernels
+    # windows that end in the prefix, behind it, and, block by block, both
+    ([70, 200, 130], [70, 200, 130], 4, 2, 64, 16, HF, 500, 1000),
+    ([1500], [1500], 2, 1, 128, 64, BF, 200, 500),
+    ([1200, 5], [700, 5], 4, 1, 64, 32, BF, 600, 333),
+    ([900, 3, 40, 1, 0, 6], [300, 1, 1, 1, 0, 2], 8, 2, 64, 64, HF, 350, 400),
+    # a pass of its own over the prefix, before the 256-row kernel's and beside both
+    ([20 + 5 * i for i in range(12)], [9 + i for i in range(12)], 4, 4, 64, 32, BF, 0, 6000),
+    ([20 + 5 * i for i in range(12)], [9 + i for i in range(12)], 12, 4, 128, 16, HF, 4000, 6000),
+    ([150] + [20 + i for i in range(30)], [100] + [1] * 30, 8, 2, 128, 64, BF, 0, 6000),
+    ([150] + [20 + i for i in range(30)], [100] + [1 + i % 3 for i in range(30)], 4, 2, 64, 16, HF, 1000, 9000),
+])
+def test_prefix_of_many_rows(cuda_lib, lens, new, Hq, Hkv, d, ps, dtype, window, prefix):
+    p = Problem(lens, new, Hq, Hkv, d, ps, dtype, window, prefix, seed=3, pad_rows=2, extra_cols=40)
+    check(*_run(p), p.reference(), p.rows)
+
+
 def test_long_sequence_among_short_ones(cuda_lib):
     """One request far longer than the others: its keys are split over many
     blocks and merged, theirs are not."""
