@@ -155,28 +155,36 @@ __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, i
     block_keys(p, r, k, prefix_lo, lo, hi);
     return block_front(p, r, k, front_lo) + range_tiles(lo, hi);
 }
-// Key tiles of all blocks of a request, for one key/value head.  The sums of
-// 32 requests, one a lane: a lane walks its own request's blocks where they
-// are few, the warp walks them together where a request has many.
-__device__ __noinline__ int request_tiles(const WideParams &p, Request r, int nb, int lane) {
-    int sum = 0;
-    const bool alone = !__any_sync(0xffffffffu, nb > 8);
-    for (int i = 0; i < (alone ? 1 : 32); ++i) {
-        Request o = r;
-        int n = nb, mine = 0;
-        if (!alone) {
-            o.n = __shfl_sync(0xffffffffu, r.n, i);
-            o.len = __shfl_sync(0xffffffffu, r.len, i);
-            n = __shfl_sync(0xffffffffu, nb, i);
+// Key tiles of all blocks of a request, for one key/value head (x), and the
+// most that a block has (y).  The sums of 32 requests, one a lane: a lane walks its own
+// request's blocks where they are few, the warp walks them together where a
+// request has many.
+__device__ __noinline__ int2 request_tiles(const WideParams &p, Request r, int nb, int lane) {
+    int sum = 0, longest = 0;
+    if (!__any_sync(0xffffffffu, nb > 8)) {
+        for (int k = 0; k < nb; ++k) {
+            const int tiles = tiles_of(p, r, k, 0);
+            sum += tiles;
+            longest = max(longest, tiles);
         }
-        for (int k = alone ? 0 : lane; k < n; k += alone ? 1 : 32) {
-            mine += tiles_of(p, o, k, 0);
+        return make_int2(sum, longest);
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, nb > 0); left; left &= left - 1) {
+        const int i = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, nb, i);
+        Request o;
+        o.row0 = 0;
+        o.n = __shfl_sync(0xffffffffu, r.n, i);
+        o.len = __shfl_sync(0xffffffffu, r.len, i);
+        int mine = 0;
+        for (int k = lane; k < n; k += 32) {
+            const int tiles = tiles_of(p, o, k, 0);
+            mine += tiles;
+            longest = max(longest, tiles);
         }
-        if (alone) return mine;
         mine = __reduce_add_sync(0xffffffffu, mine);
         if (lane == i) sum = mine;
     }
-    return sum;
+    return make_int2(sum, longest);
 }
 
 // JOINED: the shared prefix' keys are read with each request's own.
@@ -213,7 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_empty, 1);
         for (int s = 0; s < L::VS; ++s) mbar_init(&v_clean[s], 32 * kHelperWarps);
         for (int s = 0; s < L::KS; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-        for (int s = 0; s < L::VS; ++s) { mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], JOINED ? 1 + kHelperWarps : 1); }
+        for (int s = 0; s < L::VS; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], JOINED ? 1 + kHelperWarps : 1);
+        }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
             mbar_init(&p_full[x], kBM);
@@ -261,10 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (r.n > 0) beside(r);
                     r.n = 0;
                 }
-                const int nb = blocks_of(r, p.group), tiles = request_tiles(p, r, nb, lane);
-                sum.tiles += tiles;
+                const int nb = blocks_of(r, p.group);
+                const int2 tiles = request_tiles(p, r, nb, lane);
+                sum.tiles += tiles.x;
+                sum.longest = max(sum.longest, tiles.y);
                 sum.blocks += nb;
-                if (b + lane < kKept) kept[b + lane] = tiles;
+                if (b + lane < kKept) kept[b + lane] = tiles.x;
             }
         }
         sum.tiles = warp_sum(sum.tiles);
@@ -272,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum.blocks = __reduce_add_sync(0xffffffffu, sum.blocks);
         sum.beside_blocks = __reduce_add_sync(0xffffffffu, sum.beside_blocks);
         sum.low = __reduce_min_sync(0xffffffffu, sum.low);
+        sum.longest = __reduce_max_sync(0xffffffffu, sum.longest);
         if (lane == 0) sums[warp] = sum;
     }
     tc_fence_before();
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Request whole{0, 0, p.a.prefix_len};  // the prefix pass: one request of all rows
         WideWork work{0, 0};
         long long few_tiles = 0, few_pairs = 0;
-        int most = gridDim.x, prefix_lo = p.a.prefix_len;
+        int most = gridDim.x, prefix_lo = p.a.prefix_len, longest = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             work.tiles += (long long)sums[w].tiles * p.a.Hkv;
@@ -297,14 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             few_tiles += (long long)sums[w].beside * p.a.Hkv;
             few_pairs += (long long)sums[w].beside_blocks * p.a.Hkv;
             prefix_lo = min(prefix_lo, sums[w].low);
+            longest = max(longest, sums[w].longest);
         }
         if (p.prefix) {
             whole.n = end_row(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
         }
         if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));
-        const int cost = work.block_cost();
-        const long long T = work.units();
+        // Whole blocks only, where every one has a CTA: a cut one costs the
+        // merge of its parts, and a second segment in most CTAs once there are
+        // more tiles than CTAs (measured, us, cut and whole: 16 heads of a
+        // 256-token prompt, blocks of 1 or 2 tiles, 18.2 and 16.3; 512 tokens
+        // of 8 pairs of heads, 1-4, 26.8 and 21.4; of one, as many CTAs as
+        // tiles, 17.4 and 19.2; 32 blocks of 7 or 8, 24.5 and 27.5).
+        const int whole = !p.prefix && work.blocks <= most &&
+                          (work.tiles > most ? (longest - 5ll) * most < work.tiles : longest <= 2);
+        // from one lane: the compiler then sees one value for the warp (0.5 %)
+        const bool by_blocks = __shfl_sync(0xffffffffu, whole, 0);
+        // units of a block: its tiles and what it costs besides, or itself
+        const int cost = by_blocks ? 1 : work.block_cost(), per_tile = by_blocks ? 0 : 1;
+        const long long T = work.tiles * per_tile + work.blocks * cost;
         const int G = (int)min((long long)most, max(1ll, T));
         const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
@@ -339,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Request r{0, 0, 0};
                 if (b + lane < B && !load(b + lane, r)) r.n = 0;
                 const int nb = blocks_of(r, p.group);
-                const int tiles = b >= kKept ? request_tiles(p, r, nb, lane) : b + lane < B ? kept[b + lane] : 0;
-                const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
+                const int tiles = b >= kKept ? request_tiles(p, r, nb, lane).x : b + lane < B ? kept[b + lane] : 0;
+                const long long units = ((long long)tiles * per_tile + nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -372,14 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (!p.prefix) {
                     Request mine{0, 0, 0};
                     if (lane == 0) mine = r;
-                    tiles = __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, lane), 0);
+                    tiles = __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, lane).x, 0);
                 }
-                const int per_head = tiles + nb * cost;
+                const int per_head = tiles * per_tile + nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) + cost : 0;
+                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) * per_tile + cost : 0;
                     int incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
@@ -409,8 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.front = block_front(p, r, blk, sg.front_lo);
                     const int nt = sg.front + range_tiles(sg.key_lo, sg.key_hi);
                     const long long tile0 = blk0 + cost;  // unit of its first tile
-                    const int first = (int)max(0ll, u - tile0), end = (int)min((long long)nt, u1 - tile0);
-                    blk0 = tile0 + nt;
+                    const int first = by_blocks ? 0 : (int)max(0ll, u - tile0);
+                    const int end = by_blocks ? nt : (int)min((long long)nt, u1 - tile0);
+                    blk0 = tile0 + nt * per_tile;
                     u = u1 < blk0 ? u1 : blk0;
                     if (end <= first) continue;  // the range ends before the block's first tile
                     const bool is_whole = first == 0 && end == nt;

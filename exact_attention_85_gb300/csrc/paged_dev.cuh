@@ -113,7 +113,7 @@ __device__ __forceinline__ WideWork prefix_work(const PagedArgs &a, int rows, in
 struct PlanSum {
     unsigned long long tiles, beside;  // of this kernel; of the one that runs beside it
     int blocks, low;                   // row blocks or pairs; first key of the prefix that a row sees
-    int beside_blocks, pad;
+    int beside_blocks, longest;        // longest: tiles of a row block, at most
 };
 
 // Key tiles of a request's row blocks, each counted as if it saw all keys that
