@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 256-token prompt, blocks of 1 or 2 tiles, 18.2 and 16.3; 512 tokens
         // of 8 pairs of heads, 1-4, 26.8 and 21.4; of one, as many CTAs as
         // tiles, 17.4 and 19.2; 32 blocks of 7 or 8, 24.5 and 27.5).
-        const int whole = !p.prefix && work.blocks <= most &&
+        const int uncut = !p.prefix && work.blocks <= most &&
                           (work.tiles > most ? (longest - 5ll) * most < work.tiles : longest <= 2);
         // from one lane: the compiler then sees one value for the warp (0.5 %)
-        const bool by_blocks = __shfl_sync(0xffffffffu, whole, 0);
+        const bool by_blocks = __shfl_sync(0xffffffffu, uncut, 0);
         // units of a block: its tiles and what it costs besides, or itself
         const int cost = by_blocks ? 1 : work.block_cost(), per_tile = by_blocks ? 0 : 1;
         const long long T = work.tiles * per_tile + work.blocks * cost;
