@@ -18,9 +18,10 @@
 // order and every CTA (one per SM) takes an equal, contiguous range, as in
 // the few-row kernel: chunks behind contexts of any lengths then keep all SMs
 // busy to the end, at the price of merging the blocks that a range's border
-// cuts (at most one border a CTA).  The K/V ring, the barriers and the tensor
-// memory carry on from segment to segment; the next segment's Q is loaded
-// and its first S issued before the epilogue of the one before.
+// cuts (at most one border a CTA); where blocks are short, none is cut and a
+// CTA takes those that begin in its range.  The K/V ring, the barriers and
+// the tensor memory carry on from segment to segment; the next segment's Q is
+// loaded and its first S issued before the epilogue of the one before.
 //   warps 0-3 softmax + epilogue of tile A, 4-7 of tile B, 8 producer (plans
 //   the segments and tells the others), 9 MMA issuer (owns the tensor memory),
 //   10-11 helpers (Q, and the V rows that nobody may see)
@@ -318,19 +319,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
         }
         if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));
-        // Whole blocks only, where every one has a CTA: a cut one costs the
-        // merge of its parts, and a second segment in most CTAs once there are
-        // more tiles than CTAs (measured, us, cut and whole: 16 heads of a
-        // 256-token prompt, blocks of 1 or 2 tiles, 18.2 and 16.3; 512 tokens
-        // of 8 pairs of heads, 1-4, 26.8 and 21.4; of one, as many CTAs as
-        // tiles, 17.4 and 19.2; 32 blocks of 7 or 8, 24.5 and 27.5).
-        const int uncut = !p.prefix && work.blocks <= most &&
-                          (work.tiles > most ? (longest - 5ll) * most < work.tiles : longest <= 2);
+        // Whole blocks only, each by the CTA in whose range it begins: a cut
+        // one costs the merge of its parts, and a segment more in most CTAs
+        // once there are more tiles than CTAs; a whole one leaves others idle
+        // for what it takes longer than they do.  Measured, us, cut and whole:
+        //   a CTA for each block: 32 blocks of 1 or 2 tiles 18.2 and 16.3, 64
+        //     of 1-4 26.8 and 21.3, of 7 24.2 and 22.4; with as many CTAs as
+        //     tiles 16 of 1-4 17.4 and 19.2, else 32 of 7 or 8 24.5 and 27.5
+        //   several blocks a CTA: 256 of 1-4 36.9 and 34.5, 512 of 4 70 and
+        //     63, 256 of 8 57.8 and 49.5, 640 of 1-10 91.9 and 90.8, 512 of
+        //     12 118.7 and 121.4, 256 of 1-16 55.2 and 68.9
+        const long long loaded = work.tiles + work.blocks * kBlockCost;
+        const bool spare = work.blocks <= most;
+        const int uncut = !p.prefix && (!spare ? longest <= 10
+                                        : work.tiles > most ? (2ll * longest - 7) * most <= 2 * loaded
+                                                            : longest <= 2);
         // from one lane: the compiler then sees one value for the warp (0.5 %)
         const bool by_blocks = __shfl_sync(0xffffffffu, uncut, 0);
-        // units of a block: its tiles and what it costs besides, or itself
-        const int cost = by_blocks ? 1 : work.block_cost(), per_tile = by_blocks ? 0 : 1;
-        const long long T = work.tiles * per_tile + work.blocks * cost;
+        const int cost = by_blocks ? kBlockCost : work.block_cost();
+        const long long T = by_blocks ? loaded : work.units();
         const int G = (int)min((long long)most, max(1ll, T));
         const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
@@ -366,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (b + lane < B && !load(b + lane, r)) r.n = 0;
                 const int nb = blocks_of(r, p.group);
                 const int tiles = b >= kKept ? request_tiles(p, r, nb, lane).x : b + lane < B ? kept[b + lane] : 0;
-                const long long units = ((long long)tiles * per_tile + nb * cost) * p.a.Hkv;
+                const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -400,12 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mine = r;
                     tiles = __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, lane).x, 0);
                 }
-                const int per_head = tiles * per_tile + nb * cost;
+                const int per_head = tiles + nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) * per_tile + cost : 0;
+                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) + cost : 0;
                     int incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
@@ -435,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.front = block_front(p, r, blk, sg.front_lo);
                     const int nt = sg.front + range_tiles(sg.key_lo, sg.key_hi);
                     const long long tile0 = blk0 + cost;  // unit of its first tile
+                    const bool begun = blk0 < u0;  // in the range of the CTA before
                     const int first = by_blocks ? 0 : (int)max(0ll, u - tile0);
-                    const int end = by_blocks ? nt : (int)min((long long)nt, u1 - tile0);
-                    blk0 = tile0 + nt * per_tile;
+                    const int end = !by_blocks ? (int)min((long long)nt, u1 - tile0) : begun ? 0 : nt;
+                    blk0 = tile0 + nt;
                     u = u1 < blk0 ? u1 : blk0;
                     if (end <= first) continue;  // the range ends before the block's first tile
                     const bool is_whole = first == 0 && end == nt;

@@ -74,9 +74,10 @@ __device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, 
 // S with nothing to overlap, last P V and epilogue).  Counted among the units,
 // so that CTAs whose range has many short blocks get fewer tiles.  Where there
 // are only a few tiles for every SM it would only keep SMs idle.
+constexpr int kBlockCost = 3;
 struct WideWork {
     long long tiles, blocks;
-    __device__ __forceinline__ int block_cost() const { return tiles > 4 * kSms ? 3 : 0; }
+    __device__ __forceinline__ int block_cost() const { return tiles > 4 * kSms ? kBlockCost : 0; }
     __device__ __forceinline__ long long units() const { return tiles + blocks * block_cost(); }
 };
 
