@@ -218,8 +218,9 @@ def attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: in
                                window: int | None = None, workspace=None, stream=None):
     """``attention_fwd_paged`` for requests that all begin with the same
     ``prefix_len`` tokens, stored once on ``prefix_pages`` (int32, on the
-    device): the prefix is read once for the whole batch.  ``block_table`` and
-    ``seq_lens`` describe each request's own keys behind it."""
+    device): where that saves work it is read once for the whole batch.
+    ``block_table`` and ``seq_lens`` describe each request's own keys behind
+    it."""
     if stream is not None:
         with _on(stream):
             return attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens,

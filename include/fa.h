@@ -455,7 +455,8 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_cache,
  * request's keys are the prefix' prefix_len tokens and then its own.  The
  * prefix is read once for all rows of the batch (they are the query rows of
  * one tile of its keys), not once per request; only where that would save
- * little (few requests, or a short prefix) it is read with each request's own.
+ * little (few requests, a short prefix, or rows enough to fill such tiles
+ * with one request's) it is read with each request's own.
  *   prefix_pages int32 [ceil(prefix_len / page_size)] (in), prefix_len >= 1
  *   block_table, seq_lens: the requests' own keys only, on pages of their own
  *   Places count from the prefix' start: p = prefix_len + seq_lens[b] - n_b
