@@ -73,7 +73,6 @@ struct WideParams {
     PagedArgs a;
     FastDiv group;  // query heads per key/value head
     int prefix;  // 1: rows of the whole batch against the shared prefix
-    int joined;  // the kernel's JOINED, for the plan
     int shared;  // the few-row kernel runs at the same time
     int above;   // own pass: only requests of more rows a pair
     int q_box;   // tokens of a 128-row Q tile if the group divides it (TMA), else 0
@@ -141,9 +140,10 @@ __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r
     lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
 }
 // Key tiles of the shared prefix that block k sees, and the first key of them.
+template <bool JOINED>
 __device__ __forceinline__ int block_front(const WideParams &p, const Request &r, int k, int &lo) {
     lo = 0;
-    if (!p.joined) return 0;
+    if (!JOINED) return 0;
     if (p.a.window > 0) {
         const long long at = (long long)p.a.prefix_len + r.len - r.n + (k * kRows) / p.group + 1 - p.a.window;
         lo = (int)max(0ll, min(at, (long long)p.a.prefix_len));
@@ -151,26 +151,29 @@ __device__ __forceinline__ int block_front(const WideParams &p, const Request &r
     return lo < p.a.prefix_len ? range_tiles(lo, p.a.prefix_len) : 0;
 }
 // All key tiles of block k.
+template <bool JOINED>
 __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, int k, int prefix_lo) {
     int lo, hi, front_lo;
     block_keys(p, r, k, prefix_lo, lo, hi);
-    return block_front(p, r, k, front_lo) + range_tiles(lo, hi);
+    return block_front<JOINED>(p, r, k, front_lo) + range_tiles(lo, hi);
 }
 // Key tiles of all blocks of a request, for one key/value head (x), and the
-// most that a block has (y).  The sums of 32 requests, one a lane: a lane walks its own
-// request's blocks where they are few, the warp walks them together where a
-// request has many.
+// most that a block has (y).  The sums of 32 requests, one a lane: each lane
+// walks its request's blocks, or the warp one request's after the other's,
+// whichever takes fewer steps.
+template <bool JOINED>
 __device__ __noinline__ int2 request_tiles(const WideParams &p, Request r, int nb, int lane) {
     int sum = 0, longest = 0;
-    if (!__any_sync(0xffffffffu, nb > 8)) {
+    const unsigned some = __ballot_sync(0xffffffffu, nb > 0);
+    if ((int)__reduce_max_sync(0xffffffffu, nb) <= __popc(some)) {
         for (int k = 0; k < nb; ++k) {
-            const int tiles = tiles_of(p, r, k, 0);
+            const int tiles = tiles_of<JOINED>(p, r, k, 0);
             sum += tiles;
             longest = max(longest, tiles);
         }
         return make_int2(sum, longest);
     }
-    for (unsigned left = __ballot_sync(0xffffffffu, nb > 0); left; left &= left - 1) {
+    for (unsigned left = some; left; left &= left - 1) {
         const int i = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, nb, i);
         Request o;
         o.row0 = 0;
@@ -178,7 +181,7 @@ __device__ __noinline__ int2 request_tiles(const WideParams &p, Request r, int n
         o.len = __shfl_sync(0xffffffffu, r.len, i);
         int mine = 0;
         for (int k = lane; k < n; k += 32) {
-            const int tiles = tiles_of(p, o, k, 0);
+            const int tiles = tiles_of<JOINED>(p, o, k, 0);
             mine += tiles;
             longest = max(longest, tiles);
         }
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto beside = [&](const Request &r) {  // a request of the few-row kernel
             int t;
             sum.beside += pair_tiles<kFewKeys<D>>(p.a, r, t);
-            if (p.joined) sum.beside += (p.a.prefix_len - prefix_low(p.a, r)) / kFewKeys<D>;
+            if (JOINED) sum.beside += (p.a.prefix_len - prefix_low(p.a, r)) / kFewKeys<D>;
             ++sum.beside_blocks;
         };
         if (p.prefix) {
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.n = 0;
                 }
                 const int nb = blocks_of(r, p.group);
-                const int2 tiles = request_tiles(p, r, nb, lane);
+                const int2 tiles = request_tiles<JOINED>(p, r, nb, lane);
                 sum.tiles += tiles.x;
                 sum.longest = max(sum.longest, tiles.y);
                 sum.blocks += nb;
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Request r{0, 0, 0};
                 if (b + lane < B && !load(b + lane, r)) r.n = 0;
                 const int nb = blocks_of(r, p.group);
-                const int tiles = b >= kKept ? request_tiles(p, r, nb, lane).x : b + lane < B ? kept[b + lane] : 0;
+                const int tiles = b >= kKept ? request_tiles<JOINED>(p, r, nb, lane).x : b + lane < B ? kept[b + lane] : 0;
                 const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
@@ -405,14 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (!p.prefix) {
                     Request mine{0, 0, 0};
                     if (lane == 0) mine = r;
-                    tiles = __shfl_sync(0xffffffffu, request_tiles(p, mine, lane == 0 ? nb : 0, lane).x, 0);
+                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED>(p, mine, lane == 0 ? nb : 0, lane).x, 0);
                 }
                 const int per_head = tiles + nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    const int units = blk + lane < nb ? tiles_of(p, r, blk + lane, prefix_lo) + cost : 0;
+                    const int units = blk + lane < nb ? tiles_of<JOINED>(p, r, blk + lane, prefix_lo) + cost : 0;
                     int incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.r0 = blk * kRows;
                     sg.hk = hk;
                     block_keys(p, r, blk, prefix_lo, sg.key_lo, sg.key_hi);
-                    sg.front = block_front(p, r, blk, sg.front_lo);
+                    sg.front = block_front<JOINED>(p, r, blk, sg.front_lo);
                     const int nt = sg.front + range_tiles(sg.key_lo, sg.key_hi);
                     const long long tile0 = blk0 + cost;  // unit of its first tile
                     const bool begun = blk0 < u0;  // in the range of the CTA before
@@ -920,7 +923,6 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.q_box = kBM % g == 0 ? kBM / g : 0;
     if (!make_tmap_rows(&tq, a.q, BF16, D, g, a.Hkv, a.total, p.q_box ? p.q_box : 1)) return cudaErrorInvalidValue;
     p.prefix = prefix ? 1 : 0;
-    p.joined = w.joined ? 1 : 0;
     p.shared = prefix ? w.few : w.mixed;
     p.above = w.mixed ? kMaxRows : 0;
     p.after = after ? 1 : 0;
