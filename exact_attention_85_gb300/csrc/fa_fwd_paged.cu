@@ -877,8 +877,9 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         // times the rows' fp32 results are saved, at 5 KB in a tile's time.
         // (8 chunks of 512 behind 2k keys: 218 us with the pass, 152 without;
         // 16 of 100 rows behind 8k: 124 and 185.)
-        const double part = (long long)max_new * g <= kWideRows / 2 ? 0.55 : 1.0;
-        const double more = (part * (double)blocks - (double)row_blocks) * (double)(wide_front * Hkv);
+        auto part = [](long long n) { return n <= kWideRows / 2 ? 0.55 : 1.0; };
+        const double more = (part((long long)max_new * g) * (double)blocks -
+                             part((long long)total * g) * (double)row_blocks) * (double)(wide_front * Hkv);
         w.joined = more <= 150.0 + 3.0 * (double)(row_blocks * Hkv) + (double)rows * d / 5000;
     }
     long long wide_tiles = (keys + kWideKeys - 1) / kWideKeys;

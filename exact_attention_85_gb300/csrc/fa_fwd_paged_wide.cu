@@ -334,9 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         //     12 118.7 and 121.4, 256 of 1-16 55.2 and 68.9
         const long long loaded = work.tiles + work.blocks * kBlockCost;
         const bool spare = work.blocks <= most;
-        const int uncut = !p.prefix && (!spare ? longest <= 10
-                                        : work.tiles > most ? (2ll * longest - 7) * most <= 2 * loaded
-                                                            : longest <= 2);
+        const int uncut = !p.prefix && longest > 1 &&
+                          (!spare              ? longest <= 10
+                           : work.tiles > most ? (2ll * longest - 7) * most <= 2 * loaded
+                                               : longest <= 2);
         // from one lane: the compiler then sees one value for the warp (0.5 %)
         const bool by_blocks = __shfl_sync(0xffffffffu, uncut, 0);
         const int cost = by_blocks ? kBlockCost : work.block_cost();
