@@ -342,6 +342,17 @@ def test_tables_random(cuda_lib, seed):
     _tables_case(cached, new, ps, r.choice([need, need + 3, need // 2]), total=sum(new) + r.choice([1, 50]), seed=seed)
 
 
+@pytest.mark.parametrize("cached,new,page_size,free,total", [
+    ([10, 0, 5], [10, 17, 1], 16, 2, 30),                          # the last needs no page, the one before gets none
+    ([3] * 400, [200 + i % 7 for i in range(400)], 16, 5200, 81203),  # four rows a thread, the last one's fewer
+    ([3] * 400, [200 + i % 7 for i in range(400)], 16, 3000, 81203),  # and a pool that runs out on the way
+    ([7], [200000], 16, 12600, 200001),                            # one prompt of many pages
+    ([16 * (i % 9) + 15 for i in range(1024)], [i % 3 for i in range(1024)], 16, 300, 1100),
+])
+def test_tables_over_the_whole_grid(cuda_lib, cached, new, page_size, free, total):
+    _tables_case(cached, new, page_size, free, total=total)
+
+
 def test_tables_most_requests(cuda_lib):
     B = 16384
     _tables_case([i % 40 for i in range(B)], [(7 * i) % 5 for i in range(B)], 16, B)
