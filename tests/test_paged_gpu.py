@@ -292,6 +292,19 @@ def test_bad_outer_offsets_concern_their_request(cuda_lib, at, value, new, prefi
     assert _lib.fa_get_device_status() == _lib.FA_OK
 
 
+@pytest.mark.parametrize("lens,new,prefix", [([150, 90, 200], [1, 1, 1], 40), ([150, 90, 200], [1, 1, 1], 80000),
+                                             ([150, 90, 200], [90, 70, 80], 2000), ([30] * 12, [20] * 12, 6000)])
+@pytest.mark.parametrize("page", [-1, 10 ** 6, 2 ** 31 - 1])
+def test_bad_prefix_pages_are_reported(cuda_lib, lens, new, prefix, page):
+    p = Problem(lens, new, 4, 2, 64, 16, BF, 0, prefix, extra_cols=80)
+    good = list(p.front)
+    p.front[len(good) // 2] = page
+    _call(p)
+    assert _lib.fa_get_device_status() == _lib.FA_ERR_INVALID_ARG
+    p.front = good
+    check(*_run(p), p.reference(), p.rows)
+
+
 # --------------------------------------------------------------- tables
 
 
