@@ -372,7 +372,8 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, 
                   ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
         _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
                     seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
-    _need_int32(page_size=page_size, num_pages=num_pages)
+    if not (0 < page_size <= 0x7FFFFFFF and 0 < num_pages <= 0x7FFFFFFF):
+        _need_int32(page_size=page_size, num_pages=num_pages)
     num_free = free_pages.numel()
     _check("fa_paged_tables", load().fa_paged_tables(
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, _ptr(free_start),
@@ -443,7 +444,8 @@ def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, 
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
-    _need_int32(max_new=max_new, window=window)
+    if not (0 < max_new <= 0x7FFFFFFF and 0 <= window <= 0x7FFFFFFF):
+        _need_int32(max_new=max_new, window=window)
     return (o.data_ptr(), lse.data_ptr(), B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages,
             int(window), float(scale), code, None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel())
