@@ -268,7 +268,7 @@ int log2_of(int x) {
 
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     TablesParams p{a, log2_of(a.page_size), device_status_ptr()};
-    const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
+    auto smem = [](size_t requests) { return (3 * requests + 1) * sizeof(int); };
     // Threads for the rows, and for the requests and the pages they can get,
     // but no more than two blocks an SM: each forms the sums, which is most of
     // what it issues (1024 prompts, 528 thousand rows: one block an SM 10.9
@@ -277,8 +277,8 @@ cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st) {
     const int per_thread = a.total > kBlocks * kTabThreads ? 4 : 1;
     const long long items = std::max((a.total + per_thread - 1ll) / per_thread, a.B + (long long)a.total / a.page_size);
     const unsigned grid = (unsigned)std::min((items + kTabThreads - 1) / kTabThreads, (long long)kBlocks);
-    return launch_after(per_thread == 4 ? paged_tables_kernel<4> : paged_tables_kernel<1>, grid, kTabThreads, smem, st,
-                        p);
+    return launch_after(per_thread == 4 ? paged_tables_kernel<4> : paged_tables_kernel<1>, grid, kTabThreads,
+                        DynSmem(smem(a.B), smem(FA_PAGED_TABLES_MAX_B)), st, p);
 }
 
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st) {

@@ -56,22 +56,35 @@ bool make_tmap_pages_4d(CUtensorMap *map, const void *base, bool bf16, int d, in
 // (column, row of the group, group, token).  group * tokens at most 256.
 bool make_tmap_rows(CUtensorMap *map, const void *base, bool bf16, int d, int group, int heads, int total, int tokens);
 
+// Dynamic shared memory of a launch.  What a kernel may ask for is an
+// attribute of the kernel, seen by every thread: where the bytes depend on
+// the call, each call sets it to the `most` that any has, so that a call
+// beside it finds its own still allowed.
+struct DynSmem {
+    size_t bytes, most;
+    DynSmem(size_t n) : bytes(n), most(n) {}
+    DynSmem(size_t n, size_t most_) : bytes(n), most(most_) {}
+};
+
 // Launches `kernel` with `smem` bytes of dynamic shared memory, allowed to
 // start before the stream's previous kernel has finished (programmatic
 // dependent launch): at its end, or once all its CTAs have said so.  The
 // kernel waits for it (griddepcontrol.wait) before it touches memory, so that
 // only launch and set-up overlap.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, DynSmem smem, cudaStream_t st,
                          const A &...args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // A kernel gets 48 KB without being asked, its static bytes among them:
+    // 16 KB are left for those.
+    if (smem.bytes > 32 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem.most);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem.bytes;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
