@@ -45,7 +45,10 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
 
-constexpr int kKept = 256;  // requests whose tile counts the producer finds in shared memory (a multiple of 32)
+// Requests whose tile counts the producer finds in shared memory (a multiple
+// of 32), in 32 bits each: there is no room for 64.  It forms larger ones anew.
+constexpr int kKept = 256;
+constexpr unsigned kMany = 0xFFFFFFFFu;
 
 template <int D>
 struct WideLayout {
@@ -123,32 +126,18 @@ __device__ __forceinline__ int request_of(const PagedArgs &a, int row) {
     return lo;
 }
 
-// Row blocks of a request, and the keys that block k of it sees.
-__device__ __forceinline__ int blocks_of(const Request &r, const FastDiv &group) {
-    return (int)(((unsigned)(r.n * group.d) + kRows - 1) / kRows);
-}
+// Keys that block k of a request sees: its own, or the prefix' in that pass.
 __device__ __forceinline__ void block_keys(const WideParams &p, const Request &r, int k, int prefix_lo, int &lo,
                                            int &hi) {
-    if (p.prefix) {
-        lo = prefix_lo;
-        hi = r.len;
-        return;
-    }
-    const int first = (k * kRows) / p.group;
-    const int last = (r.n * p.group.d - k * kRows > kRows ? (k + 1) * kRows - 1 : r.n * p.group.d - 1) / p.group;
-    hi = max(0, r.len - r.n + last + 1);
-    lo = p.a.window > 0 ? max(0, r.len - r.n + first + 1 - p.a.window) : 0;
+    lo = prefix_lo;
+    hi = r.len;
+    if (!p.prefix) block_keys(p.a, p.group, r, k, lo, hi);
 }
 // Key tiles of the shared prefix that block k sees, and the first key of them.
 template <bool JOINED>
 __device__ __forceinline__ int block_front(const WideParams &p, const Request &r, int k, int &lo) {
     lo = 0;
-    if (!JOINED) return 0;
-    if (p.a.window > 0) {
-        const long long at = (long long)p.a.prefix_len + r.len - r.n + (k * kRows) / p.group + 1 - p.a.window;
-        lo = (int)max(0ll, min(at, (long long)p.a.prefix_len));
-    }
-    return lo < p.a.prefix_len ? range_tiles(lo, p.a.prefix_len) : 0;
+    return JOINED ? block_front(p.a, p.group, r, k, lo) : 0;
 }
 // All key tiles of block k.
 template <bool JOINED>
@@ -157,21 +146,21 @@ __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, i
     block_keys(p, r, k, prefix_lo, lo, hi);
     return block_front<JOINED>(p, r, k, front_lo) + range_tiles(lo, hi);
 }
-// Key tiles of all blocks of a request, for one key/value head (x), and the
-// most that a block has (y).  The sums of 32 requests, one a lane: each lane
-// walks its request's blocks, or the warp one request's after the other's,
-// whichever takes fewer steps.
+// Key tiles of all blocks of a request, for one key/value head, and the most
+// that a block has.
+struct RequestTiles {
+    long long sum;
+    int longest;
+};
+// The sums of 32 requests, one a lane: each lane walks its request's blocks,
+// or the warp one request's after the other's, whichever takes fewer steps.
 template <bool JOINED>
-__device__ __noinline__ int2 request_tiles(const WideParams &p, Request r, int nb, int lane) {
-    int sum = 0, longest = 0;
+__device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request r, int nb, int lane) {
+    RequestTiles t{0, 0};
     const unsigned some = __ballot_sync(0xffffffffu, nb > 0);
     if ((int)__reduce_max_sync(0xffffffffu, nb) <= __popc(some)) {
-        for (int k = 0; k < nb; ++k) {
-            const int tiles = tiles_of<JOINED>(p, r, k, 0);
-            sum += tiles;
-            longest = max(longest, tiles);
-        }
-        return make_int2(sum, longest);
+        t.sum = blocks_tiles<JOINED>(p.a, p.group, r, 0, nb, 1, t.longest);
+        return t;
     }
     for (unsigned left = some; left; left &= left - 1) {
         const int i = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, nb, i);
@@ -179,16 +168,10 @@ __device__ __noinline__ int2 request_tiles(const WideParams &p, Request r, int n
         o.row0 = 0;
         o.n = __shfl_sync(0xffffffffu, r.n, i);
         o.len = __shfl_sync(0xffffffffu, r.len, i);
-        int mine = 0;
-        for (int k = lane; k < n; k += 32) {
-            const int tiles = tiles_of<JOINED>(p, o, k, 0);
-            mine += tiles;
-            longest = max(longest, tiles);
-        }
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == i) sum = mine;
+        const long long sum = warp_count(blocks_tiles<JOINED>(p.a, p.group, o, lane, n, 32, t.longest));
+        if (lane == i) t.sum = sum;
     }
-    return make_int2(sum, longest);
+    return t;
 }
 
 // JOINED: the shared prefix' keys are read with each request's own.
@@ -217,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
-    int *kept = reinterpret_cast<int *>(smem + L::OFF_KEPT);
+    unsigned *kept = reinterpret_cast<unsigned *>(smem + L::OFF_KEPT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -277,11 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.n = 0;
                 }
                 const int nb = blocks_of(r, p.group);
-                const int2 tiles = request_tiles<JOINED>(p, r, nb, lane);
-                sum.tiles += tiles.x;
-                sum.longest = max(sum.longest, tiles.y);
+                const RequestTiles tiles = request_tiles<JOINED>(p, r, nb, lane);
+                sum.tiles += tiles.sum;
+                sum.longest = max(sum.longest, tiles.longest);
                 sum.blocks += nb;
-                if (b + lane < kKept) kept[b + lane] = tiles.x;
+                if (b + lane < kKept) kept[b + lane] = (unsigned)min(tiles.sum, (long long)kMany);
             }
         }
         sum.tiles = warp_sum(sum.tiles);
@@ -376,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Request r{0, 0, 0};
                 if (b + lane < B && !load(b + lane, r)) r.n = 0;
                 const int nb = blocks_of(r, p.group);
-                const int tiles = b >= kKept ? request_tiles<JOINED>(p, r, nb, lane).x : b + lane < B ? kept[b + lane] : 0;
-                const long long units = ((long long)tiles + nb * cost) * p.a.Hkv;
+                const unsigned held = b >= kKept ? kMany : b + lane < B ? kept[b + lane] : 0;
+                long long tiles = held;
+                if (__any_sync(0xffffffffu, held == kMany)) tiles = request_tiles<JOINED>(p, r, nb, lane).sum;
+                const long long units = (tiles + (long long)nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
                 for (int s = 1; s < 32; s <<= 1) {
@@ -403,15 +388,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!load(b, r)) continue;
             const int nb = blocks_of(r, p.group);
             if (fresh) {
-                int tiles = nb * range_tiles(prefix_lo, r.len);
-                if (!p.prefix && b < kKept) {
+                long long tiles = (long long)nb * range_tiles(prefix_lo, r.len);
+                if (!p.prefix && b < kKept && kept[b] != kMany) {
                     tiles = kept[b];
                 } else if (!p.prefix) {
                     Request mine{0, 0, 0};
                     if (lane == 0) mine = r;
-                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED>(p, mine, lane == 0 ? nb : 0, lane).x, 0);
+                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED>(p, mine, lane == 0 ? nb : 0, lane).sum, 0);
                 }
-                const int per_head = tiles + nb * cost;
+                const long long per_head = tiles + (long long)nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time

@@ -32,14 +32,26 @@ __device__ __forceinline__ bool load_request(const PagedArgs &a, int b, Request 
     return r.len >= 0 && r.len <= (a.max_pages << a.shift);
 }
 
-__device__ __forceinline__ int operator/(int x, const FastDiv &f) {
+__host__ __device__ __forceinline__ int operator/(int x, const FastDiv &f) {
+#ifdef __CUDA_ARCH__
     return (int)((__umulhi((uint32_t)x, f.mul) + (uint32_t)x) >> f.shift);
+#else
+    return x / f.d;
+#endif
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
 #pragma unroll
     for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
     return x;
+}
+
+// Sum of the lanes' counts, each below 2^48 and all of them below 2^56: in
+// two halves, as there is no 64-bit reduction.
+__device__ __forceinline__ long long warp_count(long long x) {
+    const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)x & 0xFFFFFFu);
+    const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)(x >> 24));
+    return ((long long)hi << 24) + lo;
 }
 
 // [u0, u1): the units of CTA c of G that share T units, and the CTA that has
@@ -82,8 +94,50 @@ struct WideWork {
 };
 
 // Key tiles of a range; at least one.
-__device__ __forceinline__ int range_tiles(int lo, int hi) {
+__host__ __device__ __forceinline__ int range_tiles(int lo, int hi) {
     return max(1, (hi + kWideKeys - 1) / kWideKeys - lo / kWideKeys);
+}
+
+// Row blocks of a request in the 256-row kernel, and its own keys that block
+// k of it sees.
+__host__ __device__ __forceinline__ int blocks_of(const Request &r, const FastDiv &group) {
+    return (int)(((unsigned)(r.n * group.d) + kWideRows - 1) / kWideRows);
+}
+__host__ __device__ __forceinline__ void block_keys(const PagedArgs &a, const FastDiv &group, const Request &r, int k,
+                                                    int &lo, int &hi) {
+    const int first = (k * kWideRows) / group;
+    const int last =
+        (r.n * group.d - k * kWideRows > kWideRows ? (k + 1) * kWideRows - 1 : r.n * group.d - 1) / group;
+    hi = max(0, r.len - r.n + last + 1);
+    lo = a.window > 0 ? max(0, r.len - r.n + first + 1 - a.window) : 0;
+}
+// Key tiles of the shared prefix that block k sees where they are read with
+// its own, and the first key of them.
+__host__ __device__ __forceinline__ int block_front(const PagedArgs &a, const FastDiv &group, const Request &r, int k,
+                                                    int &lo) {
+    lo = 0;
+    if (a.window > 0) {
+        const long long at = (long long)a.prefix_len + r.len - r.n + (k * kWideRows) / group + 1 - a.window;
+        lo = (int)max(0ll, min(at, (long long)a.prefix_len));
+    }
+    return lo < a.prefix_len ? range_tiles(lo, a.prefix_len) : 0;
+}
+// Key tiles of blocks from, from + step, .. below nb of a request, for one
+// key/value head, and the most that one has.  A block's fit 32 bits, but all
+// of a prompt of N tokens are N^2 g / 65536: past 2^31 at 4 million tokens of
+// 8 grouped heads.
+template <bool JOINED>
+__host__ __device__ __forceinline__ long long blocks_tiles(const PagedArgs &a, const FastDiv &group, const Request &r,
+                                                           int from, int nb, int step, int &longest) {
+    long long sum = 0;
+    for (int k = from; k < nb; k += step) {
+        int lo, hi, front_lo;
+        block_keys(a, group, r, k, lo, hi);
+        const int tiles = range_tiles(lo, hi) + (JOINED ? block_front(a, group, r, k, front_lo) : 0);
+        sum += tiles;
+        longest = max(longest, tiles);
+    }
+    return sum;
 }
 
 // Rows of q that requests have: [first_row, end_row).  Where the first or the
