@@ -130,6 +130,7 @@ template <bool JOINED>
 __host__ __device__ __forceinline__ long long blocks_tiles(const PagedArgs &a, const FastDiv &group, const Request &r,
                                                            int from, int nb, int step, int &longest) {
     long long sum = 0;
+#pragma unroll 1  // 8 chunks of 512 on a prefix of 2k: 148.6 us, unrolled 151.6
     for (int k = from; k < nb; k += step) {
         int lo, hi, front_lo;
         block_keys(a, group, r, k, lo, hi);
