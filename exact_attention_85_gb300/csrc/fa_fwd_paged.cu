@@ -528,8 +528,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                             if (k0 + 1 >= k_end || k0 + 1 < k_low) vf[e] &= 0x0000FFFFu;
                         }
                     }
+                    // a product of its own, added in fp32: as an addend of the
+                    // next product the sum would lose up to 2^-26 of itself to
+                    // every term, which the tensor cores cut down to its bits
+                    // (64 requests of a million keys, values of mean 1: 1.0e-3,
+                    // where storing fp16 makes 2.2e-4)
 #pragma unroll
-                    for (int g = 0; g < NT; ++g) mma_16x8x16<BF16>(acc[g][j], vf, pf[i][g][0], pf[i][g][1]);
+                    for (int g = 0; g < NT; ++g) {
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16x8x16<BF16>(t, vf, pf[i][g][0], pf[i][g][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[g][j][e] += t[e];
+                    }
                 }
             }
             if (t.flags & kLast) {
@@ -888,6 +898,11 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         wide_tiles += wide_front;
         prefix_len = 0;
     }
+    // a block of up to 256 tokens sees no more than these under a window, in
+    // the prefix and behind it
+    const long long in_window = window > 0 ? ((long long)window + kWideRows - 1) / kWideKeys + 3 : 1ll << 40;
+    w.own_tiles = wide_tiles < in_window ? wide_tiles : in_window;
+    w.prefix_tiles = wide_front;
     if (w.few) {
         // A CTA takes whole pairs, with nothing to merge, where the second
         // launch (some 4 us) would cost more than dividing them gains: up to
@@ -921,9 +936,11 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
         w.prefix.plane_lse2 = take<float>(at, rows);
         w.prefix.plane = take<float>(at, rows * d);
         w.prefix.slot_lse2 = take<float>(at, (size_t)w.prefix.ctas * 2 * kWideRows);
+        w.prefix.slot_sum = take<float>(at, (size_t)w.prefix.ctas * 2 * kWideRows);
         w.prefix.slot = take<float>(at, (size_t)w.prefix.ctas * 2 * kWideRows * d);
     }
     w.own.slot_lse2 = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows);
+    if (!w.few) w.own.slot_sum = take<float>(at, (size_t)w.own.ctas * 2 * kWideRows);
     w.own.slot = take<float>(at, (size_t)w.own.ctas * 2 * w.own.slot_rows * d);
     if (w.mixed) {
         w.beside.code = w.own.code;

@@ -43,6 +43,16 @@ constexpr int kThreads = 384;
 constexpr int kHelperWarps = 2;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr float kRescaleThreshold = 8.0f;
+// Key tiles of a segment where the table may hold longer blocks (LONG).  The
+// tensor cores cut every product to some 25 bits below the leading one of the
+// sum before they add it, always towards less, so a sum of n terms loses up to
+// n 2^-26 of itself: with 512 rows behind a million keys, values of mean 1, O
+// was off by 4.9e-3, where storing fp16 makes 2.2e-4 and bf16 1.7e-3.  Sums of
+// 2^15 keys (fp16) or 2^17 (bf16) lose a fraction of that; they are added up
+// in fp32, in memory.  A kernel of its own, as the others would be 2 to 3 %
+// slower for it (chunks 143.6 and 147 us).
+template <bool BF16>
+constexpr int kMaxTiles = BF16 ? 1024 : 256;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 per tile
 
 // Requests whose tile counts the producer finds in shared memory (a multiple
@@ -95,8 +105,10 @@ struct Segment {
     int key_lo, key_hi;  // keys of its own (prefix pass: of the prefix) that some row sees
     int code;            // of the block's rows (PartView), 0 if the block is whole
     int slot;            // -1: whole, else the CTA's slot that the part goes to
-    int pad[3];
+    int more;            // kBefore, kBehind: this CTA has tiles of the block before these, and behind them
+    int pad[2];
 };
+enum : int { kBefore = 1, kBehind = 2 };
 static_assert(sizeof(Segment) == 64, "shared-memory slot");
 
 // Key tile i of a segment: the prefix' tiles come first, where JOINED.
@@ -174,8 +186,79 @@ __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request 
     return t;
 }
 
-// JOINED: the shared prefix' keys are read with each request's own.
-template <int D, bool BF16, bool JOINED>
+// Epilogue of a row whose block has more tiles than a segment: adds O and the
+// sum of the segments before, which are in the slot of a part (the block's, or
+// for a whole block the one that the CTA's last block may need afterwards),
+// and leaves them there for the next, or writes the block's result.
+template <int D, bool BF16>
+__device__ __forceinline__ void joint_epilogue(const WideParams &p, uint32_t o_col, bool valid, int slot, int more,
+                                            int code, int row, size_t out_row, size_t lse_at, float m, float l_sum,
+                                            float l_exact) {
+    const size_t slot_at = ((size_t)blockIdx.x * 2 + (slot < 0 ? 1 : slot)) * kRows + row;
+    const bool before = valid && (more & kBefore), behind = more & kBehind;
+    float scale = l_sum > 0.f ? 1.0f / l_sum : 0.f, keep = 0.f;
+    if (before) {
+        const float m0 = p.part.slot_lse2[slot_at], l0 = p.part.slot_sum[slot_at];
+        const float top = fmaxf(m, m0), ref = top == -INFINITY ? 0.f : top;
+        const float a = l_exact * ex2_approx(m - ref), b = l0 * ex2_approx(m0 - ref);
+        m = top;
+        l_exact = a + b;
+        const float inv = l_exact > 0.f ? 1.0f / l_exact : 0.f;
+        scale *= a * inv;
+        keep = b * inv;
+    }
+    const bool to_slot = behind || slot >= 0;
+    float *const to_o = to_slot ? p.part.slot : p.part.plane;
+    const size_t at = to_slot ? slot_at : out_row;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t o[32];
+        tmem_ld_x32(o_col + c0, o);
+        tmem_ld_wait_x32(o);
+#pragma unroll
+        for (int q = 0; q < 32; q += 8) {
+            uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (before) ld_global_v8(x, p.part.slot + slot_at * D + c0 + q);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                o[q + k] = __float_as_uint(fmaf(__uint_as_float(x[k]), keep, __uint_as_float(o[q + k]) * scale));
+        }
+        if (valid && to_o) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) st_global_v8(to_o + at * D + c0 + q, o + q);
+        } else if (valid) {
+            uint4 *const dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.a.o) + at * D + c0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float a = __uint_as_float(o[8 * q + 2 * k]), b = __uint_as_float(o[8 * q + 2 * k + 1]);
+                    w[k] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+                }
+                dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncwarp();  // the loads above are the whole warp's
+    }
+    if (!valid) return;
+    if (behind) {
+        p.part.slot_lse2[slot_at] = m;
+        p.part.slot_sum[slot_at] = l_exact;
+        return;
+    }
+    const float lse2 = l_exact > 0.f ? m + log2f(l_exact) : -INFINITY;
+    float *const to_lse2 = to_slot ? p.part.slot_lse2 : p.part.plane_lse2;
+    if (to_lse2)
+        to_lse2[at] = lse2;
+    else
+        p.a.lse[lse_at] = lse2 * 0.69314718055994530942f;
+    if (slot != 0) p.part.code[out_row] = code ? code + part_code(0, 0, row) : 0;
+}
+
+// JOINED: the shared prefix' keys are read with each request's own.  LONG: a
+// block may have more tiles than a sum should.
+template <int D, bool BF16, bool JOINED, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const WideParams p) {
@@ -443,42 +526,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
                     // a block that goes on in the next CTA belongs to the one it began in
                     sg.code = sg.slot == 1 ? part_code(ranges.owner(blk0 - 1) - c + 1, c, 0) : 0;
-                    sg.pad[0] = sg.pad[1] = sg.pad[2] = 0;
-                    tell(sg);
-                    for (int i = 0; ok && i < sg.nj; ++i) {
-                        // pages that hold no key of the block's range are not looked up
-                        const KeyTile<JOINED> tile(sg, i, p.a.prefix_len);
-                        const int *table = tile.in_front ? p.a.prefix_pages : own_table;
-                        const int key0 = tile.kv0 + sub * page_keys;
-                        const bool live = boxed && key0 < tile.hi && key0 + page_keys > tile.lo;
-                        int page = 0;
-                        if (live) {
-                            page = table[key0 >> p.a.shift];
-                            if (page < 0 || page >= p.a.num_pages) {
-                                record_bad_args(p.status);
-                                page = p.a.num_pages;  // out of the tensor: the copy fills zeros
+                    sg.more = sg.pad[0] = sg.pad[1] = 0;
+                    auto load_tiles = [&] {
+                        tell(sg);
+                        for (int i = 0; ok && i < sg.nj; ++i) {
+                            // pages that hold no key of the block's range are not looked up
+                            const KeyTile<JOINED> tile(sg, i, p.a.prefix_len);
+                            const int *table = tile.in_front ? p.a.prefix_pages : own_table;
+                            const int key0 = tile.kv0 + sub * page_keys;
+                            const bool live = boxed && key0 < tile.hi && key0 + page_keys > tile.lo;
+                            int page = 0;
+                            if (live) {
+                                page = table[key0 >> p.a.shift];
+                                if (page < 0 || page >= p.a.num_pages) {
+                                    record_bad_args(p.status);
+                                    page = p.a.num_pages;  // out of the tensor: the copy fills zeros
+                                }
                             }
+                            const int bytes = __popc(__ballot_sync(0xffffffffu, live)) * box_bytes;
+                            const int in_page = key0 & ((1 << p.a.shift) - 1);
+                            const int ks = nk % L::KS, vs = nv % L::VS;
+                            bool got =
+                                nk < L::KS || mbar_wait(&k_empty[ks], ((nk / L::KS) + 1) & 1, abort_flag, p.status, 31);
+                            if (!(ok = __all_sync(0xffffffffu, got))) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
+                            __syncwarp();
+                            if (live)
+                                tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
+                                            &k_full[ks], half * 64, in_page, page * p.a.Hkv + hk);
+                            ++nk;
+                            got = nv < L::VS || mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
+                            if (!(ok = __all_sync(0xffffffffu, got))) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
+                            __syncwarp();
+                            if (live)
+                                tma_load_3d(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v,
+                                            &v_full[vs], half * 64, in_page, page * p.a.Hkv + hk);
+                            ++nv;
                         }
-                        const int bytes = __popc(__ballot_sync(0xffffffffu, live)) * box_bytes;
-                        const int in_page = key0 & ((1 << p.a.shift) - 1);
-                        const int ks = nk % L::KS, vs = nv % L::VS;
-                        bool got =
-                            nk < L::KS || mbar_wait(&k_empty[ks], ((nk / L::KS) + 1) & 1, abort_flag, p.status, 31);
-                        if (!(ok = __all_sync(0xffffffffu, got))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
-                        __syncwarp();
-                        if (live)
-                            tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
-                                        &k_full[ks], half * 64, in_page, page * p.a.Hkv + hk);
-                        ++nk;
-                        got = nv < L::VS || mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
-                        if (!(ok = __all_sync(0xffffffffu, got))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
-                        __syncwarp();
-                        if (live)
-                            tma_load_3d(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v,
-                                        &v_full[vs], half * 64, in_page, page * p.a.Hkv + hk);
-                        ++nv;
+                    };
+                    if (!LONG) {
+                        load_tiles();
+                        continue;
+                    }
+                    for (; ok && sg.j0 < end; sg.j0 += kMaxTiles<BF16>) {
+                        sg.nj = min(end - sg.j0, kMaxTiles<BF16>);
+                        sg.more = (sg.j0 > first ? kBefore : 0) | (sg.j0 + sg.nj < end ? kBehind : 0);
+                        load_tiles();
                     }
                 }
             }
@@ -826,7 +920,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
-            if (active) {
+            if (LONG && active && sg.more) {
+                const size_t out_row = (size_t)tok * p.a.Hq + head;
+                joint_epilogue<D, BF16>(p, lane_base + col_o, valid, sg.slot, sg.more, sg.code, row, out_row,
+                                        (size_t)head * p.a.total + tok, m_ref, l_sum, l_exact);
+                tc_fence_before();
+            } else if (active) {
                 const float inv_l = l_sum > 0.f ? 1.0f / l_sum : 0.f;
                 const size_t out_row = (size_t)tok * p.a.Hq + head;
                 // whole blocks are final, or go to the plane to be merged with
@@ -916,7 +1015,9 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    auto kernel = w.joined ? paged_wide_kernel<D, BF16, true> : paged_wide_kernel<D, BF16, false>;
+    const bool many = (prefix ? w.prefix_tiles : w.own_tiles) > kMaxTiles<BF16>;
+    auto kernel = w.joined ? (many ? paged_wide_kernel<D, BF16, true, true> : paged_wide_kernel<D, BF16, true, false>)
+                           : (many ? paged_wide_kernel<D, BF16, false, true> : paged_wide_kernel<D, BF16, false, false>);
     return launch_after(kernel, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
 }
 

@@ -66,6 +66,7 @@ struct PartView {
     int *code;                  // [total * Hq]
     float *plane_lse2, *plane;  // [total * Hq] (x d); null where one result is final
     float *slot_lse2, *slot;    // [ctas][2][slot_rows] (x d)
+    float *slot_sum;            // 256-row kernel: of a row that is being worked on (slot_lse2: its maximum)
     int slot_rows, ctas;
 };
 constexpr int kSms = 152;  // of the GPU; the workspace's size must not depend on a query
@@ -83,6 +84,7 @@ struct PagedPlan {
     bool joined;      // the shared prefix' keys too, with each request's own
     bool mixed;       // by both: requests of at most 16 rows (a pair) by the first
     bool whole;       // the 16-row kernel's CTAs take whole pairs only: nothing to merge
+    long long own_tiles, prefix_tiles;  // key tiles of a row block of the 256-row kernel, at most
     PartView own;     // ctas: of the kernel that takes the own keys
     PartView beside;  // mixed: of the 16-row kernel; codes and planes are own's
     PartView prefix;  // ctas 0: no pass over a shared prefix

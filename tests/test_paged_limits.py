@@ -4,8 +4,18 @@ import subprocess
 import sys
 
 import pytest
+import torch
+
+import exact_attention_85_gb300 as fa
+from exact_attention_85_gb300 import _lib
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def _i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
 
 
 # ------------------------------------------- shared memory of the tables
@@ -157,3 +167,80 @@ def test_plan_of_ordinary_requests(plan):
 def test_tiles_of_a_long_request_pass_32_bits(plan, case, tiles):
     assert tiles > 2 ** 31
     assert plan([case])[0][1] == tiles == _plan_by_hand(*case)[1]
+
+
+# ------------------------------------------------------- long sums of O
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,heads,keys,dtype", [
+    (1, 304, 1 << 20, HF),            # few rows: a pair for each block, 2^18 keys a warp
+    (3, 304, (1 << 20) + 77, HF),
+    (1, 304, 1 << 23, BF),
+    (200, 152, 1 << 20, HF),          # many rows: a row block for each SM
+    (40, 152, (1 << 20) + 128 * 256 + 77, HF),
+    (200, 152, 1 << 22, BF),
+    (300, 8, 1 << 22, HF),            # blocks cut among SMs
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sums_keep_small_terms(cuda_lib, rows, heads, keys, dtype, d):
+    """K is 0, so every weight is 1 (or as large as the others), and V is one
+    step s above 1 (2^-10 or 2^-7): O is the same number, and every partial
+    sum of up to 2^15 keys (fp16; 2^17 bf16) is a multiple of s below 2^16
+    (2^18), exact in 26 bits.  A sum of 2^25 s keys and more that is an addend
+    of the tensor cores' next product loses the s of every term."""
+    ps, step = 256, torch.finfo(dtype).eps
+    kc = torch.zeros(2, heads, ps, d, dtype=dtype, device="cuda")
+    vc = torch.full_like(kc, 1 + step)
+    table = (torch.arange(-(-keys // ps), dtype=torch.int32, device="cuda") % 2)[None].contiguous()
+    q = torch.randn(rows, heads, d, device="cuda").to(dtype)
+    o, lse = fa.attention_fwd_paged(q, kc, vc, table, _i32([keys]), _i32([0, rows]), rows)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    want = torch.log(torch.arange(keys - rows + 1, keys + 1, dtype=torch.float64, device="cuda"))
+    assert (lse.double() - want).abs().max() <= 2.0 ** -22 * (1 + want.max()) + 2.0 ** -23
+    assert (o == 1 + step).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,heads,window,prefix", [(200, 152, 0, 0), (40, 152, 50_000, 0), (150, 8, 0, 100_000),
+                                                      (1, 304, 0, 70_000)])
+def test_growing_scores_over_many_tiles(cuda_lib, rows, heads, window, prefix):
+    """Scores that rise through the sequence, so that what was summed is
+    scaled down again and again, before and after it leaves the tensor
+    cores' memory: against 64 bits."""
+    ps, d, keys = 256, 64, 150_000
+    pages, front = -(-keys // ps), -(-prefix // ps)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    # key j is (j / 2000, 0, ..) and q (1, 0, ..) * sqrt(d): score j / 2000 of all keys
+    place = torch.arange((pages + front) * ps, device="cuda", dtype=torch.float64)
+    at = torch.where(place < front * ps, place, place - front * ps + prefix)
+    kc = torch.zeros(pages + front, 1, ps, d, dtype=torch.float16, device="cuda")
+    kc[..., 0] = (at / 2000).to(torch.float16).view(-1, 1, ps)
+    vc = torch.randn(kc.shape, generator=g, device="cuda").to(torch.float16) + 1
+    k1, v1 = kc[:, 0].reshape(-1, d).double(), vc[:, 0].reshape(-1, d).double()
+    k1, v1 = (torch.cat([x[:prefix], x[front * ps:front * ps + keys]]) for x in (k1, v1))
+    kc, vc = (x.repeat(1, heads, 1, 1) for x in (kc, vc))
+    q = torch.zeros(rows, heads, d, device="cuda", dtype=torch.float16)
+    q[..., 0] = d ** 0.5
+    table = (front + torch.arange(pages, dtype=torch.int32, device="cuda"))[None].contiguous()
+    args = (table, _i32([keys]), _i32([0, rows]), rows)
+    if prefix:
+        pre = torch.arange(front, dtype=torch.int32, device="cuda")
+        o, lse = fa.attention_fwd_paged_prefix(q, kc, vc, pre, prefix, *args, window=window or None)
+    else:
+        o, lse = fa.attention_fwd_paged(q, kc, vc, *args, window=window or None)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    u = 2.0 ** -11
+    for r in sorted({0, rows // 2, rows - 1}):
+        hi = prefix + keys - rows + r + 1
+        lo = max(0, hi - window) if window else 0
+        x = k1[lo:hi, 0]
+        p = torch.exp(x - x.max())
+        want, weight = p @ v1[lo:hi] / p.sum(), p @ v1[lo:hi].abs() / p.sum()
+        # weights: scores up to 125 rounded twice in the exponent's argument, P to 16 bits; sums of 2^15 keys
+        # at a time lose 2^-26 a term, each fp32 sum after them 2^-24; O is stored
+        e = 2.0 ** -22 * (1 + 125 * 1.5) + 2.0 ** -17
+        tol = (2 * (e + u) + 2.0 ** -11) * weight + u * want.abs()
+        assert ((o[r].double() - want).abs() <= tol).all()
+        want_l = x.max() + torch.log(p.sum())
+        assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
