@@ -244,3 +244,25 @@ def test_growing_scores_over_many_tiles(cuda_lib, rows, heads, window, prefix):
         assert ((o[r].double() - want).abs() <= tol).all()
         want_l = x.max() + torch.log(p.sum())
         assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("behind", [0, 37])  # the last key tile full, or with keys that no row sees
+def test_a_quarter_billion_keys(cuda_lib, behind):
+    """A block of 100 rows for each SM, each over 1.8 million key tiles (more
+    than a second): warps that have nothing to do meanwhile must not take that
+    for a wait that ran out.  The table names 8 pages again and again, K is 0
+    and V is 1, so O is 1: each of the 1800 additions of 2^17 keys' sums is
+    off by three roundings at most, 3.2e-4 in all, less than half a step of
+    bf16 below 1 (2^-9)."""
+    rows, heads, d, ps, keys = 100, 152, 64, 256, 230_000_000 // 128 * 128 + behind
+    kc = torch.zeros(8, heads, ps, d, dtype=BF, device="cuda")
+    vc = torch.ones_like(kc)
+    table = (torch.arange(-(-keys // ps), dtype=torch.int32, device="cuda") % 8)[None].contiguous()
+    q = torch.randn(rows, heads, d, device="cuda").to(BF)
+    o, lse = fa.attention_fwd_paged(q, kc, vc, table, _i32([keys]), _i32([0, rows]), rows)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    want = torch.log(torch.arange(keys - rows + 1, keys + 1, dtype=torch.float64, device="cuda"))
+    # the sums are multiples of 128 below 2^28 but for the last tile's, exact in 32 bits
+    assert (lse.double() - want).abs().max() <= 2.0 ** -22 * (1 + want.max()) + 2.0 ** -23
+    assert (o == 1).all()
