@@ -140,7 +140,10 @@ def _on(stream):
     """Makes `stream` the current one: outputs are allocated on the stream
     that writes them."""
     import torch
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):
+        # torch takes the handle 0, the default stream's, for a request for a new one
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def paged_tables(cached_lens, new_lens, block_table, free_pages, page_size: int, num_pages: int, total: int,
