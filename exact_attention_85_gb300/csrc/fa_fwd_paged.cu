@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
             for (int g = 0; g < NT; ++g) {
                 // a row that has seen nothing yet keeps -inf: 0 stands in for it
-                const float n0 = m[g][0] == -INFINITY ? 0.f : -m[g][0], n1 = m[g][1] == -INFINITY ? 0.f : -m[g][1];
+                const float n0 = m[g][0] == -INFINITY ? 0.f : kWeightUnits<BF16> - m[g][0];
+                const float n1 = m[g][1] == -INFINITY ? 0.f : kWeightUnits<BF16> - m[g][1];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
 #pragma unroll
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         exact += f[w] * sm_m[2 * kConsumers * 16 + w * 16 + row];
                     }
                     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    const float lse2 = exact > 0.f ? top + log2f(exact) : -INFINITY;
+                    const float lse2 = exact > 0.f ? top - kWeightUnits<BF16> + log2f(exact) : -INFINITY;
                     const float *from = reinterpret_cast<const float *>(smem + st * 2 * L::TILE) + row * D;
                     const int tok = row / p.group;
                     const int h = t.hk * p.group.d + row - tok * p.group.d;

@@ -247,7 +247,7 @@ __device__ __forceinline__ void joint_epilogue(const WideParams &p, uint32_t o_c
         p.part.slot_sum[slot_at] = l_exact;
         return;
     }
-    const float lse2 = l_exact > 0.f ? m + log2f(l_exact) : -INFINITY;
+    const float lse2 = l_exact > 0.f ? m - kWeightUnits<BF16> + log2f(l_exact) : -INFINITY;
     float *const to_lse2 = to_slot ? p.part.slot_lse2 : p.part.plane_lse2;
     if (to_lse2)
         to_lse2[at] = lse2;
@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 const float m_use = m_ref == -INFINITY ? 0.0f : m_ref;  // nothing seen yet: P = 0
-                const float2 neg_m = make_float2(-m_use, -m_use);
+                const float2 neg_m = make_float2(kWeightUnits<BF16> - m_use, kWeightUnits<BF16> - m_use);
                 const float2 sl2x2 = make_float2(sl2, sl2);
                 float2 lr01 = make_float2(0.f, 0.f), lr23 = lr01, le01 = lr01, le23 = lr01;
                 constexpr int CH = 32;
@@ -969,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();  // the loads above are the whole warp's
                 }
                 if (valid) {
-                    const float lse2 = l_exact > 0.f ? m_ref + log2f(l_exact) : -INFINITY;
+                    const float lse2 = l_exact > 0.f ? m_ref - kWeightUnits<BF16> + log2f(l_exact) : -INFINITY;
                     if (to_lse2)
                         to_lse2[at] = lse2;
                     else

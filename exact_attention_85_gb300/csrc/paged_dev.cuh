@@ -66,6 +66,15 @@ struct Ranges {
     }
 };
 
+// Weights are formed as 2^(score - maximum + this), log2 units, and so are
+// their sums.  fp16 has no more than 2^-24 below 1, and a maximum lags by up
+// to 2^8: keys 25 units below a row's largest would drop out, and those 14
+// below lose bits, which shows where there are many of them (one key 17.6 in
+// the natural log above 2^17 others, which have 0.3 % of the weight together:
+// none of it was left).  At 2^15 of 2^16 fp16 has seven units more.
+template <bool BF16>
+constexpr float kWeightUnits = BF16 ? 0.0f : 7.0f;
+
 // ------------------------------------------------- units of the two kernels
 
 // Keys per tile of the few-row kernel (32 KB of K and V).

@@ -266,3 +266,41 @@ def test_a_quarter_billion_keys(cuda_lib, behind):
     # the sums are multiples of 128 below 2^28 but for the last tile's, exact in 32 bits
     assert (lse.double() - want).abs().max() <= 2.0 ** -22 * (1 + want.max()) + 2.0 ** -23
     assert (o == 1).all()
+
+
+# ------------------------------------------------------- small weights
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,heads", [(1, 304), (4, 304), (200, 152), (300, 4)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_beside_a_large_one(cuda_lib, rows, heads, dtype, d):
+    """Key 0 scores 17.6 above all others (25.4 in log2): their weights, 2^-25
+    each, count together.  P is rounded to the type's precision, in fp16 to no
+    less than 2^-25 / 2^7 of the largest weight: n 2^-32 of it at most."""
+    ps, keys = 256, 1 << 17
+    g = torch.Generator(device="cuda").manual_seed(d)
+    kc = torch.zeros(keys // ps, 1, ps, d, dtype=dtype, device="cuda")
+    kc[0, 0, 0, 0] = 4
+    vc = (1 + 0.1 * torch.randn(kc.shape, generator=g, device="cuda")).to(dtype)
+    vc[0, 0, 0] = 0
+    q = torch.zeros(rows, heads, d, dtype=dtype, device="cuda")
+    q[..., 0] = 4.4 * d ** 0.5
+    table = torch.arange(keys // ps, dtype=torch.int32, device="cuda")[None].contiguous()
+    o, lse = fa.attention_fwd_paged(q, kc.repeat(1, heads, 1, 1), vc.repeat(1, heads, 1, 1), table, _i32([keys]),
+                                    _i32([0, rows]), rows)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    k, v = kc.reshape(-1, d).double(), vc.reshape(-1, d).double()
+    u = torch.finfo(dtype).eps / 2
+    for r in {0, rows - 1}:
+        n = keys - rows + r + 1
+        x = k[:n] @ q[r, 0].double() / d ** 0.5
+        p = torch.exp(x - x.max())
+        want = p @ v[:n] / p.sum()
+        # dot products of one term; the exponent's argument is rounded twice; sums of 2^15 keys at a time lose 2^-11
+        e = 2.0 ** -22 * (1 + 17.6 * 1.5) + u
+        tol = (2 * e + 2.0 ** -11) * want + n * 2.0 ** -32 * v.abs().max() + u * want + 2.0 ** -25
+        assert ((o[r].double() - want).abs() <= tol).all()
+        want_l = x.max() + torch.log(p.sum())
+        assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
