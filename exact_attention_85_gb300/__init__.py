@@ -162,6 +162,8 @@ def paged_tables(cached_lens, new_lens, block_table, free_pages, page_size: int,
     if stream is not None:
         with _on(stream):
             return paged_tables(cached_lens, new_lens, block_table, free_pages, page_size, num_pages, total, free_start)
+    if total > 0x7FFFFFFF:
+        raise ValueError(f"total: {total} does not fit 32 bits")
     B, empty = block_table.shape[0], block_table.new_empty
     seq_lens, cu_seqlens, slots, counts = empty(B), empty(B + 1), empty(total), empty(2)
     _lib.fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, seq_lens, cu_seqlens, slots,

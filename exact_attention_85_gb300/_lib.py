@@ -372,13 +372,16 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_start, block_table, 
                   ("cu_seqlens", cu_seqlens, i32), ("slots", slots, i32), ("counts", counts, i32))
         _need_numel(cached_lens=(cached_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1),
                     seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), counts=(counts, 2))
-    if not (0 < page_size <= 0x7FFFFFFF and 0 < num_pages <= 0x7FFFFFFF):
-        _need_int32(page_size=page_size, num_pages=num_pages)
-    num_free = free_pages.numel()
+    num_free, total = free_pages.numel(), slots.numel()
+    # a tensor's sizes too: ctypes would pass their low 32 bits
+    if not (0 < page_size <= 0x7FFFFFFF and 0 < num_pages <= 0x7FFFFFFF and B <= 0x7FFFFFFF
+            and max_pages <= 0x7FFFFFFF and num_free <= 0x7FFFFFFF and total <= 0x7FFFFFFF):
+        _need_int32(page_size=page_size, num_pages=num_pages, B=B, max_pages=max_pages, free_pages=num_free,
+                    total=total)
     _check("fa_paged_tables", load().fa_paged_tables(
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr() if num_free else None, _ptr(free_start),
         block_table.data_ptr(), seq_lens.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), counts.data_ptr(), B,
-        max_pages, int(page_size), int(num_pages), num_free, slots.numel(), _stream(stream)))
+        max_pages, int(page_size), int(num_pages), num_free, total, _stream(stream)))
 
 
 def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
@@ -444,8 +447,10 @@ def _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, 
         raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
     if o.shape != q.shape or lse.shape != (Hq, total):
         raise ValueError("o must have q's shape and lse be [Hq,total]")
-    if not (0 < max_new <= 0x7FFFFFFF and 0 <= window <= 0x7FFFFFFF):
-        _need_int32(max_new=max_new, window=window)
+    # of the tensors' sizes the table's alone can pass 32 bits (a row of q or
+    # of a cache has 128 bytes)
+    if not (0 < max_new <= 0x7FFFFFFF and 0 <= window <= 0x7FFFFFFF and B <= 0x7FFFFFFF and max_pages <= 0x7FFFFFFF):
+        _need_int32(max_new=max_new, window=window, B=B, max_pages=max_pages)
     return (o.data_ptr(), lse.data_ptr(), B, total, int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages,
             int(window), float(scale), code, None if workspace is None else workspace.data_ptr(),
             0 if workspace is None else workspace.numel())

@@ -304,3 +304,31 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, rows, heads, dtype, d):
         assert ((o[r].double() - want).abs() <= tol).all()
         want_l = x.max() + torch.log(p.sum())
         assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
+
+
+# ------------------------------------------------------- sizes past 32 bits
+
+
+def test_rows_past_32_bits_are_refused_before_they_are_allocated():
+    i32 = dict(dtype=torch.int32)
+    one, table = torch.ones(1, **i32), torch.zeros(1, 4, **i32)
+    with pytest.raises(ValueError, match="total"):
+        fa.paged_tables(one, one, table, one, 16, 8, 2 ** 32 + 2)
+
+
+@pytest.mark.gpu
+def test_tensors_past_32_bits_are_refused(cuda_lib):
+    """Of a table of 2^32 + 2 columns or a free list as long, the low 32 bits
+    of the size would be passed on."""
+    far = torch.empty(1, 2 ** 32 + 2, dtype=torch.int32, device="cuda")
+    one, table = _i32([1]), _i32([0, 0])[None]
+    q = torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    kc = torch.zeros(2, 1, 16, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="max_pages"):
+        fa.paged_tables(one, one, far, one, 16, 8, 1)
+    with pytest.raises(ValueError, match="free_pages"):
+        fa.paged_tables(one, one, table, far[0], 16, 8, 1)
+    with pytest.raises(ValueError, match="max_pages"):
+        fa.attention_fwd_paged(q, kc, kc, far, one)
+    with pytest.raises(ValueError, match="max_pages"):
+        fa.attention_fwd_paged_prefix(q, kc, kc, one, 16, far, one)
