@@ -803,12 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     Request r;
                     if (load_request(p.a, b, r)) {
                         hi = p.a.prefix_len + r.len - r.n + (tok - r.row0) + 1;
-                        lo = p.a.window > 0 ? hi - p.a.window : 0;
+                        lo = p.a.window > 0 ? window_low(hi, p.a.window) : 0;
                     }
                 } else {
                     // no window: below every place (a prefix' first key is at -prefix_len)
                     hi = sg.len - sg.n + t + 1;
-                    lo = p.a.window > 0 ? hi - p.a.window : -0x7FFFFFFF;
+                    lo = p.a.window > 0 ? window_low(hi, p.a.window) : -0x7FFFFFFF;
                 }
             }
             const int nj = sg.nj;

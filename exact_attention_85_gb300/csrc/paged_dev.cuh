@@ -118,7 +118,13 @@ __host__ __device__ __forceinline__ void block_keys(const PagedArgs &a, const Fa
     const int last =
         (r.n * group.d - k * kWideRows > kWideRows ? (k + 1) * kWideRows - 1 : r.n * group.d - 1) / group;
     hi = max(0, r.len - r.n + last + 1);
-    lo = a.window > 0 ? max(0, r.len - r.n + first + 1 - a.window) : 0;
+    const int seen = r.len - r.n + first + 1;  // places below it, by the first row
+    lo = a.window > 0 && seen > a.window ? seen - a.window : 0;
+}
+// First place that a row which sees places below hi sees under a window; what
+// would pass 32 bits is below every place.
+__host__ __device__ __forceinline__ int window_low(int hi, int window) {
+    return max(hi, window - 0x7FFFFFFF) - window;
 }
 // Key tiles of the shared prefix that block k sees where they are read with
 // its own, and the first key of them.
@@ -185,7 +191,7 @@ struct PlanSum {
 // any of them sees: what the few-row kernel knows of the 256-row one's work.
 __device__ __forceinline__ long long block_tiles(const PagedArgs &a, const Request &r, int group, int &blocks) {
     blocks = (int)(((unsigned)(r.n * group) + kWideRows - 1) / kWideRows);
-    return (long long)blocks * range_tiles(a.window > 0 ? max(0, r.len - r.n + 1 - a.window) : 0, r.len);
+    return (long long)blocks * range_tiles(a.window > 0 ? max(0, max(0, r.len - r.n + 1) - a.window) : 0, r.len);
 }
 
 // The 256-row kernel is bound by the tensor cores and the few-row kernel by

@@ -306,6 +306,32 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, rows, heads, dtype, d):
         assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
 
 
+# ------------------------------------------------------- far places
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,lens", [([2000], [0]), ([2000, 40], [3, 60]), ([1500, 1, 1, 1, 1, 1], [0, 5, 0, 90, 1, 3])])
+def test_window_of_two_billion_in_a_wide_table(cuda_lib, new, lens):
+    """A window that is almost all of the widest table, and rows that stand
+    in the prefix (more rows than keys of their own): place - window is less
+    than 32 bits hold.  The window hides nothing, so O is that without one."""
+    ps, prefix, Hq, d = 256, 5000, 2, 64
+    cols = (2 ** 31 - 1024 - prefix) // ps
+    window = cols * ps + prefix - 50
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randn(30, 1, ps, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    q = torch.randn(sum(new), Hq, d, generator=g, device="cuda").to(BF)
+    table = torch.zeros(len(new), cols, dtype=torch.int32, device="cuda")
+    table[:, 0] = 20 + torch.arange(len(new), dtype=torch.int32, device="cuda")
+    cu = _i32([sum(new[:b]) for b in range(len(new) + 1)])
+    args = (q, kc, vc, _i32(range(20)), prefix, table, _i32(lens), cu, max(new))
+    o, lse = fa.attention_fwd_paged_prefix(*args, window=window)
+    whole, whole_lse = fa.attention_fwd_paged_prefix(*args)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    assert torch.isfinite(whole_lse).all()
+    assert torch.equal(o, whole) and torch.equal(lse, whole_lse)
+
+
 # ------------------------------------------------------- sizes past 32 bits
 
 
