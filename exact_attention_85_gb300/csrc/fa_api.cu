@@ -434,6 +434,13 @@ fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether a forward call's keys (rounded up to whole tiles and pages), rows
+// and table cells can be counted in 32 bits.
+bool paged_sizes(int B, int total, int Hq, int max_pages, int page_size, int prefix_len) {
+    return (long long)max_pages * page_size + prefix_len <= kMaxKeys && (long long)B * max_pages <= 0x7FFFFFFFll &&
+           (long long)total * Hq <= 0x7FFFFFFFll && (long long)B * Hq <= 0x7FFFFFFFll && B <= FA_PAGED_MAX_B;
+}
+
 fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_bytes) {
     if (!a.q || !a.k_cache || !a.v_cache || !a.o || !a.lse || !a.block_table || !a.seq_lens) return FA_ERR_INVALID_ARG;
     const void *ptrs[] = {a.q, a.k_cache, a.v_cache, a.o, a.lse};
@@ -448,11 +455,7 @@ fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_byt
     if (!a.cu_seqlens && (a.max_new != 1 || a.total < a.B)) return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(a.Hkv, a.d, a.page_size, a.num_pages, dtype);
     if (s != FA_OK) return s;
-    // keys are counted in 32 bits, rounded up to whole tiles and pages
-    if ((long long)a.max_pages * a.page_size + a.prefix_len > kMaxKeys) return FA_ERR_UNSUPPORTED;
-    if ((long long)a.B * a.max_pages > 0x7FFFFFFFll || (long long)a.total * a.Hq > 0x7FFFFFFFll ||
-        (long long)a.B * a.Hq > 0x7FFFFFFFll || a.B > FA_PAGED_MAX_B)
-        return FA_ERR_UNSUPPORTED;
+    if (!paged_sizes(a.B, a.total, a.Hq, a.max_pages, a.page_size, a.prefix_len)) return FA_ERR_UNSUPPORTED;
     // a window that holds every key there can be is none
     if (a.window >= (long long)a.max_pages * a.page_size + a.prefix_len) a.window = 0;
     const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
@@ -506,9 +509,9 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void
 
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
                                     int page_size, int prefix_len) {
-    if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
-        page_size < 1 || prefix_len < 0 || B > FA_PAGED_MAX_B || (long long)B * Hq > 0x7FFFFFFFll ||
-        (long long)total * Hq > 0x7FFFFFFFll || (long long)max_pages * page_size + prefix_len > kMaxKeys)
+    if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_pages < 1 || prefix_len < 0 ||
+        check_cache(Hkv, d, page_size, 1, FA_BF16) != FA_OK ||
+        !paged_sizes(B, total, Hq, max_pages, page_size, prefix_len))
         return 0;
     return fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, prefix_len, 0, nullptr).bytes;
 }

@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
                                             &k_full[ks], half * 64, in_page, page * p.a.Hkv + hk);
                             ++nk;
-                            got = nv < L::VS || mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
+                            got = nv < L::VS ||
+                                  mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
                             if (!(ok = __all_sync(0xffffffffu, got))) break;
                             if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
                             __syncwarp();
@@ -1016,8 +1017,8 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     const bool many = (prefix ? w.prefix_tiles : w.own_tiles) > kMaxTiles<BF16>;
-    auto kernel = w.joined ? (many ? paged_wide_kernel<D, BF16, true, true> : paged_wide_kernel<D, BF16, true, false>)
-                           : (many ? paged_wide_kernel<D, BF16, false, true> : paged_wide_kernel<D, BF16, false, false>);
+    auto kernel = many ? paged_wide_kernel<D, BF16, false, true> : paged_wide_kernel<D, BF16, false, false>;
+    if (w.joined) kernel = many ? paged_wide_kernel<D, BF16, true, true> : paged_wide_kernel<D, BF16, true, false>;
     return launch_after(kernel, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
 }
 

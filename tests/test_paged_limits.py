@@ -306,6 +306,22 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, rows, heads, dtype, d):
         assert (lse[:, r].double() - want_l).abs().max() <= e + 2.0 ** -22 * (1 + want_l)
 
 
+
+# ------------------------------------------------------- workspace
+
+
+@pytest.mark.parametrize("bad", [dict(d=96), dict(d=32), dict(page_size=8), dict(page_size=24), dict(page_size=512),
+                                 dict(B=1 << 20, max_pages=1 << 12), dict(total=1 << 30), dict(prefix_len=-1),
+                                 dict(prefix_len=2 ** 31 - 1), dict(Hkv=1 << 25, Hq=1 << 25)])
+def test_workspace_of_refused_sizes_is_none(bad):
+    """0 bytes for sizes that the forward refuses, whichever rule they break."""
+    from exact_attention_85_gb300 import build
+    build.build()
+    sizes = dict(B=4, total=8, max_new=2, Hq=4, Hkv=2, d=128, max_pages=64, page_size=16, prefix_len=0)
+    assert _lib.fa_fwd_paged_workspace_bytes(**sizes) > 0
+    assert _lib.fa_fwd_paged_workspace_bytes(**{**sizes, **bad}) == 0
+
+
 # ------------------------------------------------------- far places
 
 
