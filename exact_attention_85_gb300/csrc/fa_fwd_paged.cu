@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int y = 0; y < 2; ++y) {
                         const float a = ex2_approx(fmaf(s[i][g][2 * y], p.scale_log2, n0));
                         const float c = ex2_approx(fmaf(s[i][g][2 * y + 1], p.scale_log2, n1));
-                        const uint32_t pk = BF16 ? pack_bf16x2(a, c) : pack_f16x2(a, c);
+                        const uint32_t pk = BF16 ? pack_bf16x2(a, c) : pack_f16x2_sat(a, c);
                         const float2 w = unpack2<BF16>(pk);
                         l[g][0] += w.x;
                         l[g][1] += w.y;

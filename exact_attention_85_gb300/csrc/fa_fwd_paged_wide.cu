@@ -882,8 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             lr01 = add_bf16x2_f32x2(pk[k], lr01);
                             lr23 = add_bf16x2_f32x2(pk[k + 1], lr23);
                         } else {
-                            pk[k] = pack_f16x2(p0, p1);
-                            pk[k + 1] = pack_f16x2(p2, p3);
+                            pk[k] = pack_f16x2_sat(p0, p1);
+                            pk[k + 1] = pack_f16x2_sat(p2, p3);
                             lr01 = fadd2(lr01, unpack2<BF16>(pk[k]));
                             lr23 = fadd2(lr23, unpack2<BF16>(pk[k + 1]));
                         }

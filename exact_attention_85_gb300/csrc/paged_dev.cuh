@@ -71,7 +71,9 @@ struct Ranges {
 // to 2^8: keys 25 units below a row's largest would drop out, and those 14
 // below lose bits, which shows where there are many of them (one key 17.6 in
 // the natural log above 2^17 others, which have 0.3 % of the weight together:
-// none of it was left).  At 2^15 of 2^16 fp16 has seven units more.
+// none of it was left).  At 2^15 of 2^16 fp16 has seven units more; scores of
+// 10^7 and above, which are off by whole units themselves, can pass that and
+// are held to fp16's largest number.
 template <bool BF16>
 constexpr float kWeightUnits = BF16 ? 0.0f : 7.0f;
 

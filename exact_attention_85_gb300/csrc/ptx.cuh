@@ -418,6 +418,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
+// The same, where what passes fp16's range becomes its largest number.
+__device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Widens a packed 16-bit pair (lo in bits 0-15) back to two floats.
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {

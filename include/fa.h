@@ -435,7 +435,9 @@ size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq,
  *   Rows of no request are left unwritten.  What a page holds behind its
  *   request's last key has no effect, whatever it is; the values of keys that
  *   some row of the request sees must be finite, as for fa_fwd (a row that
- *   does not see such a key multiplies its value by 0).
+ *   does not see such a key multiplies its value by 0).  Scores (scale q.k)
+ *   are formed in fp32 and must stay below 2^29: from there on their rounding
+ *   alone passes the range of the exponential.
  *   workspace: at least fa_fwd_paged_workspace_bytes(..., prefix_len = 0)
  *       bytes, 256-byte aligned, contents on entry do not matter; calls that
  *       may run at the same time need workspaces of their own.

@@ -307,6 +307,40 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, rows, heads, dtype, d):
 
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,keys", [(1, 700), (4, 5000), (40, 900), (300, 3000)])
+@pytest.mark.parametrize("size", [300.0, 3000.0, 8000.0])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_huge_scores_choose_one_key(cuda_lib, rows, keys, size, dtype):
+    """Scores up to 2^29, the most that is defined: their fp32 sums are off by
+    far more than a unit of the exponent.  O stays finite, and is the value of
+    the key that is ahead by more than that error."""
+    ps, d, heads = 64, 64, 3
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    pages = -(-keys // ps)
+    kc, vc = (torch.randn(pages, heads, ps, d, generator=g, device="cuda") for _ in range(2))
+    kc, vc = kc.mul_(size).clamp_(-6e4, 6e4).to(dtype), vc.to(dtype)
+    q = torch.randn(rows, heads, d, generator=g, device="cuda").mul_(size).clamp_(-6e4, 6e4).to(dtype)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].repeat(1, 40).contiguous()
+    o, lse = fa.attention_fwd_paged(q, kc, vc, table, _i32([keys]), _i32([0, rows]), rows)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    k, v = (x.transpose(0, 1).reshape(heads, -1, d).double() for x in (kc, vc))
+    checked = 0
+    for r in range(rows):
+        n = keys - rows + r + 1
+        x = torch.einsum("hd,hnd->hn", q[r].double(), k[:, :n]) / d ** 0.5
+        error = d * 2.0 ** -23 * torch.einsum("hd,hnd->hn", q[r].double().abs(), k[:, :n].abs()).amax(1) / d ** 0.5
+        top, at = x.topk(2, 1)
+        assert x.abs().max() < 2 ** 29
+        for h in range(heads):
+            if top[h, 0] - top[h, 1] > 4 * error[h] + 60:
+                checked += 1
+                assert torch.equal(o[r, h].double(), v[h, at[h, 0]])
+                assert (lse[h, r].double() - top[h, 0]).abs() <= error[h] + 2.0 ** -21 * top[h, 0].abs()
+    assert checked > rows * heads // 2
+
+
 # ------------------------------------------------------- workspace
 
 
