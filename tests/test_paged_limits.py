@@ -408,3 +408,47 @@ def test_tensors_past_32_bits_are_refused(cuda_lib):
         fa.attention_fwd_paged(q, kc, kc, far, one)
     with pytest.raises(ValueError, match="max_pages"):
         fa.attention_fwd_paged_prefix(q, kc, kc, one, 16, far, one)
+
+
+# ------------------------------------------------------- most requests
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,long", [(1, 0), (17, 0), (1, 300)])
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_a_million_requests(cuda_lib, rows, long, prefix):
+    """FA_PAGED_MAX_B requests of one row (few-row kernel), of 17 (256-row
+    kernel), and of one but for a long one in the middle and at the end
+    (both): a sample of them against 64 bits."""
+    B, ps, d, pages = 1 << 20, 16, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    kc, vc = (torch.randn(pages, 1, ps, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    table = torch.randint(pages, (B, 24), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(rows, 49, (B,), generator=g, device="cuda", dtype=torch.int32)
+    new = torch.full((B,), rows, dtype=torch.int64, device="cuda")
+    for b in (B // 2, B - 1) if long else ():
+        new[b], lens[b] = long, 380
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1:] = new.cumsum(0)
+    q = torch.randn(int(cu[-1]), 1, d, generator=g, device="cuda").to(BF)
+    args = (table, lens, cu, max(rows, long))
+    front = _i32(range(-(-prefix // ps)))
+    if prefix:
+        o, lse = fa.attention_fwd_paged_prefix(q, kc, vc, front, prefix, *args)
+    else:
+        o, lse = fa.attention_fwd_paged(q, kc, vc, *args)
+    assert _lib.fa_get_device_status() == _lib.FA_OK
+    k1, v1 = kc[:, 0].double(), vc[:, 0].double()
+    for b in [0, 1, 31, 32, 255, 256, 257, 5000, B // 2 - 1, B // 2, B // 2 + 1, B - 2, B - 1]:
+        n, m, r0 = int(lens[b]), int(new[b]), int(cu[b])
+        ids = table[b].long()
+        k, v = (torch.cat([x[front.long()].reshape(-1, d)[:prefix], x[ids].reshape(-1, d)[:n]]) for x in (k1, v1))
+        x = q[r0:r0 + m, 0].double() @ k.T / d ** 0.5
+        place = prefix + n - m + torch.arange(m, device="cuda")
+        x.masked_fill_(torch.arange(prefix + n, device="cuda") > place[:, None], -float("inf"))
+        p = torch.softmax(x, 1)
+        want, weight = p @ v, p @ v.abs()
+        # P and O rounded to bf16 (2^-8 each, P also in the sum); the fp32 errors of scores below 8 are below 2^-17
+        tol = (2 * 2.0 ** -8 + 2.0 ** -15) * weight + 2.0 ** -8 * want.abs()
+        assert ((o[r0:r0 + m, 0].double() - want).abs() <= tol).all(), b
+        assert (lse[0, r0:r0 + m].double() - torch.logsumexp(x, 1)).abs().max() <= 2.0 ** -16, b
