@@ -206,8 +206,12 @@ def attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=N
     cu_seqlens[b+1]-1, or row b alone without ``cu_seqlens``; the last of them
     sees all seq_lens[b] keys, each row before it one less (``window`` leaves
     a row its last ``window`` ones).  ``max_new`` bounds a request's rows
-    (default: the longest, read back from the device once).  Returns
-    (O [total,Hq,d], LSE [Hq,total] fp32); rows of no request stay unwritten."""
+    (default: the longest, read back from the device once).  ``workspace``: a
+    uint8 tensor of at least ``_lib.fa_fwd_paged_workspace_bytes(B, total,
+    max_new, Hq, Hkv, d, max_pages, page_size, prefix_len)`` bytes, of which
+    calls that may run at once need one each (default: one is allocated).
+    Returns (O [total,Hq,d], LSE [Hq,total] fp32); rows of no request stay
+    unwritten."""
     if stream is not None:
         with _on(stream):
             return attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, max_new, scale, window,

@@ -15,9 +15,9 @@
 // instructions of the other way for up to 8 rows.  Measured, reading from L2
 // (one CTA alone) and from memory (42 to 72 SMs): 49 and 54 GB/s an SM with
 // the rows on the long side, 59 and 73 this way.  All SMs together are bound
-// by reading the cache: 450 us for 64 requests of 8-16k keys, 7.15 TB/s of
-// the 6.8 that a copy reaches (it writes as well).  Everything else here
-// serves to keep copies in flight.
+// by reading the cache: 461 us for 64 requests of 8-16k keys (453 on another
+// card), 7.0 TB/s where a copy, which writes as well, reaches 6.8.  Everything
+// else here serves to keep copies in flight.
 //
 // Work is cut into units of one tile of keys (32 KB of K and V).  All units
 // of all (request, key/value head) pairs are numbered in order and every CTA
@@ -50,10 +50,11 @@ namespace {
 constexpr int kConsumers = 4;  // warps
 constexpr int kFewWarps = kConsumers + 2;  // and two producers
 constexpr int kFewThreads = 32 * kFewWarps;
-// Two CTAs per SM.  Alone, 212 to 304 CTAs do as well (449-454 us for 64
-// requests of 8-16k keys, 81-82 for 32 of 333-7506; 190: 463 and 86); beside
-// the 256-row kernel, where the SMs are the limit, an even two are best (256
-// requests on a 16k prefix: 202 us, 1.64 an SM 214).
+// Two CTAs per SM.  us with 190, 212, 250 and 304 CTAs: 64 requests of 8-16k
+// keys 462, 456, 458, 461; 32 of 333-7506 87.8, 83.5, 80.8, 83.0; beside the
+// 256-row kernel 256 requests on a 16k prefix 202 with any, 64 on 8k 44.3,
+// 45.5, 48.5, 48.4 on a card where the whole call takes 48, and no difference
+// on one where it takes 44.
 constexpr int kMaxCtas = 2 * kSms;
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;   // units a CTA takes at least
@@ -234,7 +235,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         // the other (128-byte swizzled rows)
         const int page_keys = min(1 << p.a.shift, L::TK);
         const int box_bytes = page_keys * D * 2;
-        const uint64_t once = l2_evict_first();  // every key is read by one CTA only
+        // A request's own keys are read by one CTA only, unless requests share
+        // pages.  A joined prefix' are read with every request's own; the
+        // policy is the same for them.
+        const uint64_t once = l2_evict_first();
         const int sub = lane;
         const bool boxed = sub < L::TK / page_keys;
         uint8_t *const tiles_at = smem + (first_one ? 0 : L::TILE);
@@ -907,11 +911,14 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
     if (w.few) {
         // A CTA takes whole pairs, with nothing to merge, where the second
         // launch (some 4 us) would cost more than dividing them gains: up to
-        // 12 tiles a pair where every pair has a CTA of its own (24 requests
-        // of 1024 keys in the window: 16.2 us divided, 13.9 whole), or up to
-        // 8 where the CTAs that the last round leaves idle could read little
-        // meanwhile (256 requests of 512 keys in 16-key pages, 2048 pairs:
-        // 86 us divided, 94 whole).
+        // 12 tiles a pair where every pair has a CTA of its own, or up to 8
+        // where the CTAs that the last round leaves idle could read little
+        // meanwhile.  Measured, us divided and whole, four heads a pair:
+        //   8 pairs of 8 tiles 8.8 and 8.5, of 12 8.9 and 10.7, of 16 8.9 and
+        //     12.8; 192 (d = 64) of 8 12.6 and 11.7, of 12 15.3 and 15.5, of 16
+        //     17.9 and 19.5; 296 of 8 13.5 and 10.6, of 12 22.6 and 20.7
+        //   384 of 6 14.3 and 13.4, of 8 17.6 and 18.6; 512 of 8 27.3 and
+        //     24.7; 2048 of 4 50.2 and 45.7, of 8 87.7 and 84.9
         const long long seen = window > 0 ? ((long long)window + max_new + tile - 2) / tile + 2 : few_tiles;
         const long long most = seen < few_tiles ? seen : few_tiles;
         const long long idle = (pairs + kMaxCtas - 1) / kMaxCtas * kMaxCtas - pairs;

@@ -201,10 +201,13 @@ __device__ __forceinline__ long long block_tiles(const PagedArgs &a, const Reque
 // beside the few-row kernel, each on SMs of its own: the number that the
 // 256-row kernel gets.  Times in us, as measured: a unit of the 256-row
 // kernel takes 2.05 on one SM, with 14 to start and end; a few-row pair 0.35
-// and 0.5 a tile on one SM, but at least 1.6, with 6 to start; and no division
-// lets more into the SMs than 32 KB in 4.7 ns, of which a few-row tile is one
-// and a unit of the other kernel two.  Where that limit is what counts, the
-// 256-row kernel gets all SMs that cost the other nothing.  (256 requests of
+// and 0.5 a tile on one SM, but at least 1.6, with 6 to start; and both
+// together 4.7 ns for each 32 KB, of which a few-row tile is one and a unit of
+// the other kernel two.  That is 7.0 TB/s, the rate at which the few-row kernel
+// alone reads the cache, charged to the 256-row kernel's tiles as well, most
+// of which come from L2: it fits the times, but what the limit is has not been
+// measured.  Where it is what counts, the 256-row kernel gets all SMs that
+// cost the other nothing.  (256 requests of
 // 64-2048 keys on a 16k prefix: 220 us with 48 SMs, 211 with 50, 205 with 58,
 // 202 with 62, 211 with 70, 216 with 76; one after the other 272.)  32
 // candidates, one a lane; each kernel decides for itself, so a difference
