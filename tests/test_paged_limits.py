@@ -9,6 +9,9 @@ import torch
 import exact_attention_85_gb300 as fa
 from exact_attention_85_gb300 import _lib
 
+from _paged import Problem, check
+from test_paged_gpu import ATTENTION, _run
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BF, HF = torch.bfloat16, torch.float16
@@ -199,6 +202,17 @@ def test_long_sums_keep_small_terms(cuda_lib, rows, heads, keys, dtype, d):
     want = torch.log(torch.arange(keys - rows + 1, keys + 1, dtype=torch.float64, device="cuda"))
     assert (lse.double() - want).abs().max() <= 2.0 ** -22 * (1 + want.max()) + 2.0 ** -23
     assert (o == 1 + step).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [c for c in ATTENTION if max(c[1]) * c[2] // c[3] > 16 or len(c[0]) > 60])
+def test_tables_of_long_sequences(cuda_lib, case):
+    """Ordinary lengths in tables so wide that the 256-row kernel is the one
+    for long sums."""
+    lens, new, Hq, Hkv, d, ps, dtype, window, prefix = case
+    cols = (40_000 if dtype == HF else 140_000) // ps
+    p = Problem(lens, new, Hq, Hkv, d, ps, dtype, window, prefix, seed=d + ps, extra_cols=cols)
+    check(*_run(p), p.reference(), p.rows)
 
 
 @pytest.mark.gpu
