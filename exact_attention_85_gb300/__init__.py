@@ -17,7 +17,7 @@ from . import _lib
 
 __all__ = ["attention_fwd", "attention_bwd", "attention_fwd_varlen", "attention_bwd_varlen",
            "hadamard_quant_fp8", "attention_fwd_fp8", "paged_tables", "paged_append", "attention_fwd_paged",
-           "attention_fwd_paged_prefix"]
+           "attention_fwd_paged_prefix", "paged_fork", "paged_copy", "paged_compact", "paged_free"]
 
 
 def _default_scale(d: int) -> float:
@@ -176,6 +176,66 @@ def paged_append(k, v, slots, k_cache, v_cache, stream=None):
     [pages,Hkv,page_size,d] in place; a negative slot skips its row, and no
     slot may occur twice."""
     _lib.fa_paged_append(k, v, slots, k_cache, v_cache, stream)
+
+
+def paged_fork(src, dst, seq_lens, block_table, free_pages, shares, page_size: int, free_start=None, stream=None):
+    """Lets requests branch: row dst[f] of ``block_table`` [B,max_pages]
+    continues where row src[f] stands, on the same pages but for a half-full
+    last one, in whose place it gets a page of the pool.
+
+    All tensors are int32 on the device.  ``seq_lens`` [B], ``block_table``
+    and ``shares`` [pages] (how many requests hold a page beside the first)
+    are updated in place; ``free_pages`` and ``free_start`` are those of
+    ``paged_tables``.  No row may occur twice in ``dst``, or in both.  Returns
+    (copies [3,F], counts [2]): source page, new page and rows to copy for
+    each fork, to be given to ``paged_copy`` for every layer's cache (-1, -1,
+    0 where nothing is to be copied), and the next ``free_start`` with the
+    number of pages lacking.  A fork that the pool had no page for gets
+    length 0."""
+    if stream is not None:
+        with _on(stream):
+            return paged_fork(src, dst, seq_lens, block_table, free_pages, shares, page_size, free_start)
+    copies, counts = src.new_empty((3, src.numel())), src.new_empty(2)
+    _lib.fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, shares, copies, counts, page_size)
+    return copies, counts
+
+
+def paged_copy(src, dst, k_cache, v_cache, rows=None, stream=None):
+    """Copies the first rows[i] tokens (default: all) of page src[i] to page
+    dst[i] of k_cache, v_cache [pages,Hkv,page_size,d], in place.  Negative
+    page numbers skip the pair; no page may occur twice in ``dst``, or in
+    both."""
+    _lib.fa_paged_copy(src, dst, rows, k_cache, v_cache, stream)
+
+
+def paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream=None):
+    """Moves the kept ones of each request's last tokens together, in place:
+    token base_lens[b] + keep[b][i] becomes token base_lens[b] + i, for
+    i < keep_lens[b].  ``keep`` [B,max_keep] is strictly increasing within a
+    request: the accepted path of a tree of drafted tokens, or what is left of
+    a long context.  int32 tensors; the request has base_lens + keep_lens
+    tokens then (``paged_free`` takes the pages behind them back)."""
+    _lib.fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream)
+
+
+def paged_free(old_lens, new_lens, block_table, free_pages, free_start, page_size: int, num_pages: int, shares=None,
+               stream=None):
+    """Takes the pages behind new_lens [B] back from requests that had
+    old_lens [B] tokens (a request that ends keeps 0).
+
+    All tensors are int32 on the device.  A page that ``shares`` [num_pages]
+    says further requests hold loses holders, and is freed only with its last
+    one; without ``shares`` no page is shared.  Freed pages are put into
+    ``free_pages`` in front of position ``free_start`` [1] (where the pool's
+    entries that were handed out before lie), in order of request and page.
+    Returns counts [2]: the next ``free_start``, and how many pages found no
+    room there."""
+    if stream is not None:
+        with _on(stream):
+            return paged_free(old_lens, new_lens, block_table, free_pages, free_start, page_size, num_pages, shares)
+    counts = block_table.new_empty(2)
+    _lib.fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, shares, counts, page_size, num_pages)
+    return counts
 
 
 def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace):

@@ -24,6 +24,7 @@ EXPORTS = (
     "fa_hadamard_quant_workspace_bytes", "fa_fwd_fp8", "fa_get_device_status",
     "fa_selftest_bounded_wait", "fa_status_string", "fa_fwd_f32_out", "fa_probe_exp2", "fa_fwd_persistent",
     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_fwd_paged_workspace_bytes",
+    "fa_paged_fork", "fa_paged_copy", "fa_paged_compact", "fa_paged_free",
 )
 
 _lock = threading.Lock()
@@ -71,6 +72,10 @@ def load():
         lib.fa_fwd_fp8.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P]
         lib.fa_paged_tables.argtypes = [P] * 9 + [I] * 6 + [P]
         lib.fa_paged_append.argtypes = [P] * 5 + [I] * 6 + [P]
+        lib.fa_paged_fork.argtypes = [P] * 9 + [I] * 6 + [P]
+        lib.fa_paged_copy.argtypes = [P] * 5 + [I] * 6 + [P]
+        lib.fa_paged_compact.argtypes = [P] * 6 + [I] * 8 + [P]
+        lib.fa_paged_free.argtypes = [P] * 7 + [I] * 5 + [P]
         lib.fa_fwd_paged.argtypes = [P] * 8 + [I] * 10 + [F, I, P, Z, P]
         lib.fa_fwd_paged_prefix.argtypes = [P] * 4 + [I] + [P] * 5 + [I] * 10 + [F, I, P, Z, P]
         lib.fa_fwd_paged_workspace_bytes.argtypes = [I] * 9
@@ -83,8 +88,8 @@ def load():
         lib.fa_status_string.restype = ctypes.c_char_p
         for name in ("fa_fwd", "fa_fwd_local", "fa_fwd_f32_out", "fa_fwd_persistent", "fa_bwd_local", "fa_fwd_varlen", "fa_bwd_varlen",
                      "fa_bwd", "fa_bwd_two_pass", "fa_bwd_noalloc", "fa_hadamard_quant_fp8", "fa_fwd_fp8",
-                     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix",
-                     "fa_get_device_status", "fa_selftest_bounded_wait"):
+                     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_paged_fork",
+                     "fa_paged_copy", "fa_paged_compact", "fa_paged_free", "fa_get_device_status", "fa_selftest_bounded_wait"):
             getattr(lib, name).restype = I
         _lib = lib
         return lib
@@ -405,6 +410,107 @@ def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
     _check("fa_paged_append", load().fa_paged_append(
         k.data_ptr(), v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), total, Hkv, d, page_size,
         num_pages, code, _stream(stream)))
+
+
+def _are_int32(dev, *tensors) -> bool:
+    """Whether all are contiguous int32 tensors on device `dev` (None passes)."""
+    import torch
+    i32 = torch.int32
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or t.dtype != i32 or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _need_ints(block_table, **tensors):
+    """Refuses what a call on a table cannot take: tensors (None passes) off
+    the table's device, the current one, of another type than int32, or not
+    contiguous."""
+    import torch
+    dev = block_table.get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or not _are_int32(dev, block_table, *tensors.values()):
+        _need_all(("block_table", block_table, torch.int32), *((k, t, torch.int32) for k, t in tensors.items()))
+
+
+def _cache_shape(k_cache, v_cache):
+    """(pages, Hkv, page_size, d) of two caches of one type."""
+    import torch
+    dtype, dev = k_cache.dtype, k_cache.get_device()
+    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous() and v_cache.get_device() == dev
+            and v_cache.dtype == dtype and v_cache.is_contiguous()):
+        _need_all(("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype))
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must both be [pages,Hkv,page_size,d]")
+    return k_cache.shape
+
+
+def fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, shares, copies, counts, page_size: int,
+                  stream=None):
+    """Table rows dst continue where rows src stand; int32 tensors as in fa.h."""
+    B, max_pages = block_table.shape
+    F, num_pages, num_free = src.numel(), shares.numel(), free_pages.numel()
+    _need_ints(block_table, src=src, dst=dst, seq_lens=seq_lens, free_pages=free_pages, free_start=free_start,
+               shares=shares, copies=copies, counts=counts)
+    if not (dst.numel() == F and seq_lens.numel() == B and copies.numel() == 3 * F and counts.numel() == 2
+            and (free_start is None or free_start.numel() == 1)):
+        _need_numel(dst=(dst, F), seq_lens=(seq_lens, B), copies=(copies, 3 * F), counts=(counts, 2),
+                    free_start=(free_start, 1))
+    _need_int32(page_size=page_size, F=F, B=B, max_pages=max_pages, shares=num_pages, free_pages=num_free)
+    _check("fa_paged_fork", load().fa_paged_fork(
+        src.data_ptr(), dst.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+        free_pages.data_ptr() if num_free else None, _ptr(free_start), shares.data_ptr(), copies.data_ptr(),
+        counts.data_ptr(), F, B, max_pages, int(page_size), num_pages, num_free, _stream(stream)))
+
+
+def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
+    """Pages dst of the caches [pages,Hkv,page_size,d] get the first rows tokens of pages src."""
+    import torch
+    num_pages, Hkv, page_size, d = _cache_shape(k_cache, v_cache)
+    code, dev, n = _dtype_code(k_cache), k_cache.get_device(), src.numel()
+    if not _are_int32(dev, src, dst, rows):
+        i32 = torch.int32
+        _need_all(("k_cache", k_cache, k_cache.dtype), ("src", src, i32), ("dst", dst, i32), ("rows", rows, i32))
+    if dst.numel() != n or (rows is not None and rows.numel() != n):
+        _need_numel(dst=(dst, n), rows=(rows, n))
+    _need_int32(src=n)
+    _check("fa_paged_copy", load().fa_paged_copy(
+        src.data_ptr(), dst.data_ptr(), _ptr(rows), k_cache.data_ptr(), v_cache.data_ptr(), n, Hkv, d, page_size,
+        num_pages, code, _stream(stream)))
+
+
+def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream=None):
+    """Tokens base_lens + keep [B,max_keep] of the requests move to base_lens + 0, 1, .."""
+    B, max_pages = block_table.shape
+    num_pages, Hkv, page_size, d = _cache_shape(k_cache, v_cache)
+    code = _dtype_code(k_cache)
+    _need_ints(block_table, keep=keep, keep_lens=keep_lens, base_lens=base_lens)
+    if k_cache.get_device() != block_table.get_device():
+        _refuse("k_cache", k_cache, block_table.get_device())
+    if keep.dim() != 2 or keep.shape[0] != B or keep_lens.numel() != B or base_lens.numel() != B:
+        raise ValueError(f"keep must be [B,max_keep], keep_lens and base_lens [B], with the table's B = {B}")
+    max_keep = keep.shape[1]
+    _need_int32(B=B, max_keep=max_keep, max_pages=max_pages)
+    _check("fa_paged_compact", load().fa_paged_compact(
+        keep.data_ptr(), keep_lens.data_ptr(), base_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), B, max_keep, max_pages, Hkv, d, page_size, num_pages, code, _stream(stream)))
+
+
+def fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, shares, counts, page_size: int,
+                  num_pages: int, stream=None):
+    """Pages behind new_lens back to the free list; int32 tensors as in fa.h."""
+    B, max_pages = block_table.shape
+    num_free = free_pages.numel()
+    _need_ints(block_table, old_lens=old_lens, new_lens=new_lens, free_pages=free_pages, free_start=free_start,
+               shares=shares, counts=counts)
+    if not (old_lens.numel() == B and new_lens.numel() == B and free_start.numel() == 1 and counts.numel() == 2
+            and (shares is None or shares.numel() == num_pages)):
+        _need_numel(old_lens=(old_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1), counts=(counts, 2),
+                    shares=(shares, num_pages))
+    _need_int32(page_size=page_size, num_pages=num_pages, B=B, max_pages=max_pages, free_pages=num_free)
+    _check("fa_paged_free", load().fa_paged_free(
+        old_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if num_free else None,
+        free_start.data_ptr(), _ptr(shares), counts.data_ptr(), B, max_pages, int(page_size), int(num_pages), num_free,
+        _stream(stream)))
 
 
 @functools.lru_cache(maxsize=1024)  # a function of the sizes alone

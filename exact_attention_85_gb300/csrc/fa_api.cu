@@ -1,9 +1,11 @@
 // fa_api.cu -- the extern "C" boundary of libfa.so: argument validation,
 // the per-device status word, TMA descriptor encoding and dispatch to the
 // kernel launchers.  Declarations and their contracts are in include/fa.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/fa.h"
@@ -434,6 +436,22 @@ fa_status_t check_cache(int Hkv, int d, int page_size, int num_pages, fa_dtype_t
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// 4-byte aligned, and no output an input or another output (null: none).
+bool apart(std::initializer_list<const int *> in, std::initializer_list<const int *> out) {
+    for (const int *p : in)
+        if (!aligned4(p)) return false;
+    for (const int *const *o = out.begin(); o != out.end(); ++o) {
+        if (!aligned4(*o)) return false;
+        if (*o && (std::find(in.begin(), in.end(), *o) != in.end() || std::find(out.begin(), o, *o) != o)) return false;
+    }
+    return true;
+}
+
+// Whether a table's tokens and cells can be counted in 32 bits.
+bool table_sizes(int B, int max_pages, int page_size) {
+    return (long long)max_pages * page_size <= kMaxKeys && (long long)B * max_pages <= 0x7FFFFFFFll;
+}
+
 // Whether a forward call's keys (rounded up to whole tiles and pages), rows
 // and table cells can be counted in 32 bits.
 bool paged_sizes(int B, int total, int Hq, int max_pages, int page_size, int prefix_len) {
@@ -505,6 +523,70 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots, void
     if (s != FA_OK) return s;
     fa::AppendArgs a{k, v, slots, k_cache, v_cache, total, Hkv, d, page_size, num_pages};
     return from_cuda(fa::launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_paged_fork(const int *src, const int *dst, int *seq_lens, int *block_table, const int *free_pages,
+                          const int *free_start, int *shares, int *copies, int *counts, int F, int B, int max_pages,
+                          int page_size, int num_pages, int num_free, void *stream) {
+    FA_RANGE("fa_paged_fork");
+    if (!src || !dst || !seq_lens || !block_table || !shares || !copies || !counts) return FA_ERR_INVALID_ARG;
+    if (F < 1 || B < 1 || F > B || max_pages < 1 || num_free < 0 || (num_free > 0 && !free_pages))
+        return FA_ERR_INVALID_ARG;
+    if (!apart({src, dst, free_pages, free_start}, {seq_lens, block_table, shares, copies, counts}))
+        return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(1, 128, page_size, num_pages, FA_BF16);
+    if (s != FA_OK) return s;
+    if (F > FA_PAGED_FORK_MAX || !table_sizes(B, max_pages, page_size)) return FA_ERR_UNSUPPORTED;
+    fa::ForkArgs a{src, dst, free_pages, free_start, seq_lens, block_table, shares, copies, counts,
+                   F, B, max_pages, page_size, num_pages, num_free};
+    return from_cuda(fa::launch_paged_fork(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_paged_copy(const int *src, const int *dst, const int *rows, void *k_cache, void *v_cache, int n,
+                          int Hkv, int d, int page_size, int num_pages, fa_dtype_t dtype, void *stream) {
+    FA_RANGE("fa_paged_copy");
+    if (!src || !dst || !k_cache || !v_cache || n < 1) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(src) || !aligned4(dst) || !aligned4(rows))
+        return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(Hkv, d, page_size, num_pages, dtype);
+    if (s != FA_OK) return s;
+    if (fa::copy_blocks(n, Hkv, d, page_size) > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    fa::CopyArgs a{src, dst, rows, k_cache, v_cache, n, Hkv, d, page_size, num_pages};
+    return from_cuda(fa::launch_paged_copy(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_paged_compact(const int *keep, const int *keep_lens, const int *base_lens, const int *block_table,
+                             void *k_cache, void *v_cache, int B, int max_keep, int max_pages, int Hkv, int d,
+                             int page_size, int num_pages, fa_dtype_t dtype, void *stream) {
+    FA_RANGE("fa_paged_compact");
+    if (!keep || !keep_lens || !base_lens || !block_table || !k_cache || !v_cache) return FA_ERR_INVALID_ARG;
+    if (B < 1 || max_keep < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(keep) || !aligned4(keep_lens) || !aligned4(base_lens) ||
+        !aligned4(block_table))
+        return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(Hkv, d, page_size, num_pages, dtype);
+    if (s != FA_OK) return s;
+    // blocks: of every request's heads, K and V, up to 8 of a row
+    if (!table_sizes(B, max_pages, page_size) || 16ll * B * Hkv > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    fa::CompactArgs a{keep, keep_lens, base_lens, block_table, k_cache, v_cache, B, max_keep, max_pages, Hkv, d,
+                      page_size, num_pages};
+    return from_cuda(fa::launch_paged_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status_t fa_paged_free(const int *old_lens, const int *new_lens, const int *block_table, int *free_pages,
+                          const int *free_start, int *shares, int *counts, int B, int max_pages, int page_size,
+                          int num_pages, int num_free, void *stream) {
+    FA_RANGE("fa_paged_free");
+    if (!old_lens || !new_lens || !block_table || !free_start || !counts) return FA_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || num_free < 0 || (num_free > 0 && !free_pages)) return FA_ERR_INVALID_ARG;
+    if (!apart({old_lens, new_lens, block_table, free_start}, {free_pages, shares, counts})) return FA_ERR_INVALID_ARG;
+    fa_status_t s = check_cache(1, 128, page_size, num_pages, FA_BF16);
+    if (s != FA_OK) return s;
+    if (B > FA_PAGED_TABLES_MAX_B || !table_sizes(B, max_pages, page_size) || (long long)B * max_pages > (1ll << 30))
+        return FA_ERR_UNSUPPORTED;
+    fa::FreeArgs a{old_lens, new_lens, block_table, free_start, free_pages, shares, counts, B, max_pages, page_size,
+                   num_pages, num_free};
+    return from_cuda(fa::launch_paged_free(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fa_fwd_paged_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,

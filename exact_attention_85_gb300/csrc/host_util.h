@@ -71,9 +71,10 @@ struct DynSmem {
 // dependent launch): at its end, or once all its CTAs have said so.  The
 // kernel waits for it (griddepcontrol.wait) before it touches memory, so that
 // only launch and set-up overlap.
+// `cluster`: CTAs of a cluster (1: none).
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, DynSmem smem, cudaStream_t st,
-                         const A &...args) {
+cudaError_t launch_cluster_after(void (*kernel)(P...), unsigned grid, unsigned cluster, unsigned threads, DynSmem smem,
+                                 cudaStream_t st, const A &...args) {
     // A kernel gets 48 KB without being asked, its static bytes among them:
     // 16 KB are left for those.
     if (smem.bytes > 32 * 1024) {
@@ -86,12 +87,21 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, 
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem.bytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, DynSmem smem, cudaStream_t st,
+                         const A &...args) {
+    return launch_cluster_after(kernel, grid, 1, threads, smem, st, args...);
 }
 
 // Device address of this library's status words (status.cuh) on the current device

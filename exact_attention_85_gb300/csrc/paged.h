@@ -21,6 +21,30 @@ struct AppendArgs {
     int total, Hkv, d, page_size, num_pages;
 };
 
+struct ForkArgs {
+    const int *src, *dst, *free_pages, *free_start;
+    int *seq_lens, *block_table, *shares, *copies, *counts;
+    int F, B, max_pages, page_size, num_pages, num_free;
+};
+
+struct CopyArgs {
+    const int *src, *dst, *rows;
+    void *k_cache, *v_cache;
+    int n, Hkv, d, page_size, num_pages;
+};
+
+struct CompactArgs {
+    const int *keep, *keep_lens, *base_lens, *block_table;
+    void *k_cache, *v_cache;
+    int B, max_keep, max_pages, Hkv, d, page_size, num_pages;
+};
+
+struct FreeArgs {
+    const int *old_lens, *new_lens, *block_table, *free_start;
+    int *free_pages, *shares, *counts;
+    int B, max_pages, page_size, num_pages, num_free;
+};
+
 struct PagedArgs {
     const void *q, *k_cache, *v_cache;
     const int *block_table, *seq_lens;
@@ -102,6 +126,12 @@ cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStrea
 
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendArgs &a, cudaStream_t st);
+cudaError_t launch_paged_fork(const ForkArgs &a, cudaStream_t st);
+// Blocks of a copy's launch.
+long long copy_blocks(int n, int Hkv, int d, int page_size);
+cudaError_t launch_paged_copy(const CopyArgs &a, cudaStream_t st);
+cudaError_t launch_paged_compact(const CompactArgs &a, cudaStream_t st);
+cudaError_t launch_paged_free(const FreeArgs &a, cudaStream_t st);
 cudaError_t launch_fwd_paged(const PagedArgs &a, cudaStream_t st);
 
 }  // namespace fa

@@ -407,6 +407,116 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots,
                             fa_dtype_t dtype, void *stream);
 
 /*
+ * Branching requests of a paged cache: samples or beams that continue from
+ * one prompt, drafted tokens of which some are accepted, requests that end.
+ * A page may belong to several requests, whose table rows all name it:
+ *   shares int32 [num_pages]: how many requests hold a page beside the first
+ * (0 for a page of one request and for a free one, so what fa_paged_tables
+ * hands out needs no entry).  Pages that several requests hold are not to be
+ * written: fa_paged_fork gives a branch a page of its own where its next
+ * tokens go.
+ */
+
+/* Most forks of one fa_paged_fork call. */
+#define FA_PAGED_FORK_MAX 8192
+
+/*
+ * Lets row dst[f] of the table continue where row src[f] stands, for each of
+ * F forks.  With n = seq_lens[src[f]], full = n / page_size (rounded down)
+ * and part = n % page_size:
+ *   block_table[dst][0 .. full - 1] = block_table[src][0 .. full - 1], and
+ *   shares of each of those pages + 1
+ *   part > 0: block_table[dst][full] = free_pages[free_start + the number of
+ *   such forks before f], and copies = (block_table[src][full], that page,
+ *   part): what fa_paged_copy is to copy in every layer's cache
+ *   seq_lens[dst] = n
+ * A fork with part > 0 whose page would lie behind the list's end is not
+ * served: seq_lens[dst] = 0, its table row and all counts stay as they are.
+ *   src, dst [F] (in): rows of the table; no row may occur twice in dst, or
+ *       in both (what such rows then hold is not defined)
+ *   seq_lens [B], block_table [B][max_pages], shares [num_pages] (in/out)
+ *   free_pages, free_start: as in fa_paged_tables
+ *   copies [3][F] (out): source page, new page, rows of it; -1, -1, 0 for a
+ *       fork that needs no copy or was not served
+ *   counts [2] (out): the next free_start, and how many pages were lacking
+ * All arrays are int32 on the device, outputs must not overlap inputs (equal
+ * pointers are refused).  Rows outside the table, src[f] = dst[f], and a
+ * length that does not fit the row are reported by fa_get_device_status; such
+ * a fork only gets its copies (-1, -1, 0).  F <= FA_PAGED_FORK_MAX
+ * (FA_ERR_UNSUPPORTED otherwise), F <= B.
+ */
+fa_status_t fa_paged_fork(const int *src, const int *dst, int *seq_lens,
+                          int *block_table, const int *free_pages,
+                          const int *free_start, int *shares, int *copies,
+                          int *counts, int F, int B, int max_pages,
+                          int page_size, int num_pages, int num_free,
+                          void *stream);
+
+/*
+ * Copies pages of a cache: page dst[i] gets the first rows[i] tokens of page
+ * src[i], of all heads, in K and V.
+ *   src, dst int32 [n] (in): a negative number skips the pair; no page may
+ *       occur twice in dst, or in both
+ *   rows int32 [n] (in): 0 .. page_size; NULL: whole pages
+ *   k_cache, v_cache [num_pages][Hkv][page_size][d] (in/out)
+ */
+fa_status_t fa_paged_copy(const int *src, const int *dst, const int *rows,
+                          void *k_cache, void *v_cache, int n, int Hkv, int d,
+                          int page_size, int num_pages, fa_dtype_t dtype,
+                          void *stream);
+
+/*
+ * Moves the kept ones of a request's last tokens together, in place: the keys
+ * and values of token base_lens[b] + keep[b][i] go to the place of token
+ * base_lens[b] + i, i < keep_lens[b].  After a tree of drafted tokens, keep
+ * is the accepted path; with base_lens 0 any tokens of a long context may be
+ * dropped.  The request then has base_lens[b] + keep_lens[b] tokens.
+ *   keep [B][max_keep] (in): from 0 up, strictly increasing within a request;
+ *       entries behind keep_lens[b] are not read
+ *   keep_lens, base_lens [B] (in); block_table [B][max_pages] (in)
+ *   k_cache, v_cache (in/out): only the places of tokens that move are
+ *       written (keep[b][i] = i stays); the pages of those places must be the
+ *       request's own
+ * All index arrays are int32 on the device.  Entries out of order or beyond
+ * the table's row, and page numbers outside 0 .. num_pages - 1, are reported
+ * by fa_get_device_status, never read or written out of range, and their
+ * tokens not moved.
+ */
+fa_status_t fa_paged_compact(const int *keep, const int *keep_lens,
+                             const int *base_lens, const int *block_table,
+                             void *k_cache, void *v_cache, int B, int max_keep,
+                             int max_pages, int Hkv, int d, int page_size,
+                             int num_pages, fa_dtype_t dtype, void *stream);
+
+/*
+ * Takes pages back from requests that get shorter or end: request b had
+ * old_lens[b] tokens and keeps the first new_lens[b]; it gives up the pages
+ * of its table row's cells ceil(new) .. ceil(old) - 1 (in pages).  A page
+ * falls free if it is given up by more requests than its shares say, once;
+ * else its shares fall by their number.  The freed pages go in front of the
+ * free list's next entry, in the order of the first request and cell that
+ * gives each up:
+ *   free_pages[free_start - freed + i], i < freed
+ * (the list's entries below free_start are those handed out before).
+ *   old_lens, new_lens [B] (in): 0 <= new <= old <= max_pages * page_size
+ *   block_table [B][max_pages] (in); rows are left as they are
+ *   free_pages [num_free] (in/out), free_start [1] (in): 0 .. num_free
+ *   shares [num_pages] (in/out); NULL: no page is shared
+ *   counts [2] (out): the next free_start, and how many freed pages had no
+ *       room in front of it (the first ones in order; they are in no list)
+ * All arrays are int32 on the device; outputs must not overlap inputs.
+ * Requests with other lengths give up nothing, page numbers outside 0 ..
+ * num_pages - 1 are skipped, and both are reported by fa_get_device_status,
+ * as is a list without room.  B <= FA_PAGED_TABLES_MAX_B and B * max_pages <=
+ * 2^30 (FA_ERR_UNSUPPORTED otherwise).
+ */
+fa_status_t fa_paged_free(const int *old_lens, const int *new_lens,
+                          const int *block_table, int *free_pages,
+                          const int *free_start, int *shares, int *counts,
+                          int B, int max_pages, int page_size, int num_pages,
+                          int num_free, void *stream);
+
+/*
  * Device workspace of fa_fwd_paged (prefix_len = 0) and fa_fwd_paged_prefix:
  * partial results of key ranges that different blocks work on.  0 where none
  * is needed (a table so narrow that no sequence's keys are divided; NULL is
