@@ -17,7 +17,7 @@ from . import _lib
 
 __all__ = ["attention_fwd", "attention_bwd", "attention_fwd_varlen", "attention_bwd_varlen",
            "hadamard_quant_fp8", "attention_fwd_fp8", "paged_tables", "paged_append", "attention_fwd_paged",
-           "attention_fwd_paged_prefix", "paged_fork", "paged_copy", "paged_compact", "paged_free"]
+           "attention_fwd_paged_prefix", "attention_fwd_paged_tree", "paged_fork", "paged_copy", "paged_compact", "paged_free"]
 
 
 def _default_scale(d: int) -> float:
@@ -238,7 +238,7 @@ def paged_free(old_lens, new_lens, block_table, free_pages, free_start, page_siz
     return counts
 
 
-def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace):
+def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace, tree=False):
     """(O, LSE, workspace, max_new) of a paged forward call."""
     import torch
     if window is not None and window < 1:
@@ -252,8 +252,9 @@ def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_
     o = torch.empty_like(q)
     lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
     if workspace is None:
-        n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2],
-                                              prefix_len)
+        sizes = B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2]
+        n = (_lib.fa_fwd_paged_tree_workspace_bytes(*sizes) if tree else
+             _lib.fa_fwd_paged_workspace_bytes(*sizes, prefix_len))
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     return o, lse, workspace, max_new
@@ -299,4 +300,24 @@ def attention_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: in
     _lib.fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, cu_seqlens, o,
                              lse, max_new, _default_scale(q.shape[-1]) if scale is None else scale, workspace,
                              window or 0)
+    return o, lse
+
+
+def attention_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, max_new: int | None = None,
+                             scale: float | None = None, window: int | None = None, workspace=None, stream=None):
+    """``attention_fwd_paged`` for trees of drafted tokens, whose keys are the
+    last ones of each request.  ``parents`` (int32 [total], on the device):
+    the row of its request, counted from 0, that a row's token follows, below
+    its own, or -1 where it follows the context.  A row sees the context, its
+    path up to there and itself (``window``: the last ``window`` tokens of
+    these).  At most 1024 rows a request.  ``workspace``: as there, of
+    ``_lib.fa_fwd_paged_tree_workspace_bytes(B, total, max_new, Hq, Hkv, d,
+    max_pages, page_size)`` bytes."""
+    if stream is not None:
+        with _on(stream):
+            return attention_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, max_new,
+                                            scale, window, workspace)
+    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, 0, workspace, True)
+    _lib.fa_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, o, lse, max_new,
+                           _default_scale(q.shape[-1]) if scale is None else scale, workspace, window or 0)
     return o, lse

@@ -24,7 +24,7 @@ EXPORTS = (
     "fa_hadamard_quant_workspace_bytes", "fa_fwd_fp8", "fa_get_device_status",
     "fa_selftest_bounded_wait", "fa_status_string", "fa_fwd_f32_out", "fa_probe_exp2", "fa_fwd_persistent",
     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_fwd_paged_workspace_bytes",
-    "fa_paged_fork", "fa_paged_copy", "fa_paged_compact", "fa_paged_free",
+    "fa_fwd_paged_tree", "fa_fwd_paged_tree_workspace_bytes", "fa_paged_fork", "fa_paged_copy", "fa_paged_compact", "fa_paged_free",
 )
 
 _lock = threading.Lock()
@@ -78,6 +78,9 @@ def load():
         lib.fa_paged_free.argtypes = [P] * 7 + [I] * 5 + [P]
         lib.fa_fwd_paged.argtypes = [P] * 8 + [I] * 10 + [F, I, P, Z, P]
         lib.fa_fwd_paged_prefix.argtypes = [P] * 4 + [I] + [P] * 5 + [I] * 10 + [F, I, P, Z, P]
+        lib.fa_fwd_paged_tree.argtypes = [P] * 9 + [I] * 10 + [F, I, P, Z, P]
+        lib.fa_fwd_paged_tree_workspace_bytes.argtypes = [I] * 8
+        lib.fa_fwd_paged_tree_workspace_bytes.restype = Z
         lib.fa_fwd_paged_workspace_bytes.argtypes = [I] * 9
         lib.fa_fwd_paged_workspace_bytes.restype = Z
         lib.fa_get_device_status.argtypes = [P]
@@ -88,7 +91,7 @@ def load():
         lib.fa_status_string.restype = ctypes.c_char_p
         for name in ("fa_fwd", "fa_fwd_local", "fa_fwd_f32_out", "fa_fwd_persistent", "fa_bwd_local", "fa_fwd_varlen", "fa_bwd_varlen",
                      "fa_bwd", "fa_bwd_two_pass", "fa_bwd_noalloc", "fa_hadamard_quant_fp8", "fa_fwd_fp8",
-                     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_paged_fork",
+                     "fa_paged_tables", "fa_paged_append", "fa_fwd_paged", "fa_fwd_paged_prefix", "fa_fwd_paged_tree", "fa_paged_fork",
                      "fa_paged_copy", "fa_paged_compact", "fa_paged_free", "fa_get_device_status", "fa_selftest_bounded_wait"):
             getattr(lib, name).restype = I
         _lib = lib
@@ -584,6 +587,25 @@ def fa_fwd_paged_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, bloc
     _check("fa_fwd_paged_prefix", load().fa_fwd_paged_prefix(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix_pages.data_ptr(), int(prefix_len),
         block_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), *rest, _stream(stream)))
+
+
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
+def fa_fwd_paged_tree_workspace_bytes(B: int, total: int, max_new: int, Hq: int, Hkv: int, d: int, max_pages: int,
+                                      page_size: int) -> int:
+    return int(load().fa_fwd_paged_tree_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size))
+
+
+def fa_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, o, lse, max_new: int,
+                      scale: float, workspace, window: int = 0, stream=None):
+    """fa_fwd_paged for trees of drafted tokens; parents int32 [total]."""
+    rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window)
+    if not _are_int32(q.get_device(), parents) or parents.numel() != q.shape[0]:
+        import torch
+        _need_all(("q", q, q.dtype), ("parents", parents, torch.int32))
+        _need_numel(parents=(parents, q.shape[0]))
+    _check("fa_fwd_paged_tree", load().fa_fwd_paged_tree(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        _ptr(cu_seqlens), parents.data_ptr(), *rest, _stream(stream)))
 
 
 def fa_get_device_status(stream=None) -> int:

@@ -470,6 +470,8 @@ fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_byt
         return FA_ERR_INVALID_ARG;
     if (a.Hkv < 1 || a.Hq % a.Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return FA_ERR_INVALID_ARG;
+    if (a.parents && (!aligned4(a.parents) || !a.cu_seqlens)) return FA_ERR_INVALID_ARG;
+    if (a.parents && a.max_new > FA_PAGED_TREE_MAX_NEW) return FA_ERR_UNSUPPORTED;
     if (!a.cu_seqlens && (a.max_new != 1 || a.total < a.B)) return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(a.Hkv, a.d, a.page_size, a.num_pages, dtype);
     if (s != FA_OK) return s;
@@ -478,7 +480,7 @@ fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_byt
     if (a.window >= (long long)a.max_pages * a.page_size + a.prefix_len) a.window = 0;
     const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
                                            a.prefix_len, a.window, nullptr);
-    const size_t need = w.bytes;
+    const size_t need = w.bytes + (a.parents ? fa::tree_bytes(w, a.total, a.max_new) : 0);
     if (need > 0 &&
         (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)))
         return FA_ERR_WORKSPACE;
@@ -620,6 +622,30 @@ fa_status_t fa_fwd_paged_prefix(const void *q, const void *k_cache, const void *
     fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, prefix_pages, o, lse, B, total, max_new,
                     Hq, Hkv, d, max_pages, page_size, num_pages, prefix_len, window, scale, dtype == FA_BF16,
                     workspace, 0};
+    fa_status_t s = check_paged(a, dtype, workspace_bytes);
+    if (s != FA_OK) return s;
+    return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_fwd_paged_tree_workspace_bytes(int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages,
+                                         int page_size) {
+    if (B < 1 || total < 1 || max_new < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_pages < 1 ||
+        max_new > FA_PAGED_TREE_MAX_NEW || check_cache(Hkv, d, page_size, 1, FA_BF16) != FA_OK ||
+        !paged_sizes(B, total, Hq, max_pages, page_size, 0))
+        return 0;
+    const fa::PagedPlan w = fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, 0, 0, nullptr);
+    return w.bytes + fa::tree_bytes(w, total, max_new);
+}
+
+fa_status_t fa_fwd_paged_tree(const void *q, const void *k_cache, const void *v_cache, const int *block_table,
+                              const int *seq_lens, const int *cu_seqlens, const int *parents, void *o, float *lse,
+                              int B, int total, int max_new, int Hq, int Hkv, int d, int max_pages, int page_size,
+                              int num_pages, int window, float scale, fa_dtype_t dtype, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    FA_RANGE("fa_fwd_paged_tree");
+    if (!parents) return FA_ERR_INVALID_ARG;
+    fa::PagedArgs a{q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, nullptr, o, lse, B, total, max_new, Hq,
+                    Hkv, d, max_pages, page_size, num_pages, 0, window, scale, dtype == FA_BF16, workspace, 0, parents};
     fa_status_t s = check_paged(a, dtype, workspace_bytes);
     if (s != FA_OK) return s;
     return from_cuda(fa::launch_fwd_paged(a, static_cast<cudaStream_t>(stream)));

@@ -81,7 +81,8 @@ struct FewLayout {
     static constexpr int QBYTES = kMaxRows * D * 2;
     static constexpr int OFF_Q = kStages * 2 * TILE;
     static constexpr int OFF_INFO = OFF_Q + kStages * QBYTES;
-    static constexpr int OFF_BAR = OFF_INFO + kStages * (int)sizeof(TileInfo);
+    static constexpr int OFF_TREE = OFF_INFO + kStages * (int)sizeof(TileInfo);  // [kStages][16]
+    static constexpr int OFF_BAR = OFF_TREE + kStages * kMaxRows * 4;
     static constexpr int OFF_ML = OFF_BAR + 2 * kStages * 8;           // [3][4 warps][16]
     static constexpr int OFF_MISC = OFF_ML + 3 * kConsumers * 16 * 4;  // abort flag, the warps' sums
     static constexpr int BYTES = OFF_MISC + 16 + kFewWarps * (int)sizeof(PlanSum);
@@ -124,8 +125,34 @@ __device__ __forceinline__ int all_tiles(const FewParams &p, const Request &r) {
     return front + pair_tiles<TK>(p.a, r, t0);
 }
 
-// NT: 8-row groups of a pair (rows up to 8 * NT).
-template <int D, bool BF16, int NT>
+// The paths of a tree of up to 16 drafted tokens, one a lane: the tokens from
+// which lane i's hangs down, itself among them, a bit each, but for those that
+// a window hides, and its depth above them.  Twice as many with every step.
+__device__ __forceinline__ uint32_t tree_paths(const FewParams &p, const Request &r, int lane) {
+    int up = lane < r.n ? p.a.parents[r.row0 + lane] : -1;
+    if (up < -1 || up >= lane) {
+        record_bad_args(p.status);
+        up = -1;
+    }
+    uint32_t path = 1u << lane;
+#pragma unroll
+    for (int s = 1; s < kMaxRows; s *= 2) {
+        const int from = up < 0 ? lane : up;
+        const uint32_t more = __shfl_sync(0xffffffffu, path, from);
+        const int next = __shfl_sync(0xffffffffu, up, from);
+        if (up >= 0) path |= more;
+        up = up < 0 ? -1 : next;
+    }
+    path &= 0xFFFFu;  // of lanes that have no token
+    const int depth = __popc(path) - 1;
+    // the lowest are the farthest
+    for (int out = depth + 1 - p.a.window; p.a.window > 0 && out > 0; --out) path &= path - 1;
+    return path | (uint32_t)depth << 16;
+}
+
+// NT: 8-row groups of a pair (rows up to 8 * NT).  TREE: rows hang on one
+// another (PagedArgs::parents).
+template <int D, bool BF16, int NT, bool TREE>
 __global__ void __launch_bounds__(kFewThreads, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const FewParams p) {
@@ -134,6 +161,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR), *empty = full + kStages;
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::OFF_INFO);
+    uint32_t *tree = reinterpret_cast<uint32_t *>(smem + L::OFF_TREE);
     float *sm_m = reinterpret_cast<float *>(smem + L::OFF_ML);  // [4][16], then l, then exact l
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC);
     PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
@@ -255,6 +283,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             int front0, own0;  // first tiles
             const int front = front_tiles<L::TK>(p, r, front0), nt = front + pair_tiles<L::TK>(p.a, r, own0);
             const int cost = p.whole ? 0 : kPairCost, per_pair = p.whole ? 1 : nt + cost;  // units
+            const uint32_t paths = TREE && first_one ? tree_paths(p, r, lane) : 0;
             int hk = (int)((u - base) / per_pair);
             for (; ok && hk < Hkv && u < u1; ++hk) {
                 const long long pair0 = base + (long long)hk * per_pair, tile0 = pair0 + cost;
@@ -272,7 +301,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     const int shift = in_front ? p.a.prefix_len : 0, end = in_front ? p.a.prefix_len : r.len;
                     const int lo_min = p.a.window > 0 ? max(0, r.len - r.n + 1 - p.a.window + shift) : 0;
                     const int lo_max = p.a.window > 0 ? max(0, r.len - p.a.window + shift) : 0;
-                    const int hi_min = min(end, r.len - r.n + 1 + shift);
+                    const int hi_min = min(end, r.len - r.n + (TREE ? 0 : 1) + shift);
                     const int *table = in_front ? p.a.prefix_pages : p.a.block_table + (size_t)b * p.a.max_pages;
                     // pages that hold no visible key are neither looked up nor read
                     const int key0 = kv0 + sub * page_keys;
@@ -303,6 +332,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                   (kv0 < lo_max || kv0 + L::TK > hi_min ? kMask : 0) | (whole ? 0 : kPart) |
                                   (j0 == 0 ? kSlot1 : 0) | (in_front ? kFront : 0);
                         info[st] = t;
+                    }
+                    if (TREE && first_one && j == j0) {
+                        if (lane < kMaxRows) tree[st * kMaxRows + lane] = paths;
+                        __syncwarp();
                     }
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * box_bytes);
                     __syncwarp();
@@ -374,6 +407,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         float acc[NT][D / 16][4];  // columns rw, rw + 8 of each 16; rows 2 quad, + 1
         float m[NT][2], l[NT][2], le[NT][2];
         int hi[NT][2], lo[NT][2];
+        uint32_t path[NT][2];  // TREE: drafted keys that the row sees; it sees all before hi as far as lo
         int st = 0;
         uint32_t phase = 0;
         for (;;) {
@@ -413,9 +447,17 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int x = 0; x < 2; ++x) {
                         m[g][x] = -INFINITY;
                         l[g][x] = le[g][x] = 0.f;
-                        hi[g][x] = t.len - t.n + (g * 8 + quad * 2 + x) / p.group + 1;
+                        const int token = (g * 8 + quad * 2 + x) / p.group;
+                        int depth = token;
+                        if constexpr (TREE) {
+                            const uint32_t seen = tree[st * kMaxRows + min(token, kMaxRows - 1)];
+                            path[g][x] = seen & 0xFFFFu;
+                            depth = seen >> 16;
+                        }
+                        hi[g][x] = t.len - t.n + depth + 1;
                         // no window: below every place (a prefix' first key is at -prefix_len)
                         lo[g][x] = p.a.window > 0 ? hi[g][x] - p.a.window : -0x7FFFFFFF;
+                        if (TREE) hi[g][x] = t.len - t.n;
                     }
                 }
             }
@@ -444,8 +486,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = t.kv0 + w0 + i * 16 + rw + (e >> 1) * 8;
-                            if (key >= end || key - shift >= hi[g][e & 1] || key - shift < lo[g][e & 1])
-                                s[i][g][e] = -INFINITY;
+                            const int place = key - shift;
+                            bool hidden = key >= end || place < lo[g][e & 1];
+                            if constexpr (TREE) {
+                                // a drafted key is seen on the row's path, whatever its place
+                                if (key < end && place >= hi[g][e & 1])
+                                    hidden = !(path[g][e & 1] >> ((place - hi[g][e & 1]) & 15) & 1);
+                            } else {
+                                hidden |= place >= hi[g][e & 1];
+                            }
+                            if (hidden) s[i][g][e] = -INFINITY;
                         }
                     }
                 }
@@ -662,6 +712,61 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     wait_previous();
 }
 
+// For the 256-row kernel, which keys each row of a tree sees (PagedArgs).  A
+// block takes a request, a thread a row and a tile of 128 keys: it walks the
+// row's path, up as far as the tile begins, and sets the bits that fall into
+// it.  Bound by latency (one walk is as long as the path): some 2 us.
+constexpr int kTreeThreads = 128;
+
+struct TreeParams {
+    PagedArgs a;
+    int group, above;  // only requests of more rows a key/value head
+    unsigned int *status;
+};
+
+__global__ void __launch_bounds__(kTreeThreads) paged_tree_kernel(const TreeParams p) {
+    __shared__ int up[FA_PAGED_TREE_MAX_NEW];
+    wait_previous();
+    launch_dependents();
+    for (int b = blockIdx.x; b < p.a.B; b += gridDim.x) {
+        Request r;
+        const bool mine = load_request(p.a, b, r) && r.n * p.group > p.above;  // the 256-row kernel reports the others
+        if (!mine) continue;
+        __syncthreads();
+        for (int i = threadIdx.x; i < r.n; i += kTreeThreads) {
+            int j = p.a.parents[r.row0 + i];
+            if (j < -1 || j >= i) {
+                record_bad_args(p.status);
+                j = -1;
+            }
+            up[i] = j;
+        }
+        __syncthreads();
+        const int base = r.len - r.n, base0 = base & ~(kWideKeys - 1);  // of the first tile
+        const int tiles = (r.len - base0 + kWideKeys - 1) / kWideKeys;
+        for (int k = threadIdx.x; k < r.n * tiles; k += kTreeThreads) {
+            const int i = k / tiles, tile = k - i * tiles;
+            const int first = base0 + tile * kWideKeys - base;  // drafted token of the tile's first key
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // keys before the drafted ones
+                const int ctx = -first - 32 * q;
+                w[q] = ctx <= 0 ? 0u : ctx >= 32 ? 0xFFFFFFFFu : (1u << ctx) - 1;
+            }
+            int depth = 0;
+            for (int j = i; j >= 0 && (j >= first || (tile == 0 && p.a.window > 0)); j = up[j], ++depth) {
+                const int bit = j - first;
+                const bool seen = p.a.window == 0 || depth < p.a.window;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (seen && bit >> 5 == q) w[q] |= 1u << (bit & 31);
+            }
+            p.a.tree_words[(size_t)(r.row0 + i) * p.a.tree_tiles + tile] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (tile == 0 && p.a.window > 0) p.a.tree_depth[r.row0 + i] = depth - 1;
+        }
+    }
+}
+
 // Merges the parts of every row that has several.  A lane has C columns of a
 // row.  C = 8 (32 bytes of a part, 16 of O): a warp works on 2 rows (d = 128)
 // or 4, and W warps share the parts of their rows, each taking every W-th: one
@@ -828,7 +933,9 @@ cudaError_t launch_few_t(const PagedArgs &a, const PagedPlan &w, bool after, cud
     p.after = after ? 1 : 0;
     p.mixed = w.mixed ? 1 : 0;
     p.joined = w.joined ? 1 : 0;
-    auto kernel = (long long)a.max_new * p.group.d <= 8 ? paged_few_kernel<D, BF16, 1> : paged_few_kernel<D, BF16, 2>;
+    const bool eight = (long long)a.max_new * p.group.d <= 8;
+    auto kernel = eight ? paged_few_kernel<D, BF16, 1, false> : paged_few_kernel<D, BF16, 2, false>;
+    if (a.parents) kernel = eight ? paged_few_kernel<D, BF16, 1, true> : paged_few_kernel<D, BF16, 2, true>;
     return launch_after(kernel, p.part.ctas, kFewThreads, L::ALLOC, st, tk, tv, p);
 }
 
@@ -967,6 +1074,11 @@ cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after,
     return a.bf16 ? launch_few_t<64, true>(a, w, after, st) : launch_few_t<64, false>(a, w, after, st);
 }
 
+cudaError_t launch_paged_tree(const PagedArgs &a, int above, cudaStream_t st) {
+    TreeParams p{a, a.Hq / a.Hkv, above, device_status_ptr()};
+    return launch_after(paged_tree_kernel, at_most(a.B, 8 * kSms), kTreeThreads, 0, st, p);
+}
+
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st) {
     if (a.d == 128) return a.bf16 ? launch_merge_t<128, true>(a, w, st) : launch_merge_t<128, false>(a, w, st);
     return a.bf16 ? launch_merge_t<64, true>(a, w, st) : launch_merge_t<64, false>(a, w, st);
@@ -980,6 +1092,12 @@ cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
                                    a.window, a.workspace);
     cudaError_t e = cudaSuccess;
     const bool front = w.prefix.ctas > 0;
+    if (a.parents && !w.few) {
+        a.tree_tiles = tree_tiles(a.max_new);
+        a.tree_words = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.workspace) + w.bytes);
+        a.tree_depth = reinterpret_cast<int *>(a.tree_words + (size_t)a.total * a.tree_tiles);
+        if ((e = launch_paged_tree(a, w.mixed ? kMaxRows : 0, st)) != cudaSuccess) return e;
+    }
     if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;
     if (!w.few && (e = launch_paged_wide(a, w, false, front, st)) != cudaSuccess) return e;
     if (w.few || w.mixed) e = launch_paged_few(a, w, front || w.mixed, st);

@@ -257,8 +257,9 @@ __device__ __forceinline__ void joint_epilogue(const WideParams &p, uint32_t o_c
 }
 
 // JOINED: the shared prefix' keys are read with each request's own.  LONG: a
-// block may have more tiles than a sum should.
-template <int D, bool BF16, bool JOINED, bool LONG>
+// block may have more tiles than a sum should.  TREE: rows hang on one another
+// (PagedArgs::parents), and see of the drafted keys what their words say.
+template <int D, bool BF16, bool JOINED, bool LONG, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const WideParams p) {
@@ -809,7 +810,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     // no window: below every place (a prefix' first key is at -prefix_len)
                     hi = sg.len - sg.n + t + 1;
+                    if (TREE && p.a.window > 0) hi += p.a.tree_depth[tok] - t;
                     lo = p.a.window > 0 ? window_low(hi, p.a.window) : -0x7FFFFFFF;
+                    if (TREE) hi = sg.len - sg.n;  // the keys that it sees for being before the drafted ones
                 }
             }
             const int nj = sg.nj;
@@ -834,7 +837,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const KeyTile<JOINED> tile(sg, u, p.a.prefix_len);
                 const int shift = tile.in_front ? p.a.prefix_len : 0;  // the tile's keys as places
                 const int kv0 = tile.kv0 - shift, key_lo = tile.lo - shift, key_hi = tile.hi - shift;
-                if (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo)) {  // uniform in the warp
+                if (TREE && (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo))) {
+                    // keys before the tile of the first drafted one: all but those below a window
+                    uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
+                    if (valid && kv0 + kBN > hi)
+                        w = p.a.tree_words[(size_t)tok * p.a.tree_tiles + (kv0 - (hi & ~(kBN - 1))) / kBN];
+                    const uint32_t seen[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (!(seen[c >> 5] >> (c & 31) & 1) || kv0 + c >= key_hi || (kv0 + c < hi && kv0 + c < lo) || kv0 + c < key_lo)
+                            s[c] = __float_as_uint(-INFINITY);
+                } else if (!TREE && (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo))) {  // uniform in the warp
                     const int top = min(hi, key_hi), low = max(lo, key_lo);
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
@@ -1016,9 +1029,14 @@ cudaError_t launch_wide_t(const PagedArgs &a, const PagedPlan &w, bool prefix, b
     p.part = prefix ? w.prefix : w.own;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = device_status_ptr();
-    const bool many = (prefix ? w.prefix_tiles : w.own_tiles) > kMaxTiles<BF16>;
-    auto kernel = many ? paged_wide_kernel<D, BF16, false, true> : paged_wide_kernel<D, BF16, false, false>;
-    if (w.joined) kernel = many ? paged_wide_kernel<D, BF16, true, true> : paged_wide_kernel<D, BF16, true, false>;
+    // under a window a block of a tree's rows may see as many more keys as there are drafted ones
+    const long long tiles = prefix ? w.prefix_tiles : w.own_tiles + (a.parents ? a.max_new / kWideKeys + 1 : 0);
+    const bool many = tiles > kMaxTiles<BF16>;
+    auto kernel = many ? paged_wide_kernel<D, BF16, false, true, false> : paged_wide_kernel<D, BF16, false, false, false>;
+    if (w.joined)
+        kernel = many ? paged_wide_kernel<D, BF16, true, true, false> : paged_wide_kernel<D, BF16, true, false, false>;
+    if (a.parents)
+        kernel = many ? paged_wide_kernel<D, BF16, false, true, true> : paged_wide_kernel<D, BF16, false, false, true>;
     return launch_after(kernel, p.part.ctas, kThreads, L::ALLOC, st, tq, tk, tv, p);
 }
 

@@ -120,7 +120,8 @@ __host__ __device__ __forceinline__ void block_keys(const PagedArgs &a, const Fa
     const int last =
         (r.n * group.d - k * kWideRows > kWideRows ? (k + 1) * kWideRows - 1 : r.n * group.d - 1) / group;
     hi = max(0, r.len - r.n + last + 1);
-    const int seen = r.len - r.n + first + 1;  // places below it, by the first row
+    // places below it, by the first row; in a tree any may hang on the context
+    const int seen = r.len - r.n + (a.parents ? 0 : first) + 1;
     lo = a.window > 0 && seen > a.window ? seen - a.window : 0;
 }
 // First place that a row which sees places below hi sees under a window; what

@@ -586,6 +586,47 @@ fa_status_t fa_fwd_paged_prefix(const void *q, const void *k_cache,
                                 void *workspace, size_t workspace_bytes,
                                 void *stream);
 
+/* Most drafted tokens of a request in one fa_fwd_paged_tree call. */
+#define FA_PAGED_TREE_MAX_NEW 1024
+
+/*
+ * Device workspace of fa_fwd_paged_tree; 0 where none is needed and for sizes
+ * that the forward refuses.
+ */
+size_t fa_fwd_paged_tree_workspace_bytes(int B, int total, int max_new, int Hq,
+                                         int Hkv, int d, int max_pages,
+                                         int page_size);
+
+/*
+ * fa_fwd_paged for rows that are trees of drafted tokens: what a model that
+ * verifies several guesses at once computes.  The last n_b of a request's
+ * seq_lens[b] keys are its rows' own, row i's at base + i, base = seq_lens[b]
+ * - n_b; the keys before are the context.
+ *   parents int32 [total] (in): of row cu_seqlens[b] + i, the row of request
+ *       b that its token follows, 0 .. i - 1, or -1: it follows the context's
+ *       last token (there may be several such).  A chain, parents[i] = i - 1,
+ *       is fa_fwd_paged.
+ *   Row i sees the context, the tokens on its path up to the context, and
+ *   itself.  It stands at place base + (tokens of its path before it); window
+ *   > 0 leaves it the `window` last tokens of context and path.
+ *   cu_seqlens is needed; max_new <= FA_PAGED_TREE_MAX_NEW
+ *   (FA_ERR_UNSUPPORTED otherwise).  A request with fewer keys than rows has
+ *   no context, and its first rows no keys: they see of their paths what is
+ *   there.  A parent out of its range is reported by fa_get_device_status and
+ *   counts as -1.
+ *   workspace: at least fa_fwd_paged_tree_workspace_bytes(...) bytes.
+ *   Otherwise as fa_fwd_paged.
+ */
+fa_status_t fa_fwd_paged_tree(const void *q, const void *k_cache,
+                              const void *v_cache, const int *block_table,
+                              const int *seq_lens, const int *cu_seqlens,
+                              const int *parents, void *o, float *lse, int B,
+                              int total, int max_new, int Hq, int Hkv, int d,
+                              int max_pages, int page_size, int num_pages,
+                              int window, float scale, fa_dtype_t dtype,
+                              void *workspace, size_t workspace_bytes,
+                              void *stream);
+
 /*
  * Reads and clears the current device's status, which kernels set when
  * a bounded wait runs out, when packed sequence offsets read on the device
