@@ -316,8 +316,9 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
 
 // -------------------------------------------------------------------- free
 
-constexpr int kFreeThreads = 1024;
-constexpr int kFreeCtas = 8;  // of the one cluster, at most
+constexpr int kFreeThreads = 1024, kFreeWarps = kFreeThreads / 32;
+constexpr int kFreeCtas = 16;  // of the one cluster, at most
+constexpr int kFreeKept = 16;  // cells whose pages a lane keeps
 // What stands in shares[] for a page that falls free, while the call runs:
 // below every count, the lower the earlier the first cell that gives it up.
 constexpr int kFreeCode = -(1 << 30);
@@ -348,13 +349,14 @@ __device__ __forceinline__ int cluster_load(const int *mine, int rank) {
 //   3  the cell that finds its own number has the page; they are counted
 //   4  and write the pages, by the counts of the warps before, and the zeros
 // with barriers of the cluster between them.  Without, every cell has its page.
+template <bool SHARED>
 __global__ void __launch_bounds__(kFreeThreads) paged_free_kernel(const FreeParams p) {
     extern __shared__ int smem[];
     const int B = p.a.B;
     int *first = smem;      // [B] number of a request's first cell
     int *col = smem + B;    // [B] its column
-    __shared__ long long sm[kFreeThreads / 32][2];
-    __shared__ int warp_freed[kFreeThreads / 32], cta_freed;
+    __shared__ long long sm[kFreeWarps][2];
+    __shared__ int warp_freed[kFreeWarps], cta_freed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (B + kFreeThreads - 1) / kFreeThreads | 1;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
@@ -383,68 +385,86 @@ __global__ void __launch_bounds__(kFreeThreads) paged_free_kernel(const FreePara
     }
     __syncthreads();
     if (bad && rank == 0) record_bad_args(p.status);
-    const int E = (int)all;  // below 2^30: the entry point sees to it
-    const long long each = ((long long)E + (long long)ctas * (kFreeThreads / 32) * 32 - 1) /
-                           ((long long)ctas * (kFreeThreads / 32) * 32) * 32;
-    const long long at = (rank * (kFreeThreads / 32) + warp) * each;
-    const int e0 = (int)min(at, (long long)E), e1 = (int)min(at + each, (long long)E);
-    // the page of cell e, -1 if there is none of that number
+    const int E = (int)all;  // at most 2^30: the entry point sees to it
+    const int units = (E + 31) / 32, each = (units + ctas * kFreeWarps - 1) / (ctas * kFreeWarps);
+    const int u0 = min(units, (rank * kFreeWarps + warp) * each), u1 = min(units, u0 + each);  // of 32 cells
+    // the page of cell e, -1 if there is none, or none of that number
     auto page_of = [&](int e) {
+        if (e >= E) return -1;
         const int b = last_at_most(first, B, e);
         const int page = p.a.block_table[(size_t)b * p.a.max_pages + col[b] + e - first[b]];
-        return (unsigned)page < (unsigned)p.a.num_pages ? page : -1;
+        if ((unsigned)page < (unsigned)p.a.num_pages) return page;
+        record_bad_args(p.status);
+        return -1;
     };
-    if (p.a.shares) {
-        for (int e = e0 + lane; e < e1; e += 32) {
-            const int page = page_of(e);
-            if (page >= 0) atomicSub(p.a.shares + page, 1);
-        }
+    // A lane keeps the pages of its first cells, which are all of them but for
+    // very long tables, and looks the others up in every pass again.
+    int kept[kFreeKept];
+#pragma unroll
+    for (int i = 0; i < kFreeKept; ++i) kept[i] = u0 + i < u1 ? page_of((u0 + i) * 32 + lane) : -1;
+    auto for_each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kFreeKept; ++i)
+            if (u0 + i < u1) f((u0 + i) * 32 + lane, kept[i], i);
+#pragma unroll 1
+        for (int u = u0 + kFreeKept; u < u1; ++u) f(u * 32 + lane, page_of(u * 32 + lane), kFreeKept);
+    };
+    int *shares = p.a.shares;
+    if (SHARED) {
+        unsigned seen_free = 0;  // of the kept cells, whose page fell free with them or before
+        for_each([&](int, int page, int i) {
+            if (page < 0) return;
+            if (i == kFreeKept)
+                atomicSub(shares + page, 1);
+            else if (atomicSub(shares + page, 1) <= 0)
+                seen_free |= 1u << i;
+        });
         cluster_sync();
-        for (int e = e0 + lane; e < e1; e += 32) {
-            const int page = page_of(e);
-            if (page >= 0 && __ldcg(p.a.shares + page) < 0) atomicMin(p.a.shares + page, kFreeCode - (E - 1 - e));
-        }
+        for_each([&](int e, int page, int i) {
+            if (page < 0) return;
+            if ((i < kFreeKept && seen_free >> i & 1) || __ldcg(shares + page) < 0)
+                atomicMin(shares + page, kFreeCode - (E - 1 - e));
+        });
         cluster_sync();
     }
-    auto frees = [&](int e, int page) {
-        return page >= 0 && (!p.a.shares || __ldcg(p.a.shares + page) == kFreeCode - (E - 1 - e));
-    };
+    unsigned has = 0;  // of the kept cells, which have their page
     int mine = 0;
-    for (int e = e0; e < e1; e += 32) {
-        const int page = e + lane < e1 ? page_of(e + lane) : -1;
-        if (page < 0 && e + lane < e1) record_bad_args(p.status);
-        mine += __popc(__ballot_sync(0xffffffffu, frees(e + lane, page)));
-    }
+    auto frees = [&](int e, int page) {
+        return page >= 0 && (!SHARED || __ldcg(shares + page) == kFreeCode - (E - 1 - e));
+    };
+    for_each([&](int e, int page, int i) {
+        const bool f = frees(e, page);
+        if (f && i < kFreeKept) has |= 1u << i;
+        mine += __popc(__ballot_sync(0xffffffffu, f));
+    });
     if (lane == 0) warp_freed[warp] = mine;
     __syncthreads();
     int before = 0, total = 0;
-    for (int w = 0; w < kFreeThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < kFreeWarps; ++w) {
         if (w < warp) before += warp_freed[w];
         total += warp_freed[w];
     }
     if (ctas > 1) {
         if (tid == 0) cta_freed = total;
         cluster_sync();
-        total = 0;
-        for (int r = 0; r < ctas; ++r) {
-            const int x = cluster_load(&cta_freed, r);
-            if (r < rank) before += x;
-            total += x;
-        }
+        // a CTA's number by each of the first lanes
+        const int theirs = lane < ctas ? cluster_load(&cta_freed, lane) : 0;
+        total = __reduce_add_sync(0xffffffffu, theirs);
+        before += __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0);
         cluster_sync();  // no CTA leaves, and nobody clears a code, before all have read
     }
     int to = start - total + before;
-    for (int e = e0; e < e1; e += 32) {
-        const int page = e + lane < e1 ? page_of(e + lane) : -1;
-        const bool mine_too = frees(e + lane, page);
-        const unsigned who = __ballot_sync(0xffffffffu, mine_too);
-        if (mine_too) {
+    for_each([&](int e, int page, int i) {
+        const bool f = i < kFreeKept ? has >> i & 1 : frees(e, page);
+        const unsigned who = __ballot_sync(0xffffffffu, f);
+        if (f) {
             const int k = to + __popc(who & ((1u << lane) - 1));
             if (k >= 0) p.a.free_pages[k] = page;
-            if (p.a.shares) p.a.shares[page] = 0;
+            if (SHARED) shares[page] = 0;
         }
         to += __popc(who);
-    }
+    });
     if (rank == 0 && tid == 0) {
         p.a.counts[0] = max(0, start - total);
         p.a.counts[1] = max(0, total - start);
@@ -505,10 +525,16 @@ cudaError_t launch_paged_compact(const CompactArgs &a, cudaStream_t st) {
 cudaError_t launch_paged_free(const FreeArgs &a, cudaStream_t st) {
     FreeParams p{a, log2_of(a.page_size), device_status_ptr()};
     auto smem = [](size_t requests) { return 2 * requests * sizeof(int); };
-    // one CTA where a thread has few cells at most, else a cluster of eight
-    const unsigned grid = (long long)a.B * a.max_pages <= 4 * kFreeThreads ? 1 : kFreeCtas;
-    return launch_cluster_after(paged_free_kernel, grid, grid, kFreeThreads,
-                                DynSmem(smem(a.B), smem(FA_PAGED_TABLES_MAX_B)), st, p);
+    // CTAs of 4 cells a thread, as many as there can be cells for
+    unsigned grid = 1;
+    while (grid < kFreeCtas && (long long)a.B * a.max_pages > (long long)grid * 4 * kFreeThreads) grid *= 2;
+    auto kernel = a.shares ? paged_free_kernel<true> : paged_free_kernel<false>;
+    if (grid > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_cluster_after(kernel, grid, grid, kFreeThreads, DynSmem(smem(a.B), smem(FA_PAGED_TABLES_MAX_B)), st,
+                                p);
 }
 
 }  // namespace fa
