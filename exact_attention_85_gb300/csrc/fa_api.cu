@@ -568,8 +568,10 @@ fa_status_t fa_paged_compact(const int *keep, const int *keep_lens, const int *b
         return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(Hkv, d, page_size, num_pages, dtype);
     if (s != FA_OK) return s;
-    // blocks: of every request's heads, K and V, up to 8 of a row
-    if (!table_sizes(B, max_pages, page_size) || 16ll * B * Hkv > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    // blocks: of every request's heads, K and V, up to 8 of a row; a head's rows are counted in 32 bits
+    if (!table_sizes(B, max_pages, page_size) || 16ll * B * Hkv > 0x7FFFFFFFll ||
+        (long long)num_pages * Hkv * page_size >= 0xFFFFFFFFll)
+        return FA_ERR_UNSUPPORTED;
     fa::CompactArgs a{keep, keep_lens, base_lens, block_table, k_cache, v_cache, B, max_keep, max_pages, Hkv, d,
                       page_size, num_pages};
     return from_cuda(fa::launch_paged_compact(a, static_cast<cudaStream_t>(stream)));

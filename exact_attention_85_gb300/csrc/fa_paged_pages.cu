@@ -4,8 +4,10 @@
 // back (fa_paged_free).
 #include "../../include/fa.h"
 #include "host_util.h"
+#include "mma_sync.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
+#include "ptx.cuh"
 #include "status.cuh"
 
 #include <algorithm>
@@ -230,9 +232,13 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyPara
 
 // ----------------------------------------------------------------- compact
 
-constexpr int kMoveThreads = 128, kMoveUnroll = 8;
+constexpr int kMoveThreads = 256, kMoveUnroll = 4;
 constexpr int kMoveBytes = kMoveThreads * kMoveUnroll * 16;  // of a tile of rows
-constexpr int kMoveRows = kMoveBytes / 32;                   // where a block has 32 bytes of a row
+constexpr int kMoveStages = 3;                               // tiles in shared memory
+constexpr int kMoveLook = kMoveUnroll / 2;                   // rows of a tile that a thread looks up, at most
+constexpr int kMoveSlots = kMoveStages + 1;                  // tiles whose slots are known
+
+constexpr unsigned kStays = 0xFFFFFFFFu;
 
 struct CompactParams {
     CompactArgs a;
@@ -244,20 +250,24 @@ struct CompactParams {
 
 // In place: token base + i gets token base + keep[i], keep[i] >= i, increasing.
 // A block takes some columns of one head of a request, K or V, and walks the
-// kept tokens tile by tile.  A tile is read before it is written, and what
-// later tiles read lies behind everything that this one and those before it
-// write: keep[j] >= j.  So blocks never touch one another's bytes, and within
-// a block one barrier between a tile's last read and its first write suffices.
+// kept tokens tile by tile, with the loads of two tiles ahead of the stores.
+// What a later tile reads lies behind everything that this one and those
+// before it write (keep[j] >= j), so it may be read early; a tile's own reads
+// have landed, in every thread, before its first write.  Blocks never touch
+// one another's bytes.  Bound by the memory's bandwidth at short pieces: 302 MB
+// in and out in 57 us, 5.3 TB/s.  (A copy is on its way for one to two tiles;
+// 128 threads with twice the pieces each took 67 us, slots that are looked up
+// when they are needed 106, as a tile then takes two loads' latency.)
 __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const CompactParams p) {
-    // of the rows of a tile, from and to (-1: none): the one that is stored,
-    // the one that is loaded, and the one that is looked up meanwhile
-    __shared__ int slot[3][2][kMoveRows];
+    extern __shared__ __align__(16) uint8_t move_smem[];  // [kMoveStages] tiles, then slots
     const int tid = threadIdx.x;
     int unit = blockIdx.x / p.split;
     const int col0 = (blockIdx.x - unit * p.split) * p.cols;
     const int b = unit / p.heads, plane = unit - b * p.heads.d;  // K's heads, then V's
     const int h = plane >= p.a.Hkv ? plane - p.a.Hkv : plane;
     const int rows = kMoveThreads * kMoveUnroll / p.cols;  // of a tile
+    // [kMoveSlots][rows]: from and to, rows of the cache's heads (kStays: none)
+    uint2 *slots = reinterpret_cast<uint2 *>(move_smem + kMoveStages * kMoveBytes);
     wait_previous();
     launch_dependents();
     const int n = p.a.keep_lens[b], base = p.a.base_lens[b];
@@ -268,49 +278,107 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
     }
     const int *keep = p.a.keep + (size_t)b * p.a.max_keep, *table = p.a.block_table + (size_t)b * p.a.max_pages;
     uint8_t *cache = static_cast<uint8_t *>(plane >= p.a.Hkv ? p.a.v_cache : p.a.k_cache) + col0 * 16;
-    auto find_slots = [&](int i0, int buf) {
-        for (int r = tid; r < rows; r += kMoveThreads) {
-            const int i = i0 + r;
-            int from = -1, to = -1;
-            if (i < n) {
-                const int k = keep[i], before = i ? keep[i - 1] : -1;
-                if (k <= before || k < i || k >= room - base) {
-                    record_bad_args(p.status);
-                } else if (k != i) {
-                    const int pf = table[(base + k) >> p.shift], pt = table[(base + i) >> p.shift];
-                    if ((unsigned)pf >= (unsigned)p.a.num_pages || (unsigned)pt >= (unsigned)p.a.num_pages) {
-                        record_bad_args(p.status);
-                    } else {
-                        const int mask = (1 << p.shift) - 1;
-                        from = (pf << p.shift) + ((base + k) & mask);
-                        to = (pt << p.shift) + ((base + i) & mask);
-                    }
-                }
+    const int tiles = (n + rows - 1) / rows;
+    // Looking up a row's slots takes two loads, one behind the other: its kept
+    // token, and the pages of both places.  Each is started a tile before its
+    // result is needed.
+    int k[kMoveLook], prev[kMoveLook], from[kMoveLook], page_from[kMoveLook], page_to[kMoveLook];
+    const int mask = (1 << p.shift) - 1;
+    auto fetch_keep = [&](int t) {
+#pragma unroll
+        for (int q = 0; q < kMoveLook; ++q) {
+            const int r = tid + q * kMoveThreads, i = t * rows + r;
+            k[q] = i;  // stays
+            prev[q] = -1;
+            if (t >= tiles || r >= rows || i >= n) continue;
+            k[q] = keep[i];
+            if (i) prev[q] = keep[i - 1];
+        }
+    };
+    auto fetch_pages = [&](int t) {
+#pragma unroll
+        for (int q = 0; q < kMoveLook; ++q) {
+            const int i = t * rows + tid + q * kMoveThreads;
+            from[q] = -1;
+            if (k[q] == i && prev[q] < i) continue;
+            if (k[q] <= prev[q] || k[q] < i || k[q] >= room - base) {
+                record_bad_args(p.status);
+                continue;
             }
-            slot[buf][0][r] = from;
-            slot[buf][1][r] = to;
+            from[q] = base + k[q];
+            page_from[q] = table[from[q] >> p.shift];
+            page_to[q] = table[(base + i) >> p.shift];
         }
     };
-    auto at = [&](int s) {  // of slot s, this head
-        return cache + ((((size_t)(s >> p.shift) * p.a.Hkv + h) << p.shift) + (s & ((1 << p.shift) - 1))) * p.row_bytes;
+    auto put_slots = [&](int t) {
+#pragma unroll
+        for (int q = 0; q < kMoveLook; ++q) {
+            const int r = tid + q * kMoveThreads, i = t * rows + r;
+            if (t >= tiles || r >= rows) continue;
+            uint2 s = make_uint2(kStays, kStays);
+            if (from[q] >= 0) {
+                if ((unsigned)page_from[q] < (unsigned)p.a.num_pages && (unsigned)page_to[q] < (unsigned)p.a.num_pages)
+                    s = make_uint2((((unsigned)page_from[q] * p.a.Hkv + h) << p.shift) + (from[q] & mask),
+                                   (((unsigned)page_to[q] * p.a.Hkv + h) << p.shift) + ((base + i) & mask));
+                else
+                    record_bad_args(p.status);
+            }
+            slots[t % kMoveSlots * rows + r] = s;
+        }
     };
-    const int row = tid / p.cols, col = (tid - row * p.cols) * 16, step = kMoveThreads / p.cols;
-    find_slots(0, 0);
+    const int row = tid / p.cols, step = kMoveThreads / p.cols;
+    uint8_t *const column = cache + (tid - row * p.cols) * 16;
+    auto at = [&](unsigned r) { return reinterpret_cast<uint4 *>(column + (size_t)r * p.row_bytes); };
+    const uint32_t mine = smem_u32(move_smem) + tid * 16;  // a thread's pieces are its own
+    auto load = [&](int t) {
+        if (t < tiles) {
+            const uint2 *s = slots + t % kMoveSlots * rows + row;
+            const uint32_t to = mine + t % kMoveStages * kMoveBytes;
+            unsigned r[kMoveUnroll];
+#pragma unroll
+            for (int j = 0; j < kMoveUnroll; ++j) r[j] = s[j * step].x;
+#pragma unroll
+            for (int j = 0; j < kMoveUnroll; ++j)
+                if (r[j] != kStays) cp_async_16(to + j * kMoveThreads * 16, at(r[j]));
+        }
+        cp_async_commit();
+    };
+    // lines of keep[], a tile's by its threads, eight tiles ahead: from memory
+    // they would take longer than a tile
+    auto prefetch_keep = [&](int i) {
+        if (i < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(keep + i));
+    };
+    for (int i = tid * 32; i < 8 * rows; i += 32 * kMoveThreads) prefetch_keep(i);
+    for (int t = 0; t < kMoveStages - 1; ++t) {
+        fetch_keep(t);
+        fetch_pages(t);
+        put_slots(t);
+    }
     __syncthreads();
-    for (int i0 = 0, buf = 0, next = 1; i0 < n; i0 += rows, buf = next, next = next == 2 ? 0 : next + 1) {
-        uint4 x[kMoveUnroll];
-#pragma unroll
-        for (int j = 0; j < kMoveUnroll; ++j) {
-            const int s = slot[buf][0][row + j * step];
-            if (s >= 0) x[j] = *reinterpret_cast<const uint4 *>(at(s) + col);
-        }
-        if (i0 + rows < n) find_slots(i0 + rows, next);
+    for (int t = 0; t < kMoveStages - 1; ++t) load(t);
+    fetch_keep(kMoveStages - 1);
+    fetch_pages(kMoveStages - 1);
+    fetch_keep(kMoveStages);
+    for (int t = 0; t < tiles; ++t) {
+        put_slots(t + kMoveStages - 1);
+        fetch_pages(t + kMoveStages);
+        fetch_keep(t + kMoveStages + 1);
+        if (tid * 32 < rows) prefetch_keep((t + 8) * rows + tid * 32);
+        cp_async_wait<kMoveStages - 2>();
         __syncthreads();
+        load(t + kMoveStages - 1);
+        const uint2 *s = slots + t % kMoveSlots * rows + row;
+        const uint4 *x = reinterpret_cast<const uint4 *>(move_smem + t % kMoveStages * kMoveBytes) + tid;
+        unsigned r[kMoveUnroll];
+        uint4 y[kMoveUnroll];
 #pragma unroll
         for (int j = 0; j < kMoveUnroll; ++j) {
-            const int s = slot[buf][1][row + j * step];
-            if (s >= 0) *reinterpret_cast<uint4 *>(at(s) + col) = x[j];
+            r[j] = s[j * step].y;
+            y[j] = x[j * kMoveThreads];
         }
+#pragma unroll
+        for (int j = 0; j < kMoveUnroll; ++j)
+            if (r[j] != kStays) *at(r[j]) = y[j];
     }
 }
 
@@ -514,12 +582,19 @@ cudaError_t launch_paged_compact(const CompactArgs &a, cudaStream_t st) {
     p.row_bytes = 2 * a.d;
     p.heads = fast_div(2 * a.Hkv);
     p.status = device_status_ptr();
-    // blocks of a row's columns, 32 bytes at least, until there are two an SM
+    // Blocks of a row's columns, 32 bytes at least, until there is one an SM.
+    // 128 units of 4096 .. 8191 rows of 256 bytes: 78 us with a block each, 57
+    // with two, 65 with four, 72 with eight: short pieces of a row cost more
+    // instructions and more of the memory's bandwidth than they fill.
     const long long units = 2ll * a.B * a.Hkv;
     p.split = 1;
-    while (p.row_bytes / p.split > 32 && units * p.split < 2 * kSms) p.split *= 2;
+    while (p.row_bytes / p.split > 32 && units * p.split < kSms) p.split *= 2;
     p.cols = p.row_bytes / p.split / 16;
-    return launch_after(paged_compact_kernel, (unsigned)(units * p.split), kMoveThreads, 0, st, p);
+    auto smem = [](int cols) {
+        return (size_t)kMoveStages * kMoveBytes + kMoveSlots * (kMoveThreads * kMoveUnroll / cols) * sizeof(uint2);
+    };
+    return launch_after(paged_compact_kernel, (unsigned)(units * p.split), kMoveThreads,
+                        DynSmem(smem(p.cols), smem(2)), st, p);
 }
 
 cudaError_t launch_paged_free(const FreeArgs &a, cudaStream_t st) {

@@ -54,6 +54,14 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
 // Waits for this thread's cp.async copies.
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Ends a group of this thread's cp.async copies, and waits until all but the
+// last N groups have landed.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Arrives on `bar` when this thread's cp.async copies so far have landed
 // (counted among the barrier's expected arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
