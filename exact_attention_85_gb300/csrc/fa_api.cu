@@ -480,7 +480,7 @@ fa_status_t check_paged(fa::PagedArgs &a, fa_dtype_t dtype, size_t workspace_byt
     if (a.window >= (long long)a.max_pages * a.page_size + a.prefix_len) a.window = 0;
     const fa::PagedPlan w = fa::plan_paged(a.B, a.total, a.max_new, a.Hq, a.Hkv, a.d, a.max_pages, a.page_size,
                                            a.prefix_len, a.window, nullptr);
-    const size_t need = w.bytes + (a.parents ? fa::tree_bytes(w, a.total, a.max_new) : 0);
+    const size_t need = w.bytes + (a.parents ? fa::tree_bytes(w, a.Hq / a.Hkv, a.max_new) : 0);
     if (need > 0 &&
         (!a.workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(a.workspace) & 255u)))
         return FA_ERR_WORKSPACE;
@@ -636,7 +636,7 @@ size_t fa_fwd_paged_tree_workspace_bytes(int B, int total, int max_new, int Hq, 
         !paged_sizes(B, total, Hq, max_pages, page_size, 0))
         return 0;
     const fa::PagedPlan w = fa::plan_paged(B, total, max_new, Hq, Hkv, d, max_pages, page_size, 0, 0, nullptr);
-    return w.bytes + fa::tree_bytes(w, total, max_new);
+    return w.bytes + fa::tree_bytes(w, Hq / Hkv, max_new);
 }
 
 fa_status_t fa_fwd_paged_tree(const void *q, const void *k_cache, const void *v_cache, const int *block_table,

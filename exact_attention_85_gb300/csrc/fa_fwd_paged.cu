@@ -712,61 +712,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     wait_previous();
 }
 
-// For the 256-row kernel, which keys each row of a tree sees (PagedArgs).  A
-// block takes a request, a thread a row and a tile of 128 keys: it walks the
-// row's path, up as far as the tile begins, and sets the bits that fall into
-// it.  Bound by latency (one walk is as long as the path): some 2 us.
-constexpr int kTreeThreads = 128;
-
-struct TreeParams {
-    PagedArgs a;
-    int group, above;  // only requests of more rows a key/value head
-    unsigned int *status;
-};
-
-__global__ void __launch_bounds__(kTreeThreads) paged_tree_kernel(const TreeParams p) {
-    __shared__ int up[FA_PAGED_TREE_MAX_NEW];
-    wait_previous();
-    launch_dependents();
-    for (int b = blockIdx.x; b < p.a.B; b += gridDim.x) {
-        Request r;
-        const bool mine = load_request(p.a, b, r) && r.n * p.group > p.above;  // the 256-row kernel reports the others
-        if (!mine) continue;
-        __syncthreads();
-        for (int i = threadIdx.x; i < r.n; i += kTreeThreads) {
-            int j = p.a.parents[r.row0 + i];
-            if (j < -1 || j >= i) {
-                record_bad_args(p.status);
-                j = -1;
-            }
-            up[i] = j;
-        }
-        __syncthreads();
-        const int base = r.len - r.n, base0 = base & ~(kWideKeys - 1);  // of the first tile
-        const int tiles = (r.len - base0 + kWideKeys - 1) / kWideKeys;
-        for (int k = threadIdx.x; k < r.n * tiles; k += kTreeThreads) {
-            const int i = k / tiles, tile = k - i * tiles;
-            const int first = base0 + tile * kWideKeys - base;  // drafted token of the tile's first key
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {  // keys before the drafted ones
-                const int ctx = -first - 32 * q;
-                w[q] = ctx <= 0 ? 0u : ctx >= 32 ? 0xFFFFFFFFu : (1u << ctx) - 1;
-            }
-            int depth = 0;
-            for (int j = i; j >= 0 && (j >= first || (tile == 0 && p.a.window > 0)); j = up[j], ++depth) {
-                const int bit = j - first;
-                const bool seen = p.a.window == 0 || depth < p.a.window;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (seen && bit >> 5 == q) w[q] |= 1u << (bit & 31);
-            }
-            p.a.tree_words[(size_t)(r.row0 + i) * p.a.tree_tiles + tile] = make_uint4(w[0], w[1], w[2], w[3]);
-            if (tile == 0 && p.a.window > 0) p.a.tree_depth[r.row0 + i] = depth - 1;
-        }
-    }
-}
-
 // Merges the parts of every row that has several.  A lane has C columns of a
 // row.  C = 8 (32 bytes of a part, 16 of O): a warp works on 2 rows (d = 128)
 // or 4, and W warps share the parts of their rows, each taking every W-th: one
@@ -1074,11 +1019,6 @@ cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after,
     return a.bf16 ? launch_few_t<64, true>(a, w, after, st) : launch_few_t<64, false>(a, w, after, st);
 }
 
-cudaError_t launch_paged_tree(const PagedArgs &a, int above, cudaStream_t st) {
-    TreeParams p{a, a.Hq / a.Hkv, above, device_status_ptr()};
-    return launch_after(paged_tree_kernel, at_most(a.B, 8 * kSms), kTreeThreads, 0, st, p);
-}
-
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st) {
     if (a.d == 128) return a.bf16 ? launch_merge_t<128, true>(a, w, st) : launch_merge_t<128, false>(a, w, st);
     return a.bf16 ? launch_merge_t<64, true>(a, w, st) : launch_merge_t<64, false>(a, w, st);
@@ -1094,9 +1034,9 @@ cudaError_t launch_fwd_paged(const PagedArgs &args, cudaStream_t st) {
     const bool front = w.prefix.ctas > 0;
     if (a.parents && !w.few) {
         a.tree_tiles = tree_tiles(a.max_new);
+        a.tree_tokens = tree_tokens(a.Hq / a.Hkv);
         a.tree_words = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.workspace) + w.bytes);
-        a.tree_depth = reinterpret_cast<int *>(a.tree_words + (size_t)a.total * a.tree_tiles);
-        if ((e = launch_paged_tree(a, w.mixed ? kMaxRows : 0, st)) != cudaSuccess) return e;
+        a.tree_depth = reinterpret_cast<int *>(a.tree_words + 2ll * w.own.ctas * a.tree_tokens * a.tree_tiles);
     }
     if (front && (e = launch_paged_wide(a, w, true, false, st)) != cudaSuccess) return e;
     if (!w.few && (e = launch_paged_wide(a, w, false, front, st)) != cudaSuccess) return e;

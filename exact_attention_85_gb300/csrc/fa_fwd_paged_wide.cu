@@ -24,13 +24,15 @@
 // loaded and its first S issued before the epilogue of the one before.
 //   warps 0-3 softmax + epilogue of tile A, 4-7 of tile B, 8 producer (plans
 //   the segments and tells the others), 9 MMA issuer (owns the tensor memory),
-//   10-11 helpers (Q, and the V rows that nobody may see)
+//   10-11 helpers (Q, the V rows that nobody may see, and the paths of trees)
 #include "../../include/fa.h"
 #include "host_util.h"
 #include "mma_sync.cuh"
 #include "paged.h"
 #include "paged_dev.cuh"
 #include "ptx.cuh"
+
+#include <type_traits>
 
 namespace fa {
 
@@ -72,8 +74,9 @@ struct WideLayout {
     static constexpr int OFF_V = OFF_K + KS * TILE;
     static constexpr int OFF_BAR = OFF_V + VS * TILE;
     // q_full, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2],
-    // p_full[2], o_final[2], seg_full[2], seg_empty[2], q_empty, v_clean[VS], drain
-    static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2;
+    // p_full[2], o_final[2], seg_full[2], seg_empty[2], q_empty, v_clean[VS], drain,
+    // tree_full[2]
+    static constexpr int NBAR = 1 + 2 * KS + 3 * VS + 2 + 2 + 2 + 2 + 2 + 2 + 2;
     static constexpr int OFF_SEG = (OFF_BAR + NBAR * 8 + 15) & ~15;  // [2]
     static constexpr int OFF_MISC = OFF_SEG + 2 * 64;
     static constexpr int OFF_KEPT = OFF_MISC + 16 + kThreads / 32 * (int)sizeof(PlanSum);
@@ -151,6 +154,11 @@ __device__ __forceinline__ int block_front(const WideParams &p, const Request &r
     lo = 0;
     return JOINED ? block_front(p.a, p.group, r, k, lo) : 0;
 }
+// Units of a key tile of block k.
+template <bool TREE>
+__device__ __forceinline__ int units_of(const WideParams &p, const Request &r, int k) {
+    return TREE ? tree_units(r.n * p.group.d - k * kRows) : 1;
+}
 // All key tiles of block k.
 template <bool JOINED>
 __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, int k, int prefix_lo) {
@@ -158,20 +166,20 @@ __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, i
     block_keys(p, r, k, prefix_lo, lo, hi);
     return block_front<JOINED>(p, r, k, front_lo) + range_tiles(lo, hi);
 }
-// Key tiles of all blocks of a request, for one key/value head, and the most
-// that a block has.
+// Key tiles (TREE: units) of all blocks of a request, for one key/value head,
+// and the most tiles that a block has.
 struct RequestTiles {
     long long sum;
     int longest;
 };
 // The sums of 32 requests, one a lane: each lane walks its request's blocks,
 // or the warp one request's after the other's, whichever takes fewer steps.
-template <bool JOINED>
+template <bool JOINED, bool TREE>
 __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request r, int nb, int lane) {
     RequestTiles t{0, 0};
     const unsigned some = __ballot_sync(0xffffffffu, nb > 0);
     if ((int)__reduce_max_sync(0xffffffffu, nb) <= __popc(some)) {
-        t.sum = blocks_tiles<JOINED>(p.a, p.group, r, 0, nb, 1, t.longest);
+        t.sum = blocks_tiles<JOINED, TREE>(p.a, p.group, r, 0, nb, 1, t.longest);
         return t;
     }
     for (unsigned left = some; left; left &= left - 1) {
@@ -180,7 +188,7 @@ __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request 
         o.row0 = 0;
         o.n = __shfl_sync(0xffffffffu, r.n, i);
         o.len = __shfl_sync(0xffffffffu, r.len, i);
-        const long long sum = warp_count(blocks_tiles<JOINED>(p.a, p.group, o, lane, n, 32, t.longest));
+        const long long sum = warp_count(blocks_tiles<JOINED, TREE>(p.a, p.group, o, lane, n, 32, t.longest));
         if (lane == i) t.sum = sum;
     }
     return t;
@@ -256,6 +264,76 @@ __device__ __forceinline__ void joint_epilogue(const WideParams &p, uint32_t o_c
     if (slot != 0) p.part.code[out_row] = code ? code + part_code(0, 0, row) : 0;
 }
 
+// The part of the workspace for trees that segment g of this CTA has: words,
+// and depths.
+__device__ __forceinline__ size_t tree_slot(const PagedArgs &a, int g) {
+    return ((size_t)blockIdx.x * 2 + (g & 1)) * a.tree_tokens;
+}
+
+// Which drafted keys the tokens of a segment see (PagedArgs), by the helpers'
+// threads: each takes a token and a tile of 128 keys, walks the token's path,
+// up as far as the tile begins, and sets the bits that fall into it.  The
+// parents stay in L1, and the segment's first tiles are worked on meanwhile.
+__device__ __forceinline__ void tree_walk(const WideParams &p, const Segment &sg, int g, int rows, int id) {
+    const PagedArgs &a = p.a;
+    const int t0 = sg.r0 / p.group, tokens = (sg.r0 + rows - 1) / p.group - t0 + 1;
+    const int base = sg.len - sg.n, base0 = base & ~(kBN - 1);  // of the first tile
+    const int tiles = (sg.key_hi - base0 + kBN - 1) / kBN;
+    const int *parents = a.parents + sg.row0;
+    uint4 *const words = a.tree_words + tree_slot(a, g) * a.tree_tiles;
+    for (int k = id; k < tokens * tiles; k += 32 * kHelperWarps) {
+        const int t = k / tiles, tile = k - t * tiles;
+        const int first = base0 + tile * kBN - base;  // drafted token of the tile's first key
+        const bool to_root = tile == 0 && a.window > 0;
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // keys before the drafted ones
+            const int ctx = -first - 32 * q;
+            w[q] = ctx <= 0 ? 0u : ctx >= 32 ? 0xFFFFFFFFu : (1u << ctx) - 1;
+        }
+        int depth = 0;
+        for (int j = t0 + t; j >= 0 && (j >= first || to_root); ++depth) {
+            const int bit = j - first;
+            const uint32_t one = a.window > 0 && depth >= a.window ? 0u : 1u << (bit & 31);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] |= bit >> 5 == q ? one : 0u;
+            const int up = parents[j];
+            const bool sound = up >= -1 && up < j;
+            if (!sound) record_bad_args(p.status);
+            j = sound ? up : -1;
+        }
+        words[t * a.tree_tiles + tile] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (to_root) a.tree_depth[tree_slot(a, g) + t] = depth - 1;
+    }
+}
+
+// Of 32 keys, those from lo on and below hi.
+__device__ __forceinline__ uint32_t key_bits(int lo, int hi) {
+    const uint32_t from = lo <= 0 ? ~0u : lo >= 32 ? 0u : ~0u << lo;
+    return hi >= 32 ? from : hi <= 0 ? 0u : from & ((1u << hi) - 1);
+}
+
+// Masks a row's 128 scores in tensor memory: all but those of keys from low to
+// top that `words` (null: all) have a bit for.  A function of its own, so that
+// the loop which calls it for a block's last tiles is compiled as without it:
+// 64 requests of 12 thousand keys took 527 us with the bits tested there.
+__device__ __noinline__ void tree_mask(uint32_t s_addr, const uint4 *words, int low, int top) {
+    uint4 w = words ? *words : make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t bits = w.x & key_bits(low - 32 * q, top - 32 * q);
+        w = make_uint4(w.y, w.z, w.w, 0);
+        uint32_t x[32];
+        tmem_ld_x32(s_addr + 32 * q, x);
+        tmem_ld_wait_x32(x);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (!(bits >> c & 1)) x[c] = __float_as_uint(-INFINITY);
+        tmem_st_x32(s_addr + 32 * q, x);
+    }
+    tmem_st_wait();
+}
+
 // JOINED: the shared prefix' keys are read with each request's own.  LONG: a
 // block may have more tiles than a sum should.  TREE: rows hang on one another
 // (PagedArgs::parents), and see of the drafted keys what their words say.
@@ -280,11 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *q_empty = seg_empty + 2;
     uint64_t *v_clean = q_empty + 1;  // [VS]
     uint64_t *drain = v_clean + L::VS;
+    uint64_t *tree_full = drain + 1;  // [2]
     Segment *segs = reinterpret_cast<Segment *>(smem + L::OFF_SEG);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
     unsigned *kept = reinterpret_cast<unsigned *>(smem + L::OFF_KEPT);
+    constexpr int kUnit = TREE ? kTreeUnits : 1;  // of a key tile, at most
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -302,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&o_final[x], 1);
             mbar_init(&seg_full[x], 1);
             mbar_init(&seg_empty[x], 9 + kHelperWarps);  // every warp but the producer
+            mbar_init(&tree_full[x], 32 * kHelperWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -344,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.n = 0;
                 }
                 const int nb = blocks_of(r, p.group);
-                const RequestTiles tiles = request_tiles<JOINED>(p, r, nb, lane);
+                const RequestTiles tiles = request_tiles<JOINED, TREE>(p, r, nb, lane);
                 sum.tiles += tiles.sum;
                 sum.longest = max(sum.longest, tiles.longest);
                 sum.blocks += nb;
@@ -388,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             whole.n = end_row(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
         }
-        if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));
+        if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units<kUnit>() / kUnit, few_tiles, few_pairs));
         // Whole blocks only, each by the CTA in whose range it begins: a cut
         // one costs the merge of its parts, and a segment more in most CTAs
         // once there are more tiles than CTAs; a whole one leaves others idle
@@ -399,17 +480,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         //   several blocks a CTA: 256 of 1-4 36.9 and 34.5, 512 of 4 70 and
         //     63, 256 of 8 57.8 and 49.5, 640 of 1-10 91.9 and 90.8, 512 of
         //     12 118.7 and 121.4, 256 of 1-16 55.2 and 68.9
-        const long long loaded = work.tiles + work.blocks * kBlockCost;
+        const long long loaded = work.tiles + work.blocks * (kBlockCost * kUnit);
         const bool spare = work.blocks <= most;
         const int uncut = !p.prefix && longest > 1 &&
-                          (!spare              ? longest <= 10
-                           : work.tiles > most ? (2ll * longest - 7) * most <= 2 * loaded
-                                               : longest <= 2);
+                          (!spare                      ? longest <= 10
+                           : work.tiles > most * kUnit ? (2ll * longest - 7) * most <= 2 * loaded / kUnit
+                                                       : longest <= 2);
         // from one lane: the compiler then sees one value for the warp (0.5 %)
         const bool by_blocks = __shfl_sync(0xffffffffu, uncut, 0);
-        const int cost = by_blocks ? kBlockCost : work.block_cost();
-        const long long T = by_blocks ? loaded : work.units();
-        const int G = (int)min((long long)most, max(1ll, T));
+        const int cost = by_blocks ? kBlockCost * kUnit : work.block_cost<kUnit>();
+        const long long T = by_blocks ? loaded : work.units<kUnit>();
+        // a range of so many units has a tile's first one in it, wherever it lies in a block
+        const int G = (int)min((long long)most, max(1ll, T / kUnit));
         const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
         const int box_bytes = page_keys * 128;
@@ -445,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nb = blocks_of(r, p.group);
                 const unsigned held = b >= kKept ? kMany : b + lane < B ? kept[b + lane] : 0;
                 long long tiles = held;
-                if (__any_sync(0xffffffffu, held == kMany)) tiles = request_tiles<JOINED>(p, r, nb, lane).sum;
+                if (__any_sync(0xffffffffu, held == kMany)) tiles = request_tiles<JOINED, TREE>(p, r, nb, lane).sum;
                 const long long units = (tiles + (long long)nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
@@ -478,18 +560,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (!p.prefix) {
                     Request mine{0, 0, 0};
                     if (lane == 0) mine = r;
-                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED>(p, mine, lane == 0 ? nb : 0, lane).sum, 0);
+                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED, TREE>(p, mine, lane == 0 ? nb : 0, lane).sum, 0);
                 }
                 const long long per_head = tiles + (long long)nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
-                    const int units = blk + lane < nb ? tiles_of<JOINED>(p, r, blk + lane, prefix_lo) + cost : 0;
-                    int incl = units;
+                    using Count = std::conditional_t<TREE, long long, int>;  // 32 blocks' tiles, but not units, fit 32 bits
+                    const Count units = blk + lane < nb ? (Count)tiles_of<JOINED>(p, r, blk + lane, prefix_lo) *
+                                                                  units_of<TREE>(p, r, blk + lane) + cost
+                                                        : 0;
+                    Count incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
-                        const int x = __shfl_up_sync(0xffffffffu, incl, s);
+                        const Count x = __shfl_up_sync(0xffffffffu, incl, s);
                         if (lane >= s) incl += x;
                     }
                     const unsigned past = __ballot_sync(0xffffffffu, blk0 + incl > u);
@@ -516,9 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nt = sg.front + range_tiles(sg.key_lo, sg.key_hi);
                     const long long tile0 = blk0 + cost;  // unit of its first tile
                     const bool begun = blk0 < u0;  // in the range of the CTA before
-                    const int first = by_blocks ? 0 : (int)max(0ll, u - tile0);
-                    const int end = !by_blocks ? (int)min((long long)nt, u1 - tile0) : begun ? 0 : nt;
-                    blk0 = tile0 + nt;
+                    // a tile of several units belongs to the CTA that has the first one
+                    const int w = units_of<TREE>(p, r, blk);
+                    const int first = by_blocks ? 0 : (int)((max(0ll, u - tile0) + w - 1) / w);
+                    const int end =
+                        !by_blocks ? (int)((min((long long)nt * w, u1 - tile0) + w - 1) / w) : begun ? 0 : nt;
+                    blk0 = tile0 + (long long)nt * w;
                     u = u1 < blk0 ? u1 : blk0;
                     if (end <= first) continue;  // the range ends before the block's first tile
                     const bool is_whole = first == 0 && end == nt;
@@ -526,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sg.nj = end - first;
                     sg.slot = is_whole ? -1 : first == 0 ? 1 : 0;
                     // a block that goes on in the next CTA belongs to the one it began in
-                    sg.code = sg.slot == 1 ? part_code(ranges.owner(blk0 - 1) - c + 1, c, 0) : 0;
+                    sg.code = sg.slot == 1 ? part_code(ranges.owner(blk0 - w) - c + 1, c, 0) : 0;
                     sg.more = sg.pad[0] = sg.pad[1] = 0;
                     auto load_tiles = [&] {
                         tell(sg);
@@ -736,6 +824,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(q_full);
             }
+            if (TREE) {
+                // the segment two before has been seen by all: the last S of
+                // the one before, just waited for, comes behind its last P
+                tree_walk(p, sg, g, rows, id);
+                mbar_arrive(&tree_full[g & 1]);
+                __syncwarp();
+            }
             // V rows that no row of the block sees may hold anything (the rest
             // of a page, a buffer that was not filled), and 0 * NaN is NaN:
             // clear them in the tiles that have some, the first and the last
@@ -796,6 +891,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(sg.n * p.group.d - sg.r0, kRows);
             const bool two = rows > kBM, active = x == 0 || two, valid = row < rows;
             int tok = 0, head = 0, hi = 0x7FFFFFFF, lo = -0x7FFFFFFF;
+            int tree_at = 0;  // TREE: of the row's token in the workspace
+            auto tree_low = [&]() {  // first key before the drafted ones (below hi) that the row sees
+                return p.a.window > 0 && valid ? min(window_low(hi + p.a.tree_depth[tree_at] + 1, p.a.window), hi)
+                                               : -0x7FFFFFFF;
+            };
+            auto wait_tree = [&]() -> bool {
+                const bool got = mbar_wait(&tree_full[g & 1], (g >> 1) & 1, abort_flag, p.status, 47);
+                return __all_sync(0xffffffffu, got);
+            };
+            if (TREE && active && p.a.window > 0 && !(ok = wait_tree())) break;
             if (valid) {
                 const int t = (sg.r0 + row) / p.group;
                 head = sg.hk * p.group.d + (sg.r0 + row) - t * p.group.d;
@@ -810,22 +915,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     // no window: below every place (a prefix' first key is at -prefix_len)
                     hi = sg.len - sg.n + t + 1;
-                    if (TREE && p.a.window > 0) hi += p.a.tree_depth[tok] - t;
                     lo = p.a.window > 0 ? window_low(hi, p.a.window) : -0x7FFFFFFF;
-                    if (TREE) hi = sg.len - sg.n;  // the keys that it sees for being before the drafted ones
+                    if constexpr (TREE) {
+                        tree_at = (int)tree_slot(p.a, g) + t - sg.r0 / p.group;
+                        hi = sg.len - sg.n;
+                    }
                 }
             }
             const int nj = sg.nj;
             float m_ref = -INFINITY;
             float l_sum = 0.0f;    // sum of the rounded P fed to the MMA: normalises O
             float l_exact = 0.0f;  // sum of the unrounded P: gives L
-            const int hi_w = __reduce_min_sync(0xffffffffu, hi), lo_w = __reduce_max_sync(0xffffffffu, lo);
+            const int hi_w = __reduce_min_sync(0xffffffffu, hi);
+            const int lo_w = __reduce_max_sync(0xffffffffu, TREE ? tree_low() : lo);
             for (int u = 0; ok && active && u < nj; ++u, ++step) {
                 const bool got_s = mbar_wait(&s_full[x], step & 1, abort_flag, p.status, 37);
                 if (!__all_sync(0xffffffffu, got_s)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t s[128];
                 const uint32_t s_addr = lane_base + col_s;
+                const KeyTile<JOINED> tile(sg, u, p.a.prefix_len);
+                const int shift = tile.in_front ? p.a.prefix_len : 0;  // the tile's keys as places
+                const int kv0 = tile.kv0 - shift, key_lo = tile.lo - shift, key_hi = tile.hi - shift;
+                const bool hides = kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo);  // uniform in the warp
+                if (TREE && hides) {
+                    if (!(ok = wait_tree())) break;
+                    const uint4 *words = p.a.tree_words + tree_at * p.a.tree_tiles + (kv0 >> 7) - (hi >> 7);  // kBN keys
+                    tree_mask(s_addr, valid && kv0 + kBN > hi ? words : nullptr, max(tree_low(), key_lo) - kv0,
+                              key_hi - kv0);
+                }
+                uint32_t s[128];
                 tmem_ld_x32(s_addr + 0, s + 0);
                 tmem_ld_x32(s_addr + 32, s + 32);
                 tmem_ld_x32(s_addr + 64, s + 64);
@@ -834,20 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait_x32(s + 32);
                 tmem_ld_wait_x32(s + 64);
                 tmem_ld_wait_x32(s + 96);
-                const KeyTile<JOINED> tile(sg, u, p.a.prefix_len);
-                const int shift = tile.in_front ? p.a.prefix_len : 0;  // the tile's keys as places
-                const int kv0 = tile.kv0 - shift, key_lo = tile.lo - shift, key_hi = tile.hi - shift;
-                if (TREE && (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo))) {
-                    // keys before the tile of the first drafted one: all but those below a window
-                    uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
-                    if (valid && kv0 + kBN > hi)
-                        w = p.a.tree_words[(size_t)tok * p.a.tree_tiles + (kv0 - (hi & ~(kBN - 1))) / kBN];
-                    const uint32_t seen[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (!(seen[c >> 5] >> (c & 31) & 1) || kv0 + c >= key_hi || (kv0 + c < hi && kv0 + c < lo) || kv0 + c < key_lo)
-                            s[c] = __float_as_uint(-INFINITY);
-                } else if (!TREE && (kv0 + kBN > min(hi_w, key_hi) || kv0 < max(lo_w, key_lo))) {  // uniform in the warp
+                if (!TREE && hides) {
                     const int top = min(hi, key_hi), low = max(lo, key_lo);
 #pragma unroll
                     for (int c = 0; c < 128; ++c)

@@ -63,12 +63,13 @@ struct PagedArgs {
     // null: a request's rows are a chain.  Else the row that each one hangs
     // on, counted within its request, -1: the context (rows form trees).
     const int *parents;
-    // of each row, where the 256-row kernel works on trees: which of the keys
-    // from the tile on that holds its request's first drafted one it sees, a
-    // bit a key, 128 keys a tile; and its depth in the tree
+    // Workspace of the 256-row kernel for trees, a part for each of a CTA's two
+    // segments in work: which of the keys from the tile on that holds the
+    // request's first drafted one a token sees, a bit a key, tree_tiles uint4
+    // of 128 keys a token; and its depth in the tree.
     uint4 *tree_words;
     int *tree_depth;
-    int tree_tiles;
+    int tree_tiles, tree_tokens;
 };
 
 // Division of x < 2^31 by a fixed d >= 1 as a multiplication: with s the
@@ -124,13 +125,17 @@ struct PagedPlan {
     size_t bytes;     // workspace
 };
 
-// Tiles of 128 keys that max_new drafted ones can lie in.
+// Tiles of 128 keys that max_new drafted ones can lie in, and tokens that a row
+// block can hold rows of, where a token has `group` of them.
 constexpr int tree_tiles(int max_new) { return (max_new + 2 * kWideKeys - 2) / kWideKeys; }
+constexpr int tree_tokens(int group) { return kWideRows / group + 2; }
 
-// Workspace of a tree's words and depths, behind a plan's own: 0 where only
-// the few-row kernel runs, which forms them itself.
-inline size_t tree_bytes(const PagedPlan &w, int total, int max_new) {
-    return w.few ? 0 : ((size_t)total * tree_tiles(max_new) * 16 + (size_t)total * 4 + 255) / 256 * 256;
+// Workspace for trees, behind a plan's own: 0 where only the few-row kernel
+// runs, which keeps paths in registers.
+inline size_t tree_bytes(const PagedPlan &w, int group, int max_new) {
+    if (w.few) return 0;
+    const size_t tokens = 2 * (size_t)w.own.ctas * tree_tokens(group);
+    return (tokens * (tree_tiles(max_new) * 16 + 4) + 255) / 256 * 256;
 }
 
 // The workspace needed is the largest without a window.
@@ -140,7 +145,6 @@ PagedPlan plan_paged(int B, int total, int max_new, int Hq, int Hkv, int d, int 
 // The kernels of a forward call.  `after`: beside the call's kernel before.
 cudaError_t launch_paged_few(const PagedArgs &a, const PagedPlan &w, bool after, cudaStream_t st);
 cudaError_t launch_paged_wide(const PagedArgs &a, const PagedPlan &w, bool prefix, bool after, cudaStream_t st);
-cudaError_t launch_paged_tree(const PagedArgs &a, int above, cudaStream_t st);
 cudaError_t launch_paged_merge(const PagedArgs &a, const PagedPlan &w, cudaStream_t st);
 
 cudaError_t launch_paged_tables(const TablesArgs &a, cudaStream_t st);

@@ -102,13 +102,21 @@ def test_tree_of_more_rows_than_keys(cuda_lib, lens, new, kind, window):
 
 @pytest.mark.parametrize("new,Hq,Hkv,d,window", [([4, 1, 3], 8, 2, 128, 0), ([4, 1, 3], 4, 2, 64, 50),
                                                  ([300, 17], 2, 1, 128, 0), ([90, 100], 4, 1, 64, 200)])
-def test_chain_gives_the_bits_of_the_causal_forward(cuda_lib, new, Hq, Hkv, d, window):
+def test_chain_is_the_causal_forward(cuda_lib, new, Hq, Hkv, d, window):
+    """Both within the same bounds of the same numbers; the same bits where one
+    tile takes a request's rows, whose keys the few-row kernel cuts alike.  (The
+    256-row kernel weighs the blocks of trees by their rows, so that it sums a
+    row's keys in other parts.)"""
     p = TreeProblem([random_tree(None, n, "chain") for n in new], [n + 333 for n in new], Hq, Hkv, d, 32, BF, window,
                     extra_cols=60)
     o, lse = _run(p)
     a = _args(p)
     o2, lse2 = fa.attention_fwd_paged(*a[:6], p.max_new, scale=p.scale, window=p.window or None)
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    want = p.reference()
+    check(o, lse, want, p.rows)
+    check(o2, lse2, want, p.rows)
+    if max(new) * Hq // Hkv <= 16:
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_rows_of_no_request_stay(cuda_lib):
