@@ -415,50 +415,33 @@ def fa_paged_append(k, v, slots, k_cache, v_cache, stream=None):
         num_pages, code, _stream(stream)))
 
 
-def _are_int32(dev, *tensors) -> bool:
-    """Whether all are contiguous int32 tensors on device `dev` (None passes)."""
-    import torch
-    i32 = torch.int32
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or t.dtype != i32 or not t.is_contiguous()):
-            return False
-    return True
-
-
-def _need_ints(block_table, **tensors):
-    """Refuses what a call on a table cannot take: tensors (None passes) off
-    the table's device, the current one, of another type than int32, or not
-    contiguous."""
-    import torch
-    dev = block_table.get_device()
-    if dev < 0 or dev != torch.cuda.current_device() or not _are_int32(dev, block_table, *tensors.values()):
-        _need_all(("block_table", block_table, torch.int32), *((k, t, torch.int32) for k, t in tensors.items()))
-
-
-def _cache_shape(k_cache, v_cache):
-    """(pages, Hkv, page_size, d) of two caches of one type."""
-    import torch
-    dtype, dev = k_cache.dtype, k_cache.get_device()
-    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous() and v_cache.get_device() == dev
-            and v_cache.dtype == dtype and v_cache.is_contiguous()):
-        _need_all(("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype))
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("the caches must both be [pages,Hkv,page_size,d]")
-    return k_cache.shape
-
-
 def fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, shares, copies, counts, page_size: int,
                   stream=None):
     """Table rows dst continue where rows src stand; int32 tensors as in fa.h."""
+    import torch
     B, max_pages = block_table.shape
     F, num_pages, num_free = src.numel(), shares.numel(), free_pages.numel()
-    _need_ints(block_table, src=src, dst=dst, seq_lens=seq_lens, free_pages=free_pages, free_start=free_start,
-               shares=shares, copies=copies, counts=counts)
-    if not (dst.numel() == F and seq_lens.numel() == B and copies.numel() == 3 * F and counts.numel() == 2
-            and (free_start is None or free_start.numel() == 1)):
+    i32, dev = torch.int32, block_table.get_device()
+    # one expression, as for the tables: the kernel takes some 4 us
+    if not (dev >= 0 and dev == torch.cuda.current_device() and block_table.dtype == i32 and block_table.is_contiguous()
+            and src.get_device() == dev and src.dtype == i32 and src.is_contiguous()
+            and dst.get_device() == dev and dst.dtype == i32 and dst.is_contiguous()
+            and seq_lens.get_device() == dev and seq_lens.dtype == i32 and seq_lens.is_contiguous()
+            and free_pages.get_device() == dev and free_pages.dtype == i32 and free_pages.is_contiguous()
+            and shares.get_device() == dev and shares.dtype == i32 and shares.is_contiguous()
+            and copies.get_device() == dev and copies.dtype == i32 and copies.is_contiguous()
+            and counts.get_device() == dev and counts.dtype == i32 and counts.is_contiguous()
+            and (free_start is None or (free_start.get_device() == dev and free_start.dtype == i32
+                                        and free_start.numel() == 1))
+            and dst.numel() == F and seq_lens.numel() == B and copies.numel() == 3 * F and counts.numel() == 2):
+        _need_all(("block_table", block_table, i32), ("src", src, i32), ("dst", dst, i32), ("seq_lens", seq_lens, i32),
+                  ("free_pages", free_pages, i32), ("free_start", free_start, i32), ("shares", shares, i32),
+                  ("copies", copies, i32), ("counts", counts, i32))
         _need_numel(dst=(dst, F), seq_lens=(seq_lens, B), copies=(copies, 3 * F), counts=(counts, 2),
                     free_start=(free_start, 1))
-    _need_int32(page_size=page_size, F=F, B=B, max_pages=max_pages, shares=num_pages, free_pages=num_free)
+    if not (0 < page_size <= 0x7FFFFFFF and F <= 0x7FFFFFFF and B <= 0x7FFFFFFF and max_pages <= 0x7FFFFFFF
+            and num_pages <= 0x7FFFFFFF and num_free <= 0x7FFFFFFF):
+        _need_int32(page_size=page_size, src=F, B=B, max_pages=max_pages, shares=num_pages, free_pages=num_free)
     _check("fa_paged_fork", load().fa_paged_fork(
         src.data_ptr(), dst.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
         free_pages.data_ptr() if num_free else None, _ptr(free_start), shares.data_ptr(), copies.data_ptr(),
@@ -468,14 +451,22 @@ def fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, share
 def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
     """Pages dst of the caches [pages,Hkv,page_size,d] get the first rows tokens of pages src."""
     import torch
-    num_pages, Hkv, page_size, d = _cache_shape(k_cache, v_cache)
-    code, dev, n = _dtype_code(k_cache), k_cache.get_device(), src.numel()
-    if not _are_int32(dev, src, dst, rows):
-        i32 = torch.int32
-        _need_all(("k_cache", k_cache, k_cache.dtype), ("src", src, i32), ("dst", dst, i32), ("rows", rows, i32))
-    if dst.numel() != n or (rows is not None and rows.numel() != n):
+    shape = k_cache.shape
+    num_pages, Hkv, page_size, d = shape
+    code, dtype, dev, i32, n = _dtype_code(k_cache), k_cache.dtype, k_cache.get_device(), torch.int32, src.numel()
+    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
+            and src.get_device() == dev and src.dtype == i32 and src.is_contiguous()
+            and dst.get_device() == dev and dst.dtype == i32 and dst.is_contiguous() and dst.numel() == n
+            and (rows is None or (rows.get_device() == dev and rows.dtype == i32 and rows.is_contiguous()
+                                  and rows.numel() == n))):
+        _need_all(("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype), ("src", src, i32), ("dst", dst, i32),
+                  ("rows", rows, i32))
         _need_numel(dst=(dst, n), rows=(rows, n))
-    _need_int32(src=n)
+    if v_cache.shape != shape:
+        raise ValueError("the caches must both be [pages,Hkv,page_size,d]")
+    if n > 0x7FFFFFFF:
+        _need_int32(src=n)
     _check("fa_paged_copy", load().fa_paged_copy(
         src.data_ptr(), dst.data_ptr(), _ptr(rows), k_cache.data_ptr(), v_cache.data_ptr(), n, Hkv, d, page_size,
         num_pages, code, _stream(stream)))
@@ -483,16 +474,26 @@ def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
 
 def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream=None):
     """Tokens base_lens + keep [B,max_keep] of the requests move to base_lens + 0, 1, .."""
+    import torch
     B, max_pages = block_table.shape
-    num_pages, Hkv, page_size, d = _cache_shape(k_cache, v_cache)
-    code = _dtype_code(k_cache)
-    _need_ints(block_table, keep=keep, keep_lens=keep_lens, base_lens=base_lens)
-    if k_cache.get_device() != block_table.get_device():
-        _refuse("k_cache", k_cache, block_table.get_device())
+    shape = k_cache.shape
+    num_pages, Hkv, page_size, d = shape
+    code, dtype, dev, i32 = _dtype_code(k_cache), k_cache.dtype, k_cache.get_device(), torch.int32
+    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
+            and block_table.get_device() == dev and block_table.dtype == i32 and block_table.is_contiguous()
+            and keep.get_device() == dev and keep.dtype == i32 and keep.is_contiguous()
+            and keep_lens.get_device() == dev and keep_lens.dtype == i32 and keep_lens.is_contiguous()
+            and base_lens.get_device() == dev and base_lens.dtype == i32 and base_lens.is_contiguous()):
+        _need_all(("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype), ("block_table", block_table, i32),
+                  ("keep", keep, i32), ("keep_lens", keep_lens, i32), ("base_lens", base_lens, i32))
+    if v_cache.shape != shape:
+        raise ValueError("the caches must both be [pages,Hkv,page_size,d]")
     if keep.dim() != 2 or keep.shape[0] != B or keep_lens.numel() != B or base_lens.numel() != B:
         raise ValueError(f"keep must be [B,max_keep], keep_lens and base_lens [B], with the table's B = {B}")
     max_keep = keep.shape[1]
-    _need_int32(B=B, max_keep=max_keep, max_pages=max_pages)
+    if not (B <= 0x7FFFFFFF and max_keep <= 0x7FFFFFFF and max_pages <= 0x7FFFFFFF):
+        _need_int32(B=B, max_keep=max_keep, max_pages=max_pages)
     _check("fa_paged_compact", load().fa_paged_compact(
         keep.data_ptr(), keep_lens.data_ptr(), base_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), B, max_keep, max_pages, Hkv, d, page_size, num_pages, code, _stream(stream)))
@@ -501,15 +502,27 @@ def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, 
 def fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, shares, counts, page_size: int,
                   num_pages: int, stream=None):
     """Pages behind new_lens back to the free list; int32 tensors as in fa.h."""
+    import torch
     B, max_pages = block_table.shape
     num_free = free_pages.numel()
-    _need_ints(block_table, old_lens=old_lens, new_lens=new_lens, free_pages=free_pages, free_start=free_start,
-               shares=shares, counts=counts)
-    if not (old_lens.numel() == B and new_lens.numel() == B and free_start.numel() == 1 and counts.numel() == 2
-            and (shares is None or shares.numel() == num_pages)):
+    i32, dev = torch.int32, block_table.get_device()
+    if not (dev >= 0 and dev == torch.cuda.current_device() and block_table.dtype == i32 and block_table.is_contiguous()
+            and old_lens.get_device() == dev and old_lens.dtype == i32 and old_lens.is_contiguous()
+            and new_lens.get_device() == dev and new_lens.dtype == i32 and new_lens.is_contiguous()
+            and free_pages.get_device() == dev and free_pages.dtype == i32 and free_pages.is_contiguous()
+            and free_start.get_device() == dev and free_start.dtype == i32 and free_start.numel() == 1
+            and counts.get_device() == dev and counts.dtype == i32 and counts.is_contiguous()
+            and (shares is None or (shares.get_device() == dev and shares.dtype == i32 and shares.is_contiguous()
+                                    and shares.numel() == num_pages))
+            and old_lens.numel() == B and new_lens.numel() == B and counts.numel() == 2):
+        _need_all(("block_table", block_table, i32), ("old_lens", old_lens, i32), ("new_lens", new_lens, i32),
+                  ("free_pages", free_pages, i32), ("free_start", free_start, i32), ("shares", shares, i32),
+                  ("counts", counts, i32))
         _need_numel(old_lens=(old_lens, B), new_lens=(new_lens, B), free_start=(free_start, 1), counts=(counts, 2),
                     shares=(shares, num_pages))
-    _need_int32(page_size=page_size, num_pages=num_pages, B=B, max_pages=max_pages, free_pages=num_free)
+    if not (0 < page_size <= 0x7FFFFFFF and 0 < num_pages <= 0x7FFFFFFF and B <= 0x7FFFFFFF
+            and max_pages <= 0x7FFFFFFF and num_free <= 0x7FFFFFFF):
+        _need_int32(page_size=page_size, num_pages=num_pages, B=B, max_pages=max_pages, free_pages=num_free)
     _check("fa_paged_free", load().fa_paged_free(
         old_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if num_free else None,
         free_start.data_ptr(), _ptr(shares), counts.data_ptr(), B, max_pages, int(page_size), int(num_pages), num_free,
@@ -599,8 +612,9 @@ def fa_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, pa
                       scale: float, workspace, window: int = 0, stream=None):
     """fa_fwd_paged for trees of drafted tokens; parents int32 [total]."""
     rest = _paged_call(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, o, lse, max_new, scale, workspace, window)
-    if not _are_int32(q.get_device(), parents) or parents.numel() != q.shape[0]:
-        import torch
+    import torch
+    if not (parents.get_device() == q.get_device() and parents.dtype == torch.int32 and parents.is_contiguous()
+            and parents.numel() == q.shape[0]):
         _need_all(("q", q, q.dtype), ("parents", parents, torch.int32))
         _need_numel(parents=(parents, q.shape[0]))
     _check("fa_fwd_paged_tree", load().fa_fwd_paged_tree(
