@@ -154,7 +154,7 @@ __host__ __device__ __forceinline__ int block_front(const PagedArgs &a, const Fa
 // of a prompt of N tokens are N^2 g / 65536: past 2^31 at 4 million tokens of
 // 8 grouped heads.
 // TREE: in units (kTreeUnits).
-template <bool JOINED, bool TREE>
+template <bool JOINED, bool TREE = false>
 __host__ __device__ __forceinline__ long long blocks_tiles(const PagedArgs &a, const FastDiv &group, const Request &r,
                                                            int from, int nb, int step, int &longest) {
     long long sum = 0;
