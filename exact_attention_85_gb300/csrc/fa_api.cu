@@ -552,7 +552,9 @@ fa_status_t fa_paged_copy(const int *src, const int *dst, const int *rows, void 
         return FA_ERR_INVALID_ARG;
     fa_status_t s = check_cache(Hkv, d, page_size, num_pages, dtype);
     if (s != FA_OK) return s;
-    if (fa::copy_blocks(n, Hkv, d, page_size) > 0x7FFFFFFFll) return FA_ERR_UNSUPPORTED;
+    // blocks, and the 16-byte pieces of a page
+    if (fa::copy_blocks(n, Hkv, d, page_size) > 0x7FFFFFFFll || (long long)Hkv * page_size * (d / 8) > 0x40000000ll)
+        return FA_ERR_UNSUPPORTED;
     fa::CopyArgs a{src, dst, rows, k_cache, v_cache, n, Hkv, d, page_size, num_pages};
     return from_cuda(fa::launch_paged_copy(a, static_cast<cudaStream_t>(stream)));
 }

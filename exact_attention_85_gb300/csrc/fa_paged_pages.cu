@@ -190,16 +190,15 @@ constexpr int kCopyThreads = 256, kCopyUnroll = 4;
 
 struct CopyParams {
     CopyArgs a;
-    FastDiv heads, pieces;  // Hkv; blocks of a head's rows of a page
-    int shift, chunks;      // log2(page_size); 16-byte pieces of a row
+    FastDiv pieces;  // blocks of a pair of pages
+    int shift, head_shift;  // log2 of page_size, and of the 16-byte pieces of a head's rows of a page
     unsigned int *status;
 };
 
-// A block copies up to 16 KB of K and of V: a part of one head's rows of a
-// page, which lie one behind the other on both sides.
+// A block copies up to 16 KB of K and of V: the rows of some heads of a page,
+// or a part of one head's, which lie one behind the other on both sides.
 __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyParams p) {
-    const int unit = blockIdx.x / p.pieces, piece = blockIdx.x - unit * p.pieces.d;
-    const int i = unit / p.heads, h = unit - i * p.heads.d;
+    const int i = blockIdx.x / p.pieces, piece = blockIdx.x - i * p.pieces.d;
     wait_previous();
     launch_dependents();
     const int from = p.a.src[i], to = p.a.dst[i], rows = p.a.rows ? p.a.rows[i] : 1 << p.shift;
@@ -208,23 +207,23 @@ __global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const CopyPara
         record_bad_args(p.status);
         return;
     }
-    const size_t at = ((size_t)from * p.a.Hkv + h << p.shift) * p.chunks;
-    const size_t out = ((size_t)to * p.a.Hkv + h << p.shift) * p.chunks;
+    const size_t at = (size_t)from * p.a.Hkv << p.head_shift, out = (size_t)to * p.a.Hkv << p.head_shift;
     const uint4 *k = static_cast<const uint4 *>(p.a.k_cache) + at, *v = static_cast<const uint4 *>(p.a.v_cache) + at;
     uint4 *ko = static_cast<uint4 *>(p.a.k_cache) + out, *vo = static_cast<uint4 *>(p.a.v_cache) + out;
-    const int c0 = piece * (kCopyThreads * kCopyUnroll) + threadIdx.x, end = rows * p.chunks;
+    const int all = p.a.Hkv << p.head_shift, mask = (1 << p.head_shift) - 1;
+    const int c0 = piece * (kCopyThreads * kCopyUnroll) + threadIdx.x, end = rows << (p.head_shift - p.shift);
     uint4 x[kCopyUnroll], y[kCopyUnroll];
 #pragma unroll
     for (int j = 0; j < kCopyUnroll; ++j) {
         const int c = c0 + j * kCopyThreads;
-        if (c >= end) break;
+        if (c >= all || (c & mask) >= end) continue;
         x[j] = __ldcs(k + c);
         y[j] = __ldcs(v + c);
     }
 #pragma unroll
     for (int j = 0; j < kCopyUnroll; ++j) {
         const int c = c0 + j * kCopyThreads;
-        if (c >= end) break;
+        if (c >= all || (c & mask) >= end) continue;
         ko[c] = x[j];
         vo[c] = y[j];
     }
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
     };
     // lines of keep[], a tile's by its threads, eight tiles ahead: from memory
     // they would take longer than a tile
-    auto prefetch_keep = [&](int i) {
+    auto prefetch_keep = [&](long long i) {
         if (i < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(keep + i));
     };
     for (int i = tid * 32; i < 8 * rows; i += 32 * kMoveThreads) prefetch_keep(i);
@@ -363,7 +362,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const Compa
         put_slots(t + kMoveStages - 1);
         fetch_pages(t + kMoveStages);
         fetch_keep(t + kMoveStages + 1);
-        if (tid * 32 < rows) prefetch_keep((t + 8) * rows + tid * 32);
+        if (tid * 32 < rows) prefetch_keep((t + 8ll) * rows + tid * 32);
         cp_async_wait<kMoveStages - 2>();
         __syncthreads();
         load(t + kMoveStages - 1);
@@ -557,20 +556,19 @@ cudaError_t launch_paged_fork(const ForkArgs &a, cudaStream_t st) {
     return launch_after(paged_fork_kernel, grid, kForkThreads, DynSmem(smem(a.F), smem(FA_PAGED_FORK_MAX)), st, p);
 }
 
-// Blocks of one head's rows of a page.
-static int copy_pieces(int d, int page_size) {
+// Blocks of a pair of pages.
+static long long copy_pieces(int Hkv, int d, int page_size) {
     constexpr int kBlock = kCopyThreads * kCopyUnroll;
-    return (page_size * (d / 8) + kBlock - 1) / kBlock;
+    return ((long long)Hkv * page_size * (d / 8) + kBlock - 1) / kBlock;
 }
-long long copy_blocks(int n, int Hkv, int d, int page_size) { return (long long)n * Hkv * copy_pieces(d, page_size); }
+long long copy_blocks(int n, int Hkv, int d, int page_size) { return n * copy_pieces(Hkv, d, page_size); }
 
 cudaError_t launch_paged_copy(const CopyArgs &a, cudaStream_t st) {
     CopyParams p;
     p.a = a;
     p.shift = log2_of(a.page_size);
-    p.chunks = a.d / 8;
-    p.heads = fast_div(a.Hkv);
-    p.pieces = fast_div(copy_pieces(a.d, a.page_size));
+    p.head_shift = log2_of(a.page_size * (a.d / 8));
+    p.pieces = fast_div((int)copy_pieces(a.Hkv, a.d, a.page_size));
     p.status = device_status_ptr();
     return launch_after(paged_copy_kernel, (unsigned)copy_blocks(a.n, a.Hkv, a.d, a.page_size), kCopyThreads, 0, st, p);
 }

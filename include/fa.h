@@ -501,7 +501,7 @@ fa_status_t fa_paged_compact(const int *keep, const int *keep_lens,
  *   old_lens, new_lens [B] (in): 0 <= new <= old <= max_pages * page_size
  *   block_table [B][max_pages] (in); rows are left as they are
  *   free_pages [num_free] (in/out), free_start [1] (in): 0 .. num_free
- *   shares [num_pages] (in/out); NULL: no page is shared
+ *   shares [num_pages] (in/out); NULL: no page is shared, or given up twice
  *   counts [2] (out): the next free_start, and how many freed pages had no
  *       room in front of it (the first ones in order; they are in no list)
  * All arrays are int32 on the device; outputs must not overlap inputs.

@@ -42,7 +42,7 @@ def _copy(lib, src=FAKE, dst=FAKE, rows=None, kc=FAKE, vc=FAKE, n=4, Hkv=2, d=12
     (dict(src=None), 1), (dict(dst=None), 1), (dict(kc=None), 1), (dict(vc=None), 1), (dict(n=0), 1), (dict(Hkv=0), 1),
     (dict(num_pages=0), 1), (dict(dtype=2), 1), (dict(kc=FAKE + 8), 1), (dict(vc=FAKE + 8), 1), (dict(src=FAKE + 2), 1),
     (dict(dst=FAKE + 1), 1), (dict(rows=FAKE + 3), 1), (dict(d=96), 2), (dict(page_size=24), 2),
-    (dict(num_pages=1 << 30, Hkv=4), 2), (dict(n=0x7FFFFFFF, page_size=256), 2),
+    (dict(num_pages=1 << 30, Hkv=4), 2), (dict(n=0x7FFFFFFF, page_size=256), 2), (dict(Hkv=1 << 20, page_size=256, num_pages=1), 2),
 ])
 def test_copy_refuses(lib, bad, status):
     assert _copy(lib, **bad) == status
