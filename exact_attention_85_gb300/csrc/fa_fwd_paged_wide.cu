@@ -319,6 +319,7 @@ __device__ __forceinline__ uint32_t key_bits(int lo, int hi) {
 // 64 requests of 12 thousand keys took 527 us with the bits tested there.
 __device__ __noinline__ void tree_mask(uint32_t s_addr, const uint4 *words, int low, int top) {
     uint4 w = words ? *words : make_uint4(~0u, ~0u, ~0u, ~0u);
+    __syncwarp();  // the loads and stores below are the whole warp's
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
         const uint32_t bits = w.x & key_bits(low - 32 * q, top - 32 * q);
@@ -940,8 +941,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (TREE && hides) {
                     if (!(ok = wait_tree())) break;
                     const uint4 *words = p.a.tree_words + tree_at * p.a.tree_tiles + (kv0 >> 7) - (hi >> 7);  // kBN keys
-                    tree_mask(s_addr, valid && kv0 + kBN > hi ? words : nullptr, max(tree_low(), key_lo) - kv0,
-                              key_hi - kv0);
+                    const bool drafted = valid && kv0 + kBN > hi && kv0 < key_hi;
+                    tree_mask(s_addr, drafted ? words : nullptr, max(tree_low(), key_lo) - kv0, key_hi - kv0);
                 }
                 uint32_t s[128];
                 tmem_ld_x32(s_addr + 0, s + 0);

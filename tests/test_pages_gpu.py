@@ -254,7 +254,7 @@ def test_free_random(cuda_lib, seed):
     _free(old, new, table, [-1] * start + spare, start, shares, ps, num)
 
 
-@pytest.mark.parametrize("B,tokens", [(1, 16 * 9000), (500, 16 * 100), (16384, 40)])
+@pytest.mark.parametrize("B,tokens", [(1, 16 * 9000), (500, 16 * 100), (16384, 40), (3000, 16 * 120)])
 def test_free_many(cuda_lib, B, tokens):
     r = random.Random(B)
     old = [tokens] * B
