@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (!p.after) wait_previous();
     launch_dependents();
     {   // tiles of the whole batch
-        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0};
+        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0, 0};
         for (int b = threadIdx.x; b < B; b += kFewThreads) {
             Request r;
             if (!load_request(p.a, b, r)) {

@@ -154,11 +154,6 @@ __device__ __forceinline__ int block_front(const WideParams &p, const Request &r
     lo = 0;
     return JOINED ? block_front(p.a, p.group, r, k, lo) : 0;
 }
-// Units of a key tile of block k.
-template <bool TREE>
-__device__ __forceinline__ int units_of(const WideParams &p, const Request &r, int k) {
-    return TREE ? tree_units(r.n * p.group.d - k * kRows) : 1;
-}
 // All key tiles of block k.
 template <bool JOINED>
 __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, int k, int prefix_lo) {
@@ -166,20 +161,20 @@ __device__ __forceinline__ int tiles_of(const WideParams &p, const Request &r, i
     block_keys(p, r, k, prefix_lo, lo, hi);
     return block_front<JOINED>(p, r, k, front_lo) + range_tiles(lo, hi);
 }
-// Key tiles (TREE: units) of all blocks of a request, for one key/value head,
-// and the most tiles that a block has.
+// Key tiles of all blocks of a request, for one key/value head, and the most
+// that a block has.
 struct RequestTiles {
     long long sum;
     int longest;
 };
 // The sums of 32 requests, one a lane: each lane walks its request's blocks,
 // or the warp one request's after the other's, whichever takes fewer steps.
-template <bool JOINED, bool TREE>
+template <bool JOINED>
 __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request r, int nb, int lane) {
     RequestTiles t{0, 0};
     const unsigned some = __ballot_sync(0xffffffffu, nb > 0);
     if ((int)__reduce_max_sync(0xffffffffu, nb) <= __popc(some)) {
-        t.sum = blocks_tiles<JOINED, TREE>(p.a, p.group, r, 0, nb, 1, t.longest);
+        t.sum = blocks_tiles<JOINED>(p.a, p.group, r, 0, nb, 1, t.longest);
         return t;
     }
     for (unsigned left = some; left; left &= left - 1) {
@@ -188,10 +183,27 @@ __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request 
         o.row0 = 0;
         o.n = __shfl_sync(0xffffffffu, r.n, i);
         o.len = __shfl_sync(0xffffffffu, r.len, i);
-        const long long sum = warp_count(blocks_tiles<JOINED, TREE>(p.a, p.group, o, lane, n, 32, t.longest));
+        const long long sum = warp_count(blocks_tiles<JOINED>(p.a, p.group, o, lane, n, 32, t.longest));
         if (lane == i) t.sum = sum;
     }
     return t;
+}
+
+// Units that a key tile counts for in the 256-row kernel's work on trees, whose
+// batches have blocks of up to 128 rows (one MMA tile, bound by memory) beside
+// larger ones (two, bound by their chain), by turns with the requests.  us with
+// 1:1, 4:5 and 7:8: 32 requests of 333-7506 keys and 17-63 tokens 130.9, 128.1,
+// 127.6; of 4000 keys 127.7, 123.3, 123.6; 64 of 2-3k and 5-63 163.8, 156.7,
+// 157.2; 24 of 333-16k and 9-100 147.4, 143.1, 140.3.
+// Where there are only a few tiles for every SM they count alike: ranges of
+// whole tiles lie better in the blocks (one request of 64 tokens behind 4000
+// keys 23.1 us, weighed 28.0).
+constexpr int kTreeUnits = 8;
+__device__ __forceinline__ bool light(int rows) { return rows <= kBM; }
+// Tiles of a request's one block that may be light, its last, if it is.
+__device__ __forceinline__ int light_tiles(const WideParams &p, const Request &r, int nb) {
+    if (nb == 0 || !light(r.n * p.group.d - (nb - 1) * kRows)) return 0;
+    return tiles_of<false>(p, r, nb - 1, 0);
 }
 
 // Epilogue of a row whose block has more tiles than a segment: adds O and the
@@ -365,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
     PlanSum *sums = reinterpret_cast<PlanSum *>(smem + L::OFF_MISC + 16);
     unsigned *kept = reinterpret_cast<unsigned *>(smem + L::OFF_KEPT);
-    constexpr int kUnit = TREE ? kTreeUnits : 1;  // of a key tile, at most
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- the batch's units of work
     const int B = p.prefix ? 1 : p.a.B;
     {
-        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0};
+        PlanSum sum{0, 0, 0, p.a.prefix_len, 0, 0, 0};
         auto beside = [&](const Request &r) {  // a request of the few-row kernel
             int t;
             sum.beside += pair_tiles<kFewKeys<D>>(p.a, r, t);
@@ -426,8 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r.n = 0;
                 }
                 const int nb = blocks_of(r, p.group);
-                const RequestTiles tiles = request_tiles<JOINED, TREE>(p, r, nb, lane);
+                const RequestTiles tiles = request_tiles<JOINED>(p, r, nb, lane);
                 sum.tiles += tiles.sum;
+                if (TREE) sum.light += light_tiles(p, r, nb);
                 sum.longest = max(sum.longest, tiles.longest);
                 sum.blocks += nb;
                 if (b + lane < kKept) kept[b + lane] = (unsigned)min(tiles.sum, (long long)kMany);
@@ -435,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         sum.tiles = warp_sum(sum.tiles);
         sum.beside = warp_sum(sum.beside);
+        if (TREE) sum.light = warp_sum(sum.light);
         sum.blocks = __reduce_add_sync(0xffffffffu, sum.blocks);
         sum.beside_blocks = __reduce_add_sync(0xffffffffu, sum.beside_blocks);
         sum.low = __reduce_min_sync(0xffffffffu, sum.low);
@@ -457,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         WideWork work{0, 0};
         long long few_tiles = 0, few_pairs = 0;
         int most = gridDim.x, prefix_lo = p.a.prefix_len, longest = 0;
+        long long light_all = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             work.tiles += (long long)sums[w].tiles * p.a.Hkv;
@@ -465,12 +479,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             few_pairs += (long long)sums[w].beside_blocks * p.a.Hkv;
             prefix_lo = min(prefix_lo, sums[w].low);
             longest = max(longest, sums[w].longest);
+            if (TREE) light_all += (long long)sums[w].light * p.a.Hkv;
         }
         if (p.prefix) {
             whole.n = end_row(p.a);
             work = prefix_work(p.a, whole.n, p.group.d, prefix_lo);
         }
-        if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units<kUnit>() / kUnit, few_tiles, few_pairs));
+        if (p.shared && few_pairs > 0) most = min(most, wide_sms(work.units(), few_tiles, few_pairs));
         // Whole blocks only, each by the CTA in whose range it begins: a cut
         // one costs the merge of its parts, and a segment more in most CTAs
         // once there are more tiles than CTAs; a whole one leaves others idle
@@ -481,18 +496,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         //   several blocks a CTA: 256 of 1-4 36.9 and 34.5, 512 of 4 70 and
         //     63, 256 of 8 57.8 and 49.5, 640 of 1-10 91.9 and 90.8, 512 of
         //     12 118.7 and 121.4, 256 of 1-16 55.2 and 68.9
-        const long long loaded = work.tiles + work.blocks * (kBlockCost * kUnit);
+        const long long loaded = work.tiles + work.blocks * kBlockCost;
         const bool spare = work.blocks <= most;
         const int uncut = !p.prefix && longest > 1 &&
-                          (!spare                      ? longest <= 10
-                           : work.tiles > most * kUnit ? (2ll * longest - 7) * most <= 2 * loaded / kUnit
-                                                       : longest <= 2);
+                          (!spare              ? longest <= 10
+                           : work.tiles > most ? (2ll * longest - 7) * most <= 2 * loaded
+                                               : longest <= 2);
         // from one lane: the compiler then sees one value for the warp (0.5 %)
         const bool by_blocks = __shfl_sync(0xffffffffu, uncut, 0);
-        const int cost = by_blocks ? kBlockCost * kUnit : work.block_cost<kUnit>();
-        const long long T = by_blocks ? loaded : work.units<kUnit>();
+        // units of a tile, and how many fewer a light block's has
+        const int unit = TREE ? __shfl_sync(0xffffffffu, work.tiles > 4 * kSms ? kTreeUnits : 1, 0) : 1;
+        const int less = unit > 1 ? 1 : 0;
+        const int cost = (by_blocks ? kBlockCost : work.block_cost()) * unit;
+        const long long T = (by_blocks ? loaded : work.units()) * unit - light_all * less;
         // a range of so many units has a tile's first one in it, wherever it lies in a block
-        const int G = (int)min((long long)most, max(1ll, T / kUnit));
+        const int G = (int)min((long long)most, max(1ll, T / unit));
         const Ranges ranges(T, G);
         const int page_keys = min(1 << p.a.shift, kBN);
         const int box_bytes = page_keys * 128;
@@ -528,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nb = blocks_of(r, p.group);
                 const unsigned held = b >= kKept ? kMany : b + lane < B ? kept[b + lane] : 0;
                 long long tiles = held;
-                if (__any_sync(0xffffffffu, held == kMany)) tiles = request_tiles<JOINED, TREE>(p, r, nb, lane).sum;
+                if (__any_sync(0xffffffffu, held == kMany)) tiles = request_tiles<JOINED>(p, r, nb, lane).sum;
+                if (TREE) tiles = tiles * unit - light_tiles(p, r, nb) * less;
                 const long long units = (tiles + (long long)nb * cost) * p.a.Hkv;
                 long long incl = units;
 #pragma unroll
@@ -561,17 +580,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (!p.prefix) {
                     Request mine{0, 0, 0};
                     if (lane == 0) mine = r;
-                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED, TREE>(p, mine, lane == 0 ? nb : 0, lane).sum, 0);
+                    tiles = __shfl_sync(0xffffffffu, request_tiles<JOINED>(p, mine, lane == 0 ? nb : 0, lane).sum, 0);
                 }
+                if (TREE) tiles = tiles * unit - light_tiles(p, r, nb) * less;
                 const long long per_head = tiles + (long long)nb * cost;
                 hk = (int)((u - base) / per_head);
                 blk0 = base + (long long)hk * per_head;
                 // the block of that head: 32 at a time
                 for (blk = 0; blk < nb; blk += 32) {
                     using Count = std::conditional_t<TREE, long long, int>;  // 32 blocks' tiles, but not units, fit 32 bits
-                    const Count units = blk + lane < nb ? (Count)tiles_of<JOINED>(p, r, blk + lane, prefix_lo) *
-                                                                  units_of<TREE>(p, r, blk + lane) + cost
-                                                        : 0;
+                    Count units = 0;
+                    if (blk + lane < nb) {
+                        units = tiles_of<JOINED>(p, r, blk + lane, prefix_lo);
+                        if (TREE) units *= unit - (light(r.n * p.group.d - (blk + lane) * kRows) ? less : 0);
+                        units += cost;
+                    }
                     Count incl = units;
 #pragma unroll
                     for (int s = 1; s < 32; s <<= 1) {
@@ -603,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const long long tile0 = blk0 + cost;  // unit of its first tile
                     const bool begun = blk0 < u0;  // in the range of the CTA before
                     // a tile of several units belongs to the CTA that has the first one
-                    const int w = units_of<TREE>(p, r, blk);
+                    const int w = TREE && light(r.n * p.group.d - sg.r0) ? unit - less : unit;
                     const int first = by_blocks ? 0 : (int)((max(0ll, u - tile0) + w - 1) / w);
                     const int end =
                         !by_blocks ? (int)((min((long long)nt * w, u1 - tile0) + w - 1) / w) : begun ? 0 : nt;

@@ -92,12 +92,6 @@ __device__ __forceinline__ int pair_tiles(const PagedArgs &a, const Request &r, 
     return max(1, (r.len + TK - 1) / TK - t0);
 }
 
-// Units that a key tile counts for in the 256-row kernel's work on trees: a
-// batch of them has blocks of up to 128 rows beside larger ones, by turns with
-// the requests, and takes 1.6 and 2.05 us for a tile of theirs.
-constexpr int kTreeUnits = 5;  // more than 128 rows
-__host__ __device__ constexpr int tree_units(int rows) { return rows > kWideRows / 2 ? kTreeUnits : kTreeUnits - 1; }
-
 // Work of the 256-row kernel, in key tiles.  A row block costs its tiles and
 // as much as three more for the change from the block before (first Q, K and
 // S with nothing to overlap, last P V and epilogue).  Counted among the units,
@@ -106,11 +100,8 @@ __host__ __device__ constexpr int tree_units(int rows) { return rows > kWideRows
 constexpr int kBlockCost = 3;
 struct WideWork {
     long long tiles, blocks;
-    // U: units of a tile
-    template <int U = 1>
-    __device__ __forceinline__ int block_cost() const { return tiles > 4 * kSms * U ? kBlockCost * U : 0; }
-    template <int U = 1>
-    __device__ __forceinline__ long long units() const { return tiles + blocks * block_cost<U>(); }
+    __device__ __forceinline__ int block_cost() const { return tiles > 4 * kSms ? kBlockCost : 0; }
+    __device__ __forceinline__ long long units() const { return tiles + blocks * block_cost(); }
 };
 
 // Key tiles of a range; at least one.
@@ -153,8 +144,7 @@ __host__ __device__ __forceinline__ int block_front(const PagedArgs &a, const Fa
 // key/value head, and the most that one has.  A block's fit 32 bits, but all
 // of a prompt of N tokens are N^2 g / 65536: past 2^31 at 4 million tokens of
 // 8 grouped heads.
-// TREE: in units (kTreeUnits).
-template <bool JOINED, bool TREE = false>
+template <bool JOINED>
 __host__ __device__ __forceinline__ long long blocks_tiles(const PagedArgs &a, const FastDiv &group, const Request &r,
                                                            int from, int nb, int step, int &longest) {
     long long sum = 0;
@@ -163,7 +153,7 @@ __host__ __device__ __forceinline__ long long blocks_tiles(const PagedArgs &a, c
         int lo, hi, front_lo;
         block_keys(a, group, r, k, lo, hi);
         const int tiles = range_tiles(lo, hi) + (JOINED ? block_front(a, group, r, k, front_lo) : 0);
-        sum += TREE ? (long long)tiles * tree_units(r.n * group.d - k * kWideRows) : tiles;
+        sum += tiles;
         longest = max(longest, tiles);
     }
     return sum;
@@ -198,6 +188,7 @@ struct PlanSum {
     unsigned long long tiles, beside;  // of this kernel; of the one that runs beside it
     int blocks, low;                   // row blocks or pairs; first key of the prefix that a row sees
     int beside_blocks, longest;        // longest: tiles of a row block, at most
+    unsigned long long light;          // 256-row kernel, trees: tiles of blocks of up to 128 rows
 };
 
 // Key tiles of a request's row blocks, each counted as if it saw all keys that
