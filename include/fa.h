@@ -414,7 +414,8 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots,
  * (0 for a page of one request and for a free one, so what fa_paged_tables
  * hands out needs no entry).  Pages that several requests hold are not to be
  * written: fa_paged_fork gives a branch a page of its own where its next
- * tokens go.
+ * tokens go.  Calls that update the same table, pool, counts or pages are to
+ * follow one another (on one stream, or ordered by events).
  */
 
 /* Most forks of one fa_paged_fork call. */
