@@ -532,6 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++ns;
         };
+        // A tree's keys are read by one CTA, once, where its rows fit a block.
+        const uint64_t once = l2_evict_first();
+        bool read_once = false;
+        auto load_box = [&](void *dst, const CUtensorMap *tm, uint64_t *bar, int row, int plane) {
+            if (TREE && read_once)
+                tma_load_3d_hint(dst, tm, bar, half * 64, row, plane, once);
+            else
+                tma_load_3d(dst, tm, bar, half * 64, row, plane);
+        };
         auto load = [&](int b, Request &r) -> bool {
             if (!p.prefix) return load_request(p.a, b, r) && r.n * p.group.d > p.above;
             r = whole;
@@ -574,6 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Request r;
             if (!load(b, r)) continue;
             const int nb = blocks_of(r, p.group);
+            read_once = TREE && nb == 1;
             if (fresh) {
                 long long tiles = (long long)nb * range_tiles(prefix_lo, r.len);
                 if (!p.prefix && b < kKept && kept[b] != kMany) {
@@ -666,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) mbar_arrive_expect_tx(&k_full[ks], bytes);
                             __syncwarp();
                             if (live)
-                                tma_load_3d(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
-                                            &k_full[ks], half * 64, in_page, page * p.a.Hkv + hk);
+                                load_box(smem + L::OFF_K + ks * L::TILE + half * L::BOX + sub * box_bytes, &tm_k,
+                                         &k_full[ks], in_page, page * p.a.Hkv + hk);
                             ++nk;
                             got = nv < L::VS ||
                                   mbar_wait(&v_empty[vs], ((nv / L::VS) + 1) & 1, abort_flag, p.status, 32);
@@ -675,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) mbar_arrive_expect_tx(&v_full[vs], bytes);
                             __syncwarp();
                             if (live)
-                                tma_load_3d(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v,
-                                            &v_full[vs], half * 64, in_page, page * p.a.Hkv + hk);
+                                load_box(smem + L::OFF_V + vs * L::TILE + half * L::BOX + sub * box_bytes, &tm_v,
+                                         &v_full[vs], in_page, page * p.a.Hkv + hk);
                             ++nv;
                         }
                     };
