@@ -238,7 +238,15 @@ def paged_free(old_lens, new_lens, block_table, free_pages, free_start, page_siz
     return counts
 
 
-def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace, tree=False):
+def _most_rows(cu_seqlens) -> int:
+    """Rows of the request that has the most, read back from the device."""
+    most = 1 if cu_seqlens is None else int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
+    if most == 0:
+        raise ValueError("no request has a row")
+    return most
+
+
+def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_len, workspace):
     """(O, LSE, workspace, max_new) of a paged forward call."""
     import torch
     if window is not None and window < 1:
@@ -246,15 +254,12 @@ def _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, prefix_
     total, Hq, d = q.shape
     B, max_pages = block_table.shape
     if max_new is None:
-        max_new = 1 if cu_seqlens is None else int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item())
-        if max_new == 0:
-            raise ValueError("no request has a row")
+        max_new = _most_rows(cu_seqlens)
     o = torch.empty_like(q)
     lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
     if workspace is None:
-        sizes = B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2]
-        n = (_lib.fa_fwd_paged_tree_workspace_bytes(*sizes) if tree else
-             _lib.fa_fwd_paged_workspace_bytes(*sizes, prefix_len))
+        n = _lib.fa_fwd_paged_workspace_bytes(B, total, max_new, Hq, k_cache.shape[1], d, max_pages, k_cache.shape[2],
+                                              prefix_len)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     return o, lse, workspace, max_new
@@ -317,7 +322,9 @@ def attention_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seql
         with _on(stream):
             return attention_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, max_new,
                                             scale, window, workspace)
-    o, lse, workspace, max_new = _paged_buffers(q, k_cache, block_table, cu_seqlens, max_new, window, 0, workspace, True)
-    _lib.fa_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, o, lse, max_new,
-                           _default_scale(q.shape[-1]) if scale is None else scale, workspace, window or 0)
-    return o, lse
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    if max_new is None:
+        max_new = _most_rows(cu_seqlens)
+    return _lib.paged_tree_forward(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, max_new,
+                                   _default_scale(q.shape[-1]) if scale is None else scale, window or 0, workspace)

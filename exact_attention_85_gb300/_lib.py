@@ -116,6 +116,14 @@ def _stream(stream) -> int | None:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _handle(stream, dev: int) -> int | None:
+    """_stream for a call whose tensors are known to be on the current device, `dev`."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -423,7 +431,7 @@ def fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, share
     F, num_pages, num_free = src.numel(), shares.numel(), free_pages.numel()
     i32, dev = torch.int32, block_table.get_device()
     # one expression, as for the tables: the kernel takes some 4 us
-    if not (dev >= 0 and dev == torch.cuda.current_device() and block_table.dtype == i32 and block_table.is_contiguous()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and block_table.dtype == i32 and block_table.is_contiguous()
             and src.get_device() == dev and src.dtype == i32 and src.is_contiguous()
             and dst.get_device() == dev and dst.dtype == i32 and dst.is_contiguous()
             and seq_lens.get_device() == dev and seq_lens.dtype == i32 and seq_lens.is_contiguous()
@@ -445,7 +453,7 @@ def fa_paged_fork(src, dst, seq_lens, block_table, free_pages, free_start, share
     _check("fa_paged_fork", load().fa_paged_fork(
         src.data_ptr(), dst.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
         free_pages.data_ptr() if num_free else None, _ptr(free_start), shares.data_ptr(), copies.data_ptr(),
-        counts.data_ptr(), F, B, max_pages, int(page_size), num_pages, num_free, _stream(stream)))
+        counts.data_ptr(), F, B, max_pages, int(page_size), num_pages, num_free, _handle(stream, dev)))
 
 
 def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
@@ -454,7 +462,7 @@ def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
     shape = k_cache.shape
     num_pages, Hkv, page_size, d = shape
     code, dtype, dev, i32, n = _dtype_code(k_cache), k_cache.dtype, k_cache.get_device(), torch.int32, src.numel()
-    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and k_cache.is_contiguous()
             and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
             and src.get_device() == dev and src.dtype == i32 and src.is_contiguous()
             and dst.get_device() == dev and dst.dtype == i32 and dst.is_contiguous() and dst.numel() == n
@@ -469,7 +477,7 @@ def fa_paged_copy(src, dst, rows, k_cache, v_cache, stream=None):
         _need_int32(src=n)
     _check("fa_paged_copy", load().fa_paged_copy(
         src.data_ptr(), dst.data_ptr(), _ptr(rows), k_cache.data_ptr(), v_cache.data_ptr(), n, Hkv, d, page_size,
-        num_pages, code, _stream(stream)))
+        num_pages, code, _handle(stream, dev)))
 
 
 def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream=None):
@@ -479,7 +487,7 @@ def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, 
     shape = k_cache.shape
     num_pages, Hkv, page_size, d = shape
     code, dtype, dev, i32 = _dtype_code(k_cache), k_cache.dtype, k_cache.get_device(), torch.int32
-    if not (dev >= 0 and dev == torch.cuda.current_device() and k_cache.is_contiguous()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and k_cache.is_contiguous()
             and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
             and block_table.get_device() == dev and block_table.dtype == i32 and block_table.is_contiguous()
             and keep.get_device() == dev and keep.dtype == i32 and keep.is_contiguous()
@@ -496,7 +504,7 @@ def fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, 
         _need_int32(B=B, max_keep=max_keep, max_pages=max_pages)
     _check("fa_paged_compact", load().fa_paged_compact(
         keep.data_ptr(), keep_lens.data_ptr(), base_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), B, max_keep, max_pages, Hkv, d, page_size, num_pages, code, _stream(stream)))
+        v_cache.data_ptr(), B, max_keep, max_pages, Hkv, d, page_size, num_pages, code, _handle(stream, dev)))
 
 
 def fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, shares, counts, page_size: int,
@@ -506,7 +514,7 @@ def fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, share
     B, max_pages = block_table.shape
     num_free = free_pages.numel()
     i32, dev = torch.int32, block_table.get_device()
-    if not (dev >= 0 and dev == torch.cuda.current_device() and block_table.dtype == i32 and block_table.is_contiguous()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and block_table.dtype == i32 and block_table.is_contiguous()
             and old_lens.get_device() == dev and old_lens.dtype == i32 and old_lens.is_contiguous()
             and new_lens.get_device() == dev and new_lens.dtype == i32 and new_lens.is_contiguous()
             and free_pages.get_device() == dev and free_pages.dtype == i32 and free_pages.is_contiguous()
@@ -526,7 +534,7 @@ def fa_paged_free(old_lens, new_lens, block_table, free_pages, free_start, share
     _check("fa_paged_free", load().fa_paged_free(
         old_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr() if num_free else None,
         free_start.data_ptr(), _ptr(shares), counts.data_ptr(), B, max_pages, int(page_size), int(num_pages), num_free,
-        _stream(stream)))
+        _handle(stream, dev)))
 
 
 @functools.lru_cache(maxsize=1024)  # a function of the sizes alone
@@ -620,6 +628,52 @@ def fa_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, pa
     _check("fa_fwd_paged_tree", load().fa_fwd_paged_tree(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
         _ptr(cu_seqlens), parents.data_ptr(), *rest, _stream(stream)))
+
+
+def paged_tree_forward(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, parents, max_new: int, scale: float,
+                       window: int, workspace):
+    """fa_fwd_paged_tree on the current stream with outputs, and a workspace if
+    none is given, that are made here: (O, LSE).  The checks of that and of
+    _paged_call but for those outputs, in one place: of the 22 to 29 us of a
+    call of few tokens 4 went to doing more."""
+    import torch
+    total, Hq, d = q.shape
+    shape = k_cache.shape
+    num_pages, Hkv, page_size, dc = shape
+    B, max_pages = block_table.shape
+    code, dtype, i32, dev = _dtype_code(q), q.dtype, torch.int32, q.get_device()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice() and q.is_contiguous()
+            and k_cache.get_device() == dev and k_cache.dtype == dtype and k_cache.is_contiguous()
+            and v_cache.get_device() == dev and v_cache.dtype == dtype and v_cache.is_contiguous()
+            and block_table.get_device() == dev and block_table.dtype == i32 and block_table.is_contiguous()
+            and seq_lens.get_device() == dev and seq_lens.dtype == i32 and seq_lens.is_contiguous()
+            and parents.get_device() == dev and parents.dtype == i32 and parents.is_contiguous()
+            and (cu_seqlens is None or (cu_seqlens.get_device() == dev and cu_seqlens.dtype == i32
+                                        and cu_seqlens.is_contiguous() and cu_seqlens.numel() == B + 1))
+            and (workspace is None or (workspace.get_device() == dev and workspace.dtype == torch.uint8
+                                       and workspace.is_contiguous()))
+            and seq_lens.numel() == B and parents.numel() == total):
+        _need_all(("q", q, dtype), ("k_cache", k_cache, dtype), ("v_cache", v_cache, dtype),
+                  ("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("cu_seqlens", cu_seqlens, i32),
+                  ("parents", parents, i32), ("workspace", workspace, torch.uint8))
+        _need_numel(seq_lens=(seq_lens, B), cu_seqlens=(cu_seqlens, B + 1), parents=(parents, total))
+    if dc != d or v_cache.shape != shape:
+        raise ValueError("the caches must both be [pages,Hkv,page_size,d] with q's d")
+    if not (0 < max_new <= 0x7FFFFFFF and 0 <= window <= 0x7FFFFFFF and B <= 0x7FFFFFFF and max_pages <= 0x7FFFFFFF):
+        _need_int32(max_new=max_new, window=window, B=B, max_pages=max_pages)
+    o, lse = torch.empty_like(q), q.new_empty((Hq, total), dtype=torch.float32)
+    if workspace is None:
+        n = fa_fwd_paged_tree_workspace_bytes(B, total, max_new, Hq, Hkv, d, max_pages, page_size)
+        if n:
+            workspace = q.new_empty(n, dtype=torch.uint8)
+    else:
+        n = workspace.numel()
+    _check("fa_fwd_paged_tree", load().fa_fwd_paged_tree(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), parents.data_ptr(), o.data_ptr(), lse.data_ptr(), B, total,
+        int(max_new), Hq, Hkv, d, max_pages, page_size, num_pages, int(window), float(scale), code,
+        None if workspace is None else workspace.data_ptr(), n, torch._C._cuda_getCurrentRawStream(dev)))
+    return o, lse
 
 
 def fa_get_device_status(stream=None) -> int:
