@@ -221,7 +221,9 @@ def paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, str
 def paged_free(old_lens, new_lens, block_table, free_pages, free_start, page_size: int, num_pages: int, shares=None,
                stream=None):
     """Takes the pages behind new_lens [B] back from requests that had
-    old_lens [B] tokens (a request that ends keeps 0).
+    old_lens [B] tokens (a request that ends keeps 0).  The lengths are the
+    caller's: they have to become new_lens before the next call that reads
+    them, or it takes pages that are in the pool for the request's.
 
     All tensors are int32 on the device.  A page that ``shares`` [num_pages]
     says further requests hold loses holders, and is freed only with its last

@@ -498,7 +498,9 @@ fa_status_t fa_paged_compact(const int *keep, const int *keep_lens,
  * free list's next entry, in the order of the first request and cell that
  * gives each up:
  *   free_pages[free_start - freed + i], i < freed
- * (the list's entries below free_start are those handed out before).
+ * (the list's entries below free_start are those handed out before).  Lengths
+ * and table rows are left to the caller: a call that still took a request for
+ * old_lens[b] tokens would read, write or share pages that are in the list.
  *   old_lens, new_lens [B] (in): 0 <= new <= old <= max_pages * page_size
  *   block_table [B][max_pages] (in); rows are left as they are
  *   free_pages [num_free] (in/out), free_start [1] (in): 0 .. num_free
