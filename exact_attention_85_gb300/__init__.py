@@ -191,7 +191,8 @@ def paged_fork(src, dst, seq_lens, block_table, free_pages, shares, page_size: i
     each fork, to be given to ``paged_copy`` for every layer's cache (-1, -1,
     0 where nothing is to be copied), and the next ``free_start`` with the
     number of pages lacking.  A fork that the pool had no page for gets
-    length 0."""
+    length 0.  Pages that row dst[f] held before are not given back: end its
+    request by ``paged_free`` first."""
     if stream is not None:
         with _on(stream):
             return paged_fork(src, dst, seq_lens, block_table, free_pages, shares, page_size, free_start)
@@ -213,8 +214,12 @@ def paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, str
     token base_lens[b] + keep[b][i] becomes token base_lens[b] + i, for
     i < keep_lens[b].  ``keep`` [B,max_keep] is strictly increasing within a
     request: the accepted path of a tree of drafted tokens, or what is left of
-    a long context.  int32 tensors; the request has base_lens + keep_lens
-    tokens then (``paged_free`` takes the pages behind them back)."""
+    a long context.  Tokens may only move to pages that no other request holds:
+    on one that ``paged_fork`` shared, the other holders' tokens would be
+    overwritten, and nothing reports it.  (A branch's shared pages
+    lie before the place where it branched, its drafted tokens behind.)  int32 tensors; the
+    request has base_lens + keep_lens tokens then (``paged_free`` takes the
+    pages behind them back)."""
     _lib.fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream)
 
 
@@ -317,7 +322,8 @@ def attention_fwd_paged_tree(q, k_cache, v_cache, block_table, seq_lens, cu_seql
     the row of its request, counted from 0, that a row's token follows, below
     its own, or -1 where it follows the context.  A row sees the context, its
     path up to there and itself (``window``: the last ``window`` tokens of
-    these).  At most 1024 rows a request.  ``workspace``: as there, of
+    these).  At most 1024 rows a request; paths of hundreds of tokens take many
+    times as long as the same rows in ``attention_fwd_paged``.  ``workspace``: as there, of
     ``_lib.fa_fwd_paged_tree_workspace_bytes(B, total, max_new, Hq, Hkv, d,
     max_pages, page_size)`` bytes."""
     if stream is not None:

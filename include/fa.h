@@ -434,7 +434,8 @@ fa_status_t fa_paged_append(const void *k, const void *v, const int *slots,
  * A fork with part > 0 whose page would lie behind the list's end is not
  * served: seq_lens[dst] = 0, its table row and all counts stay as they are.
  *   src, dst [F] (in): rows of the table; no row may occur twice in dst, or
- *       in both (what such rows then hold is not defined)
+ *       in both (what such rows then hold is not defined).  Pages that row
+ *       dst[f] held before are not given back: fa_paged_free is to come first
  *   seq_lens [B], block_table [B][max_pages], shares [num_pages] (in/out)
  *   free_pages, free_start: as in fa_paged_tables
  *   copies [3][F] (out): source page, new page, rows of it; -1, -1, 0 for a
@@ -477,7 +478,8 @@ fa_status_t fa_paged_copy(const int *src, const int *dst, const int *rows,
  *   keep_lens, base_lens [B] (in); block_table [B][max_pages] (in)
  *   k_cache, v_cache (in/out): only the places of tokens that move are
  *       written (keep[b][i] = i stays); the pages of those places must be the
- *       request's own
+ *       request's own (not shared: the call does not know who else holds a
+ *       page, and would overwrite the others' tokens)
  * All index arrays are int32 on the device.  Entries out of order or beyond
  * the table's row, and page numbers outside 0 .. num_pages - 1, are reported
  * by fa_get_device_status, never read or written out of range, and their
@@ -617,6 +619,9 @@ size_t fa_fwd_paged_tree_workspace_bytes(int B, int total, int max_new, int Hq,
  *   no context, and its first rows no keys: they see of their paths what is
  *   there.  A parent out of its range is reported by fa_get_device_status and
  *   counts as -1.
+ *   Paths are walked token by token where a key/value head has more than 16
+ *   rows: time grows with their lengths, to many times the attention's for
+ *   paths of hundreds (fa_fwd_paged takes chains of any length as they are).
  *   workspace: at least fa_fwd_paged_tree_workspace_bytes(...) bytes.
  *   Otherwise as fa_fwd_paged.
  */
