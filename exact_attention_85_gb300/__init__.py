@@ -216,9 +216,9 @@ def paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, str
     request: the accepted path of a tree of drafted tokens, or what is left of
     a long context.  Tokens may only move to pages that no other request holds:
     on one that ``paged_fork`` shared, the other holders' tokens would be
-    overwritten, and nothing reports it.  (A branch's shared pages
-    lie before the place where it branched, its drafted tokens behind.)  int32 tensors; the
-    request has base_lens + keep_lens tokens then (``paged_free`` takes the
+    overwritten, and nothing reports it.  (A branch's shared pages lie before
+    the place where it branched, its drafted tokens behind.)  int32 tensors;
+    the request has base_lens + keep_lens tokens then (``paged_free`` takes the
     pages behind them back)."""
     _lib.fa_paged_compact(keep, keep_lens, base_lens, block_table, k_cache, v_cache, stream)
 

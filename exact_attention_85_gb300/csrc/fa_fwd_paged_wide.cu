@@ -194,7 +194,8 @@ __device__ __noinline__ RequestTiles request_tiles(const WideParams &p, Request 
 // larger ones (two, bound by their chain), by turns with the requests.  us with
 // 1:1, 4:5 and 7:8: 32 requests of 333-7506 keys and 17-63 tokens 130.9, 128.1,
 // 127.6; of 4000 keys 127.7, 123.3, 123.6; 64 of 2-3k and 5-63 163.8, 156.7,
-// 157.2; 24 of 333-16k and 9-100 147.4, 143.1, 140.3.
+// 157.2; 24 of 333-16k and 9-100 147.4, 143.1, 140.3.  Either weight is better
+// than none; between the two these do not decide.
 // Where there are only a few tiles for every SM they count alike: ranges of
 // whole tiles lie better in the blocks (one request of 64 tokens behind 4000
 // keys 23.1 us, weighed 28.0).
@@ -285,7 +286,14 @@ __device__ __forceinline__ size_t tree_slot(const PagedArgs &a, int g) {
 // Which drafted keys the tokens of a segment see (PagedArgs), by the helpers'
 // threads: each takes a token and a tile of 128 keys, walks the token's path,
 // up as far as the tile begins, and sets the bits that fall into it.  The
-// parents stay in L1, and the segment's first tiles are worked on meanwhile.
+// parents stay in L1.  Without a window the segment's first tiles are worked on
+// meanwhile; under one a row needs its depth before its first.  A step up the
+// path is a load that waits for the one before, and every segment walks anew:
+// where tokens hang on random ones (paths of a few ln n) that does not show, on
+// long paths it is what a call takes.  One request behind 333 keys, 8 heads in
+// groups of 1, us with random parents, as a chain, and by the causal forward:
+// 63 tokens 15, 29, 13; 256 tokens 37, 175, 17; 1024 tokens 125, 2740, 29; in
+// groups of 4 19, 33, 16; 27, 79, 21; 57, 930, 33.
 __device__ __forceinline__ void tree_walk(const WideParams &p, const Segment &sg, int g, int rows, int id) {
     const PagedArgs &a = p.a;
     const int t0 = sg.r0 / p.group, tokens = (sg.r0 + rows - 1) / p.group - t0 + 1;
@@ -532,10 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++ns;
         };
-        // A tree's keys are read by one CTA, once, where its rows fit a block:
-        // evicted first, they leave L2 to the parts that the merge reads (32
-        // requests of 17-63 tokens 127.8 us and 122.8, 64 of 8-16k keys 528
-        // and 519; all of one size as long as their chains again).
+        // A tree's keys are read by one CTA, once, where its rows fit a block
+        // and its pages are its own: evicted first, they leave L2 to the parts
+        // that the merge reads (32 requests of 17-63 tokens 127.8 us and 122.8,
+        // 64 of 8-16k keys 528 and 519; all of one size as long as their chains
+        // again).  Pages that requests share are read once by each holder, at
+        // about the same time, and lose nothing: 8, 15 and 32 branches of 32
+        // tokens behind one prompt of 16k keys 102, 176 and 348 us without,
+        // 100, 172 and 344; of 64k keys 341, 640 and 1302, and 336, 631, 1289.
         const uint64_t once = l2_evict_first();
         bool read_once = false;
         auto load_box = [&](void *dst, const CUtensorMap *tm, uint64_t *bar, int row, int plane) {

@@ -81,7 +81,7 @@ struct ForkParams {
 // a page are counted once for all forks of a row: the first fork of the row
 // that is served adds their number.  Bound by latency (lengths, cells, counts
 // one behind the other) and, beside it, the calling program: 8 forks of 31
-// pages 3.0 us, 960 forks of 500 thousand cells 7.2.
+// pages 3.3 us, 960 forks of 500 thousand cells 7.2.
 __global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const ForkParams p) {
     extern __shared__ int smem[];
     const int F = p.a.F;
@@ -420,10 +420,11 @@ __device__ __forceinline__ int cluster_load(const int *mine, int rank) {
 //   3  the cell that finds its own number has the page; they are counted
 //   4  and write the pages, by the counts of the warps before, and the zeros
 // with barriers of the cluster between them.  Without, every cell has its page.
-// Bound by scattered accesses, four a cell, of the SMs of one cluster: 131
-// thousand cells of 1024 requests 35 us, without counts 16 (with 8 CTAs that
-// looked the pages up in every pass 87); 30 cells of 16 requests 7.2, most of
-// it start and sums.
+// Bound by scattered accesses, four a cell, of at most 16 SMs: one launch with
+// one cluster is what this takes for its barriers, at the price of the GPU's
+// other SMs.  131 thousand cells of 1024 requests 35 us, without counts 16 (with
+// 8 CTAs that looked the pages up in every pass 87); 30 cells of 16 requests
+// 7.3, most of it start and sums.
 template <bool SHARED>
 __global__ void __launch_bounds__(kFreeThreads) paged_free_kernel(const FreeParams p) {
     extern __shared__ int smem[];
